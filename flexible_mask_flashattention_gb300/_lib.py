@@ -6,6 +6,7 @@ There is no fallback: if the library is missing, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Iterable, Optional, Sequence, Tuple
@@ -47,6 +48,12 @@ class PlanInfoC(ctypes.Structure):
                 ("row_intervals", ctypes.c_int64), ("key_intervals", ctypes.c_int64),
                 ("bwd_items", ctypes.c_int64), ("plan_bytes", ctypes.c_int64),
                 ("bwd_chunk_tiles", ctypes.c_int32), ("plan_launches", ctypes.c_int32)]
+
+
+class KVCacheC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -109,6 +116,23 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.ffa_bwd_noalloc.restype = ctypes.c_int
     lib.ffa_bwd_noalloc.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _vp,
                                     ctypes.c_float, _vp, _vp, _vp, _vp]
+    norm_args = [_vp, _i64, _vp, _i64, _i64, _i32, _i32, _i32, _vp, _vp, ctypes.c_float, _vp, _i64, _i32, _i32, _vp]
+    lib.ffa_qk_norm_rope.restype = ctypes.c_int
+    lib.ffa_qk_norm_rope.argtypes = norm_args + [_vp, _vp, _vp]
+    lib.ffa_qk_norm_rope_bwd_workspace_size.restype = ctypes.c_size_t
+    lib.ffa_qk_norm_rope_bwd_workspace_size.argtypes = [_i32]
+    lib.ffa_qk_norm_rope_bwd.restype = ctypes.c_int
+    lib.ffa_qk_norm_rope_bwd.argtypes = norm_args + [_vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    cache = ctypes.POINTER(KVCacheC)
+    lib.ffa_kv_cache_write.restype = ctypes.c_int
+    lib.ffa_kv_cache_write.argtypes = [_vp, _i64, _vp, _i64, _i64, _vp, cache, _vp]
+    lib.ffa_kv_cache_read.restype = ctypes.c_int
+    lib.ffa_kv_cache_read.argtypes = [cache, _vp, _i64, _i32, _i32, _vp, _i64, _vp, _vp, _vp]
+    lib.ffa_fwd_decode_workspace_size.restype = ctypes.c_size_t
+    lib.ffa_fwd_decode_workspace_size.argtypes = [_i32, _i32, _i32]
+    lib.ffa_fwd_decode.restype = ctypes.c_int
+    lib.ffa_fwd_decode.argtypes = [_vp, _i64, cache, _vp, _i64, _i32, _i32, _i32, _vp, _vp, ctypes.c_float, _vp, _vp,
+                                   _vp, _vp, ctypes.c_size_t, _vp]
     lib.ffa_selftest_bounded_wait.restype = ctypes.c_int
     lib.ffa_selftest_bounded_wait.argtypes = [_vp, ctypes.POINTER(ctypes.c_uint32), ctypes.POINTER(ctypes.c_uint32)]
     lib.ffa_plan_enable_cta_trace.restype = ctypes.c_int
@@ -451,3 +475,218 @@ def bwd(q, k, v, out, lse, dout, plan: Plan, scale: float, dq=None, dk=None, dv=
                                   dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), workspace.numel(),
                                   _stream_handle(stream)), "ffa_bwd")
     return dq, dk, dv
+
+
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _on(stream):
+    """The context in which tensors are allocated for use on `stream` (None: the current stream)."""
+    if stream is None:
+        return _NO_CONTEXT
+    import torch
+    if isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    handle = int(_stream_handle(stream))
+    return torch.cuda.stream(torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream())
+
+
+def _rows_stride(t, name, heads=None, d=None, tokens=None):
+    """The token stride of a bf16 CUDA tensor [tokens, heads, d] whose heads are contiguous within a token."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3:
+        raise FFAError(1, f"{name} must be a CUDA bfloat16 tensor [tokens, heads, d]")
+    n, h, w = t.shape
+    if (heads is not None and h != heads) or (d is not None and w != d) or (tokens is not None and n != tokens):
+        raise FFAError(1, f"{name} has shape {tuple(t.shape)}, expected {(tokens, heads, d)}")
+    s = t.stride()
+    if (w > 1 and s[2] != 1) or (h > 1 and s[1] != w):
+        raise FFAError(1, f"{name} must hold each token's heads contiguously")
+    return s[0] if n > 1 else h * w
+
+
+def _same_device(first, *rest):
+    """Check that the tensors (None: absent) are all on the current device."""
+    import torch
+    dev = first.get_device()
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            raise FFAError(1, "all tensors must be on one device")
+    if dev != torch.cuda.current_device():
+        raise FFAError(1, f"the tensors are on cuda:{dev}, which is not the current device")
+
+
+def _kv_cache(k_cache, v_cache, k_exp, v_exp) -> KVCacheC:
+    """The C description of a cache: k, v [pages, hkv, page_size, d] bf16, or float8_e4m3fn with exponent bytes."""
+    import torch
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise FFAError(1, "k_cache must be a bfloat16 or float8_e4m3fn tensor")
+    if k_cache.dim() != 4:
+        raise FFAError(1, "k_cache must be [pages, hkv, page_size, d]")
+    _need(k_cache, k_cache.dtype, "k_cache")
+    _need(v_cache, k_cache.dtype, "v_cache", k_cache.shape)
+    pages, hkv, page_size, d = k_cache.shape
+    quantised = k_cache.dtype == torch.float8_e4m3fn
+    if quantised:
+        _need(k_exp, torch.uint8, "k_exp", (pages, hkv, page_size))
+        _need(v_exp, torch.uint8, "v_exp", (pages, hkv, page_size))
+    elif k_exp is not None or v_exp is not None:
+        raise FFAError(1, "a bfloat16 cache has no exponent bytes")
+    return KVCacheC(k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr() if quantised else None,
+                    v_exp.data_ptr() if quantised else None, pages, page_size, hkv, d, int(quantised))
+
+
+def _page_table(t, batch: int) -> int:
+    """The row stride of an int32 page table [batch, max_pages]."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or t.dim() != 2:
+        raise FFAError(1, "page_table must be a CUDA int32 tensor [batch, max_pages]")
+    if t.shape[0] != batch:
+        raise FFAError(1, f"page_table has {t.shape[0]} rows, expected {batch}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise FFAError(1, "page_table rows must be contiguous")
+    return t.stride(0) if batch > 1 else t.shape[1]
+
+
+def _norm_rope_inputs(q, k, q_weight, k_weight, cos_sin, positions):
+    """Checked (token strides of q and k, sizes) of the inputs both directions share."""
+    import torch
+    qs = _rows_stride(q, "q")
+    tokens, hq, d = q.shape
+    ks = _rows_stride(k, "k", None, d, tokens)
+    _need(q_weight, torch.float32, "q_weight", (d,))
+    _need(k_weight, torch.float32, "k_weight", (d,))
+    _need(positions, torch.int32, "positions", (tokens,))
+    _need(cos_sin, torch.float32, "cos_sin")
+    if cos_sin.dim() != 2:
+        raise FFAError(1, "cos_sin must be [max_pos, rot_dim]")
+    _same_device(q, k, q_weight, k_weight, cos_sin, positions)
+    return qs, ks, tokens, hq, k.shape[1], d
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6, interleaved: bool = False,
+                 q_out=None, k_out=None, stream=None):
+    """(q_out, k_out): every head row of q [S, Hq, d] and k [S, Hkv, d] divided by its RMS, times its
+    weight [d] (fp32), and rotated by its token's position (int32 [S]) with cos_sin [max_pos, rot_dim]
+    (fp32; the cosines first).  q and k may be views of one projection's output."""
+    import torch
+    qs, ks, tokens, hq, hkv, d = _norm_rope_inputs(q, k, q_weight, k_weight, cos_sin, positions)
+    with _on(stream):
+        if q_out is None:
+            q_out = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=q.device)
+        if k_out is None:
+            k_out = torch.empty((tokens, hkv, d), dtype=torch.bfloat16, device=q.device)
+    _need(q_out, torch.bfloat16, "q_out", (tokens, hq, d))
+    _need(k_out, torch.bfloat16, "k_out", (tokens, hkv, d))
+    _same_device(q, q_out, k_out)
+    _check(load_library().ffa_qk_norm_rope(
+        q.data_ptr(), qs, k.data_ptr(), ks, tokens, hq, hkv, d, q_weight.data_ptr(), k_weight.data_ptr(), eps,
+        cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(interleaved), positions.data_ptr(),
+        q_out.data_ptr(), k_out.data_ptr(), _stream_handle(stream)), "ffa_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk_out, eps: float = 1e-6,
+                     interleaved: bool = False, workspace=None, stream=None):
+    """dq, dk (bf16) and dq_weight, dk_weight (fp32 [d]) of qk_norm_rope, from the gradients of its outputs."""
+    import torch
+    qs, ks, tokens, hq, hkv, d = _norm_rope_inputs(q, k, q_weight, k_weight, cos_sin, positions)
+    _need(dq_out, torch.bfloat16, "dq_out", (tokens, hq, d))
+    _need(dk_out, torch.bfloat16, "dk_out", (tokens, hkv, d))
+    with _on(stream):
+        dq = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=q.device)
+        dk = torch.empty((tokens, hkv, d), dtype=torch.bfloat16, device=q.device)
+        dw = torch.empty((2, d), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8, device=q.device)
+    _need(workspace, torch.uint8, "workspace")
+    _same_device(q, dq_out, dk_out, workspace)
+    dqw, dkw = dw[0], dw[1]
+    _check(load_library().ffa_qk_norm_rope_bwd(
+        q.data_ptr(), qs, k.data_ptr(), ks, tokens, hq, hkv, d, q_weight.data_ptr(), k_weight.data_ptr(), eps,
+        cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(interleaved), positions.data_ptr(),
+        dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _stream_handle(stream)), "ffa_qk_norm_rope_bwd")
+    return dq, dk, dqw, dkw
+
+
+def qk_norm_rope_bwd_workspace_size(d: int) -> int:
+    return int(load_library().ffa_qk_norm_rope_bwd_workspace_size(int(d)))
+
+
+def kv_cache_write(k, v, k_cache, v_cache, slots, k_exp=None, v_exp=None, stream=None):
+    """Write the rows of k, v [T, Hkv, d] into the cache [pages, Hkv, page_size, d] at slots (int64 [T]: page *
+    page_size + offset; negative or outside: not written).  A float8_e4m3fn cache holds codes and, in k_exp / v_exp
+    [pages, Hkv, page_size] uint8, each row's exponent: value = code * 2^(byte - 127)."""
+    import torch
+    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp)
+    ks = _rows_stride(k, "k", cache.hkv, cache.d)
+    vs = _rows_stride(v, "v", cache.hkv, cache.d, k.shape[0])
+    _need(slots, torch.int64, "slots", (k.shape[0],))
+    _same_device(k, v, k_cache, v_cache, slots, k_exp, v_exp)
+    _check(load_library().ffa_kv_cache_write(k.data_ptr(), ks, v.data_ptr(), vs, k.shape[0], slots.data_ptr(),
+                                             ctypes.byref(cache), _stream_handle(stream)), "ffa_kv_cache_write")
+
+
+def kv_cache_read(k_cache, v_cache, page_table, cu_seqlens, total: int, k=None, v=None, k_exp=None, v_exp=None,
+                  stream=None):
+    """k, v [total, Hkv, d] bf16: the first cu_seqlens[b + 1] - cu_seqlens[b] (int32 [B + 1]) keys and values of
+    every sequence, back to back; page_table [B, max_pages] int32.  Rows behind the last sequence are left as they
+    were (undefined where k and v are allocated here)."""
+    import torch
+    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp)
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise FFAError(1, "cu_seqlens must be an int32 tensor [batch + 1]")
+    _need(cu_seqlens, torch.int32, "cu_seqlens")
+    batch = cu_seqlens.shape[0] - 1
+    ts = _page_table(page_table, batch)
+    shape = (int(total), cache.hkv, cache.d)
+    if shape[0] < 0:
+        raise FFAError(1, "total must not be negative")
+    with _on(stream):
+        k = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) if k is None else k
+        v = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) if v is None else v
+    _need(k, torch.bfloat16, "k", shape)
+    _need(v, torch.bfloat16, "v", shape)
+    _same_device(k_cache, v_cache, page_table, cu_seqlens, k, v, k_exp, v_exp)
+    _check(load_library().ffa_kv_cache_read(ctypes.byref(cache), page_table.data_ptr(), ts, page_table.shape[1], batch,
+                                            cu_seqlens.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(),
+                                            _stream_handle(stream)), "ffa_kv_cache_read")
+    return k, v
+
+
+def fwd_decode_workspace_size(hq: int, hkv: int, d: int) -> int:
+    return int(load_library().ffa_fwd_decode_workspace_size(int(hq), int(hkv), int(d)))
+
+
+def fwd_decode(q, k_cache, v_cache, page_table, kv_lens, scale: float, k_exp=None, v_exp=None, kv_starts=None,
+               sink=None, out=None, lse=None, workspace=None, stream=None):
+    """out [B, Hq, d] bf16 and lse [Hq, B] fp32 of one new token a sequence, q [B, Hq, d], over the keys
+    [kv_starts[b], kv_lens[b]) (int32 [B]) of the paged cache; sink [Hq] fp32 as in fwd_sink."""
+    import torch
+    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp)
+    qs = _rows_stride(q, "q", None, cache.d)
+    b, hq, d = q.shape
+    ts = _page_table(page_table, b)
+    _need(kv_lens, torch.int32, "kv_lens", (b,))
+    if kv_starts is not None:
+        _need(kv_starts, torch.int32, "kv_starts", (b,))
+    if sink is not None:
+        _need(sink, torch.float32, "sink", (hq,))
+    with _on(stream):
+        if out is None:
+            out = torch.empty((b, hq, d), dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty((hq, b), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(fwd_decode_workspace_size(hq, cache.hkv, d), dtype=torch.uint8, device=q.device)
+    _need(out, torch.bfloat16, "out", (b, hq, d))
+    _need(lse, torch.float32, "lse", (hq, b))
+    _need(workspace, torch.uint8, "workspace")
+    _same_device(q, k_cache, v_cache, page_table, kv_lens, kv_starts, k_exp, v_exp, sink, out, lse, workspace)
+    _check(load_library().ffa_fwd_decode(
+        q.data_ptr(), qs, ctypes.byref(cache), page_table.data_ptr(), ts, page_table.shape[1], b, hq,
+        kv_lens.data_ptr(), None if kv_starts is None else kv_starts.data_ptr(), scale,
+        None if sink is None else sink.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _stream_handle(stream)), "ffa_fwd_decode")
+    return out, lse

@@ -1,0 +1,746 @@
+// Attention of one new token a sequence over the paged key-value cache, split over the cache's length and joined.
+//
+// For sequence b, q head h (kv head h / (hq / hkv)) and the keys j in [start_b, len_b):
+//   s_j = scale q . k_j,  lse = ln(sum_j e^{s_j} [+ e^{sink_h}]),  out = sum_j e^{s_j - lse} v_j.
+//
+// Bound by HBM: every stored key and value is read once, 4 hq / hkv FLOPs a byte (e4m3) or half that (bf16), far under what the tensor cores need
+// to be busy.  So the design is about keeping loads in flight:
+//   - The batch's keys are counted in blocks of 16 keys a warp; all (sequence, kv head) units' blocks form one list,
+//     dealt to the CTAs in equal contiguous shares (paged.cuh: share_begin).  Ragged lengths and few long sequences
+//     balance the same way, and no length has to be known on the host.
+//   - A warp streams its own 16-key strips (K, V, exponent bytes) through a ring in shared memory with cp.async, across
+//     unit borders, and never waits for another warp until a unit's part ends.
+//   - Scores are computed transposed, S^T = K Q^T, with 16 keys as the rows and up to 8 q heads of the group as the
+//     columns of mma.m16n8k16, and out^T = V^T P^T.  A group rarely has more than 8 heads, and this shape wastes
+//     half of what 16 query rows would.  (tcgen05 wants 64 rows at least and its operands in shared
+//     memory in their multiplied type; here the codes are widened on the way from shared memory to registers.)
+//   - The contraction order of an MMA is free as long as both operands agree: a thread takes 16 consecutive bytes of a K
+//     row as the contraction elements of several MMAs, and of V it owns whole column chunks, so both are read by
+//     16-byte loads without a transposition; a byte permutation pairs two keys' values.
+//
+// Types.  bf16 cache: bf16 MMAs; P goes in as a bf16 value plus the bf16 value of its remainder, so that its rounding
+// does not add to the output's.  e4m3 cache: codes are exact in f16; q is scaled by a power of two a row to f16's top range (its bf16
+// mantissa fits, values 2^-29 of the row's largest and below round); the scale of a key's row multiplies its score, the scale
+// of a value's row its weight, relative to the largest seen; P is f16 (11 bits).  Scores, maxima, sums and the output
+// accumulate in fp32.
+//
+// Split parts go to the workspace as (m, l, O) and a second kernel joins them in a fixed order.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "ffa_internal.h"
+#include "kv_cache.h"
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace ffa {
+namespace {
+
+constexpr int kW = 8;                  // warps a CTA
+constexpr int kThreads = 32 * kW;
+constexpr int kBlock = 16 * kW;        // keys of a block
+constexpr int kMaxCtas = 512;          // split parts the workspace holds: two a CTA
+constexpr int kSmemMax = 226 * 1024;   // of 227 KB
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// What a CTA leaves for the join: the unit that begins in its last part and goes on in later CTAs.
+struct JoinDesc {
+  int32_t parts;   // 0: none
+  int32_t batch, unit;
+  int32_t first_slot;
+  int32_t pad[4];
+};
+
+struct DecodeParams {
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  const void* k;
+  const void* v;
+  const uint8_t* k_exp;
+  const uint8_t* v_exp;
+  PageGeom geom;
+  const int32_t* table;
+  int64_t table_stride;
+  int32_t max_pages;
+  int32_t batch, hq, group, subs;   // group = hq / hkv; subs = units a kv head (group / (8 NT) rounded up)
+  const int32_t* lens;
+  const int32_t* starts;
+  float scale_log2;
+  const float* sink;
+  __nv_bfloat16* out;
+  float* lse;
+  JoinDesc* desc;     // [kMaxCtas]
+  float* ml;          // [2 kMaxCtas][8 NT][2]
+  float* part;        // [2 kMaxCtas][8 NT][D]
+};
+
+template <int D, bool FP8, int NT>
+struct Cfg {
+  static constexpr int ES = FP8 ? 1 : 2;
+  static constexpr int ROW = D * ES;                    // bytes a stored row
+  static constexpr int CPR = ROW / 16;                  // 16-byte chunks a row
+  static constexpr int STRIP = 16 * ROW;                // bytes of 16 rows
+  static constexpr int STAGE = 2 * STRIP + (FP8 ? 32 : 0);
+  static constexpr int JOIN = (kW / 2) * 8 * NT * D * 4 + kW * 8 * NT * 8;   // O buffers, (m, l) a warp
+  static constexpr int MISC = 1024;
+  static constexpr int STAGES = (kSmemMax - JOIN - MISC) / (kW * STAGE) < 8 ? (kSmemMax - JOIN - MISC) / (kW * STAGE) : 8;
+  static constexpr int SMEM = MISC + JOIN + kW * STAGE * STAGES;
+  static constexpr int KSTEPS = D / 16;
+  static constexpr int MT = D / 16;                     // 16-column tiles of the output
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t v) {   // transpose of an 8 x 8 matrix of 16-bit values
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+template <bool F16>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float pow2i(int e) {   // 2^e, 0 below the normal range; e <= 127
+  return e < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// Where a walk over the CTA's share of the block list stands: unit (b, u) with u = kv head * subs + sub, and block `blk` of its `nblk`.
+struct Cursor {
+  int b, u;
+  int64_t blk, nblk;
+  KeyRange r;
+  __device__ __forceinline__ void set_sequence(const DecodeParams& p, int seq) {
+    b = seq;
+    r = key_range(p.lens[seq], p.starts ? p.starts[seq] : 0, p.max_pages, p.geom.page_log2);
+    nblk = range_blocks(r, kBlock);
+  }
+  __device__ __forceinline__ void next(const DecodeParams& p, int units, bool more) {
+    if (++blk < nblk) return;
+    blk = 0;
+    if (++u < units) return;
+    u = 0;
+    if (more) set_sequence(p, b + 1);
+  }
+};
+
+// One row's four columns: sink, normalisation, the single rounding; lse by the first column's thread.
+template <int D>
+__device__ __forceinline__ void write_row(const DecodeParams& p, int b, int head, int col, float4 v, float mx, float sum, float bias) {
+  float f = 1.f;
+  mx -= bias;   // sums are held times 2^bias
+  if (p.sink) {
+    const float s2 = p.sink[head] * kLog2e;
+    const float top = fmaxf(mx, s2);
+    f = mx == -INFINITY ? 0.f : ex2_approx(mx - top);
+    sum = (mx == -INFINITY && sum == 0.f ? 0.f : sum * f) + (s2 == -INFINITY ? 0.f : ex2_approx(s2 - top));
+    mx = top;
+  }
+  const float inv = sum == 0.f ? 0.f : f / sum;
+  const float r[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+  uint2 w = make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
+  if (sum != sum) w = make_uint2(0x7fff7fffu, 0x7fff7fffu);
+  *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(b) * p.hq + head) * D + col) = w;
+  if (col == 0) p.lse[static_cast<int64_t>(head) * p.batch + b] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+}
+
+template <int D, bool FP8, int NT>
+__global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeParams p) {
+  using C = Cfg<D, FP8, NT>;
+  constexpr int NQ = 8 * NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* join_o = reinterpret_cast<float*>(smem + C::MISC);                       // [kW / 2][NQ][D]
+  float* join_ml = join_o + (kW / 2) * NQ * D;                                    // [kW][NQ][2]
+  int64_t* scan = reinterpret_cast<int64_t*>(smem);                               // [kW] warp sums, then the total
+  struct Begin { int32_t b; int64_t off; };
+  Begin* begin = reinterpret_cast<Begin*>(smem + 512);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = lane >> 2, t = lane & 3;   // an MMA fragment's row (or column) group and position in it
+  const int units = p.geom.hkv * p.subs;
+
+  // ---- this CTA's share of the block list
+  const int per = (p.batch + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b)
+    mine += range_blocks(key_range(p.lens[b], p.starts ? p.starts[b] : 0, p.max_pages, p.geom.page_log2), kBlock);
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kW; ++w) {
+    if (w < warp) before += scan[w];
+    total += scan[w];
+  }
+  total *= units;
+  const int64_t parts = total < gridDim.x ? total : gridDim.x;
+  const int64_t cta = blockIdx.x;
+  if (cta >= parts) {
+    if (tid == 0) p.desc[cta].parts = 0;
+    return;
+  }
+  const int64_t t0 = share_begin(total, parts, cta), t1 = share_begin(total, parts, cta + 1);
+  {
+    int64_t x = before * units;
+    if (t0 >= x && t0 < x + mine * units) {
+      int b = b0;
+      for (;; ++b) {
+        const int64_t nb = units * range_blocks(key_range(p.lens[b], p.starts ? p.starts[b] : 0, p.max_pages, p.geom.page_log2), kBlock);
+        if (t0 < x + nb) break;
+        x += nb;
+      }
+      begin->b = b;
+      begin->off = t0 - x;
+    }
+  }
+  __syncthreads();
+  Cursor cur;
+  cur.set_sequence(p, begin->b);
+  cur.u = static_cast<int>(begin->off / cur.nblk);
+  cur.blk = begin->off - cur.u * cur.nblk;
+  Cursor ld = cur;   // the loads' cursor runs ahead
+
+  // ---- loading one strip of this warp
+  const uint32_t ring = smem_u32(smem + C::MISC + C::JOIN) + warp * (C::STAGE * C::STAGES);
+  uint32_t stage_bad = 0;   // stages whose page the cache does not have
+  auto load_strip = [&](int stage) {
+    const int64_t first = range_first(ld.r);
+    const int64_t key0 = first + (ld.blk * kW + warp) * 16;
+    const int64_t have = ld.r.end - key0;
+    stage_bad &= ~(1u << stage);
+    if (have > 0) {
+      const int64_t page = p.table[ld.b * p.table_stride + (key0 >> p.geom.page_log2)];
+      const int off = static_cast<int>(key0 & ((1 << p.geom.page_log2) - 1));
+      const bool ok = page_ok(p.geom, page);
+      if (!ok) stage_bad |= 1u << stage;
+      const int lo = static_cast<int>(max(ld.r.start - key0, int64_t{0})), hi = ok ? static_cast<int>(min(have, int64_t{16})) : 0;
+      const int64_t row = cache_row(p.geom, ok ? page : 0, ld.u / p.subs, ok ? off : 0);
+      const uint8_t* ksrc = static_cast<const uint8_t*>(p.k) + row * C::ROW;
+      const uint8_t* vsrc = static_cast<const uint8_t*>(p.v) + row * C::ROW;
+      const uint32_t dst = ring + stage * C::STAGE;
+#pragma unroll
+      for (int i = 0; i < C::CPR / 2; ++i) {
+        const int id = lane + 32 * i, key = id / C::CPR;
+        const int bytes = key >= lo && key < hi ? 16 : 0;   // rows outside the range are filled with zeros, not read
+        const uint32_t at = dst + 16 * strip_chunk(key, id % C::CPR, C::CPR);
+        cp_async16(at, ksrc + id * 16, bytes);
+        cp_async16(at + C::STRIP, vsrc + id * 16, bytes);
+      }
+      if constexpr (FP8) {
+        if (lane < 2) cp_async16(dst + 2 * C::STRIP + 16 * lane, (lane ? p.v_exp : p.k_exp) + row, hi > 0 ? 16 : 0);
+      }
+    }
+  };
+
+  int64_t ahead = t0;
+#pragma unroll
+  for (int s = 0; s < C::STAGES - 1; ++s) {
+    if (ahead < t1) {
+      load_strip(s);
+      ++ahead;
+      ld.next(p, units, ahead < t1);
+    }
+    cp_async_commit();
+  }
+
+  // ---- per-unit state
+  uint32_t qf[NT][C::KSTEPS][2];   // Q^T fragments in the contraction order of the K loads
+  float qs[NT][2];                 // per query column: scale_log2, with the e4m3 path's power of two taken back
+  float o[NT][C::MT][4];
+  float m[NT][2], l[NT][2];
+  int ev_ref = 0;                  // e4m3: exponent byte that O's unit stands for
+  bool bad = false;
+  auto begin_unit = [&]() {
+    const int h0 = (cur.u / p.subs) * p.group, s0 = (cur.u % p.subs) * NQ;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int qi = s0 + nt * 8 + n;
+      const bool act = qi < p.group;
+      const __nv_bfloat16* src = p.q + cur.b * p.q_stride + static_cast<int64_t>(h0 + (act ? qi : 0)) * D;
+      float amax = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < C::KSTEPS; ++ks) {
+        const int at = FP8 ? (t + 4 * (ks / 4)) * 16 + 4 * (ks % 4) : (t + 4 * (ks / 2)) * 8 + 4 * (ks % 2);
+        const uint2 w = act ? __ldg(reinterpret_cast<const uint2*>(src + at)) : uint2{};
+        qf[nt][ks][0] = w.x;
+        qf[nt][ks][1] = w.y;
+        if constexpr (FP8) {
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w.x << 16)), fabsf(__uint_as_float(w.x & 0xffff0000u))));
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w.y << 16)), fabsf(__uint_as_float(w.y & 0xffff0000u))));
+        }
+      }
+      if constexpr (FP8) {
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // 2^(14 - e) brings the largest to [2^14, 2^15); the exponent kept in range for rows of zeros and of tiny values
+        const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
+        const float f = pow2i(14 - e);
+#pragma unroll
+        for (int ks = 0; ks < C::KSTEPS; ++ks)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t w = qf[nt][ks][i];
+            qf[nt][ks][i] = pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
+          }
+        // query columns 2t, 2t + 1 of the scores are rows 2t, 2t + 1 here: lanes 4 (2t), 4 (2t + 1)
+        const int e0 = __shfl_sync(0xffffffffu, e, 8 * t), e1 = __shfl_sync(0xffffffffu, e, 8 * t + 4);
+        qs[nt][0] = p.scale_log2 * pow2i(e0 - 14);
+        qs[nt][1] = p.scale_log2 * pow2i(e1 - 14);
+      } else {
+        qs[nt][0] = qs[nt][1] = p.scale_log2;
+      }
+#pragma unroll
+      for (int i = 0; i < C::MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+    ev_ref = 0;
+    bad = cur.r.bad;
+  };
+
+  // ---- one strip
+  // A row maximum is raised only when a score passes it by kLazy (log2 units): most strips then cost one vote.
+  constexpr float kLazy = FP8 ? 5.f : 8.f;
+  constexpr float kBias = FP8 ? 10.f : 0.f;   // e4m3: P is held times 2^10, at most 2^15: f16 reaches 2^-34 of the largest
+  auto strip = [&](int stage) {
+    const int64_t key0 = range_first(cur.r) + (cur.blk * kW + warp) * 16;
+    const int64_t have = cur.r.end - key0;
+    if (have <= 0) return;
+    const uint32_t kb = ring + stage * C::STAGE, vb = kb + C::STRIP;
+    bad |= (stage_bad >> stage & 1u) != 0;
+    float s[NT][2][4] = {};
+#pragma unroll
+    for (int h = 0; h < C::CPR / 4; ++h) {
+      const uint4 x = lds128(kb + 16 * strip_chunk(n, t + 4 * h, C::CPR));
+      const uint4 y = lds128(kb + 16 * strip_chunk(n + 8, t + 4 * h, C::CPR));
+      const uint32_t xa[4] = {x.x, x.y, x.z, x.w}, ya[4] = {y.x, y.y, y.z, y.w};
+      if constexpr (FP8) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a0 = e4m3x2_to_f16x2(xa[j]), a2 = e4m3x2_to_f16x2(xa[j] >> 16);
+          const uint32_t a1 = e4m3x2_to_f16x2(ya[j]), a3 = e4m3x2_to_f16x2(ya[j] >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma<true>(s[nt][j & 1], a0, a1, a2, a3, qf[nt][4 * h + j][0], qf[nt][4 * h + j][1]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma<false>(s[nt][j & 1], xa[2 * j], ya[2 * j], xa[2 * j + 1], ya[2 * j + 1], qf[nt][2 * h + j][0], qf[nt][2 * h + j][1]);
+      }
+    }
+    // keys n and n + 8 of the strip are this lane's; columns 2t, 2t + 1 of each query tile
+    const int lo = static_cast<int>(max(cur.r.start - key0, int64_t{0})), hi = static_cast<int>(min(have, int64_t{16}));
+    const bool in0 = n >= lo && n < hi, in1 = n + 8 >= lo && n + 8 < hi;
+    float ks0 = 1.f, ks1 = 1.f, vs0 = 1.f, vs1 = 1.f;
+    if constexpr (FP8) {
+      const uint32_t eb = vb + C::STRIP;
+      ks0 = exp_scale(lds8(eb + n));
+      ks1 = exp_scale(lds8(eb + n + 8));
+      const int v0 = in0 ? lds8(eb + 16 + n) : 0, v1 = in1 ? lds8(eb + 16 + n + 8) : 0;
+      const int top = max(v0, v1);
+      if (__any_sync(0xffffffffu, top > ev_ref)) {
+        const int ref = max(ev_ref, static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(top))));
+        const float f = pow2i(ev_ref - ref);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[nt][i][c] *= f;
+        ev_ref = ref;
+      }
+      vs0 = pow2i(v0 - ev_ref);
+      vs1 = pow2i(v1 - ev_ref);
+    }
+    float x[NT][4];
+    bool raise = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float v = (s[nt][0][c] + s[nt][1][c]) * qs[nt][c & 1] * (c < 2 ? ks0 : ks1);
+        x[nt][c] = (c < 2 ? in0 : in1) ? v : -INFINITY;
+        raise |= x[nt][c] > m[nt][c & 1] + kLazy;
+      }
+    }
+    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float mx = fmaxf(x[nt][c], x[nt][c + 2]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          mx = fmaxf(mx, m[nt][c]);
+          const float f = mx == -INFINITY ? 1.f : ex2_approx(m[nt][c] - mx);
+          m[nt][c] = mx;
+          l[nt][c] *= f;
+#pragma unroll
+          for (int i = 0; i < C::MT; ++i) {
+            o[nt][i][c] *= f;
+            o[nt][i][c + 2] *= f;
+          }
+        }
+    }
+    uint32_t pf[NT][2], pl[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float e[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float mm = m[nt][c & 1] == -INFINITY ? 0.f : m[nt][c & 1];
+        e[c] = ex2_approx(x[nt][c] - mm + kBias);
+      }
+      l[nt][0] += e[0] + e[2];
+      l[nt][1] += e[1] + e[3];
+      if constexpr (FP8) {
+        pf[nt][0] = movmatrix(pack_f16x2(e[0] * vs0, e[1] * vs0));
+        pf[nt][1] = movmatrix(pack_f16x2(e[2] * vs1, e[3] * vs1));
+      } else {
+        const uint32_t h0 = pack_bf16x2(e[0], e[1]), h1 = pack_bf16x2(e[2], e[3]);
+        pf[nt][0] = movmatrix(h0);
+        pf[nt][1] = movmatrix(h1);
+        pl[nt][0] = movmatrix(pack_bf16x2(e[0] - __uint_as_float(h0 << 16), e[1] - __uint_as_float(h0 & 0xffff0000u)));
+        pl[nt][1] = movmatrix(pack_bf16x2(e[2] - __uint_as_float(h1 << 16), e[3] - __uint_as_float(h1 & 0xffff0000u)));
+      }
+    }
+    // out^T += V^T P^T: this lane's four keys 2t, 2t + 1, 2t + 8, 2t + 9 and its columns
+    if constexpr (FP8) {
+      constexpr int WORDS = C::MT / 2;   // 32-bit words of a row this lane owns: 2 (d = 64) or 4
+      uint32_t r[4][WORDS];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = 2 * t + (i & 1) + 8 * (i >> 1);
+        if constexpr (D == 128) {
+          const uint4 w = lds128(vb + 16 * strip_chunk(key, n, C::CPR));
+          r[i][0] = w.x, r[i][1] = w.y, r[i][2] = w.z, r[i][3] = w.w;
+        } else {
+          const uint2 w = lds64(vb + 16 * strip_chunk(key, n >> 1, C::CPR) + 8 * (n & 1));
+          r[i][0] = w.x, r[i][1] = w.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < C::MT; ++i) {
+        const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;   // columns 2i, 2i + 1 of two keys, paired by column
+        const uint32_t w0 = __byte_perm(r[0][i / 2], r[1][i / 2], sel), w1 = __byte_perm(r[2][i / 2], r[3][i / 2], sel);
+        const uint32_t a0 = e4m3x2_to_f16x2(w0), a1 = e4m3x2_to_f16x2(w0 >> 16);
+        const uint32_t a2 = e4m3x2_to_f16x2(w1), a3 = e4m3x2_to_f16x2(w1 >> 16);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma<true>(o[nt][i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+      }
+    } else {
+#pragma unroll
+      for (int hh = 0; hh < D / 64; ++hh) {
+        uint32_t r[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 w = lds128(vb + 16 * strip_chunk(2 * t + (i & 1) + 8 * (i >> 1), n + 8 * hh, C::CPR));
+          r[i][0] = w.x, r[i][1] = w.y, r[i][2] = w.z, r[i][3] = w.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a0 = __byte_perm(r[0][i], r[1][i], 0x5410), a1 = __byte_perm(r[0][i], r[1][i], 0x7632);
+          const uint32_t a2 = __byte_perm(r[2][i], r[3][i], 0x5410), a3 = __byte_perm(r[2][i], r[3][i], 0x7632);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma<false>(o[nt][4 * hh + i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+            mma<false>(o[nt][4 * hh + i], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+          }
+        }
+      }
+    }
+  };
+
+  // ---- the end of a unit's part: join the warps, then write the rows or the part
+  auto end_part = [&](bool whole, int slot) {
+    // per-warp sums over its lanes; a bad page or length makes the part NaN
+    const float poison = __any_sync(0xffffffffu, bad) ? __int_as_float(0x7fffffff) : 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float s = l[nt][c];
+        s += __shfl_xor_sync(0xffffffffu, s, 4);
+        s += __shfl_xor_sync(0xffffffffu, s, 8);
+        s += __shfl_xor_sync(0xffffffffu, s, 16);
+        if (n == 0) {
+          float* ml = join_ml + (warp * NQ + nt * 8 + 2 * t + c) * 2;
+          ml[0] = m[nt][c];
+          ml[1] = s + poison;
+        }
+      }
+    __syncthreads();
+    float f[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) mx = fmaxf(mx, join_ml[(w * NQ + nt * 8 + 2 * t + c) * 2]);
+        f[nt][c] = m[nt][c] == -INFINITY ? 0.f : ex2_approx(m[nt][c] - mx) * (FP8 ? pow2i(ev_ref - 127) : 1.f);
+      }
+    auto column = [&](int i) { return FP8 ? (D / 8) * n + 2 * i : (i / 4) * 64 + 8 * n + 2 * (i % 4); };
+    if (warp >= kW / 2) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            *reinterpret_cast<float2*>(join_o + ((warp - kW / 2) * NQ + nt * 8 + 2 * t + c) * D + column(i)) =
+                make_float2(o[nt][i][c] * f[nt][c], o[nt][i][c + 2] * f[nt][c]);
+    }
+    __syncthreads();
+    if (warp < kW / 2) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float2* at = reinterpret_cast<float2*>(join_o + (warp * NQ + nt * 8 + 2 * t + c) * D + column(i));
+            const float2 b = *at;
+            *at = make_float2(fmaf(o[nt][i][c], f[nt][c], b.x), fmaf(o[nt][i][c + 2], f[nt][c], b.y));
+          }
+    }
+    __syncthreads();
+    const int h0 = (cur.u / p.subs) * p.group, s0 = (cur.u % p.subs) * NQ;
+    for (int i = tid; i < NQ * (D / 4); i += kThreads) {
+      const int qi = i / (D / 4), col = 4 * (i % (D / 4));
+      if (s0 + qi >= p.group) continue;
+      float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kW; ++w) mx = fmaxf(mx, join_ml[(w * NQ + qi) * 2]);
+#pragma unroll
+      for (int w = 0; w < kW; ++w) {
+        const float mw = join_ml[(w * NQ + qi) * 2], lw = join_ml[(w * NQ + qi) * 2 + 1];
+        sum += mw == -INFINITY ? lw : lw * ex2_approx(mw - mx);   // lw is 0 or NaN there
+      }
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kW / 2; ++w) {
+        const float4 a = *reinterpret_cast<const float4*>(join_o + (w * NQ + qi) * D + col);
+        v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+      }
+      if (!whole) {
+        *reinterpret_cast<float4*>(p.part + (static_cast<int64_t>(slot) * NQ + qi) * D + col) = v;
+        if (col == 0) *reinterpret_cast<float2*>(p.ml + (static_cast<int64_t>(slot) * NQ + qi) * 2) = make_float2(mx, sum);
+        continue;
+      }
+      write_row<D>(p, cur.b, h0 + s0 + qi, col, v, mx, sum, kBias);
+    }
+    __syncthreads();
+  };
+
+  // ---- the share
+  bool fresh = true, first_part = true;
+  int64_t part_begin = cur.blk;
+  int32_t opened = 0;   // parts of the unit this CTA leaves open to later ones
+  int stage = 0, fill = C::STAGES - 1;
+  for (int64_t x = t0; x < t1; ++x) {
+    if (ahead < t1) {
+      load_strip(fill);
+      ++ahead;
+      ld.next(p, units, ahead < t1);
+    }
+    cp_async_commit();
+    fill = fill + 1 == C::STAGES ? 0 : fill + 1;
+    cp_async_wait<C::STAGES - 1>();
+    __syncwarp();
+    if (fresh) {
+      begin_unit();
+      part_begin = cur.blk;
+      fresh = false;
+    }
+    strip(stage);
+    __syncwarp();   // the stage has been read by every lane before the next iteration refills it
+    stage = stage + 1 == C::STAGES ? 0 : stage + 1;
+    const bool last = cur.blk + 1 == cur.nblk;
+    if (last || x + 1 == t1) {
+      const bool whole = last && part_begin == 0;
+      const int slot = static_cast<int>(2 * cta) + (first_part ? 0 : 1);
+      end_part(whole, slot);
+      if (!last && part_begin == 0) {
+        const int64_t unit0 = x - cur.blk;
+        opened = static_cast<int32_t>(share_of(total, parts, unit0 + cur.nblk - 1) - cta + 1);
+        if (tid == 0) {
+          JoinDesc d{};
+          d.parts = opened;
+          d.batch = cur.b;
+          d.unit = cur.u;
+          d.first_slot = slot;
+          p.desc[cta] = d;
+        }
+      }
+      first_part = false;
+      fresh = true;
+    }
+    cur.next(p, units, x + 1 < t1);
+  }
+  if (opened == 0 && tid == 0) p.desc[cta].parts = 0;
+}
+
+// Joins the parts of the unit that CTA blockIdx.x of the main kernel opened, in the order of their keys.
+template <int D, int NT>
+__global__ void __launch_bounds__(256) decode_join_kernel(DecodeParams p, float bias) {
+  constexpr int NQ = 8 * NT;
+  const JoinDesc d = p.desc[blockIdx.x];
+  if (d.parts == 0) return;
+  const int h0 = (d.unit / p.subs) * p.group, s0 = (d.unit % p.subs) * NQ;
+  for (int i = threadIdx.x; i < NQ * (D / 4); i += 256) {
+    const int qi = i / (D / 4), col = 4 * (i % (D / 4));
+    if (s0 + qi >= p.group) continue;
+    float mx = -INFINITY;
+    for (int k = 0; k < d.parts; ++k) {
+      const int64_t slot = k == 0 ? d.first_slot : 2 * (static_cast<int64_t>(blockIdx.x) + k);
+      mx = fmaxf(mx, p.ml[(slot * NQ + qi) * 2]);
+    }
+    float sum = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < d.parts; ++k) {
+      const int64_t slot = k == 0 ? d.first_slot : 2 * (static_cast<int64_t>(blockIdx.x) + k);
+      const float2 ml = *reinterpret_cast<const float2*>(p.ml + (slot * NQ + qi) * 2);
+      const float4 a = *reinterpret_cast<const float4*>(p.part + (slot * NQ + qi) * D + col);
+      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
+      sum += ml.x == -INFINITY ? ml.y : ml.y * f;
+      v.x = fmaf(a.x, f, v.x), v.y = fmaf(a.y, f, v.y), v.z = fmaf(a.z, f, v.z), v.w = fmaf(a.w, f, v.w);
+    }
+    write_row<D>(p, d.batch, h0 + s0 + qi, col, v, mx, sum, bias);
+  }
+}
+
+constexpr size_t kDescBytes = sizeof(JoinDesc) * kMaxCtas;
+size_t ml_bytes(int nt) { return size_t{2} * kMaxCtas * 8 * nt * 2 * sizeof(float); }
+size_t part_bytes(int nt, int d) { return size_t{2} * kMaxCtas * 8 * nt * d * sizeof(float); }
+int tiles_of(int group) { return group > 8 ? 2 : 1; }   // query tiles of 8 a unit
+
+template <int D, bool FP8, int NT>
+ffa_status launch(const DecodeParams& p, int sms, cudaStream_t s) {
+  using C = Cfg<D, FP8, NT>;
+  static_assert(C::STAGES >= 2, "ring");
+  auto* kernel = decode_kernel<D, FP8, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return FFA_ERR_CUDA;
+  const int grid = std::min(sms, kMaxCtas);
+  kernel<<<grid, kThreads, C::SMEM, s>>>(p);
+  decode_join_kernel<D, NT><<<grid, 256, 0, s>>>(p, FP8 ? 10.f : 0.f);
+  return cuda_status(cudaGetLastError());
+}
+
+}  // namespace
+}  // namespace ffa
+
+using namespace ffa;
+
+extern "C" {
+
+size_t ffa_fwd_decode_workspace_size(int32_t hq, int32_t hkv, int32_t d) {
+  if (hq <= 0 || hkv <= 0 || hq % hkv != 0 || (d != 64 && d != 128)) return 0;
+  const int nt = tiles_of(hq / hkv);
+  return kDescBytes + ml_bytes(nt) + part_bytes(nt, d);
+}
+
+ffa_status ffa_fwd_decode(const void* q, int64_t q_stride, const ffa_kv_cache* cache, const int32_t* page_table,
+                          int64_t table_stride, int32_t max_pages, int32_t batch, int32_t hq, const int32_t* kv_lens,
+                          const int32_t* kv_starts, float scale, const float* sink, void* out, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  DecodeParams p{};
+  const ffa_status st = check_cache(cache, p.geom);
+  if (st != FFA_OK) return st;
+  if (batch < 0 || max_pages < 0 || hq <= 0 || hq % cache->hkv != 0) return FFA_ERR_INVALID_ARG;
+  if (!(scale > -INFINITY && scale < INFINITY)) return FFA_ERR_INVALID_ARG;
+  if (batch > 1 && table_stride < max_pages) return FFA_ERR_INVALID_ARG;
+  if (hq > (1 << 16) || batch > (1 << 20)) return FFA_ERR_OVERFLOW;
+  if (batch == 0) return FFA_OK;
+  const int32_t d = cache->d;
+  if (!q || !out || !lse || !kv_lens || !workspace) return FFA_ERR_INVALID_ARG;
+  if (!kv_aligned16(q) || !kv_aligned16(out) || !kv_aligned16(lse) || !kv_aligned16(workspace)) return FFA_ERR_INVALID_ARG;
+  if (max_pages > 0 && !page_table) return FFA_ERR_INVALID_ARG;
+  for (const void* a : {static_cast<const void*>(page_table), static_cast<const void*>(kv_lens),
+                        static_cast<const void*>(kv_starts), static_cast<const void*>(sink)})
+    if (reinterpret_cast<uintptr_t>(a) & 3u) return FFA_ERR_INVALID_ARG;
+  if (q_stride % 8 != 0 || (batch > 1 && q_stride < static_cast<int64_t>(hq) * d)) return FFA_ERR_INVALID_ARG;
+  if (workspace_bytes < ffa_fwd_decode_workspace_size(hq, cache->hkv, d)) return FFA_ERR_INVALID_ARG;
+  const int group = hq / cache->hkv, nt = tiles_of(group);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_stride = q_stride;
+  p.k = cache->k;
+  p.v = cache->v;
+  p.k_exp = cache->k_exp;
+  p.v_exp = cache->v_exp;
+  p.table = page_table;
+  p.table_stride = table_stride;
+  p.max_pages = max_pages;
+  p.batch = batch;
+  p.hq = hq;
+  p.group = group;
+  p.subs = (group + 8 * nt - 1) / (8 * nt);
+  p.lens = kv_lens;
+  p.starts = kv_starts;
+  p.scale_log2 = scale * kLog2e;
+  p.sink = sink;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.desc = reinterpret_cast<JoinDesc*>(ws);
+  p.ml = reinterpret_cast<float*>(ws + kDescBytes);
+  p.part = reinterpret_cast<float*>(ws + kDescBytes + ml_bytes(nt));
+  int device = 0, sms = 0;
+  if (cudaGetDevice(&device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+    return FFA_ERR_CUDA;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool fp8 = cache->dtype == FFA_KV_E4M3;
+  if (d == 128) {
+    if (nt == 1) return fp8 ? launch<128, true, 1>(p, sms, s) : launch<128, false, 1>(p, sms, s);
+    return fp8 ? launch<128, true, 2>(p, sms, s) : launch<128, false, 2>(p, sms, s);
+  }
+  if (nt == 1) return fp8 ? launch<64, true, 1>(p, sms, s) : launch<64, false, 1>(p, sms, s);
+  return fp8 ? launch<64, true, 2>(p, sms, s) : launch<64, false, 2>(p, sms, s);
+}
+
+}  // extern "C"

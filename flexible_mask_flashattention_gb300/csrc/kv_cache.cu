@@ -1,0 +1,298 @@
+// Writing rows into a paged key-value cache, quantising them on the way, and reading them back.
+//
+// The cache is [num_pages][hkv][page_size][d], so that what one kv head holds of a page is contiguous.  Stored types:
+//   bf16  the row as it is;
+//   e4m3  8-bit codes and one exponent byte a row: value = code * 2^(byte - 127), with 2^n, n >= -126, the smallest power of
+//         two for which max|x| <= 448 * 2^n.  A power of two rather than max|x| / 448: codes have an exponent of
+//         their own, so the scale's rounding up costs no mantissa bit, the division by it is exact (each value is rounded once),
+//         and every stored value is exact in bf16 down to bf16's smallest, so that reading back does not round again.
+//         A row that holds a NaN or an infinity is stored as NaN throughout (byte 127).
+//
+// Both kernels are bound by HBM: 2 d bytes a row on the tensors' side, 2 d or d + 1 on the cache's.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "ffa_internal.h"
+#include "kv_cache.h"
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace ffa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kUnroll = 4;
+
+// Parameter pair's entry by a run-time index, as a select (an indexed one would copy the parameters to local memory).
+template <typename T>
+__device__ __forceinline__ T pick(T const (&pair)[2], int i) {
+  return i ? pair[1] : pair[0];
+}
+
+struct WriteParams {
+  const __nv_bfloat16* x[2];   // k, v
+  int64_t stride[2];
+  void* cache[2];
+  uint8_t* exps[2];
+  const int64_t* slots;
+  PageGeom geom;
+  int64_t units;
+  int32_t chunks;              // warp units a token
+};
+
+__device__ __forceinline__ uint32_t absmax2(uint32_t m, uint32_t v) {   // of both bf16 halves, as bit patterns
+  const uint32_t a = v & 0x7fffu, b = (v >> 16) & 0x7fffu;
+  return max(m, max(a, b));
+}
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// A warp takes one token and up to kUnroll passes over its 2 hkv rows (k's, then v's), d / 8 lanes a row.
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kThreads) kv_cache_write_kernel(WriteParams p) {
+  constexpr int L = D / 8, RW = 32 / L;
+  const int lane = threadIdx.x & 31, l = lane & (L - 1), sub = lane / L;
+  const int64_t u = blockIdx.x * static_cast<int64_t>(kWarps) + (threadIdx.x >> 5);
+  if (u >= p.units) return;
+  const int64_t token = u / p.chunks;
+  const int row0 = static_cast<int>(u - token * p.chunks) * (kUnroll * RW);
+  const int64_t slot = p.slots[token];
+  if (!slot_ok(p.geom, slot)) return;   // padding, or no slot of this cache: nothing is written
+  const int64_t page = slot >> p.geom.page_log2;
+  const int off = static_cast<int>(slot & ((1 << p.geom.page_log2) - 1));
+  uint4 v[kUnroll];
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i) {
+    const int row = row0 + i * RW + sub, t = row >= p.geom.hkv, h = t ? row - p.geom.hkv : row;
+    v[i] = row < 2 * p.geom.hkv
+               ? __ldg(reinterpret_cast<const uint4*>(pick(p.x, t) + token * pick(p.stride, t) + static_cast<int64_t>(h) * D + 8 * l))
+               : uint4{};
+  }
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i) {
+    const int row = row0 + i * RW + sub, t = row >= p.geom.hkv, h = t ? row - p.geom.hkv : row;
+    const bool act = row < 2 * p.geom.hkv;
+    const int64_t dst = cache_row(p.geom, page, h, off);
+    if constexpr (!FP8) {
+      if (act) reinterpret_cast<uint4*>(pick(p.cache, t))[dst * (D / 8) + l] = v[i];
+    } else {
+      // bf16 magnitudes order as integers: the row's largest, by its bits
+      uint32_t m = absmax2(absmax2(absmax2(absmax2(0, v[i].x), v[i].y), v[i].z), v[i].w);
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      // max|x| = 1.f * 2^(e - 127), 448 = 1.75 * 2^8: the scale's byte is e - 8, one more where 1.f > 1.75
+      const bool finite = m < 0x7f80u;
+      const int e = static_cast<int>(m >> 7) - 8 + ((m & 0x7fu) > 0x60u);
+      const int byte = finite ? max(e, 1) : 127;
+      const float inv = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);   // 2^-(byte - 127), exact
+      const uint32_t u4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      uint32_t c[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        c[j] = e4m3x2(__uint_as_float(u4[j] << 16) * inv, __uint_as_float(u4[j] & 0xffff0000u) * inv);
+      uint2 codes = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+      if (!finite) codes = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+      if (act) {
+        reinterpret_cast<uint2*>(pick(p.cache, t))[dst * (D / 8) + l] = codes;
+        if (l == 0) pick(p.exps, t)[dst] = static_cast<uint8_t>(byte);
+      }
+    }
+  }
+}
+
+struct ReadParams {
+  const void* cache[2];
+  const uint8_t* exps[2];
+  __nv_bfloat16* out[2];
+  const int32_t* table;
+  int64_t table_stride;
+  int32_t max_pages, batch;
+  const int32_t* cu;
+  int64_t total;
+  PageGeom geom;
+};
+
+constexpr int kReadTile = 32;   // output rows (tokens) a CTA
+
+// A CTA takes kReadTile consecutive output rows; one thread a row finds its sequence and page once.
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kThreads) kv_cache_read_kernel(ReadParams p) {
+  constexpr int L = D / 8, RW = 32 / L;
+  __shared__ int64_t src[kReadTile];   // row of head 0 in the cache; -1: outside the batch, -2: no page of this cache
+  const int64_t t0 = blockIdx.x * static_cast<int64_t>(kReadTile);
+  if (threadIdx.x < kReadTile) {
+    const int64_t t = t0 + threadIdx.x;
+    int64_t at = -1;
+    if (t < p.total && t < p.cu[p.batch]) {
+      int lo = 0, hi = p.batch;   // the last sequence with cu <= t
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (p.cu[mid] <= t) lo = mid + 1; else hi = mid;
+      }
+      if (lo > 0) {
+        const int64_t pos = t - p.cu[lo - 1];
+        const int64_t pi = pos >> p.geom.page_log2;
+        at = -2;
+        if (pi < p.max_pages) {
+          const int64_t page = p.table[(lo - 1) * p.table_stride + pi];
+          if (page_ok(p.geom, page))
+            at = cache_row(p.geom, page, 0, static_cast<int>(pos & ((1 << p.geom.page_log2) - 1)));
+        }
+      }
+    }
+    src[threadIdx.x] = at;
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (L - 1), sub = lane / L;
+  const int rows = 2 * p.geom.hkv;
+  const int n = kReadTile * rows;   // head rows of the tile, a token's together
+  for (int i0 = warp * (RW * kUnroll); i0 < n; i0 += kWarps * RW * kUnroll) {
+    uint4 v[kUnroll];
+    uint32_t e[kUnroll];
+    int64_t to[kUnroll];
+    int which[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int idx = i0 + i * RW + sub;
+      const int tok = idx / rows, row = idx - tok * rows, t = row >= p.geom.hkv, h = t ? row - p.geom.hkv : row;
+      const int64_t at = idx < n ? src[tok] : -1;
+      which[i] = t;
+      to[i] = at == -1 ? -1 : ((t0 + tok) * p.geom.hkv + h) * (D / 8) + l;
+      v[i] = uint4{};
+      e[i] = 0x7fc0u;   // NaN where there is no page
+      if (at >= 0) {
+        const int64_t r = at + (static_cast<int64_t>(h) << p.geom.page_log2);
+        if constexpr (FP8) {
+          const uint2 c = __ldg(reinterpret_cast<const uint2*>(pick(p.cache, t)) + r * (D / 8) + l);
+          v[i].x = c.x, v[i].y = c.y;
+          e[i] = pick(p.exps, t)[r];
+        } else {
+          v[i] = __ldg(reinterpret_cast<const uint4*>(pick(p.cache, t)) + r * (D / 8) + l);
+          e[i] = 0;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      if (to[i] < 0) continue;
+      uint4 o = v[i];
+      if (e[i] == 0x7fc0u) {
+        o = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+      } else if constexpr (FP8) {
+        const float s = exp_scale(e[i]);
+        const uint32_t c[4] = {v[i].x & 0xffffu, v[i].x >> 16, v[i].y & 0xffffu, v[i].y >> 16};
+        uint32_t r[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = e4m3x2_to_float2(c[j]);
+          r[j] = pack_bf16x2(f.x * s, f.y * s);
+        }
+        o = make_uint4(r[0], r[1], r[2], r[3]);
+      }
+      reinterpret_cast<uint4*>(pick(p.out, which[i]))[to[i]] = o;
+    }
+  }
+}
+
+}  // namespace
+
+ffa_status check_cache(const ffa_kv_cache* c, PageGeom& g) {
+  if (!c) return FFA_ERR_INVALID_ARG;
+  if (c->num_pages <= 0 || c->hkv <= 0 || c->page_size <= 0) return FFA_ERR_INVALID_ARG;
+  if (c->d != 64 && c->d != 128) return FFA_ERR_UNSUPPORTED;
+  if (c->dtype != FFA_KV_BF16 && c->dtype != FFA_KV_E4M3) return FFA_ERR_UNSUPPORTED;
+  if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1))) return FFA_ERR_UNSUPPORTED;
+  if (c->hkv > (1 << 16) || c->num_pages > (int64_t{1} << 31)) return FFA_ERR_OVERFLOW;
+  if (!c->k || !c->v || !kv_aligned16(c->k) || !kv_aligned16(c->v)) return FFA_ERR_INVALID_ARG;
+  if (c->dtype == FFA_KV_E4M3 && (!c->k_exp || !c->v_exp || !kv_aligned16(c->k_exp) || !kv_aligned16(c->v_exp)))
+    return FFA_ERR_INVALID_ARG;
+  g.num_pages = c->num_pages;
+  g.hkv = c->hkv;
+  g.page_log2 = 0;
+  while ((1 << g.page_log2) < c->page_size) ++g.page_log2;
+  return FFA_OK;
+}
+
+}  // namespace ffa
+
+using namespace ffa;
+
+extern "C" {
+
+ffa_status ffa_kv_cache_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t tokens,
+                              const int64_t* slots, const ffa_kv_cache* cache, void* stream) {
+  WriteParams p{};
+  const ffa_status st = check_cache(cache, p.geom);
+  if (st != FFA_OK) return st;
+  if (tokens < 0) return FFA_ERR_INVALID_ARG;
+  if (tokens == 0) return FFA_OK;
+  if (!k || !v || !slots || !kv_aligned16(k) || !kv_aligned16(v) || (reinterpret_cast<uintptr_t>(slots) & 7u))
+    return FFA_ERR_INVALID_ARG;
+  const int64_t row = static_cast<int64_t>(cache->hkv) * cache->d;
+  if (k_stride % 8 != 0 || v_stride % 8 != 0 || (tokens > 1 && (k_stride < row || v_stride < row)))
+    return FFA_ERR_INVALID_ARG;
+  p.x[0] = static_cast<const __nv_bfloat16*>(k);
+  p.x[1] = static_cast<const __nv_bfloat16*>(v);
+  p.stride[0] = k_stride;
+  p.stride[1] = v_stride;
+  p.cache[0] = cache->k;
+  p.cache[1] = cache->v;
+  p.exps[0] = cache->k_exp;
+  p.exps[1] = cache->v_exp;
+  p.slots = slots;
+  const int per = kUnroll * 256 / cache->d;
+  p.chunks = (2 * cache->hkv + per - 1) / per;
+  if (tokens > (int64_t{1} << 36)) return FFA_ERR_OVERFLOW;
+  p.units = tokens * p.chunks;
+  const int64_t blocks = (p.units + kWarps - 1) / kWarps;
+  if (blocks > 0x7fffffff) return FFA_ERR_OVERFLOW;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool fp8 = cache->dtype == FFA_KV_E4M3;
+  const unsigned grid = static_cast<unsigned>(blocks);
+  if (cache->d == 128)
+    (fp8 ? kv_cache_write_kernel<128, true> : kv_cache_write_kernel<128, false>)<<<grid, kThreads, 0, s>>>(p);
+  else
+    (fp8 ? kv_cache_write_kernel<64, true> : kv_cache_write_kernel<64, false>)<<<grid, kThreads, 0, s>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
+ffa_status ffa_kv_cache_read(const ffa_kv_cache* cache, const int32_t* page_table, int64_t table_stride,
+                             int32_t max_pages, int32_t batch, const int32_t* cu_seqlens, int64_t total, void* k,
+                             void* v, void* stream) {
+  ReadParams p{};
+  const ffa_status st = check_cache(cache, p.geom);
+  if (st != FFA_OK) return st;
+  if (total < 0 || batch < 0 || max_pages < 0 || (batch > 1 && table_stride < max_pages)) return FFA_ERR_INVALID_ARG;
+  if (total == 0 || batch == 0) return FFA_OK;
+  if (!cu_seqlens || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u)) return FFA_ERR_INVALID_ARG;
+  if (max_pages > 0 && (!page_table || (reinterpret_cast<uintptr_t>(page_table) & 3u))) return FFA_ERR_INVALID_ARG;
+  if (!k || !v || !kv_aligned16(k) || !kv_aligned16(v)) return FFA_ERR_INVALID_ARG;
+  if (total > 0x7fffffff) return FFA_ERR_OVERFLOW;   // cu_seqlens is int32
+  p.cache[0] = cache->k;
+  p.cache[1] = cache->v;
+  p.exps[0] = cache->k_exp;
+  p.exps[1] = cache->v_exp;
+  p.out[0] = static_cast<__nv_bfloat16*>(k);
+  p.out[1] = static_cast<__nv_bfloat16*>(v);
+  p.table = page_table;
+  p.table_stride = table_stride;
+  p.max_pages = max_pages;
+  p.batch = batch;
+  p.cu = cu_seqlens;
+  p.total = total;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool fp8 = cache->dtype == FFA_KV_E4M3;
+  const unsigned grid = static_cast<unsigned>((total + kReadTile - 1) / kReadTile);
+  if (cache->d == 128)
+    (fp8 ? kv_cache_read_kernel<128, true> : kv_cache_read_kernel<128, false>)<<<grid, kThreads, 0, s>>>(p);
+  else
+    (fp8 ? kv_cache_read_kernel<64, true> : kv_cache_read_kernel<64, false>)<<<grid, kThreads, 0, s>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
+}  // extern "C"

@@ -1,0 +1,30 @@
+// What the kernels over the paged key-value cache share.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "ffa_internal.h"
+#include "paged.cuh"
+
+namespace ffa {
+
+inline bool kv_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Host check of a cache description; fills its geometry.
+ffa_status check_cache(const ffa_kv_cache* c, PageGeom& g);
+
+// 2^(byte - 127), the scale an exponent byte stands for (0 for byte 0, which no write stores).
+__device__ __forceinline__ float exp_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// Two e4m3 codes as two f16 values, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
+  return r;
+}
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
+  const uint32_t h = e4m3x2_to_f16x2(codes);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+}  // namespace ffa

@@ -379,6 +379,157 @@ ffa_status ffa_range_gather(const void* src, int64_t src_rows, int64_t row_bytes
 ffa_status ffa_range_scatter_reduce(const void* src, const int64_t* ranges, int64_t n_ranges, int64_t row_elems,
                                     int32_t dtype, void* dst, int64_t dst_rows, void* stream);
 
+/*
+ * RMS norm of every query and key head row with the position rotation in the
+ * same pass: what comes between the q/k projections and ffa_fwd or
+ * ffa_kv_cache_write (no counterpart on the pages).  For a head row x with
+ * weight w at position p, r = 1 / sqrt(mean(x^2) + eps) and y = r x w:
+ *   out_a = y_a cos_i - y_b sin_i,  out_b = y_b cos_i + y_a sin_i
+ * for the pairs (a, b) = (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved,
+ * i < rot_dim / 2; columns from rot_dim on are y.
+ *
+ *  q, k       bf16 [tokens][hq or hkv][d]; a token's heads are contiguous, tokens
+ *             are q_stride / k_stride values apart (multiples of 8, at least
+ *             heads * d), so that both may be views of one projection's output
+ *  q_weight, k_weight  fp32 [d]
+ *  cos_sin    fp32 [max_pos][rot_dim]: the cosines of position p's rot_dim / 2
+ *             angles, then their sines
+ *  rot_dim    a multiple of 16 in [16, d]; d in {64, 128}
+ *  positions  int32 device array [tokens].  A token with a negative position is
+ *             padding: its outputs are 0.  One with a position >= max_pos gets
+ *             NaN outputs (the table is not read).
+ *  q_out, k_out  bf16, contiguous; they must not overlap an input or each other
+ * All pointers 16-byte aligned (positions: 4).  Norms and rotation in fp32, one
+ * rounding to bf16.  No workspace.
+ * Errors: FFA_ERR_INVALID_ARG, FFA_ERR_UNSUPPORTED (d, rot_dim),
+ * FFA_ERR_OVERFLOW, FFA_ERR_CUDA.
+ */
+ffa_status ffa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int64_t tokens,
+                            int32_t hq, int32_t hkv, int32_t d, const float* q_weight, const float* k_weight, float eps,
+                            const float* cos_sin, int64_t max_pos, int32_t rot_dim, int32_t interleaved,
+                            const int32_t* positions, void* q_out, void* k_out, void* stream);
+
+/* Bytes of device workspace ffa_qk_norm_rope_bwd needs: fp32 partial sums of the
+ * two weight gradients.  Returns 0 for an unsupported d. */
+size_t ffa_qk_norm_rope_bwd_workspace_size(int32_t d);
+
+/*
+ * Backward pass of ffa_qk_norm_rope, given its inputs and the gradients of its
+ * outputs (e.g. ffa_bwd's dq and dk; bf16, contiguous).  dq, dk (bf16,
+ * contiguous) receive the gradients of q and k; dq_weight, dk_weight (fp32 [d])
+ * those of the weights, summed over all tokens and heads in fp32 in a fixed
+ * order.  Padding tokens get zero gradients and add nothing to the weights'; a
+ * position >= max_pos makes its row's and the weight's gradients NaN.  tokens =
+ * 0 gives zero weight gradients.
+ *  workspace  at least ffa_qk_norm_rope_bwd_workspace_size() bytes, contents on
+ *             entry ignored; calls that run at the same time need one each
+ * No output may overlap an input, the workspace or another output.
+ * Other arguments and errors as ffa_qk_norm_rope.
+ */
+ffa_status ffa_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int64_t tokens,
+                                int32_t hq, int32_t hkv, int32_t d, const float* q_weight, const float* k_weight,
+                                float eps, const float* cos_sin, int64_t max_pos, int32_t rot_dim, int32_t interleaved,
+                                const int32_t* positions, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                                float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* Types a key-value cache stores. */
+typedef enum {
+  FFA_KV_BF16 = 0,
+  FFA_KV_E4M3 = 1 /* 8-bit codes and one exponent byte a row: value = code * 2^(byte - 127), 0 where byte = 0 */
+} ffa_kv_dtype;
+
+/* A paged key-value cache (read during the call only).  k and v are
+ * [num_pages][hkv][page_size][d] in dtype; k_exp and v_exp (FFA_KV_E4M3 only)
+ * [num_pages][hkv][page_size] bytes.  page_size is a power of two in [16, 1024],
+ * d in {64, 128}; all pointers 16-byte aligned. */
+typedef struct {
+  void *k, *v;
+  uint8_t *k_exp, *v_exp;
+  int64_t num_pages;
+  int32_t page_size, hkv, d;
+  int32_t dtype; /* ffa_kv_dtype */
+} ffa_kv_cache;
+
+/*
+ * Write rows of k and v into a paged cache, quantising them where the cache is
+ * FFA_KV_E4M3 (no counterpart on the pages).  A row (token, kv head) with
+ * largest magnitude a is stored with n the smallest integer >= -126 for which
+ * a <= 448 * 2^n: codes e4m3(x / 2^n), exact division and one rounding to
+ * nearest even, and the byte n + 127.  A row that holds a NaN or an infinity is
+ * stored as NaN throughout.
+ *
+ *  k, v   bf16 [tokens][hkv][d] with token strides k_stride / v_stride as in
+ *         ffa_qk_norm_rope; 16-byte aligned, not overlapping the cache
+ *  slots  int64 device array [tokens]: page * page_size + offset.  A token
+ *         whose slot is negative (padding) or outside the cache is not written.
+ *         Slots of one call must differ: of two tokens with one slot, each 16
+ *         bytes of the slot's rows may be either's.
+ * Errors: FFA_ERR_INVALID_ARG, FFA_ERR_UNSUPPORTED, FFA_ERR_OVERFLOW,
+ * FFA_ERR_CUDA.
+ */
+ffa_status ffa_kv_cache_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t tokens,
+                              const int64_t* slots, const ffa_kv_cache* cache, void* stream);
+
+/*
+ * Read the first cu_seqlens[b + 1] - cu_seqlens[b] keys and values of every
+ * sequence back to back, as ffa_fwd takes them (e.g. to prefill a next chunk
+ * over a cached prefix with bottom-right CAUSAL slices).  Stored e4m3 values
+ * are exact in bf16 (down to bf16's smallest).
+ *
+ *  page_table  int32 device array, row b (table_stride apart) the pages of
+ *              sequence b in order, max_pages of them
+ *  cu_seqlens  int32 device array [batch + 1], ascending from 0
+ *  total       rows of k and v (bf16 [total][hkv][d], contiguous, 16-byte
+ *              aligned, not overlapping the cache).  Rows from
+ *              cu_seqlens[batch] on are left as they were.
+ * Rows whose page is not one of the cache's, or lies behind the table's row,
+ * are NaN.  Errors as ffa_kv_cache_write.
+ */
+ffa_status ffa_kv_cache_read(const ffa_kv_cache* cache, const int32_t* page_table, int64_t table_stride,
+                             int32_t max_pages, int32_t batch, const int32_t* cu_seqlens, int64_t total, void* k,
+                             void* v, void* stream);
+
+/* Bytes of device workspace ffa_fwd_decode needs (for any batch and lengths).
+ * Returns 0 for sizes it does not take. */
+size_t ffa_fwd_decode_workspace_size(int32_t hq, int32_t hkv, int32_t d);
+
+/*
+ * Attention of one new token a sequence over the paged cache (no counterpart on
+ * the pages): for sequence b and q head h, with the keys j in
+ * [kv_starts[b], kv_lens[b]),
+ *   lse = ln(sum_j e^(scale q . k_j) [+ e^sink[h]]),
+ *   out = sum_j e^(scale q . k_j - lse) v_j.
+ * The work is split over the length of the cache and joined, so that one long
+ * sequence uses the whole GPU.  out and lse have ffa_fwd's layouts with the
+ * batch in the place of seqlen_q, so ffa_lse_combine merges calls over disjoint
+ * key ranges (e.g. the first keys and a sliding window).
+ *
+ *  q           bf16 [batch][hq][d], rows q_stride values apart as in
+ *              ffa_qk_norm_rope; hq % hkv == 0
+ *  page_table  as in ffa_kv_cache_read; entries that no key range reaches are
+ *              not read
+ *  kv_lens     int32 device array [batch], the new token included; <= 0 gives an
+ *              empty row (out 0, lse -inf, or lse = sink)
+ *  kv_starts   int32 device array [batch] or NULL (0); clamped into
+ *              [0, kv_lens[b]].  Only the pages from kv_starts[b] on are read.
+ *  sink        fp32 device array [hq] or NULL, as in ffa_fwd_sink
+ *  out, lse    bf16 [batch][hq][d], fp32 [hq][batch]
+ *  workspace   at least ffa_fwd_decode_workspace_size() bytes, contents on entry
+ *              ignored; calls that run at the same time need one each
+ * A sequence with a page that is not one of the cache's, or with more keys than
+ * its table row holds, gets NaN rows (nothing out of range is read); the other
+ * sequences are not affected.
+ * Scores, maxima and sums are fp32; results do not depend on timing, but
+ * where a sequence is split depends on the batch's lengths.
+ * Errors: FFA_ERR_INVALID_ARG, FFA_ERR_UNSUPPORTED, FFA_ERR_OVERFLOW,
+ * FFA_ERR_CUDA.
+ */
+ffa_status ffa_fwd_decode(const void* q, int64_t q_stride, const ffa_kv_cache* cache, const int32_t* page_table,
+                          int64_t table_stride, int32_t max_pages, int32_t batch, int32_t hq, const int32_t* kv_lens,
+                          const int32_t* kv_starts, float scale, const float* sink, void* out, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronize `stream`, read and clear the plan's device status word.
  * Returns FFA_ERR_DEVICE_CHECK (and the word in *status_out, if not NULL)
  * when a kernel recorded a timeout or a metadata error since the last check.

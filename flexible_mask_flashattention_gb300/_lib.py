@@ -6,7 +6,6 @@ There is no fallback: if the library is missing, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Iterable, Optional, Sequence, Tuple
@@ -477,91 +476,120 @@ def bwd(q, k, v, out, lse, dout, plan: Plan, scale: float, dq=None, dk=None, dv=
     return dq, dk, dv
 
 
-_NO_CONTEXT = contextlib.nullcontext()
+# The calls below take a few microseconds on the host and run many times a second in a decode loop, so their checks are
+# single expressions, and what went wrong is worked out only once something did.
 
-
-def _on(stream):
-    """The context in which tensors are allocated for use on `stream` (None: the current stream)."""
+def _on(stream, device: int):
+    """(handle, context): the stream a call launches on, and the context in which tensors are allocated for use on it, or
+    None for the current stream, on which they are anyway."""
+    import torch
     if stream is None:
-        return _NO_CONTEXT
-    import torch
+        return torch._C._cuda_getCurrentRawStream(device), None
     if isinstance(stream, torch.cuda.Stream):
-        return torch.cuda.stream(stream)
+        return stream.cuda_stream, torch.cuda.stream(stream)
     handle = int(_stream_handle(stream))
-    return torch.cuda.stream(torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream())
+    return handle, torch.cuda.stream(torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream())
 
 
-def _rows_stride(t, name, heads=None, d=None, tokens=None):
-    """The token stride of a bf16 CUDA tensor [tokens, heads, d] whose heads are contiguous within a token."""
+def _empty(like, context, *specs):
+    """One new tensor a (shape, dtype) of specs, on the device of `like`, for use on the stream of `context`."""
+    if context is None:
+        return [like.new_empty(shape, dtype=dtype) for shape, dtype in specs]
+    with context:
+        return [like.new_empty(shape, dtype=dtype) for shape, dtype in specs]
+
+
+def _device(t, name) -> int:
+    """The device of tensor t, which must be the current one."""
     import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3:
-        raise FFAError(1, f"{name} must be a CUDA bfloat16 tensor [tokens, heads, d]")
-    n, h, w = t.shape
-    if (heads is not None and h != heads) or (d is not None and w != d) or (tokens is not None and n != tokens):
-        raise FFAError(1, f"{name} has shape {tuple(t.shape)}, expected {(tokens, heads, d)}")
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise FFAError(1, f"{name} must be a CUDA tensor")
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise FFAError(1, f"{name} is on cuda:{dev}, which is not the current device")
+    return dev
+
+
+def _check_dense(t, dtype, shape, dev, name):
+    """t is a contiguous tensor of that type and shape on device dev."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _need(t, dtype, name, shape)
+    raise FFAError(1, f"{name} must be on the device of the other tensors")
+
+
+def _rows_stride(t, name, shape, dev):
+    """The token stride of a bf16 tensor of `shape` [tokens, heads, d] whose heads are contiguous within a token."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        raise FFAError(1, f"{name} must be a bfloat16 tensor on the device of the other tensors")
+    if t.shape != shape:
+        raise FFAError(1, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    n, h, w = shape
     s = t.stride()
     if (w > 1 and s[2] != 1) or (h > 1 and s[1] != w):
         raise FFAError(1, f"{name} must hold each token's heads contiguously")
     return s[0] if n > 1 else h * w
 
 
-def _same_device(first, *rest):
-    """Check that the tensors (None: absent) are all on the current device."""
-    import torch
-    dev = first.get_device()
-    for t in rest:
-        if t is not None and t.get_device() != dev:
-            raise FFAError(1, "all tensors must be on one device")
-    if dev != torch.cuda.current_device():
-        raise FFAError(1, f"the tensors are on cuda:{dev}, which is not the current device")
+def _dims(t, name, n):
+    if t.dim() != n:
+        raise FFAError(1, f"{name} must have {n} dimensions")
+    return t.shape
 
 
-def _kv_cache(k_cache, v_cache, k_exp, v_exp) -> KVCacheC:
+def _kv_cache(k_cache, v_cache, k_exp, v_exp, dev) -> KVCacheC:
     """The C description of a cache: k, v [pages, hkv, page_size, d] bf16, or float8_e4m3fn with exponent bytes."""
     import torch
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+    dtype = k_cache.dtype
+    quantised = dtype is torch.float8_e4m3fn
+    if not quantised and dtype is not torch.bfloat16:
         raise FFAError(1, "k_cache must be a bfloat16 or float8_e4m3fn tensor")
-    if k_cache.dim() != 4:
-        raise FFAError(1, "k_cache must be [pages, hkv, page_size, d]")
-    _need(k_cache, k_cache.dtype, "k_cache")
-    _need(v_cache, k_cache.dtype, "v_cache", k_cache.shape)
-    pages, hkv, page_size, d = k_cache.shape
-    quantised = k_cache.dtype == torch.float8_e4m3fn
-    if quantised:
-        _need(k_exp, torch.uint8, "k_exp", (pages, hkv, page_size))
-        _need(v_exp, torch.uint8, "v_exp", (pages, hkv, page_size))
-    elif k_exp is not None or v_exp is not None:
-        raise FFAError(1, "a bfloat16 cache has no exponent bytes")
-    return KVCacheC(k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr() if quantised else None,
-                    v_exp.data_ptr() if quantised else None, pages, page_size, hkv, d, int(quantised))
+    shape = pages, hkv, page_size, d = _dims(k_cache, "k_cache", 4)
+    _check_dense(k_cache, dtype, shape, dev, "k_cache")
+    _check_dense(v_cache, dtype, shape, dev, "v_cache")
+    if not quantised:
+        if k_exp is not None or v_exp is not None:
+            raise FFAError(1, "a bfloat16 cache has no exponent bytes")
+        return KVCacheC(k_cache.data_ptr(), v_cache.data_ptr(), None, None, pages, page_size, hkv, d, 0)
+    _check_dense(k_exp, torch.uint8, shape[:3], dev, "k_exp")
+    _check_dense(v_exp, torch.uint8, shape[:3], dev, "v_exp")
+    return KVCacheC(k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), pages, page_size, hkv, d, 1)
 
 
-def _page_table(t, batch: int) -> int:
-    """The row stride of an int32 page table [batch, max_pages]."""
+def _page_table(t, batch: int, dev):
+    """(row stride, max_pages) of an int32 page table [batch, max_pages]."""
     import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or t.dim() != 2:
-        raise FFAError(1, "page_table must be a CUDA int32 tensor [batch, max_pages]")
-    if t.shape[0] != batch:
-        raise FFAError(1, f"page_table has {t.shape[0]} rows, expected {batch}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.get_device() != dev:
+        raise FFAError(1, "page_table must be an int32 tensor on the device of the other tensors")
+    rows, width = _dims(t, "page_table", 2)
+    if rows != batch:
+        raise FFAError(1, f"page_table has {rows} rows, expected {batch}")
+    s = t.stride()
+    if width > 1 and s[1] != 1:
         raise FFAError(1, "page_table rows must be contiguous")
-    return t.stride(0) if batch > 1 else t.shape[1]
+    return s[0] if batch > 1 else width, width
 
 
-def _norm_rope_inputs(q, k, q_weight, k_weight, cos_sin, positions):
-    """Checked (token strides of q and k, sizes) of the inputs both directions share."""
+def _norm_rope_inputs(q, k, q_weight, k_weight, cos_sin, positions, dev):
+    """Checked (q's stride, k's stride, tokens, hq, hkv, d, max_pos, rot_dim) of the inputs both directions share."""
     import torch
-    qs = _rows_stride(q, "q")
-    tokens, hq, d = q.shape
-    ks = _rows_stride(k, "k", None, d, tokens)
-    _need(q_weight, torch.float32, "q_weight", (d,))
-    _need(k_weight, torch.float32, "k_weight", (d,))
-    _need(positions, torch.int32, "positions", (tokens,))
-    _need(cos_sin, torch.float32, "cos_sin")
-    if cos_sin.dim() != 2:
-        raise FFAError(1, "cos_sin must be [max_pos, rot_dim]")
-    _same_device(q, k, q_weight, k_weight, cos_sin, positions)
-    return qs, ks, tokens, hq, k.shape[1], d
+    if not isinstance(k, torch.Tensor) or not isinstance(cos_sin, torch.Tensor):
+        raise FFAError(1, "k and cos_sin must be CUDA tensors")
+    tokens, hq, d = _dims(q, "q", 3)
+    hkv = _dims(k, "k", 3)[1]
+    table = _dims(cos_sin, "cos_sin", 2)
+    f32 = torch.float32
+    qs = _rows_stride(q, "q", (tokens, hq, d), dev)
+    ks = _rows_stride(k, "k", (tokens, hkv, d), dev)
+    _check_dense(q_weight, f32, (d,), dev, "q_weight")
+    _check_dense(k_weight, f32, (d,), dev, "k_weight")
+    _check_dense(positions, torch.int32, (tokens,), dev, "positions")
+    _check_dense(cos_sin, f32, table, dev, "cos_sin")
+    return qs, ks, tokens, hq, hkv, d, table[0], table[1]
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6, interleaved: bool = False,
@@ -570,19 +598,22 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6
     weight [d] (fp32), and rotated by its token's position (int32 [S]) with cos_sin [max_pos, rot_dim]
     (fp32; the cosines first).  q and k may be views of one projection's output."""
     import torch
-    qs, ks, tokens, hq, hkv, d = _norm_rope_inputs(q, k, q_weight, k_weight, cos_sin, positions)
-    with _on(stream):
-        if q_out is None:
-            q_out = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=q.device)
-        if k_out is None:
-            k_out = torch.empty((tokens, hkv, d), dtype=torch.bfloat16, device=q.device)
-    _need(q_out, torch.bfloat16, "q_out", (tokens, hq, d))
-    _need(k_out, torch.bfloat16, "k_out", (tokens, hkv, d))
-    _same_device(q, q_out, k_out)
+    dev = _device(q, "q")
+    qs, ks, tokens, hq, hkv, d, max_pos, rot = _norm_rope_inputs(q, k, q_weight, k_weight, cos_sin, positions, dev)
+    handle, context = _on(stream, dev)
+    bf16, qshape, kshape = torch.bfloat16, (tokens, hq, d), (tokens, hkv, d)
+    if q_out is None:
+        q_out, = _empty(q, context, (qshape, bf16))
+    else:
+        _check_dense(q_out, bf16, qshape, dev, "q_out")
+    if k_out is None:
+        k_out, = _empty(q, context, (kshape, bf16))
+    else:
+        _check_dense(k_out, bf16, kshape, dev, "k_out")
     _check(load_library().ffa_qk_norm_rope(
         q.data_ptr(), qs, k.data_ptr(), ks, tokens, hq, hkv, d, q_weight.data_ptr(), k_weight.data_ptr(), eps,
-        cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(interleaved), positions.data_ptr(),
-        q_out.data_ptr(), k_out.data_ptr(), _stream_handle(stream)), "ffa_qk_norm_rope")
+        cos_sin.data_ptr(), max_pos, rot, interleaved, positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
+        handle), "ffa_qk_norm_rope")
     return q_out, k_out
 
 
@@ -590,28 +621,27 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk_ou
                      interleaved: bool = False, workspace=None, stream=None):
     """dq, dk (bf16) and dq_weight, dk_weight (fp32 [d]) of qk_norm_rope, from the gradients of its outputs."""
     import torch
-    qs, ks, tokens, hq, hkv, d = _norm_rope_inputs(q, k, q_weight, k_weight, cos_sin, positions)
-    _need(dq_out, torch.bfloat16, "dq_out", (tokens, hq, d))
-    _need(dk_out, torch.bfloat16, "dk_out", (tokens, hkv, d))
-    with _on(stream):
-        dq = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=q.device)
-        dk = torch.empty((tokens, hkv, d), dtype=torch.bfloat16, device=q.device)
-        dw = torch.empty((2, d), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = torch.empty(qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8, device=q.device)
-    _need(workspace, torch.uint8, "workspace")
-    _same_device(q, dq_out, dk_out, workspace)
-    dqw, dkw = dw[0], dw[1]
+    dev = _device(q, "q")
+    qs, ks, tokens, hq, hkv, d, max_pos, rot = _norm_rope_inputs(q, k, q_weight, k_weight, cos_sin, positions, dev)
+    bf16, f32, qshape, kshape = torch.bfloat16, torch.float32, (tokens, hq, d), (tokens, hkv, d)
+    _check_dense(dq_out, bf16, qshape, dev, "dq_out")
+    _check_dense(dk_out, bf16, kshape, dev, "dk_out")
+    handle, context = _on(stream, dev)
+    dq, dk, dqw, dkw = _empty(q, context, (qshape, bf16), (kshape, bf16), ((d,), f32), ((d,), f32))
+    if workspace is None:
+        workspace, = _empty(q, context, ((qk_norm_rope_bwd_workspace_size(d),), torch.uint8))
+    else:
+        _check_dense(workspace, torch.uint8, workspace.shape, dev, "workspace")
     _check(load_library().ffa_qk_norm_rope_bwd(
         q.data_ptr(), qs, k.data_ptr(), ks, tokens, hq, hkv, d, q_weight.data_ptr(), k_weight.data_ptr(), eps,
-        cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(interleaved), positions.data_ptr(),
-        dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(),
-        workspace.data_ptr(), workspace.numel(), _stream_handle(stream)), "ffa_qk_norm_rope_bwd")
+        cos_sin.data_ptr(), max_pos, rot, interleaved, positions.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(),
+        dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), workspace.data_ptr(), workspace.numel(), handle),
+        "ffa_qk_norm_rope_bwd")
     return dq, dk, dqw, dkw
 
 
 def qk_norm_rope_bwd_workspace_size(d: int) -> int:
-    return int(load_library().ffa_qk_norm_rope_bwd_workspace_size(int(d)))
+    return load_library().ffa_qk_norm_rope_bwd_workspace_size(d)
 
 
 def kv_cache_write(k, v, k_cache, v_cache, slots, k_exp=None, v_exp=None, stream=None):
@@ -619,13 +649,17 @@ def kv_cache_write(k, v, k_cache, v_cache, slots, k_exp=None, v_exp=None, stream
     page_size + offset; negative or outside: not written).  A float8_e4m3fn cache holds codes and, in k_exp / v_exp
     [pages, Hkv, page_size] uint8, each row's exponent: value = code * 2^(byte - 127)."""
     import torch
-    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp)
-    ks = _rows_stride(k, "k", cache.hkv, cache.d)
-    vs = _rows_stride(v, "v", cache.hkv, cache.d, k.shape[0])
-    _need(slots, torch.int64, "slots", (k.shape[0],))
-    _same_device(k, v, k_cache, v_cache, slots, k_exp, v_exp)
-    _check(load_library().ffa_kv_cache_write(k.data_ptr(), ks, v.data_ptr(), vs, k.shape[0], slots.data_ptr(),
-                                             ctypes.byref(cache), _stream_handle(stream)), "ffa_kv_cache_write")
+    dev = _device(k_cache, "k_cache")
+    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp, dev)
+    if not isinstance(slots, torch.Tensor):
+        raise FFAError(1, "slots must be a CUDA tensor")
+    tokens, = _dims(slots, "slots", 1)
+    shape = (tokens, cache.hkv, cache.d)
+    ks = _rows_stride(k, "k", shape, dev)
+    vs = _rows_stride(v, "v", shape, dev)
+    _check_dense(slots, torch.int64, (tokens,), dev, "slots")
+    _check(load_library().ffa_kv_cache_write(k.data_ptr(), ks, v.data_ptr(), vs, tokens, slots.data_ptr(),
+                                             ctypes.byref(cache), _on(stream, dev)[0]), "ffa_kv_cache_write")
 
 
 def kv_cache_read(k_cache, v_cache, page_table, cu_seqlens, total: int, k=None, v=None, k_exp=None, v_exp=None,
@@ -634,29 +668,33 @@ def kv_cache_read(k_cache, v_cache, page_table, cu_seqlens, total: int, k=None, 
     every sequence, back to back; page_table [B, max_pages] int32.  Rows behind the last sequence are left as they
     were (undefined where k and v are allocated here)."""
     import torch
-    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp)
+    dev = _device(k_cache, "k_cache")
+    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp, dev)
     if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise FFAError(1, "cu_seqlens must be an int32 tensor [batch + 1]")
-    _need(cu_seqlens, torch.int32, "cu_seqlens")
+    _check_dense(cu_seqlens, torch.int32, cu_seqlens.shape, dev, "cu_seqlens")
     batch = cu_seqlens.shape[0] - 1
-    ts = _page_table(page_table, batch)
-    shape = (int(total), cache.hkv, cache.d)
+    ts, width = _page_table(page_table, batch, dev)
+    shape, bf16 = (int(total), cache.hkv, cache.d), torch.bfloat16
     if shape[0] < 0:
         raise FFAError(1, "total must not be negative")
-    with _on(stream):
-        k = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) if k is None else k
-        v = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) if v is None else v
-    _need(k, torch.bfloat16, "k", shape)
-    _need(v, torch.bfloat16, "v", shape)
-    _same_device(k_cache, v_cache, page_table, cu_seqlens, k, v, k_exp, v_exp)
-    _check(load_library().ffa_kv_cache_read(ctypes.byref(cache), page_table.data_ptr(), ts, page_table.shape[1], batch,
-                                            cu_seqlens.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(),
-                                            _stream_handle(stream)), "ffa_kv_cache_read")
+    handle, context = _on(stream, dev)
+    if k is None:
+        k, = _empty(k_cache, context, (shape, bf16))
+    else:
+        _check_dense(k, bf16, shape, dev, "k")
+    if v is None:
+        v, = _empty(k_cache, context, (shape, bf16))
+    else:
+        _check_dense(v, bf16, shape, dev, "v")
+    _check(load_library().ffa_kv_cache_read(ctypes.byref(cache), page_table.data_ptr(), ts, width, batch,
+                                            cu_seqlens.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(), handle),
+           "ffa_kv_cache_read")
     return k, v
 
 
 def fwd_decode_workspace_size(hq: int, hkv: int, d: int) -> int:
-    return int(load_library().ffa_fwd_decode_workspace_size(int(hq), int(hkv), int(d)))
+    return load_library().ffa_fwd_decode_workspace_size(hq, hkv, d)
 
 
 def fwd_decode(q, k_cache, v_cache, page_table, kv_lens, scale: float, k_exp=None, v_exp=None, kv_starts=None,
@@ -664,29 +702,34 @@ def fwd_decode(q, k_cache, v_cache, page_table, kv_lens, scale: float, k_exp=Non
     """out [B, Hq, d] bf16 and lse [Hq, B] fp32 of one new token a sequence, q [B, Hq, d], over the keys
     [kv_starts[b], kv_lens[b]) (int32 [B]) of the paged cache; sink [Hq] fp32 as in fwd_sink."""
     import torch
-    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp)
-    qs = _rows_stride(q, "q", None, cache.d)
-    b, hq, d = q.shape
-    ts = _page_table(page_table, b)
-    _need(kv_lens, torch.int32, "kv_lens", (b,))
+    dev = _device(q, "q")
+    if not isinstance(k_cache, torch.Tensor):
+        raise FFAError(1, "k_cache must be a CUDA tensor")
+    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp, dev)
+    b, hq, d = _dims(q, "q", 3)
+    qs = _rows_stride(q, "q", (b, hq, cache.d), dev)
+    ts, width = _page_table(page_table, b, dev)
+    bf16, f32 = torch.bfloat16, torch.float32
+    _check_dense(kv_lens, torch.int32, (b,), dev, "kv_lens")
     if kv_starts is not None:
-        _need(kv_starts, torch.int32, "kv_starts", (b,))
+        _check_dense(kv_starts, torch.int32, (b,), dev, "kv_starts")
     if sink is not None:
-        _need(sink, torch.float32, "sink", (hq,))
-    with _on(stream):
-        if out is None:
-            out = torch.empty((b, hq, d), dtype=torch.bfloat16, device=q.device)
-        if lse is None:
-            lse = torch.empty((hq, b), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = torch.empty(fwd_decode_workspace_size(hq, cache.hkv, d), dtype=torch.uint8, device=q.device)
-    _need(out, torch.bfloat16, "out", (b, hq, d))
-    _need(lse, torch.float32, "lse", (hq, b))
-    _need(workspace, torch.uint8, "workspace")
-    _same_device(q, k_cache, v_cache, page_table, kv_lens, kv_starts, k_exp, v_exp, sink, out, lse, workspace)
+        _check_dense(sink, f32, (hq,), dev, "sink")
+    handle, context = _on(stream, dev)
+    if out is None:
+        out, = _empty(q, context, ((b, hq, d), bf16))
+    else:
+        _check_dense(out, bf16, (b, hq, d), dev, "out")
+    if lse is None:
+        lse, = _empty(q, context, ((hq, b), f32))
+    else:
+        _check_dense(lse, f32, (hq, b), dev, "lse")
+    if workspace is None:
+        workspace, = _empty(q, context, ((fwd_decode_workspace_size(hq, cache.hkv, d),), torch.uint8))
+    else:
+        _check_dense(workspace, torch.uint8, workspace.shape, dev, "workspace")
     _check(load_library().ffa_fwd_decode(
-        q.data_ptr(), qs, ctypes.byref(cache), page_table.data_ptr(), ts, page_table.shape[1], b, hq,
-        kv_lens.data_ptr(), None if kv_starts is None else kv_starts.data_ptr(), scale,
-        None if sink is None else sink.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), _stream_handle(stream)), "ffa_fwd_decode")
+        q.data_ptr(), qs, ctypes.byref(cache), page_table.data_ptr(), ts, width, b, hq, kv_lens.data_ptr(),
+        None if kv_starts is None else kv_starts.data_ptr(), scale, None if sink is None else sink.data_ptr(),
+        out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), handle), "ffa_fwd_decode")
     return out, lse

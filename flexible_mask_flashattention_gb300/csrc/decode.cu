@@ -37,9 +37,7 @@
 namespace ffa {
 namespace {
 
-constexpr int kW = 8;                  // warps a CTA
-constexpr int kThreads = 32 * kW;
-constexpr int kBlock = 16 * kW;        // keys of a block
+constexpr int warps_of(bool fp8, int nt) { return fp8 && nt == 1 ? 12 : 8; }   // warps a CTA
 constexpr int kMaxCtas = 512;          // split parts the workspace holds: two a CTA
 constexpr int kSmemMax = 226 * 1024;   // of 227 KB
 constexpr float kLog2e = 1.4426950408889634f;
@@ -78,27 +76,22 @@ struct DecodeParams {
 
 template <int D, bool FP8, int NT>
 struct Cfg {
+  static constexpr int W = warps_of(FP8, NT);
+  static constexpr int THREADS = 32 * W;
+  static constexpr int BLOCK = 16 * W;                  // keys of a block
   static constexpr int ES = FP8 ? 1 : 2;
   static constexpr int ROW = D * ES;                    // bytes a stored row
   static constexpr int CPR = ROW / 16;                  // 16-byte chunks a row
   static constexpr int STRIP = 16 * ROW;                // bytes of 16 rows
   static constexpr int STAGE = 2 * STRIP + (FP8 ? 32 : 0);
-  static constexpr int JOIN = (kW / 2) * 8 * NT * D * 4 + kW * 8 * NT * 8;   // O buffers, (m, l) a warp
+  static constexpr int JOIN = (W / 2) * 8 * NT * D * 4 + W * 8 * NT * 8;   // O buffers, (m, l) a warp
   static constexpr int MISC = 1024;
-  static constexpr int STAGES = (kSmemMax - JOIN - MISC) / (kW * STAGE) < 8 ? (kSmemMax - JOIN - MISC) / (kW * STAGE) : 8;
-  static constexpr int SMEM = MISC + JOIN + kW * STAGE * STAGES;
+  static constexpr int STAGES = (kSmemMax - JOIN - MISC) / (W * STAGE) < 8 ? (kSmemMax - JOIN - MISC) / (W * STAGE) : 8;
+  static constexpr int SMEM = MISC + JOIN + W * STAGE * STAGES;
   static constexpr int KSTEPS = D / 16;
   static constexpr int MT = D / 16;                     // 16-column tiles of the output
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 r;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
@@ -137,22 +130,33 @@ __device__ __forceinline__ float pow2i(int e) {   // 2^e, 0 below the normal ran
   return e < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// Where a walk over the CTA's share of the block list stands: unit (b, u) with u = kv head * subs + sub, and block `blk` of its `nblk`.
-struct Cursor {
-  int b, u;
-  int64_t blk, nblk;
-  KeyRange r;
-  __device__ __forceinline__ void set_sequence(const DecodeParams& p, int seq) {
+// Where a walk over the CTA's share of the block list stands: unit (b, u) with u = kv head * subs + sub, `left` blocks of it from
+// the current one on, and the first key of this warp's strip in the current block.
+template <int W>
+struct Walk {
+  static constexpr int kBlock = 16 * W;
+  int b, u, left, key, start, end;
+  bool bad;
+  // The first of the unit's blocks that is walked is `blk`.
+  __device__ __forceinline__ void set(const DecodeParams& p, int seq, int unit, int64_t blk, int warp) {
+    const KeyRange r = key_range(p.lens[seq], p.starts ? p.starts[seq] : 0, p.max_pages, p.geom.page_log2);
     b = seq;
-    r = key_range(p.lens[seq], p.starts ? p.starts[seq] : 0, p.max_pages, p.geom.page_log2);
-    nblk = range_blocks(r, kBlock);
+    u = unit;
+    start = static_cast<int>(r.start);
+    end = static_cast<int>(r.end);
+    bad = r.bad;
+    left = static_cast<int>(range_blocks(r, kBlock) - blk);
+    // a warp's strip may lie behind the end, by a block at most: as keys are below 2^31, unsigned arithmetic and a clamp
+    const int64_t k = range_first(r) + (blk * W + warp) * 16;
+    key = static_cast<int>(k < r.end ? k : r.end);
   }
-  __device__ __forceinline__ void next(const DecodeParams& p, int units, bool more) {
-    if (++blk < nblk) return;
-    blk = 0;
-    if (++u < units) return;
-    u = 0;
-    if (more) set_sequence(p, b + 1);
+  __device__ __forceinline__ void step() {   // to the unit's next block
+    --left;
+    key = end - key > kBlock ? key + kBlock : end;
+  }
+  __device__ __forceinline__ void next_unit(const DecodeParams& p, int units, int warp) {
+    const bool wrap = u + 1 == units;
+    set(p, wrap ? b + 1 : b, wrap ? 0 : u + 1, 0, warp);
   }
 };
 
@@ -177,9 +181,9 @@ __device__ __forceinline__ void write_row(const DecodeParams& p, int b, int head
 }
 
 template <int D, bool FP8, int NT>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeParams p) {
+__global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(DecodeParams p) {
   using C = Cfg<D, FP8, NT>;
-  constexpr int NQ = 8 * NT;
+  constexpr int NQ = 8 * NT, kW = C::W, kThreads = C::THREADS, kBlock = C::BLOCK;
   extern __shared__ __align__(128) uint8_t smem[];
   float* join_o = reinterpret_cast<float*>(smem + C::MISC);                       // [kW / 2][NQ][D]
   float* join_ml = join_o + (kW / 2) * NQ * D;                                    // [kW][NQ][2]
@@ -233,60 +237,79 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeParams p) {
     }
   }
   __syncthreads();
-  Cursor cur;
-  cur.set_sequence(p, begin->b);
-  cur.u = static_cast<int>(begin->off / cur.nblk);
-  cur.blk = begin->off - cur.u * cur.nblk;
-  Cursor ld = cur;   // the loads' cursor runs ahead
+  Walk<kW> cur;
+  {
+    const int64_t nb = range_blocks(key_range(p.lens[begin->b], p.starts ? p.starts[begin->b] : 0, p.max_pages, p.geom.page_log2), kBlock);
+    const int u = static_cast<int>(begin->off / nb);
+    cur.set(p, begin->b, u, begin->off - u * nb, warp);
+  }
+  const bool opens_mid = begin->off % range_blocks(key_range(p.lens[cur.b], p.starts ? p.starts[cur.b] : 0, p.max_pages, p.geom.page_log2), kBlock) != 0;
 
-  // ---- loading one strip of this warp
+  // ---- loading one strip of this warp; the loads' walk runs ahead of the products'
   const uint32_t ring = smem_u32(smem + C::MISC + C::JOIN) + warp * (C::STAGE * C::STAGES);
   uint32_t stage_bad = 0;   // stages whose page the cache does not have
-  auto load_strip = [&](int stage) {
-    const int64_t first = range_first(ld.r);
-    const int64_t key0 = first + (ld.blk * kW + warp) * 16;
-    const int64_t have = ld.r.end - key0;
-    stage_bad &= ~(1u << stage);
-    if (have > 0) {
-      const int64_t page = p.table[ld.b * p.table_stride + (key0 >> p.geom.page_log2)];
-      const int off = static_cast<int>(key0 & ((1 << p.geom.page_log2) - 1));
-      const bool ok = page_ok(p.geom, page);
-      if (!ok) stage_bad |= 1u << stage;
-      const int lo = static_cast<int>(max(ld.r.start - key0, int64_t{0})), hi = ok ? static_cast<int>(min(have, int64_t{16})) : 0;
-      const int64_t row = cache_row(p.geom, ok ? page : 0, ld.u / p.subs, ok ? off : 0);
-      const uint8_t* ksrc = static_cast<const uint8_t*>(p.k) + row * C::ROW;
-      const uint8_t* vsrc = static_cast<const uint8_t*>(p.v) + row * C::ROW;
-      const uint32_t dst = ring + stage * C::STAGE;
+  Walk<kW> ld = cur;
+  auto page_of = [&]() -> int { return ld.key < ld.end ? __ldg(p.table + ld.b * p.table_stride + (ld.key >> p.geom.page_log2)) : 0; };
+  int page = page_of();     // the page of the next strip to load, read one strip ahead
+  // this lane's chunks of a strip: chunk lane + 32 i, rows 32 / CPR apart; source and destination offsets
+  uint32_t dst_of[C::CPR / 2];
 #pragma unroll
-      for (int i = 0; i < C::CPR / 2; ++i) {
-        const int id = lane + 32 * i, key = id / C::CPR;
-        const int bytes = key >= lo && key < hi ? 16 : 0;   // rows outside the range are filled with zeros, not read
-        const uint32_t at = dst + 16 * strip_chunk(key, id % C::CPR, C::CPR);
-        cp_async16(at, ksrc + id * 16, bytes);
-        cp_async16(at + C::STRIP, vsrc + id * 16, bytes);
+  for (int i = 0; i < C::CPR / 2; ++i) dst_of[i] = 16 * strip_chunk((lane + 32 * i) / C::CPR, (lane + 32 * i) % C::CPR, C::CPR);
+  auto load_strip = [&](int stage, bool more) {
+    const int have = ld.end - ld.key;
+    if (have > 0) {
+      const int off = ld.key & ((1 << p.geom.page_log2) - 1);
+      const bool ok = page_ok(p.geom, page);
+      const uint32_t bit = 1u << stage;
+      stage_bad = ok ? stage_bad & ~bit : stage_bad | bit;
+      const int64_t row = ok ? cache_row(p.geom, page, p.subs == 1 ? ld.u : ld.u / p.subs, off) : 0;
+      const uint8_t* ksrc = static_cast<const uint8_t*>(p.k) + row * C::ROW + lane * 16;
+      const uint8_t* vsrc = static_cast<const uint8_t*>(p.v) + row * C::ROW + lane * 16;
+      const uint32_t dst = ring + stage * C::STAGE;
+      if (ok && have >= 16 && ld.key >= ld.start) {
+#pragma unroll
+        for (int i = 0; i < C::CPR / 2; ++i) {
+          cp_async16(dst + dst_of[i], ksrc + 512 * i);
+          cp_async16(dst + C::STRIP + dst_of[i], vsrc + 512 * i);
+        }
+      } else {   // rows outside the range are filled with zeros, not read
+        const int lo = max(ld.start - ld.key, 0), hi = ok ? min(have, 16) : 0;
+#pragma unroll
+        for (int i = 0; i < C::CPR / 2; ++i) {
+          const int key = (lane + 32 * i) / C::CPR, bytes = key >= lo && key < hi ? 16 : 0;
+          cp_async16(dst + dst_of[i], ksrc + 512 * i, bytes);
+          cp_async16(dst + C::STRIP + dst_of[i], vsrc + 512 * i, bytes);
+        }
       }
       if constexpr (FP8) {
-        if (lane < 2) cp_async16(dst + 2 * C::STRIP + 16 * lane, (lane ? p.v_exp : p.k_exp) + row, hi > 0 ? 16 : 0);
+        if (lane < 2) cp_async16(dst + 2 * C::STRIP + 16 * lane, (lane ? p.v_exp : p.k_exp) + row, ok ? 16 : 0);
       }
     }
+    if (!more) return;
+    if (ld.left > 1) ld.step(); else ld.next_unit(p, units, warp);
+    page = page_of();
   };
 
   int64_t ahead = t0;
-#pragma unroll
+#pragma unroll 1
   for (int s = 0; s < C::STAGES - 1; ++s) {
     if (ahead < t1) {
-      load_strip(s);
       ++ahead;
-      ld.next(p, units, ahead < t1);
+      load_strip(s, ahead < t1);
     }
     cp_async_commit();
   }
+
+  // A row maximum is raised only when a score passes it by kLazy (log2 units): most strips then cost one vote.
+  constexpr float kLazy = FP8 ? 5.f : 8.f;
+  constexpr float kBias = FP8 ? 10.f : 0.f;   // e4m3: P is held times 2^10, at most 2^15: f16 reaches 2^-34 of the largest
 
   // ---- per-unit state
   uint32_t qf[NT][C::KSTEPS][2];   // Q^T fragments in the contraction order of the K loads
   float qs[NT][2];                 // per query column: scale_log2, with the e4m3 path's power of two taken back
   float o[NT][C::MT][4];
   float m[NT][2], l[NT][2];
+  float mb[NT][2], thr[NT][2];     // what a score's exponent is taken against, and what raises the maximum
   int ev_ref = 0;                  // e4m3: exponent byte that O's unit stands for
   bool bad = false;
   auto begin_unit = [&]() {
@@ -330,21 +353,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeParams p) {
       }
 #pragma unroll
       for (int i = 0; i < C::MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
-      m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = thr[nt][0] = thr[nt][1] = -INFINITY;
+      mb[nt][0] = mb[nt][1] = -kBias;
       l[nt][0] = l[nt][1] = 0.f;
     }
     ev_ref = 0;
-    bad = cur.r.bad;
+    bad = cur.bad;
   };
 
   // ---- one strip
-  // A row maximum is raised only when a score passes it by kLazy (log2 units): most strips then cost one vote.
-  constexpr float kLazy = FP8 ? 5.f : 8.f;
-  constexpr float kBias = FP8 ? 10.f : 0.f;   // e4m3: P is held times 2^10, at most 2^15: f16 reaches 2^-34 of the largest
   auto strip = [&](int stage) {
-    const int64_t key0 = range_first(cur.r) + (cur.blk * kW + warp) * 16;
-    const int64_t have = cur.r.end - key0;
+    const int have = cur.end - cur.key;
     if (have <= 0) return;
+    const bool whole = have >= 16 && cur.key >= cur.start;
     const uint32_t kb = ring + stage * C::STAGE, vb = kb + C::STRIP;
     bad |= (stage_bad >> stage & 1u) != 0;
     float s[NT][2][4] = {};
@@ -371,14 +392,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeParams p) {
       }
     }
     // keys n and n + 8 of the strip are this lane's; columns 2t, 2t + 1 of each query tile
-    const int lo = static_cast<int>(max(cur.r.start - key0, int64_t{0})), hi = static_cast<int>(min(have, int64_t{16}));
-    const bool in0 = n >= lo && n < hi, in1 = n + 8 >= lo && n + 8 < hi;
+    const int lo = cur.start - cur.key;
+    const bool in0 = whole || (n >= lo && n < have), in1 = whole || (n + 8 >= lo && n + 8 < have);
     float ks0 = 1.f, ks1 = 1.f, vs0 = 1.f, vs1 = 1.f;
     if constexpr (FP8) {
-      const uint32_t eb = vb + C::STRIP;
-      ks0 = exp_scale(lds8(eb + n));
-      ks1 = exp_scale(lds8(eb + n + 8));
-      const int v0 = in0 ? lds8(eb + 16 + n) : 0, v1 = in1 ? lds8(eb + 16 + n + 8) : 0;
+      const uint32_t eb = vb + C::STRIP + n;
+      ks0 = exp_scale(lds8(eb));
+      ks1 = exp_scale(lds8(eb + 8));
+      int v0 = lds8(eb + 16), v1 = lds8(eb + 24);
+      if (!whole) v0 = in0 ? v0 : 0, v1 = in1 ? v1 : 0;
       const int top = max(v0, v1);
       if (__any_sync(0xffffffffu, top > ev_ref)) {
         const int ref = max(ev_ref, static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(top))));
@@ -391,8 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeParams p) {
             for (int c = 0; c < 4; ++c) o[nt][i][c] *= f;
         ev_ref = ref;
       }
-      vs0 = pow2i(v0 - ev_ref);
-      vs1 = pow2i(v1 - ev_ref);
+      vs0 = __uint_as_float(static_cast<uint32_t>(max(v0 - ev_ref + 127, 0)) << 23);   // 2^(v0 - ev_ref), 0 below 2^-126
+      vs1 = __uint_as_float(static_cast<uint32_t>(max(v1 - ev_ref + 127, 0)) << 23);
     }
     float x[NT][4];
     bool raise = false;
@@ -400,9 +422,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeParams p) {
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const float v = (s[nt][0][c] + s[nt][1][c]) * qs[nt][c & 1] * (c < 2 ? ks0 : ks1);
-        x[nt][c] = (c < 2 ? in0 : in1) ? v : -INFINITY;
-        raise |= x[nt][c] > m[nt][c & 1] + kLazy;
+        x[nt][c] = (s[nt][0][c] + s[nt][1][c]) * (qs[nt][c & 1] * (c < 2 ? ks0 : ks1));
+        if (!whole) x[nt][c] = (c < 2 ? in0 : in1) ? x[nt][c] : -INFINITY;
+        raise |= x[nt][c] > thr[nt][c & 1];
       }
     }
     if (__any_sync(0xffffffffu, raise)) {
@@ -417,6 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeParams p) {
           mx = fmaxf(mx, m[nt][c]);
           const float f = mx == -INFINITY ? 1.f : ex2_approx(m[nt][c] - mx);
           m[nt][c] = mx;
+          thr[nt][c] = mx + kLazy;
+          mb[nt][c] = mx == -INFINITY ? -kBias : mx - kBias;
           l[nt][c] *= f;
 #pragma unroll
           for (int i = 0; i < C::MT; ++i) {
@@ -430,10 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeParams p) {
     for (int nt = 0; nt < NT; ++nt) {
       float e[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float mm = m[nt][c & 1] == -INFINITY ? 0.f : m[nt][c & 1];
-        e[c] = ex2_approx(x[nt][c] - mm + kBias);
-      }
+      for (int c = 0; c < 4; ++c) e[c] = ex2_approx(x[nt][c] - mb[nt][c & 1]);
       l[nt][0] += e[0] + e[2];
       l[nt][1] += e[1] + e[3];
       if constexpr (FP8) {
@@ -577,49 +598,45 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeParams p) {
   };
 
   // ---- the share
-  bool fresh = true, first_part = true;
-  int64_t part_begin = cur.blk;
+  bool fresh = true, first_part = true, from_start = !opens_mid;
   int32_t opened = 0;   // parts of the unit this CTA leaves open to later ones
   int stage = 0, fill = C::STAGES - 1;
+#pragma unroll 1
   for (int64_t x = t0; x < t1; ++x) {
     if (ahead < t1) {
-      load_strip(fill);
       ++ahead;
-      ld.next(p, units, ahead < t1);
+      load_strip(fill, ahead < t1);
     }
     cp_async_commit();
     fill = fill + 1 == C::STAGES ? 0 : fill + 1;
+    if (fresh) begin_unit();
+    fresh = false;
     cp_async_wait<C::STAGES - 1>();
     __syncwarp();
-    if (fresh) {
-      begin_unit();
-      part_begin = cur.blk;
-      fresh = false;
-    }
     strip(stage);
     __syncwarp();   // the stage has been read by every lane before the next iteration refills it
     stage = stage + 1 == C::STAGES ? 0 : stage + 1;
-    const bool last = cur.blk + 1 == cur.nblk;
-    if (last || x + 1 == t1) {
-      const bool whole = last && part_begin == 0;
-      const int slot = static_cast<int>(2 * cta) + (first_part ? 0 : 1);
-      end_part(whole, slot);
-      if (!last && part_begin == 0) {
-        const int64_t unit0 = x - cur.blk;
-        opened = static_cast<int32_t>(share_of(total, parts, unit0 + cur.nblk - 1) - cta + 1);
-        if (tid == 0) {
-          JoinDesc d{};
-          d.parts = opened;
-          d.batch = cur.b;
-          d.unit = cur.u;
-          d.first_slot = slot;
-          p.desc[cta] = d;
-        }
-      }
-      first_part = false;
-      fresh = true;
+    if (cur.left > 1 && x + 1 < t1) {
+      cur.step();
+      continue;
     }
-    cur.next(p, units, x + 1 < t1);
+    const bool last = cur.left == 1;
+    const int slot = static_cast<int>(2 * cta) + (first_part ? 0 : 1);
+    end_part(last && from_start, slot);
+    if (!last && from_start) {
+      opened = static_cast<int32_t>(share_of(total, parts, x + cur.left - 1) - cta + 1);
+      if (tid == 0) {
+        JoinDesc d{};
+        d.parts = opened;
+        d.batch = cur.b;
+        d.unit = cur.u;
+        d.first_slot = slot;
+        p.desc[cta] = d;
+      }
+    }
+    first_part = false;
+    from_start = fresh = true;
+    if (x + 1 < t1) cur.next_unit(p, units, warp);
   }
   if (opened == 0 && tid == 0) p.desc[cta].parts = 0;
 }
@@ -666,7 +683,7 @@ ffa_status launch(const DecodeParams& p, int sms, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return FFA_ERR_CUDA;
   const int grid = std::min(sms, kMaxCtas);
-  kernel<<<grid, kThreads, C::SMEM, s>>>(p);
+  kernel<<<grid, C::THREADS, C::SMEM, s>>>(p);
   decode_join_kernel<D, NT><<<grid, 256, 0, s>>>(p, FP8 ? 10.f : 0.f);
   return cuda_status(cudaGetLastError());
 }

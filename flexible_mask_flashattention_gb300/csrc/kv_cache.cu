@@ -8,7 +8,9 @@
 //         and every stored value is exact in bf16 down to bf16's smallest, so that reading back does not round again.
 //         A row that holds a NaN or an infinity is stored as NaN throughout (byte 127).
 //
-// Both kernels are bound by HBM: 2 d bytes a row on the tensors' side, 2 d or d + 1 on the cache's.
+// Both kernels are bound by HBM: 2 d bytes a row on the tensors' side, 2 d or d + 1 on the cache's.  A grid's second
+// dimension is k or v; a warp holds 2 or 4 head rows of a token at once (a pass), 8 values a lane, and starts the loads of
+// kUnroll passes before it uses the first.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -25,7 +27,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;
 
-// Parameter pair's entry by a run-time index, as a select (an indexed one would copy the parameters to local memory).
+// A parameter pair's entry by a run-time index, as a select (an indexed one would copy the parameters to local memory).
 template <typename T>
 __device__ __forceinline__ T pick(T const (&pair)[2], int i) {
   return i ? pair[1] : pair[0];
@@ -39,67 +41,62 @@ struct WriteParams {
   const int64_t* slots;
   PageGeom geom;
   int64_t units;
-  int32_t chunks;              // warp units a token
+  uint32_t chunks;             // warp units of a token's k or v rows
 };
 
-__device__ __forceinline__ uint32_t absmax2(uint32_t m, uint32_t v) {   // of both bf16 halves, as bit patterns
-  const uint32_t a = v & 0x7fffu, b = (v >> 16) & 0x7fffu;
-  return max(m, max(a, b));
-}
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+__device__ __forceinline__ uint32_t e4m3x2(float2 f) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(f.y), "f"(f.x));
   return r;
 }
 
-// A warp takes one token and up to kUnroll passes over its 2 hkv rows (k's, then v's), d / 8 lanes a row.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads) kv_cache_write_kernel(WriteParams p) {
   constexpr int L = D / 8, RW = 32 / L;
-  const int lane = threadIdx.x & 31, l = lane & (L - 1), sub = lane / L;
+  const int lane = threadIdx.x & 31, l = lane & (L - 1), sub = lane / L, which = blockIdx.y;
   const int64_t u = blockIdx.x * static_cast<int64_t>(kWarps) + (threadIdx.x >> 5);
   if (u >= p.units) return;
-  const int64_t token = u / p.chunks;
-  const int row0 = static_cast<int>(u - token * p.chunks) * (kUnroll * RW);
-  const int64_t slot = p.slots[token];
-  if (!slot_ok(p.geom, slot)) return;   // padding, or no slot of this cache: nothing is written
-  const int64_t page = slot >> p.geom.page_log2;
-  const int off = static_cast<int>(slot & ((1 << p.geom.page_log2) - 1));
-  uint4 v[kUnroll];
-#pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
-    const int row = row0 + i * RW + sub, t = row >= p.geom.hkv, h = t ? row - p.geom.hkv : row;
-    v[i] = row < 2 * p.geom.hkv
-               ? __ldg(reinterpret_cast<const uint4*>(pick(p.x, t) + token * pick(p.stride, t) + static_cast<int64_t>(h) * D + 8 * l))
-               : uint4{};
+  int64_t token = u;
+  int h = sub;
+  if (p.chunks > 1) {
+    token = u / p.chunks;
+    h += static_cast<int>(u - token * p.chunks) * (kUnroll * RW);
   }
+  const int64_t slot = __ldg(p.slots + token);
+  uint4 v[kUnroll];
+  const __nv_bfloat16* x = pick(p.x, which) + token * pick(p.stride, which) + h * D + 8 * l;
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i)
+    v[i] = h + i * RW < p.geom.hkv ? __ldg(reinterpret_cast<const uint4*>(x + i * (RW * D))) : uint4{};
+  if (!slot_ok(p.geom, slot)) return;   // padding, or no slot of this cache: nothing is written
+  const int64_t row = cache_row(p.geom, slot >> p.geom.page_log2, h, static_cast<int>(slot & ((1 << p.geom.page_log2) - 1)));
+  const int64_t step = static_cast<int64_t>(RW) << p.geom.page_log2;   // cache rows from one pass to the next
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
-    const int row = row0 + i * RW + sub, t = row >= p.geom.hkv, h = t ? row - p.geom.hkv : row;
-    const bool act = row < 2 * p.geom.hkv;
-    const int64_t dst = cache_row(p.geom, page, h, off);
+    const bool act = h + i * RW < p.geom.hkv;
+    const int64_t dst = row + i * step;
     if constexpr (!FP8) {
-      if (act) reinterpret_cast<uint4*>(pick(p.cache, t))[dst * (D / 8) + l] = v[i];
+      if (act) reinterpret_cast<uint4*>(pick(p.cache, which))[dst * (D / 8) + l] = v[i];
     } else {
-      // bf16 magnitudes order as integers: the row's largest, by its bits
-      uint32_t m = absmax2(absmax2(absmax2(absmax2(0, v[i].x), v[i].y), v[i].z), v[i].w);
+      // bf16 magnitudes order as 15-bit integers: the row's largest, two at a time
+      uint32_t m = __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu), __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
 #pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      // max|x| = 1.f * 2^(e - 127), 448 = 1.75 * 2^8: the scale's byte is e - 8, one more where 1.f > 1.75
+      for (int o = L / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+      m = max(m & 0xffffu, m >> 16);
+      // max|x| = 1.f * 2^(e - 127), 448 = 1.75 * 2^8: the scale's byte is e - 8, one more where 1.f > 1.75 (mantissa 0x60)
       const bool finite = m < 0x7f80u;
-      const int e = static_cast<int>(m >> 7) - 8 + ((m & 0x7fu) > 0x60u);
-      const int byte = finite ? max(e, 1) : 127;
+      const int byte = finite ? max(static_cast<int>((m + 0x1fu) >> 7) - 8, 1) : 127;
       const float inv = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);   // 2^-(byte - 127), exact
       const uint32_t u4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
       uint32_t c[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        c[j] = e4m3x2(__uint_as_float(u4[j] << 16) * inv, __uint_as_float(u4[j] & 0xffff0000u) * inv);
+        c[j] = e4m3x2(mul2(make_float2(__uint_as_float(u4[j] << 16), __uint_as_float(u4[j] & 0xffff0000u)), make_float2(inv, inv)));
       uint2 codes = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
       if (!finite) codes = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
       if (act) {
-        reinterpret_cast<uint2*>(pick(p.cache, t))[dst * (D / 8) + l] = codes;
-        if (l == 0) pick(p.exps, t)[dst] = static_cast<uint8_t>(byte);
+        reinterpret_cast<uint2*>(pick(p.cache, which))[dst * (D / 8) + l] = codes;
+        if (l == 0) pick(p.exps, which)[dst] = static_cast<uint8_t>(byte);
       }
     }
   }
@@ -148,53 +145,50 @@ __global__ void __launch_bounds__(kThreads) kv_cache_read_kernel(ReadParams p) {
     src[threadIdx.x] = at;
   }
   __syncthreads();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (L - 1), sub = lane / L;
-  const int rows = 2 * p.geom.hkv;
-  const int n = kReadTile * rows;   // head rows of the tile, a token's together
-  for (int i0 = warp * (RW * kUnroll); i0 < n; i0 += kWarps * RW * kUnroll) {
-    uint4 v[kUnroll];
-    uint32_t e[kUnroll];
-    int64_t to[kUnroll];
-    int which[kUnroll];
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int idx = i0 + i * RW + sub;
-      const int tok = idx / rows, row = idx - tok * rows, t = row >= p.geom.hkv, h = t ? row - p.geom.hkv : row;
-      const int64_t at = idx < n ? src[tok] : -1;
-      which[i] = t;
-      to[i] = at == -1 ? -1 : ((t0 + tok) * p.geom.hkv + h) * (D / 8) + l;
-      v[i] = uint4{};
-      e[i] = 0x7fc0u;   // NaN where there is no page
-      if (at >= 0) {
-        const int64_t r = at + (static_cast<int64_t>(h) << p.geom.page_log2);
-        if constexpr (FP8) {
-          const uint2 c = __ldg(reinterpret_cast<const uint2*>(pick(p.cache, t)) + r * (D / 8) + l);
-          v[i].x = c.x, v[i].y = c.y;
-          e[i] = pick(p.exps, t)[r];
-        } else {
-          v[i] = __ldg(reinterpret_cast<const uint4*>(pick(p.cache, t)) + r * (D / 8) + l);
-          e[i] = 0;
-        }
-      }
+  const int lane = threadIdx.x & 31, l = lane & (L - 1), sub = lane / L, which = blockIdx.y;
+  const int64_t step = static_cast<int64_t>(RW) << p.geom.page_log2;   // cache rows from one pass to the next
+  for (int tok = threadIdx.x >> 5; tok < kReadTile; tok += kWarps) {
+    const int64_t at = src[tok];
+    if (at == -1) continue;
+    __nv_bfloat16* out = pick(p.out, which) + ((t0 + tok) * p.geom.hkv + sub) * D + 8 * l;
+    if (at == -2) {
+      for (int h = sub; h < p.geom.hkv; h += RW, out += RW * D)
+        *reinterpret_cast<uint4*>(out) = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+      continue;
     }
+    int64_t row = at + (static_cast<int64_t>(sub) << p.geom.page_log2);
+    for (int h = sub; h < p.geom.hkv; h += kUnroll * RW, row += kUnroll * step, out += kUnroll * RW * D) {
+      uint4 v[kUnroll];
+      uint32_t e[kUnroll];
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      if (to[i] < 0) continue;
-      uint4 o = v[i];
-      if (e[i] == 0x7fc0u) {
-        o = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
-      } else if constexpr (FP8) {
-        const float s = exp_scale(e[i]);
-        const uint32_t c[4] = {v[i].x & 0xffffu, v[i].x >> 16, v[i].y & 0xffffu, v[i].y >> 16};
-        uint32_t r[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = e4m3x2_to_float2(c[j]);
-          r[j] = pack_bf16x2(f.x * s, f.y * s);
+      for (int i = 0; i < kUnroll; ++i) {
+        if (h + i * RW >= p.geom.hkv) continue;
+        const int64_t r = row + i * step;
+        if constexpr (FP8) {
+          const uint2 c = __ldg(reinterpret_cast<const uint2*>(pick(p.cache, which)) + r * (D / 8) + l);
+          v[i].x = c.x, v[i].y = c.y;
+          e[i] = __ldg(pick(p.exps, which) + r);
+        } else {
+          v[i] = __ldg(reinterpret_cast<const uint4*>(pick(p.cache, which)) + r * (D / 8) + l);
         }
-        o = make_uint4(r[0], r[1], r[2], r[3]);
       }
-      reinterpret_cast<uint4*>(pick(p.out, which[i]))[to[i]] = o;
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        if (h + i * RW >= p.geom.hkv) continue;
+        uint4 o = v[i];
+        if constexpr (FP8) {
+          const float s = exp_scale(e[i]);
+          const uint32_t c[4] = {v[i].x & 0xffffu, v[i].x >> 16, v[i].y & 0xffffu, v[i].y >> 16};
+          uint32_t r[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = mul2(e4m3x2_to_float2(c[j]), make_float2(s, s));
+            r[j] = pack_bf16x2(f.x, f.y);
+          }
+          o = make_uint4(r[0], r[1], r[2], r[3]);
+        }
+        *reinterpret_cast<uint4*>(out + i * (RW * D)) = o;
+      }
     }
   }
 }
@@ -246,14 +240,14 @@ ffa_status ffa_kv_cache_write(const void* k, int64_t k_stride, const void* v, in
   p.exps[1] = cache->v_exp;
   p.slots = slots;
   const int per = kUnroll * 256 / cache->d;
-  p.chunks = (2 * cache->hkv + per - 1) / per;
+  p.chunks = (cache->hkv + per - 1) / per;
   if (tokens > (int64_t{1} << 36)) return FFA_ERR_OVERFLOW;
   p.units = tokens * p.chunks;
   const int64_t blocks = (p.units + kWarps - 1) / kWarps;
   if (blocks > 0x7fffffff) return FFA_ERR_OVERFLOW;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool fp8 = cache->dtype == FFA_KV_E4M3;
-  const unsigned grid = static_cast<unsigned>(blocks);
+  const dim3 grid(static_cast<unsigned>(blocks), 2);
   if (cache->d == 128)
     (fp8 ? kv_cache_write_kernel<128, true> : kv_cache_write_kernel<128, false>)<<<grid, kThreads, 0, s>>>(p);
   else
@@ -287,7 +281,7 @@ ffa_status ffa_kv_cache_read(const ffa_kv_cache* cache, const int32_t* page_tabl
   p.total = total;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool fp8 = cache->dtype == FFA_KV_E4M3;
-  const unsigned grid = static_cast<unsigned>((total + kReadTile - 1) / kReadTile);
+  const dim3 grid(static_cast<unsigned>((total + kReadTile - 1) / kReadTile), 2);
   if (cache->d == 128)
     (fp8 ? kv_cache_read_kernel<128, true> : kv_cache_read_kernel<128, false>)<<<grid, kThreads, 0, s>>>(p);
   else

@@ -9,12 +9,15 @@
 // r is recomputed in the backward from x, which it reads anyway, so the forward stores nothing for it.
 //
 // Both are bound by HBM: 4 bytes a value forward (x in, out out), 6 backward (x, dout in, dx out).  A lane holds 8
-// consecutive values of a row (one 16-byte load), d / 8 lanes a row; a warp takes one token and up to kUnroll passes
-// over its heads, all loads issued first, and reads the token's table row once for them.  Norm statistics, rotation
-// and every gradient sum are fp32; the one rounding to bf16 is the store's.
+// consecutive values of a row (16 bytes), d / 8 lanes a row.  The kernels are persistent: a warp walks over units of a
+// token's passes (a pass is the 2 or 4 head rows a warp holds at once), and cp.async keeps the next units' values and
+// table rows on their way to shared memory, where every lane reads back only what it copied itself (the table row is the
+// warp's).  Loads in flight then cost neither registers nor barriers.  Norm statistics, rotation and every
+// gradient sum are fp32, two values an instruction (fma.rn.f32x2); the one rounding to bf16 is the store's.
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "ffa_internal.h"
 #include "ptx.cuh"
@@ -22,10 +25,13 @@
 namespace ffa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;          // head passes of one warp unit, loaded together
+constexpr int kDevices = 64;         // devices whose figures are kept
 constexpr int kMaxBwdCtas = 1024;   // partial weight gradients the workspace holds
+constexpr int kStages = 2;          // units in shared memory: one being used, one on its way
+template <bool BWD>
+constexpr int kUnitPasses = BWD ? 5 : 10;   // passes of a unit at most
 
 struct NormRopeParams {
   const __nv_bfloat16* x[2];      // q, k
@@ -34,7 +40,9 @@ struct NormRopeParams {
   __nv_bfloat16* out[2];          // forward: outputs; backward: dx; contiguous
   const float* w[2];
   int32_t heads[2];
-  int32_t chunks[2];              // warp units a token
+  int32_t passes[2];              // a token's passes over its q heads, and over both
+  int32_t unit;                   // passes of a unit
+  int32_t per;                    // units a token
   int64_t units;
   float eps;
   const float* cos_sin;
@@ -44,16 +52,13 @@ struct NormRopeParams {
   float* partial;                 // backward: [CTAs][2][d]
 };
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+__device__ __forceinline__ void unpack8(const uint4& v, float2 (&f)[4]) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(u[i] << 16);
-    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
+  return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
 }
 __device__ __forceinline__ uint4 shfl4(const uint4& v, int src) {
   uint4 r;
@@ -63,10 +68,9 @@ __device__ __forceinline__ uint4 shfl4(const uint4& v, int src) {
   r.w = __shfl_sync(0xffffffffu, v.w, src);
   return r;
 }
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-  f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+__device__ __forceinline__ void load8(const float* p, float2 (&f)[4]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
+  f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w), f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
 }
 
 // A lane's part of one token's rotation, for the 8 values it holds of each row: value j becomes
@@ -74,23 +78,20 @@ __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
 // the partners (itself when pairs are interleaved).
 template <int D, bool INTER>
 struct Rotation {
-  float c[8], s[8];
+  float2 c[4], s[4];
   int src;
-  __device__ __forceinline__ void identity(int lane) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = 1.f, s[j] = 0.f;
-    src = lane;
-  }
   __device__ __forceinline__ void load(const float* row, int rot, int lane) {
-    identity(lane);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = make_float2(1.f, 1.f), s[j] = make_float2(0.f, 0.f);
+    src = lane;
     const int l = lane & (D / 8 - 1);
     if (8 * l >= rot) return;
     if constexpr (INTER) {
-      const float4 c4 = __ldg(reinterpret_cast<const float4*>(row + 4 * l));
-      const float4 s4 = __ldg(reinterpret_cast<const float4*>(row + rot / 2 + 4 * l));
+      const float4 c4 = *reinterpret_cast<const float4*>(row + 4 * l);
+      const float4 s4 = *reinterpret_cast<const float4*>(row + rot / 2 + 4 * l);
       const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) c[2 * i] = c[2 * i + 1] = cc[i], s[2 * i] = -ss[i], s[2 * i + 1] = ss[i];
+      for (int i = 0; i < 4; ++i) c[i] = make_float2(cc[i], cc[i]), s[i] = make_float2(-ss[i], ss[i]);
     } else {   // rot_dim is a multiple of 16, so a lane's values are all in one half
       const int half = rot >> 4;   // lanes a half
       const bool lo = l < half;
@@ -99,16 +100,16 @@ struct Rotation {
       load8(row + rot / 2 + i, s);
       if (lo) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] = -s[j];
+        for (int j = 0; j < 4; ++j) s[j] = make_float2(-s[j].x, -s[j].y);
       }
       src = lo ? lane + half : lane - half;
     }
   }
   // The values of f's pair partners; v is f in its packed form.
-  __device__ __forceinline__ void partners(const uint4& v, const float (&f)[8], float (&p)[8]) const {
+  __device__ __forceinline__ void partners(const uint4& v, const float2 (&f)[4], float2 (&p)[4]) const {
     if constexpr (INTER) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) p[j] = f[j ^ 1];
+      for (int j = 0; j < 4; ++j) p[j] = make_float2(f[j].y, f[j].x);
     } else {
       unpack8(shfl4(v, src), p);
     }
@@ -123,150 +124,245 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-struct Unit {
-  int64_t token;
-  int which;    // 0 q, 1 k
-  int head0;    // first head of the unit
-  int64_t pos;
+// Where a warp stands in its units: unit `c` of token `token`, and the position of that token.
+struct UnitWalk {
+  int64_t token, u, step_token;
+  int c, step_c, pos;
+  __device__ __forceinline__ void read_pos(const NormRopeParams& p) { pos = u < p.units ? __ldg(p.pos + token) : -1; }
+  __device__ __forceinline__ void init(const NormRopeParams& p, int64_t first, int64_t stride) {
+    u = first;
+    token = first / p.per;
+    c = static_cast<int>(first - token * p.per);
+    step_token = stride / p.per;
+    step_c = static_cast<int>(stride - step_token * p.per);
+    read_pos(p);
+  }
+  __device__ __forceinline__ void next(int64_t stride, int per) {
+    u += stride;
+    token += step_token;
+    c += step_c;
+    if (c >= per) c -= per, ++token;
+  }
 };
-__device__ __forceinline__ Unit unit_of(const NormRopeParams& p, int64_t u, int heads_per_unit) {
-  const int per = p.chunks[0] + p.chunks[1];
-  Unit r;
-  r.token = u / per;
-  const int c = static_cast<int>(u - r.token * per);
-  r.which = c >= p.chunks[0];
-  r.head0 = (r.which ? c - p.chunks[0] : c) * heads_per_unit;
-  r.pos = p.pos[r.token];
-  return r;
+
+// The stages of a CTA in shared memory, in 16-byte chunks: of every stage a chunk a thread and pass (two in the backward: x
+// and dout), then the warps' table rows (32 chunks at most each).
+template <int D, bool BWD>
+struct Stages {
+  uint4* base;
+  int unit;
+  __device__ __forceinline__ uint4* chunk(int stage, int i) const {
+    return base + (stage * (unit * (BWD ? 2 : 1) + 1) + i) * kThreads + threadIdx.x;
+  }
+  __device__ __forceinline__ const float* table(int stage) const {
+    return reinterpret_cast<const float*>(chunk(stage, unit * (BWD ? 2 : 1)) - (threadIdx.x & 31));
+  }
+  static __host__ __device__ constexpr int bytes(int unit) { return kStages * (unit * (BWD ? 2 : 1) + 1) * kThreads * 16; }
+};
+
+// Start the copies of one unit into `stage`.  Rows behind the last head are filled with zeros.
+template <int D, bool BWD>
+__device__ __forceinline__ void copy_unit(const NormRopeParams& p, const Stages<D, BWD>& st, int stage, const UnitWalk& w, int lane) {
+  constexpr int L = D / 8, RW = 32 / L;
+  const int l = lane & (L - 1), sub = lane / L;
+  const int j0 = w.c * p.unit, j1 = min(j0 + p.unit, p.passes[1]);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int from = t ? p.passes[0] : 0, a = max(j0, from), b = min(j1, p.passes[t]);
+    int h = (a - from) * RW + sub;
+    const __nv_bfloat16* x = p.x[t] + w.token * p.x_stride[t] + static_cast<int64_t>(h) * D + 8 * l;
+    const __nv_bfloat16* g = BWD ? p.dout[t] + (w.token * p.heads[t] + h) * D + 8 * l : nullptr;
+    for (int j = a; j < b; ++j) {
+      const int bytes = h < p.heads[t] ? 16 : 0;
+      cp_async16(smem_u32(st.chunk(stage, j - j0)), bytes ? x : p.x[t], bytes);
+      if constexpr (BWD) cp_async16(smem_u32(st.chunk(stage, p.unit + j - j0)), bytes ? g : p.dout[t], bytes);
+      h += RW;
+      x += RW * D;
+      if constexpr (BWD) g += RW * D;
+    }
+  }
+  if (w.pos >= 0 && w.pos < p.max_pos && 4 * lane < p.rot)
+    cp_async16(smem_u32(st.chunk(stage, p.unit * (BWD ? 2 : 1))), p.cos_sin + static_cast<int64_t>(w.pos) * p.rot + 4 * lane, 16);
 }
 
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(NormRopeParams p) {
   constexpr int L = D / 8, RW = 32 / L;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* weights = reinterpret_cast<float*>(smem);   // [2][D]
+  const Stages<D, false> st{reinterpret_cast<uint4*>(smem + 2 * D * 4), p.unit};
   const int lane = threadIdx.x & 31, l = lane & (L - 1), sub = lane / L;
-  const int64_t u = blockIdx.x * static_cast<int64_t>(kWarps) + (threadIdx.x >> 5);
-  if (u >= p.units) return;
-  const Unit un = unit_of(p, u, kUnroll * RW);
-  const int heads = p.heads[un.which];
-  const __nv_bfloat16* x = p.x[un.which] + un.token * p.x_stride[un.which] + 8 * l;
-  uint4 v[kUnroll];
+  const int64_t stride = gridDim.x * static_cast<int64_t>(kWarps);
+  UnitWalk cur, ld;
+  cur.init(p, blockIdx.x * static_cast<int64_t>(kWarps) + (threadIdx.x >> 5), stride);
+  ld = cur;
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
-    const int h = un.head0 + i * RW + sub;
-    v[i] = h < heads ? __ldg(reinterpret_cast<const uint4*>(x + h * D)) : uint4{};
+  for (int s = 0; s < kStages - 1; ++s) {
+    if (ld.u < p.units) copy_unit<D, false>(p, st, s, ld, lane);
+    cp_async_commit();
+    ld.next(stride, p.per);
+    ld.read_pos(p);
   }
-  Rotation<D, INTER> rot;
-  rot.identity(lane);
-  if (un.pos >= 0 && un.pos < p.max_pos) rot.load(p.cos_sin + un.pos * p.rot, p.rot, lane);
-  // own and partner coefficients with their weights: out_j = r (x_j a_j + partner_j b_j)
-  float a[8], b[8];
-  {
-    float w[8];
-    load8(p.w[un.which] + 8 * l, w);
-    const int pl = (rot.src & (L - 1)) * 8;
-    float wp[8];
-    load8(p.w[un.which] + pl, wp);
+  for (int i = threadIdx.x; i < 2 * D; i += kThreads) weights[i] = p.w[i / D][i % D];
+  __syncthreads();
+  int stage = 0, fill = kStages - 1;
+  for (; cur.u < p.units; cur.next(stride, p.per)) {
+    const int pos = __ldg(p.pos + cur.token);
+    if (ld.u < p.units) copy_unit<D, false>(p, st, fill, ld, lane);
+    cp_async_commit();
+    ld.next(stride, p.per);
+    ld.read_pos(p);   // a unit ahead of its use
+    cp_async_wait<kStages - 1>();
+    __syncwarp();
+    const int j0 = cur.c * p.unit, j1 = min(j0 + p.unit, p.passes[1]);
+    const bool live = pos >= 0 && pos < p.max_pos;
+    Rotation<D, INTER> rot;
+    if (live) rot.load(st.table(stage), p.rot, lane);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      a[j] = rot.c[j] * w[j];
-      b[j] = rot.s[j] * (INTER ? w[j ^ 1] : wp[j]);
+    for (int t = 0; t < 2; ++t) {
+      const int from = t ? p.passes[0] : 0, a0 = max(j0, from), b0 = min(j1, p.passes[t]);
+      if (a0 >= b0) continue;
+      int h = (a0 - from) * RW + sub;
+      __nv_bfloat16* out = p.out[t] + (cur.token * p.heads[t] + h) * D + 8 * l;
+      if (!live) {   // a padded token (negative position) gives zeros, one behind the table NaN
+        const uint32_t c = pos < 0 ? 0u : 0x7fff7fffu;
+        for (int j = a0; j < b0; ++j, h += RW, out += RW * D)
+          if (h < p.heads[t]) *reinterpret_cast<uint4*>(out) = make_uint4(c, c, c, c);
+        continue;
+      }
+      // coefficients with the weights: out_j = r (x_j a_j + partner_j b_j)
+      float2 a[4], b[4];
+      load8(weights + t * D + 8 * l, a);
+      if constexpr (INTER) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = make_float2(a[j].y, a[j].x);
+      } else {
+        load8(weights + t * D + 8 * (rot.src & (L - 1)), b);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a[j] = mul2(a[j], rot.c[j]), b[j] = mul2(b[j], rot.s[j]);
+#pragma unroll 2
+      for (int j = a0; j < b0; ++j) {
+        const uint4 v = *st.chunk(stage, j - j0);
+        float2 f[4], q[4], ss = make_float2(0.f, 0.f);
+        unpack8(v, f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ss = fma2(f[i], f[i], ss);
+        const float r = rsqrtf(row_sum<D>(ss.x + ss.y) * (1.f / D) + p.eps);
+        rot.partners(v, f, q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = mul2(fma2(f[i], a[i], mul2(q[i], b[i])), make_float2(r, r));
+        if (h < p.heads[t]) *reinterpret_cast<uint4*>(out) = pack8(f);
+        h += RW;
+        out += RW * D;
+      }
     }
-  }
-  // a padded token (negative position) gives zeros, one behind the table NaN
-  const float keep = un.pos < 0 ? 0.f : un.pos < p.max_pos ? 1.f : __int_as_float(0x7fffffff);
-  __nv_bfloat16* out = p.out[un.which] + un.token * heads * D + 8 * l;
-#pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
-    float f[8], q[8], o[8], ss = 0.f;
-    unpack8(v[i], f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
-    const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + p.eps);
-    rot.partners(v[i], f, q);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = r * fmaf(f[j], a[j], q[j] * b[j]);
-    if (keep != 1.f) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = keep;
-    }
-    const int h = un.head0 + i * RW + sub;
-    if (h < heads) *reinterpret_cast<uint4*>(out + h * D) = pack8(o);
+    __syncwarp();   // the stage's table row has been read by every lane before the next iteration refills it
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    fill = fill + 1 == kStages ? 0 : fill + 1;
   }
 }
 
-// Persistent: each warp strides over the units and keeps its 8 columns' weight-gradient sums for q and k in registers;
-// a CTA adds its warps' in a fixed order and writes one partial row pair, which norm_rope_dw_kernel adds up.  The
-// assignment of units to warps is static, so the result does not depend on timing.
+// Each lane keeps its 8 columns' weight-gradient sums for q and k in registers; a CTA adds its warps' in a fixed order and writes
+// one partial row pair, which norm_rope_dw_kernel adds up.  The assignment of units to warps is static, so
+// the result does not depend on timing.
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NormRopeParams p) {
   constexpr int L = D / 8, RW = 32 / L;
-  constexpr int kU = 2;   // passes loaded together: x and dout each
-  __shared__ float red[kWarps][2][D];
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* weights = reinterpret_cast<float*>(smem);   // [2][D]
+  float* red = weights + 2 * D;                      // [kWarps][2][D]
+  const Stages<D, true> st{reinterpret_cast<uint4*>(smem + (1 + kWarps) * 2 * D * 4), p.unit};
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (L - 1), sub = lane / L;
-  float acc[2][8] = {};
   const int64_t stride = gridDim.x * static_cast<int64_t>(kWarps);
-  for (int64_t u = blockIdx.x * static_cast<int64_t>(kWarps) + warp; u < p.units; u += stride) {
-    const Unit un = unit_of(p, u, kU * RW);
-    const int heads = p.heads[un.which];
-    const __nv_bfloat16* x = p.x[un.which] + un.token * p.x_stride[un.which] + 8 * l;
-    const __nv_bfloat16* dy = p.dout[un.which] + un.token * heads * D + 8 * l;
-    uint4 v[kU], g[kU];
+  UnitWalk cur, ld;
+  cur.init(p, blockIdx.x * static_cast<int64_t>(kWarps) + warp, stride);
+  ld = cur;
 #pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      const int h = un.head0 + i * RW + sub;
-      v[i] = h < heads ? __ldg(reinterpret_cast<const uint4*>(x + h * D)) : uint4{};
-      g[i] = h < heads ? __ldg(reinterpret_cast<const uint4*>(dy + h * D)) : uint4{};
-    }
+  for (int s = 0; s < kStages - 1; ++s) {
+    if (ld.u < p.units) copy_unit<D, true>(p, st, s, ld, lane);
+    cp_async_commit();
+    ld.next(stride, p.per);
+    ld.read_pos(p);
+  }
+  for (int i = threadIdx.x; i < 2 * D; i += kThreads) weights[i] = p.w[i / D][i % D];
+  __syncthreads();
+  float2 acc[2][4] = {};
+  int stage = 0, fill = kStages - 1;
+  for (; cur.u < p.units; cur.next(stride, p.per)) {
+    const int pos = __ldg(p.pos + cur.token);
+    if (ld.u < p.units) copy_unit<D, true>(p, st, fill, ld, lane);
+    cp_async_commit();
+    ld.next(stride, p.per);
+    ld.read_pos(p);
+    cp_async_wait<kStages - 1>();
+    __syncwarp();
+    const int j0 = cur.c * p.unit, j1 = min(j0 + p.unit, p.passes[1]);
+    const bool live = pos >= 0 && pos < p.max_pos;
     Rotation<D, INTER> rot;
-    rot.identity(lane);
-    if (un.pos >= 0 && un.pos < p.max_pos) rot.load(p.cos_sin + un.pos * p.rot, p.rot, lane);
-    float w[8];
-    load8(p.w[un.which] + 8 * l, w);
-    __nv_bfloat16* dx = p.out[un.which] + un.token * heads * D + 8 * l;
+    if (live) rot.load(st.table(stage), p.rot, lane);
 #pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      float f[8], gf[8], gp[8], ss = 0.f, hx = 0.f;
-      unpack8(v[i], f);
-      unpack8(g[i], gf);
-      rot.partners(g[i], gf, gp);
+    for (int j = 0; j < 4; ++j) rot.s[j] = make_float2(-rot.s[j].x, -rot.s[j].y);   // R^T turns by the negative angle
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        gf[j] = fmaf(gf[j], rot.c[j], -gp[j] * rot.s[j]);   // R^T dout: the transposed rotation turns the sign of s
-        ss = fmaf(f[j], f[j], ss);
-        hx = fmaf(gf[j] * w[j], f[j], hx);
-      }
-      const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + p.eps);
-      const float c = row_sum<D>(hx) * r * r * (1.f / D);
-      const int h = un.head0 + i * RW + sub;
-      if (un.pos < 0) {   // padded: no gradient
-        if (h < heads) *reinterpret_cast<uint4*>(dx + h * D) = uint4{};
+    for (int t = 0; t < 2; ++t) {
+      const int from = t ? p.passes[0] : 0, a0 = max(j0, from), b0 = min(j1, p.passes[t]);
+      if (a0 >= b0) continue;
+      int h = (a0 - from) * RW + sub;
+      __nv_bfloat16* dx = p.out[t] + (cur.token * p.heads[t] + h) * D + 8 * l;
+      if (!live) {   // padding: no gradient; behind the table: NaN, in the weight's gradient too
+        const uint32_t c = pos < 0 ? 0u : 0x7fff7fffu;
+        for (int j = a0; j < b0; ++j, h += RW, dx += RW * D)
+          if (h < p.heads[t]) *reinterpret_cast<uint4*>(dx) = make_uint4(c, c, c, c);
+        if (pos >= 0) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
         continue;
       }
-      const float bad = un.pos < p.max_pos ? 0.f : __int_as_float(0x7fffffff);
-      float o[8];
+      float2 w[4];
+      load8(weights + t * D + 8 * l, w);
+#pragma unroll 2
+      for (int j = a0; j < b0; ++j) {
+        const uint4 v = *st.chunk(stage, j - j0), gv = *st.chunk(stage, p.unit + j - j0);
+        float2 f[4], g[4], q[4], ss = make_float2(0.f, 0.f), hx = make_float2(0.f, 0.f);
+        unpack8(v, f);
+        unpack8(gv, g);
+        rot.partners(gv, g, q);
+        float2 hw[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        o[j] = r * fmaf(gf[j], w[j], -f[j] * c) + bad;
-        acc[0][j] += un.which == 0 ? gf[j] * (f[j] * r) + bad : 0.f;
-        acc[1][j] += un.which == 1 ? gf[j] * (f[j] * r) + bad : 0.f;
+        for (int i = 0; i < 4; ++i) {
+          g[i] = fma2(g[i], rot.c[i], mul2(q[i], rot.s[i]));
+          hw[i] = mul2(g[i], w[i]);
+          ss = fma2(f[i], f[i], ss);
+          hx = fma2(hw[i], f[i], hx);
+        }
+        const float r = rsqrtf(row_sum<D>(ss.x + ss.y) * (1.f / D) + p.eps);
+        const float c = -row_sum<D>(hx.x + hx.y) * (r * r) * (r * (1.f / D));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          hw[i] = fma2(f[i], make_float2(c, c), mul2(hw[i], make_float2(r, r)));   // dx = r h - x r^3 mean(h x)
+          acc[t][i] = fma2(g[i], mul2(f[i], make_float2(r, r)), acc[t][i]);
+        }
+        if (h < p.heads[t]) *reinterpret_cast<uint4*>(dx) = pack8(hw);
+        h += RW;
+        dx += RW * D;
       }
-      if (h < heads) *reinterpret_cast<uint4*>(dx + h * D) = pack8(o);
     }
+    __syncwarp();
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    fill = fill + 1 == kStages ? 0 : fill + 1;
   }
 #pragma unroll
   for (int t = 0; t < 2; ++t)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      float s = acc[t][j];
+      float s = j & 1 ? acc[t][j / 2].y : acc[t][j / 2].x;
 #pragma unroll
       for (int o = L; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (sub == 0) red[warp][t][8 * l + j] = s;
+      if (sub == 0) red[(warp * 2 + t) * D + 8 * l + j] = s;
     }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
     float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) s += red[k][i / D][i % D];
+    for (int k = 0; k < kWarps; ++k) s += red[k * 2 * D + i];
     p.partial[blockIdx.x * static_cast<int64_t>(2 * D) + i] = s;
   }
 }
@@ -336,9 +432,68 @@ ffa_status check_common(const void* q, int64_t q_stride, const void* k, int64_t 
   return FFA_OK;
 }
 
-void set_units(NormRopeParams& p, int64_t tokens, int heads_per_unit) {
-  for (int i = 0; i < 2; ++i) p.chunks[i] = (p.heads[i] + heads_per_unit - 1) / heads_per_unit;
-  p.units = tokens * (p.chunks[0] + p.chunks[1]);
+// Passes and units for `warps` resident warps: a token is cut into units of equal size, kUnitPasses at most, and smaller ones where
+// there would be fewer units than warps.
+template <bool BWD>
+void set_units(NormRopeParams& p, int64_t tokens, int d, int64_t warps) {
+  const int rows = 256 / d;
+  p.passes[0] = (p.heads[0] + rows - 1) / rows;
+  p.passes[1] = p.passes[0] + (p.heads[1] + rows - 1) / rows;
+  const int64_t all = p.passes[1];
+  int64_t per = std::max((all + kUnitPasses<BWD> - 1) / kUnitPasses<BWD>, std::min(all, warps / std::max<int64_t>(tokens, 1)));
+  p.unit = static_cast<int32_t>((all + per - 1) / per);
+  p.per = static_cast<int32_t>((all + p.unit - 1) / p.unit);
+  p.units = tokens * p.per;
+}
+
+template <int D, bool BWD>
+constexpr int smem_bytes(int unit) {
+  return (BWD ? 1 + kWarps : 1) * 2 * D * 4 + Stages<D, BWD>::bytes(unit);
+}
+
+// CTAs of `kernel` the whole device holds at its largest shared memory.  The figure depends on the kernel and the device's
+// type alone, so it is asked for once a device (`known`, 0 before; two threads would store the same).
+template <typename K>
+int resident(K* kernel, int smem, int device, std::atomic<int> (&known)[kDevices]) {
+  int n = device < kDevices ? known[device].load(std::memory_order_relaxed) : 0;
+  if (n) return n;
+  int sms = 0, per = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, smem) != cudaSuccess)
+    return 0;
+  n = per * sms;
+  if (device < kDevices) known[device].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+template <int D, bool INTER, bool BWD>
+ffa_status launch(NormRopeParams p, int64_t tokens, cudaStream_t s, int* ctas) {
+  auto* kernel = [] {
+    if constexpr (BWD) return norm_rope_bwd_kernel<D, INTER>;
+    else return norm_rope_fwd_kernel<D, INTER>;
+  }();
+  static std::atomic<int> known[kDevices];
+  constexpr int kMost = smem_bytes<D, BWD>(kUnitPasses<BWD>);
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return FFA_ERR_CUDA;
+  // over the default limit, set on every such call: the attribute belongs to the current context's copy of the kernel
+  if (kMost > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess)
+    return FFA_ERR_CUDA;
+  const int held = resident(kernel, kMost, device, known);
+  if (held == 0) return FFA_ERR_CUDA;
+  set_units<BWD>(p, tokens, D, static_cast<int64_t>(held) * kWarps);
+  const int64_t want = (p.units + kWarps - 1) / kWarps;
+  const int grid = static_cast<int>(std::min<int64_t>({want, held, kMaxBwdCtas}));
+  *ctas = grid;
+  if (grid > 0) kernel<<<grid, kThreads, smem_bytes<D, BWD>(p.unit), s>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
+template <bool BWD>
+ffa_status launch_any(const NormRopeParams& p, int64_t tokens, int d, bool interleaved, cudaStream_t s, int* ctas) {
+  if (d == 128) return interleaved ? launch<128, true, BWD>(p, tokens, s, ctas) : launch<128, false, BWD>(p, tokens, s, ctas);
+  return interleaved ? launch<64, true, BWD>(p, tokens, s, ctas) : launch<64, false, BWD>(p, tokens, s, ctas);
 }
 
 // Bytes from the first to the last value of a strided [tokens][heads][d] bf16 tensor.
@@ -379,16 +534,8 @@ ffa_status ffa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int6
   if (any_meet(outs, 2, in, 6)) return FFA_ERR_INVALID_ARG;
   p.out[0] = static_cast<__nv_bfloat16*>(q_out);
   p.out[1] = static_cast<__nv_bfloat16*>(k_out);
-  set_units(p, tokens, kUnroll * 256 / d);
-  const int64_t blocks = (p.units + kWarps - 1) / kWarps;
-  if (blocks > 0x7fffffff) return FFA_ERR_OVERFLOW;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const dim3 grid(static_cast<unsigned>(blocks));
-  if (d == 128)
-    (interleaved ? norm_rope_fwd_kernel<128, true> : norm_rope_fwd_kernel<128, false>)<<<grid, kThreads, 0, s>>>(p);
-  else
-    (interleaved ? norm_rope_fwd_kernel<64, true> : norm_rope_fwd_kernel<64, false>)<<<grid, kThreads, 0, s>>>(p);
-  return cuda_status(cudaGetLastError());
+  int ctas = 0;
+  return launch_any<false>(p, tokens, d, interleaved != 0, static_cast<cudaStream_t>(stream), &ctas);
 }
 
 size_t ffa_qk_norm_rope_bwd_workspace_size(int32_t d) {
@@ -423,20 +570,10 @@ ffa_status ffa_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, 
   p.out[0] = static_cast<__nv_bfloat16*>(dq);
   p.out[1] = static_cast<__nv_bfloat16*>(dk);
   p.partial = static_cast<float*>(workspace);
-  set_units(p, tokens, 2 * 256 / d);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int device = 0, sms = 0;
-  if (cudaGetDevice(&device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
-    return FFA_ERR_CUDA;
-  const int64_t want = (p.units + kWarps - 1) / kWarps;
-  const int blocks = static_cast<int>(std::min<int64_t>({want, int64_t{4} * sms, int64_t{kMaxBwdCtas}}));
-  if (blocks > 0) {
-    if (d == 128)
-      (interleaved ? norm_rope_bwd_kernel<128, true> : norm_rope_bwd_kernel<128, false>)<<<blocks, kThreads, 0, s>>>(p);
-    else
-      (interleaved ? norm_rope_bwd_kernel<64, true> : norm_rope_bwd_kernel<64, false>)<<<blocks, kThreads, 0, s>>>(p);
-  }
+  int blocks = 0;
+  const ffa_status sl = launch_any<true>(p, tokens, d, interleaved != 0, s, &blocks);
+  if (sl != FFA_OK) return sl;
   if (d == 128)
     norm_rope_dw_kernel<128><<<8, 1024, 0, s>>>(p.partial, blocks, dq_weight, dk_weight);
   else

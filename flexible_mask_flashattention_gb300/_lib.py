@@ -479,10 +479,12 @@ def bwd(q, k, v, out, lse, dout, plan: Plan, scale: float, dq=None, dk=None, dv=
 # The calls below take a few microseconds on the host and run many times a second in a decode loop, so their checks are
 # single expressions, and what went wrong is worked out only once something did.
 
+torch = None   # imported by the first of these calls, once
+
+
 def _on(stream, device: int):
     """(handle, context): the stream a call launches on, and the context in which tensors are allocated for use on it, or
     None for the current stream, on which they are anyway."""
-    import torch
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device), None
     if isinstance(stream, torch.cuda.Stream):
@@ -501,7 +503,9 @@ def _empty(like, context, *specs):
 
 def _device(t, name) -> int:
     """The device of tensor t, which must be the current one."""
-    import torch
+    global torch
+    if torch is None:
+        import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise FFAError(1, f"{name} must be a CUDA tensor")
     dev = t.get_device()
@@ -523,7 +527,6 @@ def _check_dense(t, dtype, shape, dev, name):
 
 def _rows_stride(t, name, shape, dev):
     """The token stride of a bf16 tensor of `shape` [tokens, heads, d] whose heads are contiguous within a token."""
-    import torch
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.get_device() != dev:
         raise FFAError(1, f"{name} must be a bfloat16 tensor on the device of the other tensors")
     if t.shape != shape:
@@ -543,7 +546,6 @@ def _dims(t, name, n):
 
 def _kv_cache(k_cache, v_cache, k_exp, v_exp, dev) -> KVCacheC:
     """The C description of a cache: k, v [pages, hkv, page_size, d] bf16, or float8_e4m3fn with exponent bytes."""
-    import torch
     dtype = k_cache.dtype
     quantised = dtype is torch.float8_e4m3fn
     if not quantised and dtype is not torch.bfloat16:
@@ -562,7 +564,6 @@ def _kv_cache(k_cache, v_cache, k_exp, v_exp, dev) -> KVCacheC:
 
 def _page_table(t, batch: int, dev):
     """(row stride, max_pages) of an int32 page table [batch, max_pages]."""
-    import torch
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.get_device() != dev:
         raise FFAError(1, "page_table must be an int32 tensor on the device of the other tensors")
     rows, width = _dims(t, "page_table", 2)
@@ -576,7 +577,6 @@ def _page_table(t, batch: int, dev):
 
 def _norm_rope_inputs(q, k, q_weight, k_weight, cos_sin, positions, dev):
     """Checked (q's stride, k's stride, tokens, hq, hkv, d, max_pos, rot_dim) of the inputs both directions share."""
-    import torch
     if not isinstance(k, torch.Tensor) or not isinstance(cos_sin, torch.Tensor):
         raise FFAError(1, "k and cos_sin must be CUDA tensors")
     tokens, hq, d = _dims(q, "q", 3)
@@ -597,7 +597,6 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6
     """(q_out, k_out): every head row of q [S, Hq, d] and k [S, Hkv, d] divided by its RMS, times its
     weight [d] (fp32), and rotated by its token's position (int32 [S]) with cos_sin [max_pos, rot_dim]
     (fp32; the cosines first).  q and k may be views of one projection's output."""
-    import torch
     dev = _device(q, "q")
     qs, ks, tokens, hq, hkv, d, max_pos, rot = _norm_rope_inputs(q, k, q_weight, k_weight, cos_sin, positions, dev)
     handle, context = _on(stream, dev)
@@ -620,7 +619,6 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6
 def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk_out, eps: float = 1e-6,
                      interleaved: bool = False, workspace=None, stream=None):
     """dq, dk (bf16) and dq_weight, dk_weight (fp32 [d]) of qk_norm_rope, from the gradients of its outputs."""
-    import torch
     dev = _device(q, "q")
     qs, ks, tokens, hq, hkv, d, max_pos, rot = _norm_rope_inputs(q, k, q_weight, k_weight, cos_sin, positions, dev)
     bf16, f32, qshape, kshape = torch.bfloat16, torch.float32, (tokens, hq, d), (tokens, hkv, d)
@@ -648,7 +646,6 @@ def kv_cache_write(k, v, k_cache, v_cache, slots, k_exp=None, v_exp=None, stream
     """Write the rows of k, v [T, Hkv, d] into the cache [pages, Hkv, page_size, d] at slots (int64 [T]: page *
     page_size + offset; negative or outside: not written).  A float8_e4m3fn cache holds codes and, in k_exp / v_exp
     [pages, Hkv, page_size] uint8, each row's exponent: value = code * 2^(byte - 127)."""
-    import torch
     dev = _device(k_cache, "k_cache")
     cache = _kv_cache(k_cache, v_cache, k_exp, v_exp, dev)
     if not isinstance(slots, torch.Tensor):
@@ -667,7 +664,6 @@ def kv_cache_read(k_cache, v_cache, page_table, cu_seqlens, total: int, k=None, 
     """k, v [total, Hkv, d] bf16: the first cu_seqlens[b + 1] - cu_seqlens[b] (int32 [B + 1]) keys and values of
     every sequence, back to back; page_table [B, max_pages] int32.  Rows behind the last sequence are left as they
     were (undefined where k and v are allocated here)."""
-    import torch
     dev = _device(k_cache, "k_cache")
     cache = _kv_cache(k_cache, v_cache, k_exp, v_exp, dev)
     if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
@@ -701,7 +697,6 @@ def fwd_decode(q, k_cache, v_cache, page_table, kv_lens, scale: float, k_exp=Non
                sink=None, out=None, lse=None, workspace=None, stream=None):
     """out [B, Hq, d] bf16 and lse [Hq, B] fp32 of one new token a sequence, q [B, Hq, d], over the keys
     [kv_starts[b], kv_lens[b]) (int32 [B]) of the paged cache; sink [Hq] fp32 as in fwd_sink."""
-    import torch
     dev = _device(q, "q")
     if not isinstance(k_cache, torch.Tensor):
         raise FFAError(1, "k_cache must be a CUDA tensor")

@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
   struct Begin { int32_t b; int64_t off; };
   Begin* begin = reinterpret_cast<Begin*>(smem + 512);
 
+  allow_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = lane >> 2, t = lane & 3;   // an MMA fragment's row (or column) group and position in it
   const int units = p.geom.hkv * p.subs;
@@ -645,6 +646,7 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
 template <int D, int NT>
 __global__ void __launch_bounds__(256) decode_join_kernel(DecodeParams p, float bias) {
   constexpr int NQ = 8 * NT;
+  wait_for_primary();
   const JoinDesc d = p.desc[blockIdx.x];
   if (d.parts == 0) return;
   const int h0 = (d.unit / p.subs) * p.group, s0 = (d.unit % p.subs) * NQ;
@@ -684,8 +686,8 @@ ffa_status launch(const DecodeParams& p, int sms, cudaStream_t s) {
   if (e != cudaSuccess) return FFA_ERR_CUDA;
   const int grid = std::min(sms, kMaxCtas);
   kernel<<<grid, C::THREADS, C::SMEM, s>>>(p);
-  decode_join_kernel<D, NT><<<grid, 256, 0, s>>>(p, FP8 ? 10.f : 0.f);
-  return cuda_status(cudaGetLastError());
+  if (cudaGetLastError() != cudaSuccess) return FFA_ERR_CUDA;
+  return cuda_status(launch_after(decode_join_kernel<D, NT>, grid, 256, s, p, FP8 ? 10.f : 0.f));
 }
 
 }  // namespace

@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NormRopeParams 
   }
   for (int i = threadIdx.x; i < 2 * D; i += kThreads) weights[i] = p.w[i / D][i % D];
   __syncthreads();
+  allow_dependents();
   float2 acc[2][4] = {};
   int stage = 0, fill = kStages - 1;
   for (; cur.u < p.units; cur.next(stride, p.per)) {
@@ -371,6 +372,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NormRopeParams 
 template <int D>
 __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* partial, int n, float* dqw, float* dkw) {
   __shared__ float red[32][33];
+  wait_for_primary();
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
   float s = 0.f;
   for (int i = r; i < n; i += 32) s += partial[static_cast<int64_t>(i) * (2 * D) + c];
@@ -574,11 +576,9 @@ ffa_status ffa_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, 
   int blocks = 0;
   const ffa_status sl = launch_any<true>(p, tokens, d, interleaved != 0, s, &blocks);
   if (sl != FFA_OK) return sl;
-  if (d == 128)
-    norm_rope_dw_kernel<128><<<8, 1024, 0, s>>>(p.partial, blocks, dq_weight, dk_weight);
-  else
-    norm_rope_dw_kernel<64><<<4, 1024, 0, s>>>(p.partial, blocks, dq_weight, dk_weight);
-  return cuda_status(cudaGetLastError());
+  const cudaError_t e = d == 128 ? launch_after(norm_rope_dw_kernel<128>, 8, 1024, s, p.partial, blocks, dq_weight, dk_weight)
+                                 : launch_after(norm_rope_dw_kernel<64>, 4, 1024, s, p.partial, blocks, dq_weight, dk_weight);
+  return cuda_status(e);
 }
 
 }  // extern "C"

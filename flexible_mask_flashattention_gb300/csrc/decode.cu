@@ -197,54 +197,81 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
   const int units = p.geom.hkv * p.subs;
 
   // ---- this CTA's share of the block list
-  const int per = (p.batch + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b)
-    mine += range_blocks(key_range(p.lens[b], p.starts ? p.starts[b] : 0, p.max_pages, p.geom.page_log2), kBlock);
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  if (lane == 31) scan[warp] = incl;
-  __syncthreads();
-  int64_t before = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kW; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
-  }
-  total *= units;
-  const int64_t parts = total < gridDim.x ? total : gridDim.x;
+  auto blocks_of = [&](int b) {
+    return range_blocks(key_range(p.lens[b], p.starts ? p.starts[b] : 0, p.max_pages, p.geom.page_log2), kBlock);
+  };
+  int64_t total, t0, t1, parts, off;   // off: of the share's first block in its sequence b
+  int b;
   const int64_t cta = blockIdx.x;
-  if (cta >= parts) {
-    if (tid == 0) p.desc[cta].parts = 0;
-    return;
-  }
-  const int64_t t0 = share_begin(total, parts, cta), t1 = share_begin(total, parts, cta + 1);
-  {
+  if (p.batch <= 32) {   // a sequence a lane, every warp for itself
+    const int64_t mine = lane < p.batch ? blocks_of(lane) : 0;
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    total = __shfl_sync(0xffffffffu, incl, 31) * units;
+    parts = total < gridDim.x ? total : gridDim.x;
+    if (cta >= parts) {
+      if (tid == 0) p.desc[cta].parts = 0;
+      return;
+    }
+    t0 = share_begin(total, parts, cta);
+    t1 = share_begin(total, parts, cta + 1);
+    b = __ffs(__ballot_sync(0xffffffffu, t0 < incl * units)) - 1;
+    off = t0 - __shfl_sync(0xffffffffu, incl - mine, b) * units;
+  } else {
+    const int per = (p.batch + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
+    int64_t mine = 0;
+    for (int i = b0; i < b1; ++i) mine += blocks_of(i);
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - mine;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      if (w < warp) before += scan[w];
+      total += scan[w];
+    }
+    total *= units;
+    parts = total < gridDim.x ? total : gridDim.x;
+    if (cta >= parts) {
+      if (tid == 0) p.desc[cta].parts = 0;
+      return;
+    }
+    t0 = share_begin(total, parts, cta);
+    t1 = share_begin(total, parts, cta + 1);
     int64_t x = before * units;
     if (t0 >= x && t0 < x + mine * units) {
-      int b = b0;
-      for (;; ++b) {
-        const int64_t nb = units * range_blocks(key_range(p.lens[b], p.starts ? p.starts[b] : 0, p.max_pages, p.geom.page_log2), kBlock);
+      int i = b0;
+      for (;; ++i) {
+        const int64_t nb = units * blocks_of(i);
         if (t0 < x + nb) break;
         x += nb;
       }
-      begin->b = b;
+      begin->b = i;
       begin->off = t0 - x;
     }
+    __syncthreads();
+    b = begin->b;
+    off = begin->off;
   }
-  __syncthreads();
   Walk<kW> cur;
+  bool opens_mid;
   {
-    const int64_t nb = range_blocks(key_range(p.lens[begin->b], p.starts ? p.starts[begin->b] : 0, p.max_pages, p.geom.page_log2), kBlock);
-    const int u = static_cast<int>(begin->off / nb);
-    cur.set(p, begin->b, u, begin->off - u * nb, warp);
+    const int64_t nb = blocks_of(b);
+    const int u = off < nb ? 0 : off <= 0x7fffffff ? static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(nb)) : static_cast<int>(off / nb);
+    cur.set(p, b, u, off - u * nb, warp);
+    opens_mid = off != u * nb;
   }
-  const bool opens_mid = begin->off % range_blocks(key_range(p.lens[cur.b], p.starts ? p.starts[cur.b] : 0, p.max_pages, p.geom.page_log2), kBlock) != 0;
 
   // ---- loading one strip of this warp; the loads' walk runs ahead of the products'
   const uint32_t ring = smem_u32(smem + C::MISC + C::JOIN) + warp * (C::STAGE * C::STAGES);
@@ -642,34 +669,50 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
   if (opened == 0 && tid == 0) p.desc[cta].parts = 0;
 }
 
-// Joins the parts of the unit that CTA blockIdx.x of the main kernel opened, in the order of their keys.
+// Joins the parts of the unit that CTA blockIdx.x of the main kernel opened: a CTA a q head of the unit (blockIdx.y), D / 4
+// threads to a part and as many parts at once as 256 threads hold, then those by the order of their first part.  Every load
+// of a round is independent, so a unit of 152 parts takes a few memory latencies.
 template <int D, int NT>
 __global__ void __launch_bounds__(256) decode_join_kernel(DecodeParams p, float bias) {
-  constexpr int NQ = 8 * NT;
+  constexpr int NQ = 8 * NT, COLS = D / 4, LANES = 256 / COLS, UNROLL = 4;
+  __shared__ float4 so[LANES][COLS];
+  __shared__ float2 sm[LANES];
   wait_for_primary();
   const JoinDesc d = p.desc[blockIdx.x];
-  if (d.parts == 0) return;
-  const int h0 = (d.unit / p.subs) * p.group, s0 = (d.unit % p.subs) * NQ;
-  for (int i = threadIdx.x; i < NQ * (D / 4); i += 256) {
-    const int qi = i / (D / 4), col = 4 * (i % (D / 4));
-    if (s0 + qi >= p.group) continue;
-    float mx = -INFINITY;
-    for (int k = 0; k < d.parts; ++k) {
-      const int64_t slot = k == 0 ? d.first_slot : 2 * (static_cast<int64_t>(blockIdx.x) + k);
-      mx = fmaxf(mx, p.ml[(slot * NQ + qi) * 2]);
+  const int qi = blockIdx.y, row = (d.unit % p.subs) * NQ + qi;
+  if (d.parts == 0 || row >= p.group) return;
+  const int c = threadIdx.x % COLS, lane = threadIdx.x / COLS;
+  float mx = -INFINITY, sum = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto merge = [&](float2 ml, float4 a) {
+    const float top = fmaxf(mx, ml.x);
+    const float fo = mx == -INFINITY ? 0.f : ex2_approx(mx - top), fn = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
+    sum = (mx == -INFINITY ? sum : sum * fo) + (ml.x == -INFINITY ? ml.y : ml.y * fn);   // sums without a maximum are 0 or NaN
+    v = make_float4(v.x * fo + a.x * fn, v.y * fo + a.y * fn, v.z * fo + a.z * fn, v.w * fo + a.w * fn);
+    mx = top;
+  };
+  for (int k0 = lane; k0 < d.parts; k0 += UNROLL * LANES) {
+    float2 ml[UNROLL];
+    float4 a[UNROLL];
+#pragma unroll
+    for (int i = 0; i < UNROLL; ++i) {
+      const int k = k0 + i * LANES;
+      if (k >= d.parts) continue;
+      const int64_t at = (k == 0 ? d.first_slot : 2 * (static_cast<int64_t>(blockIdx.x) + k)) * NQ + qi;
+      ml[i] = *reinterpret_cast<const float2*>(p.ml + at * 2);
+      a[i] = *reinterpret_cast<const float4*>(p.part + at * D + 4 * c);
     }
-    float sum = 0.f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < d.parts; ++k) {
-      const int64_t slot = k == 0 ? d.first_slot : 2 * (static_cast<int64_t>(blockIdx.x) + k);
-      const float2 ml = *reinterpret_cast<const float2*>(p.ml + (slot * NQ + qi) * 2);
-      const float4 a = *reinterpret_cast<const float4*>(p.part + (slot * NQ + qi) * D + col);
-      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
-      sum += ml.x == -INFINITY ? ml.y : ml.y * f;
-      v.x = fmaf(a.x, f, v.x), v.y = fmaf(a.y, f, v.y), v.z = fmaf(a.z, f, v.z), v.w = fmaf(a.w, f, v.w);
-    }
-    write_row<D>(p, d.batch, h0 + s0 + qi, col, v, mx, sum, bias);
+#pragma unroll
+    for (int i = 0; i < UNROLL; ++i)
+      if (k0 + i * LANES < d.parts) merge(ml[i], a[i]);
   }
+  so[lane][c] = v;
+  if (c == 0) sm[lane] = make_float2(mx, sum);
+  __syncthreads();
+  if (lane != 0) return;
+#pragma unroll
+  for (int i = 1; i < LANES; ++i) merge(sm[i], so[i][c]);
+  write_row<D>(p, d.batch, (d.unit / p.subs) * p.group + row, 4 * c, v, mx, sum, bias);
 }
 
 constexpr size_t kDescBytes = sizeof(JoinDesc) * kMaxCtas;
@@ -687,7 +730,7 @@ ffa_status launch(const DecodeParams& p, int sms, cudaStream_t s) {
   const int grid = std::min(sms, kMaxCtas);
   kernel<<<grid, C::THREADS, C::SMEM, s>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FFA_ERR_CUDA;
-  return cuda_status(launch_after(decode_join_kernel<D, NT>, grid, 256, s, p, FP8 ? 10.f : 0.f));
+  return cuda_status(launch_after(decode_join_kernel<D, NT>, dim3(grid, std::min(8 * NT, p.group)), 256, s, p, FP8 ? 10.f : 0.f));
 }
 
 }  // namespace

@@ -76,6 +76,15 @@ int main() {
       CHECK(share_of(total, parts, a) == c && share_of(total, parts, b - 1) == c, "share_of");
     }
   }
+  for (int i = 0; i < 3000; ++i) {   // around the border of the 32-bit form, and far behind it
+    const int64_t total = i % 2 ? (int64_t{1} << 21) - 3 + rnd(6) : (int64_t{1} << 21) + (rnd(1 << 30) << (i % 13));
+    const int64_t parts = 1 + rnd(1024);
+    for (int64_t c : {int64_t{0}, rnd(parts), parts - 1}) {
+      const int64_t a = share_begin(total, parts, c), b = share_begin(total, parts, c + 1);
+      CHECK(a == static_cast<int64_t>(static_cast<__int128>(total) * c / parts), "share_begin");
+      CHECK(a < b && share_of(total, parts, a) == c && share_of(total, parts, b - 1) == c, "share_of, total %lld", static_cast<long long>(total));
+    }
+  }
   // a strip's chunks: a permutation of its 16-byte places, and no bank conflict in either read pattern
   for (int cpr : {4, 8, 16}) {
     std::set<int> all;

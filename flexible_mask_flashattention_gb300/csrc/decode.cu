@@ -84,7 +84,7 @@ struct Cfg {
   static constexpr int CPR = ROW / 16;                  // 16-byte chunks a row
   static constexpr int STRIP = 16 * ROW;                // bytes of 16 rows
   static constexpr int STAGE = 2 * STRIP + (FP8 ? 32 : 0);
-  static constexpr int JOIN = (W / 2) * 8 * NT * D * 4 + W * 8 * NT * 8;   // O buffers, (m, l) a warp
+  static constexpr int JOIN = (W / 2) * 8 * NT * D * 4 + (W + 1) * 8 * NT * 8;   // O buffers; (m, l) of every warp and of all
   static constexpr int MISC = 1024;
   static constexpr int STAGES = (kSmemMax - JOIN - MISC) / (W * STAGE) < 8 ? (kSmemMax - JOIN - MISC) / (W * STAGE) : 8;
   static constexpr int SMEM = MISC + JOIN + W * STAGE * STAGES;
@@ -160,11 +160,14 @@ struct Walk {
   }
 };
 
-// One row's four columns: sink, normalisation, the single rounding; lse by the first column's thread.
-template <int D>
-__device__ __forceinline__ void write_row(const DecodeParams& p, int b, int head, int col, float4 v, float mx, float sum, float bias) {
+// The end of a row whose sums, times 2^bias, are relative to the maximum mx: the sink, then what its columns are multiplied by
+// (NaN where the sum is) and its lse.
+struct RowEnd {
+  float inv, lse;
+};
+__device__ __forceinline__ RowEnd row_end(const DecodeParams& p, int head, float mx, float sum, float bias) {
   float f = 1.f;
-  mx -= bias;   // sums are held times 2^bias
+  mx -= bias;
   if (p.sink) {
     const float s2 = p.sink[head] * kLog2e;
     const float top = fmaxf(mx, s2);
@@ -172,12 +175,10 @@ __device__ __forceinline__ void write_row(const DecodeParams& p, int b, int head
     sum = (mx == -INFINITY && sum == 0.f ? 0.f : sum * f) + (s2 == -INFINITY ? 0.f : ex2_approx(s2 - top));
     mx = top;
   }
-  const float inv = sum == 0.f ? 0.f : f / sum;
-  const float r[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-  uint2 w = make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
-  if (sum != sum) w = make_uint2(0x7fff7fffu, 0x7fff7fffu);
-  *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(b) * p.hq + head) * D + col) = w;
-  if (col == 0) p.lse[static_cast<int64_t>(head) * p.batch + b] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+  RowEnd r;
+  r.inv = sum == 0.f ? 0.f : f / sum;
+  r.lse = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+  return r;
 }
 
 template <int D, bool FP8, int NT>
@@ -185,8 +186,8 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
   using C = Cfg<D, FP8, NT>;
   constexpr int NQ = 8 * NT, kW = C::W, kThreads = C::THREADS, kBlock = C::BLOCK;
   extern __shared__ __align__(128) uint8_t smem[];
-  float* join_o = reinterpret_cast<float*>(smem + C::MISC);                       // [kW / 2][NQ][D]
-  float* join_ml = join_o + (kW / 2) * NQ * D;                                    // [kW][NQ][2]
+  float2* join_o = reinterpret_cast<float2*>(smem + C::MISC);   // [kW / 2][an MMA's result registers in pairs][32 lanes]
+  float2* join_ml = join_o + (kW / 2) * NQ * D / 2;             // [kW][NQ], then [NQ] of all warps
   int64_t* scan = reinterpret_cast<int64_t*>(smem);                               // [kW] warp sums, then the total
   struct Begin { int32_t b; int64_t off; };
   Begin* begin = reinterpret_cast<Begin*>(smem + 512);
@@ -543,10 +544,11 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
     }
   };
 
-  // ---- the end of a unit's part: join the warps, then write the rows or the part
+  // ---- the end of a unit's part: join the warps, then write the rows or the part.  The buffers hold the values as the MMAs'
+  // results lie in a warp (pair, lane), so that neither side has a bank conflict.
+  constexpr int kPairs = NT * C::MT * 2;
   auto end_part = [&](bool whole, int slot) {
-    // per-warp sums over its lanes; a bad page or length makes the part NaN
-    const float poison = __any_sync(0xffffffffu, bad) ? __int_as_float(0x7fffffff) : 0.f;
+    const float poison = __any_sync(0xffffffffu, bad) ? __int_as_float(0x7fffffff) : 0.f;   // a bad page or length
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -555,11 +557,7 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
         s += __shfl_xor_sync(0xffffffffu, s, 4);
         s += __shfl_xor_sync(0xffffffffu, s, 8);
         s += __shfl_xor_sync(0xffffffffu, s, 16);
-        if (n == 0) {
-          float* ml = join_ml + (warp * NQ + nt * 8 + 2 * t + c) * 2;
-          ml[0] = m[nt][c];
-          ml[1] = s + poison;
-        }
+        if (n == 0) join_ml[warp * NQ + nt * 8 + 2 * t + c] = make_float2(m[nt][c], s + poison);
       }
     __syncthreads();
     float f[NT][2];
@@ -569,10 +567,9 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
       for (int c = 0; c < 2; ++c) {
         float mx = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kW; ++w) mx = fmaxf(mx, join_ml[(w * NQ + nt * 8 + 2 * t + c) * 2]);
+        for (int w = 0; w < kW; ++w) mx = fmaxf(mx, join_ml[w * NQ + nt * 8 + 2 * t + c].x);
         f[nt][c] = m[nt][c] == -INFINITY ? 0.f : ex2_approx(m[nt][c] - mx) * (FP8 ? pow2i(ev_ref - 127) : 1.f);
       }
-    auto column = [&](int i) { return FP8 ? (D / 8) * n + 2 * i : (i / 4) * 64 + 8 * n + 2 * (i % 4); };
     if (warp >= kW / 2) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -580,8 +577,18 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
         for (int i = 0; i < C::MT; ++i)
 #pragma unroll
           for (int c = 0; c < 2; ++c)
-            *reinterpret_cast<float2*>(join_o + ((warp - kW / 2) * NQ + nt * 8 + 2 * t + c) * D + column(i)) =
+            join_o[((warp - kW / 2) * kPairs + (nt * C::MT + i) * 2 + c) * 32 + lane] =
                 make_float2(o[nt][i][c] * f[nt][c], o[nt][i][c + 2] * f[nt][c]);
+    } else if (tid < NQ) {
+      float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kW; ++w) mx = fmaxf(mx, join_ml[w * NQ + tid].x);
+#pragma unroll
+      for (int w = 0; w < kW; ++w) {
+        const float2 v = join_ml[w * NQ + tid];
+        sum += v.x == -INFINITY ? v.y : v.y * ex2_approx(v.x - mx);   // v.y is 0 or NaN without a maximum
+      }
+      join_ml[kW * NQ + tid] = make_float2(mx, sum);
     }
     __syncthreads();
     if (warp < kW / 2) {
@@ -591,38 +598,35 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
         for (int i = 0; i < C::MT; ++i)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float2* at = reinterpret_cast<float2*>(join_o + (warp * NQ + nt * 8 + 2 * t + c) * D + column(i));
-            const float2 b = *at;
-            *at = make_float2(fmaf(o[nt][i][c], f[nt][c], b.x), fmaf(o[nt][i][c + 2], f[nt][c], b.y));
+            float2* at = join_o + (warp * kPairs + (nt * C::MT + i) * 2 + c) * 32 + lane;
+            const float2 v = *at;
+            *at = make_float2(fmaf(o[nt][i][c], f[nt][c], v.x), fmaf(o[nt][i][c + 2], f[nt][c], v.y));
           }
     }
     __syncthreads();
+    // what is read from here on (the buffers, the joint (m, l)) is written again only behind the next part's first barrier
     const int h0 = (cur.u / p.subs) * p.group, s0 = (cur.u % p.subs) * NQ;
-    for (int i = tid; i < NQ * (D / 4); i += kThreads) {
-      const int qi = i / (D / 4), col = 4 * (i % (D / 4));
-      if (s0 + qi >= p.group) continue;
-      float mx = -INFINITY, sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < kW; ++w) mx = fmaxf(mx, join_ml[(w * NQ + qi) * 2]);
-#pragma unroll
-      for (int w = 0; w < kW; ++w) {
-        const float mw = join_ml[(w * NQ + qi) * 2], lw = join_ml[(w * NQ + qi) * 2 + 1];
-        sum += mw == -INFINITY ? lw : lw * ex2_approx(mw - mx);   // lw is 0 or NaN there
-      }
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int e = warp; e < kPairs; e += kW) {
+      const int i = e / 2 % C::MT, qi = e / (2 * C::MT) * 8 + 2 * t + (e & 1);
+      const int col = FP8 ? (D / 8) * n + 2 * i : (i / 4) * 64 + 8 * n + 2 * (i % 4);
+      float2 v = make_float2(0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kW / 2; ++w) {
-        const float4 a = *reinterpret_cast<const float4*>(join_o + (w * NQ + qi) * D + col);
-        v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+        const float2 a = join_o[(w * kPairs + e) * 32 + lane];
+        v.x += a.x, v.y += a.y;
       }
+      if (s0 + qi >= p.group) continue;
+      const float2 ml = join_ml[kW * NQ + qi];
+      const int64_t at = static_cast<int64_t>(slot) * NQ + qi;
       if (!whole) {
-        *reinterpret_cast<float4*>(p.part + (static_cast<int64_t>(slot) * NQ + qi) * D + col) = v;
-        if (col == 0) *reinterpret_cast<float2*>(p.ml + (static_cast<int64_t>(slot) * NQ + qi) * 2) = make_float2(mx, sum);
-        continue;
+        *reinterpret_cast<float2*>(p.part + at * D + col) = v;
+        if (col == 0) *reinterpret_cast<float2*>(p.ml + at * 2) = ml;
+      } else {
+        const RowEnd r = row_end(p, h0 + s0 + qi, ml.x, ml.y, kBias);
+        *reinterpret_cast<uint32_t*>(p.out + (static_cast<int64_t>(cur.b) * p.hq + h0 + s0 + qi) * D + col) = pack_bf16x2(v.x * r.inv, v.y * r.inv);
+        if (col == 0) p.lse[static_cast<int64_t>(h0 + s0 + qi) * p.batch + cur.b] = r.lse;
       }
-      write_row<D>(p, cur.b, h0 + s0 + qi, col, v, mx, sum, kBias);
     }
-    __syncthreads();
   };
 
   // ---- the share
@@ -712,7 +716,11 @@ __global__ void __launch_bounds__(256) decode_join_kernel(DecodeParams p, float 
   if (lane != 0) return;
 #pragma unroll
   for (int i = 1; i < LANES; ++i) merge(sm[i], so[i][c]);
-  write_row<D>(p, d.batch, (d.unit / p.subs) * p.group + row, 4 * c, v, mx, sum, bias);
+  const int head = (d.unit / p.subs) * p.group + row;
+  const RowEnd r = row_end(p, head, mx, sum, bias);
+  *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(d.batch) * p.hq + head) * D + 4 * c) =
+      make_uint2(pack_bf16x2(v.x * r.inv, v.y * r.inv), pack_bf16x2(v.z * r.inv, v.w * r.inv));
+  if (c == 0) p.lse[static_cast<int64_t>(head) * p.batch + d.batch] = r.lse;
 }
 
 constexpr size_t kDescBytes = sizeof(JoinDesc) * kMaxCtas;

@@ -160,38 +160,64 @@ struct Stages {
   static __host__ __device__ constexpr int bytes(int unit) { return kStages * (unit * (BWD ? 2 : 1) + 1) * kThreads * 16; }
 };
 
+// The part of a unit in one tensor: a token's heads are contiguous and a pass is 512 bytes of them whatever d is, so pass i of the
+// part is at byte 512 i behind the lane's 16 of the first.  `full`: every lane has a head in every pass.
+constexpr int kPass = 256;   // values a pass
+struct UnitPart {
+  int n, first, heads_left;   // passes; the first one in the unit's stage; of this lane's head in the first pass, heads from it on
+  int64_t at;                 // of this lane's first value in a token's heads
+  bool full;
+};
+template <int D>
+__device__ __forceinline__ UnitPart part_of(const NormRopeParams& p, int c, int t, int lane) {
+  const int j0 = c * p.unit, j1 = min(j0 + p.unit, p.passes[1]);
+  const int from = t ? p.passes[0] : 0, a = max(j0, from), b = min(j1, p.passes[t]);
+  UnitPart r;
+  r.n = b - a;
+  r.first = a - j0;
+  r.at = (a - from) * kPass + 8 * lane;
+  r.heads_left = p.heads[t] - (static_cast<int>(r.at) / D);
+  r.full = (b - from) * kPass <= p.heads[t] * D;
+  return r;
+}
+// Has the lane a head in pass i of the part?
+template <int D>
+__device__ __forceinline__ bool has_head(const UnitPart& r, int i) { return r.full || i * (kPass / D) < r.heads_left; }
+
 // Start the copies of one unit into `stage`.  Rows behind the last head are filled with zeros.
 template <int D, bool BWD>
 __device__ __forceinline__ void copy_unit(const NormRopeParams& p, const Stages<D, BWD>& st, int stage, const UnitWalk& w, int lane) {
-  constexpr int L = D / 8, RW = 32 / L;
-  const int l = lane & (L - 1), sub = lane / L;
-  const int j0 = w.c * p.unit, j1 = min(j0 + p.unit, p.passes[1]);
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int from = t ? p.passes[0] : 0, a = max(j0, from), b = min(j1, p.passes[t]);
-    int h = (a - from) * RW + sub;
-    const __nv_bfloat16* x = p.x[t] + w.token * p.x_stride[t] + static_cast<int64_t>(h) * D + 8 * l;
-    const __nv_bfloat16* g = BWD ? p.dout[t] + (w.token * p.heads[t] + h) * D + 8 * l : nullptr;
-    for (int j = a; j < b; ++j) {
-      const int bytes = h < p.heads[t] ? 16 : 0;
-      cp_async16(smem_u32(st.chunk(stage, j - j0)), bytes ? x : p.x[t], bytes);
-      if constexpr (BWD) cp_async16(smem_u32(st.chunk(stage, p.unit + j - j0)), bytes ? g : p.dout[t], bytes);
-      h += RW;
-      x += RW * D;
-      if constexpr (BWD) g += RW * D;
+    const UnitPart r = part_of<D>(p, w.c, t, lane);
+    if (r.n <= 0) continue;
+    const __nv_bfloat16* x = p.x[t] + w.token * p.x_stride[t] + r.at;
+    const __nv_bfloat16* g = BWD ? p.dout[t] + w.token * p.heads[t] * D + r.at : nullptr;
+    const uint32_t to = smem_u32(st.chunk(stage, r.first)), to_g = smem_u32(st.chunk(stage, p.unit + r.first));
+#pragma unroll
+    for (int i = 0; i < kUnitPasses<BWD>; ++i) {
+      if (i >= r.n) break;
+      if (r.full) {
+        cp_async16(to + i * kThreads * 16, x + i * kPass);
+        if constexpr (BWD) cp_async16(to_g + i * kThreads * 16, g + i * kPass);
+      } else {
+        const int bytes = has_head<D>(r, i) ? 16 : 0;
+        cp_async16(to + i * kThreads * 16, bytes ? x + i * kPass : p.x[t], bytes);
+        if constexpr (BWD) cp_async16(to_g + i * kThreads * 16, bytes ? g + i * kPass : p.dout[t], bytes);
+      }
     }
   }
   if (w.pos >= 0 && w.pos < p.max_pos && 4 * lane < p.rot)
-    cp_async16(smem_u32(st.chunk(stage, p.unit * (BWD ? 2 : 1))), p.cos_sin + static_cast<int64_t>(w.pos) * p.rot + 4 * lane, 16);
+    cp_async16(smem_u32(st.chunk(stage, p.unit * (BWD ? 2 : 1))), p.cos_sin + static_cast<int64_t>(w.pos) * p.rot + 4 * lane);
 }
 
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(NormRopeParams p) {
-  constexpr int L = D / 8, RW = 32 / L;
+  constexpr int L = D / 8;
   extern __shared__ __align__(128) uint8_t smem[];
   float* weights = reinterpret_cast<float*>(smem);   // [2][D]
   const Stages<D, false> st{reinterpret_cast<uint4*>(smem + 2 * D * 4), p.unit};
-  const int lane = threadIdx.x & 31, l = lane & (L - 1), sub = lane / L;
+  const int lane = threadIdx.x & 31, l = lane & (L - 1);
   const int64_t stride = gridDim.x * static_cast<int64_t>(kWarps);
   UnitWalk cur, ld;
   cur.init(p, blockIdx.x * static_cast<int64_t>(kWarps) + (threadIdx.x >> 5), stride);
@@ -214,22 +240,21 @@ __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(NormRopeParams 
     ld.read_pos(p);   // a unit ahead of its use
     cp_async_wait<kStages - 1>();
     __syncwarp();
-    const int j0 = cur.c * p.unit, j1 = min(j0 + p.unit, p.passes[1]);
     const bool live = pos >= 0 && pos < p.max_pos;
     Rotation<D, INTER> rot;
     if (live) rot.load(st.table(stage), p.rot, lane);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int from = t ? p.passes[0] : 0, a0 = max(j0, from), b0 = min(j1, p.passes[t]);
-      if (a0 >= b0) continue;
-      int h = (a0 - from) * RW + sub;
-      __nv_bfloat16* out = p.out[t] + (cur.token * p.heads[t] + h) * D + 8 * l;
+      const UnitPart u = part_of<D>(p, cur.c, t, lane);
+      if (u.n <= 0) continue;
+      __nv_bfloat16* out = p.out[t] + cur.token * p.heads[t] * D + u.at;
       if (!live) {   // a padded token (negative position) gives zeros, one behind the table NaN
         const uint32_t c = pos < 0 ? 0u : 0x7fff7fffu;
-        for (int j = a0; j < b0; ++j, h += RW, out += RW * D)
-          if (h < p.heads[t]) *reinterpret_cast<uint4*>(out) = make_uint4(c, c, c, c);
+        for (int i = 0; i < u.n; ++i)
+          if (has_head<D>(u, i)) *reinterpret_cast<uint4*>(out + i * kPass) = make_uint4(c, c, c, c);
         continue;
       }
+      const uint4* in = st.chunk(stage, u.first);
       // coefficients with the weights: out_j = r (x_j a_j + partner_j b_j)
       float2 a[4], b[4];
       load8(weights + t * D + 8 * l, a);
@@ -242,19 +267,17 @@ __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(NormRopeParams 
 #pragma unroll
       for (int j = 0; j < 4; ++j) a[j] = mul2(a[j], rot.c[j]), b[j] = mul2(b[j], rot.s[j]);
 #pragma unroll 2
-      for (int j = a0; j < b0; ++j) {
-        const uint4 v = *st.chunk(stage, j - j0);
+      for (int i = 0; i < u.n; ++i) {
+        const uint4 v = in[i * kThreads];
         float2 f[4], q[4], ss = make_float2(0.f, 0.f);
         unpack8(v, f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ss = fma2(f[i], f[i], ss);
+        for (int j = 0; j < 4; ++j) ss = fma2(f[j], f[j], ss);
         const float r = rsqrtf(row_sum<D>(ss.x + ss.y) * (1.f / D) + p.eps);
         rot.partners(v, f, q);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = mul2(fma2(f[i], a[i], mul2(q[i], b[i])), make_float2(r, r));
-        if (h < p.heads[t]) *reinterpret_cast<uint4*>(out) = pack8(f);
-        h += RW;
-        out += RW * D;
+        for (int j = 0; j < 4; ++j) f[j] = mul2(fma2(f[j], a[j], mul2(q[j], b[j])), make_float2(r, r));
+        if (has_head<D>(u, i)) *reinterpret_cast<uint4*>(out + i * kPass) = pack8(f);
       }
     }
     __syncwarp();   // the stage's table row has been read by every lane before the next iteration refills it
@@ -268,7 +291,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(NormRopeParams 
 // the result does not depend on timing.
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NormRopeParams p) {
-  constexpr int L = D / 8, RW = 32 / L;
+  constexpr int L = D / 8;
   extern __shared__ __align__(128) uint8_t smem[];
   float* weights = reinterpret_cast<float*>(smem);   // [2][D]
   float* red = weights + 2 * D;                      // [kWarps][2][D]
@@ -298,7 +321,6 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NormRopeParams 
     ld.read_pos(p);
     cp_async_wait<kStages - 1>();
     __syncwarp();
-    const int j0 = cur.c * p.unit, j1 = min(j0 + p.unit, p.passes[1]);
     const bool live = pos >= 0 && pos < p.max_pos;
     Rotation<D, INTER> rot;
     if (live) rot.load(st.table(stage), p.rot, lane);
@@ -306,22 +328,22 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NormRopeParams 
     for (int j = 0; j < 4; ++j) rot.s[j] = make_float2(-rot.s[j].x, -rot.s[j].y);   // R^T turns by the negative angle
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int from = t ? p.passes[0] : 0, a0 = max(j0, from), b0 = min(j1, p.passes[t]);
-      if (a0 >= b0) continue;
-      int h = (a0 - from) * RW + sub;
-      __nv_bfloat16* dx = p.out[t] + (cur.token * p.heads[t] + h) * D + 8 * l;
+      const UnitPart u = part_of<D>(p, cur.c, t, lane);
+      if (u.n <= 0) continue;
+      __nv_bfloat16* dx = p.out[t] + cur.token * p.heads[t] * D + u.at;
       if (!live) {   // padding: no gradient; behind the table: NaN, in the weight's gradient too
         const uint32_t c = pos < 0 ? 0u : 0x7fff7fffu;
-        for (int j = a0; j < b0; ++j, h += RW, dx += RW * D)
-          if (h < p.heads[t]) *reinterpret_cast<uint4*>(dx) = make_uint4(c, c, c, c);
+        for (int i = 0; i < u.n; ++i)
+          if (has_head<D>(u, i)) *reinterpret_cast<uint4*>(dx + i * kPass) = make_uint4(c, c, c, c);
         if (pos >= 0) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
         continue;
       }
+      const uint4 *in = st.chunk(stage, u.first), *in_g = st.chunk(stage, p.unit + u.first);
       float2 w[4];
       load8(weights + t * D + 8 * l, w);
 #pragma unroll 2
-      for (int j = a0; j < b0; ++j) {
-        const uint4 v = *st.chunk(stage, j - j0), gv = *st.chunk(stage, p.unit + j - j0);
+      for (int k = 0; k < u.n; ++k) {
+        const uint4 v = in[k * kThreads], gv = in_g[k * kThreads];
         float2 f[4], g[4], q[4], ss = make_float2(0.f, 0.f), hx = make_float2(0.f, 0.f);
         unpack8(v, f);
         unpack8(gv, g);
@@ -341,9 +363,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NormRopeParams 
           hw[i] = fma2(f[i], make_float2(c, c), mul2(hw[i], make_float2(r, r)));   // dx = r h - x r^3 mean(h x)
           acc[t][i] = fma2(g[i], mul2(f[i], make_float2(r, r)), acc[t][i]);
         }
-        if (h < p.heads[t]) *reinterpret_cast<uint4*>(dx) = pack8(hw);
-        h += RW;
-        dx += RW * D;
+        if (has_head<D>(u, k)) *reinterpret_cast<uint4*>(dx + k * kPass) = pack8(hw);
       }
     }
     __syncwarp();
@@ -438,7 +458,7 @@ ffa_status check_common(const void* q, int64_t q_stride, const void* k, int64_t 
 // there would be fewer units than warps.
 template <bool BWD>
 void set_units(NormRopeParams& p, int64_t tokens, int d, int64_t warps) {
-  const int rows = 256 / d;
+  const int rows = kPass / d;
   p.passes[0] = (p.heads[0] + rows - 1) / rows;
   p.passes[1] = p.passes[0] + (p.heads[1] + rows - 1) / rows;
   const int64_t all = p.passes[1];

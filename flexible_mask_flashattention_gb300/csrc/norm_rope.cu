@@ -478,6 +478,7 @@ int resident(K* kernel, int smem, int device, std::atomic<int> (&known)[kDevices
   if (n) return n;
   int sms = 0, per = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
       cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, smem) != cudaSuccess)
     return 0;
   n = per * sms;
@@ -495,10 +496,6 @@ ffa_status launch(NormRopeParams p, int64_t tokens, cudaStream_t s, int* ctas) {
   constexpr int kMost = smem_bytes<D, BWD>(kUnitPasses<BWD>);
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) return FFA_ERR_CUDA;
-  // over the default limit, set on every such call: the attribute belongs to the current context's copy of the kernel
-  if (kMost > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess)
-    return FFA_ERR_CUDA;
   const int held = resident(kernel, kMost, device, known);
   if (held == 0) return FFA_ERR_CUDA;
   set_units<BWD>(p, tokens, D, static_cast<int64_t>(held) * kWarps);
@@ -510,7 +507,12 @@ ffa_status launch(NormRopeParams p, int64_t tokens, cudaStream_t s, int* ctas) {
   if (p.span > 0x40000000) return FFA_ERR_OVERFLOW;
   const int grid = static_cast<int>((p.units + p.span - 1) / p.span);
   *ctas = grid;
-  if (grid > 0) kernel<<<grid, kThreads, smem_bytes<D, BWD>(p.unit), s>>>(p);
+  if (grid == 0) return FFA_OK;
+  const int smem = smem_bytes<D, BWD>(p.unit);
+  // over the default limit, set on every such call: the attribute belongs to the current context's copy of the kernel
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess)
+    return FFA_ERR_CUDA;
+  kernel<<<grid, kThreads, smem, s>>>(p);
   return cuda_status(cudaGetLastError());
 }
 

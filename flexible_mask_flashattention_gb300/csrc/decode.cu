@@ -37,7 +37,12 @@
 namespace ffa {
 namespace {
 
-constexpr int warps_of(bool fp8, int nt) { return fp8 && nt == 1 ? 12 : 8; }   // warps a CTA
+// Warps a CTA, and groups of 16 keys a strip.  Warps hide each other's latencies, as far as registers and the ring allow; longer strips
+// spread a strip's fixed instructions over more keys.  Measured (us; 50 x 20K keys, 64 + 8 heads, d = 64, e4m3): 8 warps x 1 group 165,
+// 8 x 2 137, 8 x 4 120, 12 x 4 118, 16 x 2 118; (1M keys, 16 + 4 heads, d = 128, e4m3): 8 x 1 181, 12 x 1 170, 8 x 2 169; (24 x 8K
+// keys, 32 heads, d = 64, bf16): 8 x 1 119, 8 x 2 122, 12 x 2 117; (380K keys, 32 + 2 heads, d = 128, e4m3): 8 x 1 46, 8 x 2 43.
+constexpr int warps_of(int d, bool fp8, int nt) { return nt == 2 || d == 128 ? 8 : fp8 ? 16 : 12; }
+constexpr int groups_of(int d, bool fp8) { return d == 128 && !fp8 ? 1 : 2; }
 constexpr int kMaxCtas = 512;          // split parts the workspace holds: two a CTA
 constexpr int kSmemMax = 226 * 1024;   // of 227 KB
 constexpr float kLog2e = 1.4426950408889634f;
@@ -70,21 +75,24 @@ struct DecodeParams {
   __nv_bfloat16* out;
   float* lse;
   JoinDesc* desc;     // [kMaxCtas]
-  float* ml;          // [2 kMaxCtas][8 NT][2]
+  float2* ml;         // [2 kMaxCtas][8 NT]
   float* part;        // [2 kMaxCtas][8 NT][D]
 };
 
 template <int D, bool FP8, int NT>
 struct Cfg {
-  static constexpr int W = warps_of(FP8, NT);
+  static constexpr int W = warps_of(D, FP8, NT);
   static constexpr int THREADS = 32 * W;
-  static constexpr int BLOCK = 16 * W;                  // keys of a block
+  static constexpr int SK = groups_of(D, FP8);
+  static constexpr int KEYS = 16 * SK;                  // keys of a strip
+  static constexpr int BLOCK = KEYS * W;                // keys of a block
   static constexpr int ES = FP8 ? 1 : 2;
   static constexpr int ROW = D * ES;                    // bytes a stored row
   static constexpr int CPR = ROW / 16;                  // 16-byte chunks a row
   static constexpr int STRIP = 16 * ROW;                // bytes of 16 rows
-  static constexpr int STAGE = 2 * STRIP + (FP8 ? 32 : 0);
-  static constexpr int JOIN = (W / 2) * 8 * NT * D * 4 + (W + 1) * 8 * NT * 8;   // O buffers; (m, l) of every warp and of all
+  static constexpr int GROUP = 2 * STRIP + (FP8 ? 32 : 0);   // of 16 keys: K, V, exponents
+  static constexpr int STAGE = SK * GROUP;
+  static constexpr int JOIN = (W / 2) * 8 * NT * D * 4 + (W + 1) * 8 * NT * 8;   // O buffers; (m, l) of every warp, the rows' factors
   static constexpr int MISC = 1024;
   static constexpr int STAGES = (kSmemMax - JOIN - MISC) / (W * STAGE) < 8 ? (kSmemMax - JOIN - MISC) / (W * STAGE) : 8;
   static constexpr int SMEM = MISC + JOIN + W * STAGE * STAGES;
@@ -106,6 +114,9 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   uint32_t r;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a) : "memory");
   return r;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t v) {   // four times v
+  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(v) : "memory");
 }
 __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {   // transpose of an 8 x 8 matrix of 16-bit values
   uint32_t r;
@@ -131,34 +142,41 @@ __device__ __forceinline__ float pow2i(int e) {   // 2^e, 0 below the normal ran
 }
 
 // Where a walk over the CTA's share of the block list stands: unit (b, u) with u = kv head * subs + sub, `left` blocks of it from
-// the current one on, and the first key of this warp's strip in the current block.
-template <int W>
+// the current one on, and the first key of this warp's strip in the current block.  Which of a block's strips is a warp's turns with
+// every unit, so that units of one strip keep all warps busy.
+template <int W, int KEYS>
 struct Walk {
-  static constexpr int kBlock = 16 * W;
-  int b, u, left, key, start, end;
+  static constexpr int kBlock = KEYS * W;
+  int b, u, left, key, start, end, turn;   // turn: of the block's strips, the one that is this warp's
   bool bad;
   // The first of the unit's blocks that is walked is `blk`.
-  __device__ __forceinline__ void set(const DecodeParams& p, int seq, int unit, int64_t blk, int warp) {
-    const KeyRange r = key_range(p.lens[seq], p.starts ? p.starts[seq] : 0, p.max_pages, p.geom.page_log2);
+  __device__ __forceinline__ void set(const KeyRange& r, int seq, int unit, int64_t blk) {
     b = seq;
     u = unit;
     start = static_cast<int>(r.start);
     end = static_cast<int>(r.end);
     bad = r.bad;
-    left = static_cast<int>(range_blocks(r, kBlock) - blk);
-    // a warp's strip may lie behind the end, by a block at most: as keys are below 2^31, unsigned arithmetic and a clamp
-    const int64_t k = range_first(r) + (blk * W + warp) * 16;
-    key = static_cast<int>(k < r.end ? k : r.end);
+    left = static_cast<int>(range_blocks(r, kBlock, KEYS) - blk);
+    const int64_t k = range_first(r, KEYS) + (blk * W + turn) * KEYS;
+    key = static_cast<int>(k < r.end ? k : r.end);   // a strip behind the end is empty
   }
   __device__ __forceinline__ void step() {   // to the unit's next block
     --left;
     key = end - key > kBlock ? key + kBlock : end;
   }
-  __device__ __forceinline__ void next_unit(const DecodeParams& p, int units, int warp) {
+  __device__ __forceinline__ void next_unit(const DecodeParams& p, int units) {
+    turn = turn == 0 ? W - 1 : turn - 1;
     const bool wrap = u + 1 == units;
-    set(p, wrap ? b + 1 : b, wrap ? 0 : u + 1, 0, warp);
+    const int seq = wrap ? b + 1 : b;
+    set(key_range(p.lens[seq], p.starts ? p.starts[seq] : 0, p.max_pages, p.geom.page_log2), seq, wrap ? 0 : u + 1, 0);
   }
 };
+
+// The first of the two neighbouring columns that a lane's MMA results of tile i are.
+template <int D, bool FP8>
+__device__ __forceinline__ int column(int i, int n) {
+  return FP8 ? (D / 8) * n + 2 * i : (i / 4) * 64 + 8 * n + 2 * (i % 4);
+}
 
 // The end of a row whose sums, times 2^bias, are relative to the maximum mx: the sink, then what its columns are multiplied by
 // (NaN where the sum is) and its lse.
@@ -182,13 +200,14 @@ __device__ __forceinline__ RowEnd row_end(const DecodeParams& p, int head, float
 }
 
 template <int D, bool FP8, int NT>
-__global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(DecodeParams p) {
+__global__ void __launch_bounds__(32 * warps_of(D, FP8, NT), 1) decode_kernel(DecodeParams p) {
   using C = Cfg<D, FP8, NT>;
-  constexpr int NQ = 8 * NT, kW = C::W, kThreads = C::THREADS, kBlock = C::BLOCK;
+  constexpr int NQ = 8 * NT, kW = C::W, kThreads = C::THREADS, kBlock = C::BLOCK, SK = C::SK;
   extern __shared__ __align__(128) uint8_t smem[];
   float2* join_o = reinterpret_cast<float2*>(smem + C::MISC);   // [kW / 2][an MMA's result registers in pairs][32 lanes]
-  float2* join_ml = join_o + (kW / 2) * NQ * D / 2;             // [kW][NQ], then [NQ] of all warps
+  float2* join_ml = join_o + (kW / 2) * NQ * D / 2;             // (m, l) [kW][NQ], then the rows' factors [NQ]
   int64_t* scan = reinterpret_cast<int64_t*>(smem);                               // [kW] warp sums, then the total
+  int64_t* kept = scan + 32;                                                      // [3]
   struct Begin { int32_t b; int64_t off; };
   Begin* begin = reinterpret_cast<Begin*>(smem + 512);
 
@@ -198,14 +217,16 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
   const int units = p.geom.hkv * p.subs;
 
   // ---- this CTA's share of the block list
-  auto blocks_of = [&](int b) {
-    return range_blocks(key_range(p.lens[b], p.starts ? p.starts[b] : 0, p.max_pages, p.geom.page_log2), kBlock);
-  };
+  auto range_of = [&](int seq) { return key_range(p.lens[seq], p.starts ? p.starts[seq] : 0, p.max_pages, p.geom.page_log2); };
+  auto blocks_of = [&](int seq) { return range_blocks(range_of(seq), kBlock, C::KEYS); };
   int64_t total, t0, t1, parts, off;   // off: of the share's first block in its sequence b
   int b;
+  KeyRange range;
   const int64_t cta = blockIdx.x;
   if (p.batch <= 32) {   // a sequence a lane, every warp for itself
-    const int64_t mine = lane < p.batch ? blocks_of(lane) : 0;
+    KeyRange r{0, 0, false};
+    if (lane < p.batch) r = range_of(lane);
+    const int64_t mine = lane < p.batch ? range_blocks(r, kBlock, C::KEYS) : 0;
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -222,6 +243,9 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
     t1 = share_begin(total, parts, cta + 1);
     b = __ffs(__ballot_sync(0xffffffffu, t0 < incl * units)) - 1;
     off = t0 - __shfl_sync(0xffffffffu, incl - mine, b) * units;
+    range.start = __shfl_sync(0xffffffffu, static_cast<int>(r.start), b);
+    range.end = __shfl_sync(0xffffffffu, static_cast<int>(r.end), b);
+    range.bad = __shfl_sync(0xffffffffu, static_cast<int>(r.bad), b) != 0;
   } else {
     const int per = (p.batch + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
@@ -264,68 +288,93 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
     __syncthreads();
     b = begin->b;
     off = begin->off;
+    range = range_of(b);
   }
-  Walk<kW> cur;
+  Walk<kW, C::KEYS> cur;
   bool opens_mid;
   {
-    const int64_t nb = blocks_of(b);
-    const int u = off < nb ? 0 : off <= 0x7fffffff ? static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(nb)) : static_cast<int>(off / nb);
-    cur.set(p, b, u, off - u * nb, warp);
+    const int64_t nb = range_blocks(range, kBlock, C::KEYS);
+    int u = 0;
+    if (off >= nb) u = off <= 0x7fffffff ? static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(nb)) : static_cast<int>(off / nb);
+    cur.turn = warp;
+    cur.set(range, b, u, off - u * nb);
     opens_mid = off != u * nb;
   }
 
   // ---- loading one strip of this warp; the loads' walk runs ahead of the products'
   const uint32_t ring = smem_u32(smem + C::MISC + C::JOIN) + warp * (C::STAGE * C::STAGES);
-  uint32_t stage_bad = 0;   // stages whose page the cache does not have
-  Walk<kW> ld = cur;
-  auto page_of = [&]() -> int { return ld.key < ld.end ? __ldg(p.table + ld.b * p.table_stride + (ld.key >> p.geom.page_log2)) : 0; };
-  int page = page_of();     // the page of the next strip to load, read one strip ahead
-  // this lane's chunks of a strip: chunk lane + 32 i, rows 32 / CPR apart; source and destination offsets
-  uint32_t dst_of[C::CPR / 2];
+  Walk<kW, C::KEYS> ld = cur;
+  const int page_rows = p.geom.hkv << p.geom.page_log2, page_mask = (1 << p.geom.page_log2) - 1;
+  int head_row;           // the loading unit's head's first row in a page
+  int page[SK];           // of the next strip's groups of 16 keys, read a strip ahead; -1 for a group outside the range
+  auto read_pages = [&]() {
+    const int32_t* row = p.table + ld.b * p.table_stride;
 #pragma unroll
-  for (int i = 0; i < C::CPR / 2; ++i) dst_of[i] = 16 * strip_chunk((lane + 32 * i) / C::CPR, (lane + 32 * i) % C::CPR, C::CPR);
+    for (int g = 0; g < SK; ++g) {
+      const bool in = ld.end - ld.key > 16 * g && ld.start - ld.key < 16 * (g + 1);
+      page[g] = in ? __ldg(row + ((ld.key + 16 * g) >> p.geom.page_log2)) : -1;
+    }
+  };
+  auto open_unit = [&]() {
+    head_row = (p.subs == 1 ? ld.u : ld.u / p.subs) << p.geom.page_log2;
+    read_pages();
+  };
+  // this lane's chunks of a strip: chunk lane + 32 i, 512 bytes apart in the cache; their places repeat every kPeriod of them
+  constexpr int kPeriod = strip_period(C::CPR);
+  uint32_t dst_of[kPeriod];
+#pragma unroll
+  for (int i = 0; i < kPeriod; ++i) dst_of[i] = ring + 16 * strip_chunk((lane + 32 * i) / C::CPR, (lane + 32 * i) % C::CPR, C::CPR);
   auto load_strip = [&](int stage, bool more) {
     const int have = ld.end - ld.key;
     if (have > 0) {
-      const int off = ld.key & ((1 << p.geom.page_log2) - 1);
-      const bool ok = page_ok(p.geom, page);
-      const uint32_t bit = 1u << stage;
-      stage_bad = ok ? stage_bad & ~bit : stage_bad | bit;
-      const int64_t row = ok ? cache_row(p.geom, page, p.subs == 1 ? ld.u : ld.u / p.subs, off) : 0;
-      const uint8_t* ksrc = static_cast<const uint8_t*>(p.k) + row * C::ROW + lane * 16;
-      const uint8_t* vsrc = static_cast<const uint8_t*>(p.v) + row * C::ROW + lane * 16;
-      const uint32_t dst = ring + stage * C::STAGE;
-      if (ok && have >= 16 && ld.key >= ld.start) {
+      const bool full = have >= C::KEYS && ld.key >= ld.start;
 #pragma unroll
-        for (int i = 0; i < C::CPR / 2; ++i) {
-          cp_async16(dst + dst_of[i], ksrc + 512 * i);
-          cp_async16(dst + C::STRIP + dst_of[i], vsrc + 512 * i);
-        }
-      } else {   // rows outside the range are filled with zeros, not read
-        const int lo = max(ld.start - ld.key, 0), hi = ok ? min(have, 16) : 0;
+      for (int g = 0; g < SK; ++g) {
+        const bool ok = static_cast<uint32_t>(page[g]) < static_cast<uint32_t>(p.geom.num_pages);   // as page_ok, for pages of 32 bits
+        const int64_t row = static_cast<int64_t>(ok ? page[g] : 0) * page_rows + (head_row + ((ld.key + 16 * g) & page_mask));
+        const int64_t at = row * C::ROW + lane * 16;
+        const uint8_t *k = static_cast<const uint8_t*>(p.k) + at, *v = static_cast<const uint8_t*>(p.v) + at;
+        const uint32_t base = stage * C::STAGE + g * C::GROUP;
+        if (full && ok) {
 #pragma unroll
-        for (int i = 0; i < C::CPR / 2; ++i) {
-          const int key = (lane + 32 * i) / C::CPR, bytes = key >= lo && key < hi ? 16 : 0;
-          cp_async16(dst + dst_of[i], ksrc + 512 * i, bytes);
-          cp_async16(dst + C::STRIP + dst_of[i], vsrc + 512 * i, bytes);
+          for (int i = 0; i < C::CPR / 2; ++i) {
+            const uint32_t to = base + dst_of[i % kPeriod] + i / kPeriod * (kPeriod * 512);
+            cp_async16(to, k + 512 * i);
+            cp_async16(to + C::STRIP, v + 512 * i);
+          }
+        } else {   // rows outside the range are filled with zeros, not read
+          const int lo = ld.start - ld.key - 16 * g, hi = min(have - 16 * g, 16);
+          const bool none = lo >= 16 || hi <= 0;
+#pragma unroll
+          for (int i = 0; i < C::CPR / 2; ++i) {
+            const uint32_t to = base + dst_of[i % kPeriod] + i / kPeriod * (kPeriod * 512);
+            const int key = (lane + 32 * i) / C::CPR, bytes = ok && key >= lo && key < hi ? 16 : 0;
+            if (ok || none) cp_async16(to, k + 512 * i, bytes);
+            else sts128(to, 0x7fff7fffu);   // no such page: keys of NaN, which make the row NaN
+            cp_async16(to + C::STRIP, v + 512 * i, bytes);
+          }
         }
-      }
-      if constexpr (FP8) {
-        if (lane < 2) cp_async16(dst + 2 * C::STRIP + 16 * lane, (lane ? p.v_exp : p.k_exp) + row, ok ? 16 : 0);
+        if constexpr (FP8) {
+          if (lane < 2) cp_async16(ring + base + 2 * C::STRIP + 16 * lane, (lane ? p.v_exp : p.k_exp) + row);
+        }
       }
     }
     if (!more) return;
-    if (ld.left > 1) ld.step(); else ld.next_unit(p, units, warp);
-    page = page_of();
+    if (ld.left > 1) {
+      ld.step();
+      read_pages();
+    } else {
+      ld.next_unit(p, units);
+      open_unit();
+    }
   };
 
-  int64_t ahead = t0;
+  open_unit();
+  int64_t todo = t1 - t0;   // blocks from the current one on; the loads are STAGES - 1 of them ahead
+  if (tid == 0) kept[0] = t1, kept[1] = total, kept[2] = parts;   // wanted again at the end: not held in registers meanwhile
 #pragma unroll 1
   for (int s = 0; s < C::STAGES - 1; ++s) {
-    if (ahead < t1) {
-      ++ahead;
-      load_strip(s, ahead < t1);
-    }
+    if (s < todo) load_strip(s, s + 1 < todo);
     cp_async_commit();
   }
 
@@ -340,13 +389,12 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
   float m[NT][2], l[NT][2];
   float mb[NT][2], thr[NT][2];     // what a score's exponent is taken against, and what raises the maximum
   int ev_ref = 0;                  // e4m3: exponent byte that O's unit stands for
-  bool bad = false;
   auto begin_unit = [&]() {
     const int h0 = (cur.u / p.subs) * p.group, s0 = (cur.u % p.subs) * NQ;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int qi = s0 + nt * 8 + n;
-      const bool act = qi < p.group;
+      const bool act = qi < p.group && cur.key < cur.end;   // a warp without a key in this part needs no query
       const __nv_bfloat16* src = p.q + cur.b * p.q_stride + static_cast<int64_t>(h0 + (act ? qi : 0)) * D;
       float amax = 0.f;
 #pragma unroll
@@ -387,50 +435,57 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
       l[nt][0] = l[nt][1] = 0.f;
     }
     ev_ref = 0;
-    bad = cur.bad;
   };
 
-  // ---- one strip
+  // ---- one strip: all groups' scores, their exponentials, then all groups' values
   auto strip = [&](int stage) {
     const int have = cur.end - cur.key;
     if (have <= 0) return;
-    const bool whole = have >= 16 && cur.key >= cur.start;
-    const uint32_t kb = ring + stage * C::STAGE, vb = kb + C::STRIP;
-    bad |= (stage_bad >> stage & 1u) != 0;
-    float s[NT][2][4] = {};
+    const bool whole = have >= C::KEYS && cur.key >= cur.start;
+    const uint32_t sb = ring + stage * C::STAGE;
+    constexpr int CH = SK == 1 ? 2 : 1;   // accumulators a score tile: one group alone would be one long chain of MMAs
+    float s[SK][NT][CH][4] = {};
 #pragma unroll
-    for (int h = 0; h < C::CPR / 4; ++h) {
-      const uint4 x = lds128(kb + 16 * strip_chunk(n, t + 4 * h, C::CPR));
-      const uint4 y = lds128(kb + 16 * strip_chunk(n + 8, t + 4 * h, C::CPR));
-      const uint32_t xa[4] = {x.x, x.y, x.z, x.w}, ya[4] = {y.x, y.y, y.z, y.w};
-      if constexpr (FP8) {
+    for (int h = 0; h < C::CPR / 4; ++h)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t a0 = e4m3x2_to_f16x2(xa[j]), a2 = e4m3x2_to_f16x2(xa[j] >> 16);
-          const uint32_t a1 = e4m3x2_to_f16x2(ya[j]), a3 = e4m3x2_to_f16x2(ya[j] >> 16);
+      for (int g = 0; g < SK; ++g) {
+        const uint32_t kb = sb + g * C::GROUP;
+        const uint4 x = lds128(kb + 16 * strip_chunk(n, t + 4 * h, C::CPR));
+        const uint4 y = lds128(kb + 16 * strip_chunk(n + 8, t + 4 * h, C::CPR));
+        const uint32_t xa[4] = {x.x, x.y, x.z, x.w}, ya[4] = {y.x, y.y, y.z, y.w};
+        if constexpr (FP8) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma<true>(s[nt][j & 1], a0, a1, a2, a3, qf[nt][4 * h + j][0], qf[nt][4 * h + j][1]);
+          for (int j = 0; j < 4; ++j) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16x2(xa[j], a0, a2);
+            e4m3x4_to_f16x2(ya[j], a1, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma<true>(s[g][nt][j % CH], a0, a1, a2, a3, qf[nt][4 * h + j][0], qf[nt][4 * h + j][1]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma<false>(s[g][nt][j % CH], xa[2 * j], ya[2 * j], xa[2 * j + 1], ya[2 * j + 1], qf[nt][2 * h + j][0], qf[nt][2 * h + j][1]);
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma<false>(s[nt][j & 1], xa[2 * j], ya[2 * j], xa[2 * j + 1], ya[2 * j + 1], qf[nt][2 * h + j][0], qf[nt][2 * h + j][1]);
       }
-    }
-    // keys n and n + 8 of the strip are this lane's; columns 2t, 2t + 1 of each query tile
-    const int lo = cur.start - cur.key;
-    const bool in0 = whole || (n >= lo && n < have), in1 = whole || (n + 8 >= lo && n + 8 < have);
-    float ks0 = 1.f, ks1 = 1.f, vs0 = 1.f, vs1 = 1.f;
+    // keys n and n + 8 of a group are this lane's; columns 2t, 2t + 1 of each query tile
+    auto inside = [&](int key) { return whole || (key >= cur.start - cur.key && key < have); };
+    float ks[SK][2], vs[SK][2];
     if constexpr (FP8) {
-      const uint32_t eb = vb + C::STRIP + n;
-      ks0 = exp_scale(lds8(eb));
-      ks1 = exp_scale(lds8(eb + 8));
-      int v0 = lds8(eb + 16), v1 = lds8(eb + 24);
-      if (!whole) v0 = in0 ? v0 : 0, v1 = in1 ? v1 : 0;
-      const int top = max(v0, v1);
+      int v[SK][2], top = 0;
+#pragma unroll
+      for (int g = 0; g < SK; ++g)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t eb = sb + g * C::GROUP + 2 * C::STRIP + n + 8 * r;
+          ks[g][r] = exp_scale(lds8(eb));
+          v[g][r] = lds8(eb + 16);
+          if (!whole && !inside(16 * g + n + 8 * r)) v[g][r] = 0;
+          top = max(top, v[g][r]);
+        }
       if (__any_sync(0xffffffffu, top > ev_ref)) {
         const int ref = max(ev_ref, static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(top))));
         const float f = pow2i(ev_ref - ref);
@@ -442,26 +497,35 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
             for (int c = 0; c < 4; ++c) o[nt][i][c] *= f;
         ev_ref = ref;
       }
-      vs0 = __uint_as_float(static_cast<uint32_t>(max(v0 - ev_ref + 127, 0)) << 23);   // 2^(v0 - ev_ref), 0 below 2^-126
-      vs1 = __uint_as_float(static_cast<uint32_t>(max(v1 - ev_ref + 127, 0)) << 23);
+#pragma unroll
+      for (int g = 0; g < SK; ++g)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)   // 2^(v - ev_ref), 0 below 2^-126
+          vs[g][r] = __uint_as_float(static_cast<uint32_t>(max(v[g][r] - ev_ref + 127, 0)) << 23);
     }
-    float x[NT][4];
+    float x[SK][NT][4];
     bool raise = false;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int g = 0; g < SK; ++g)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        x[nt][c] = (s[nt][0][c] + s[nt][1][c]) * (qs[nt][c & 1] * (c < 2 ? ks0 : ks1));
-        if (!whole) x[nt][c] = (c < 2 ? in0 : in1) ? x[nt][c] : -INFINITY;
-        raise |= x[nt][c] > thr[nt][c & 1];
-      }
-    }
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v = s[g][nt][0][c];
+          if constexpr (CH == 2) v += s[g][nt][1][c];
+          v *= FP8 ? qs[nt][c & 1] * ks[g][c >> 1] : qs[nt][c & 1];
+          if (!whole && !inside(16 * g + n + 8 * (c >> 1))) v = -INFINITY;
+          x[g][nt][c] = v;
+          raise |= v > thr[nt][c & 1];
+        }
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float mx = fmaxf(x[nt][c], x[nt][c + 2]);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int g = 0; g < SK; ++g) mx = fmaxf(mx, fmaxf(x[g][nt][c], x[g][nt][c + 2]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -478,66 +542,73 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
           }
         }
     }
-    uint32_t pf[NT][2], pl[NT][2];
+    uint32_t pf[SK][NT][2], pl[SK][NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float e[4];
+    for (int g = 0; g < SK; ++g)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) e[c] = ex2_approx(x[nt][c] - mb[nt][c & 1]);
-      l[nt][0] += e[0] + e[2];
-      l[nt][1] += e[1] + e[3];
-      if constexpr (FP8) {
-        pf[nt][0] = movmatrix(pack_f16x2(e[0] * vs0, e[1] * vs0));
-        pf[nt][1] = movmatrix(pack_f16x2(e[2] * vs1, e[3] * vs1));
-      } else {
-        const uint32_t h0 = pack_bf16x2(e[0], e[1]), h1 = pack_bf16x2(e[2], e[3]);
-        pf[nt][0] = movmatrix(h0);
-        pf[nt][1] = movmatrix(h1);
-        pl[nt][0] = movmatrix(pack_bf16x2(e[0] - __uint_as_float(h0 << 16), e[1] - __uint_as_float(h0 & 0xffff0000u)));
-        pl[nt][1] = movmatrix(pack_bf16x2(e[2] - __uint_as_float(h1 << 16), e[3] - __uint_as_float(h1 & 0xffff0000u)));
-      }
-    }
-    // out^T += V^T P^T: this lane's four keys 2t, 2t + 1, 2t + 8, 2t + 9 and its columns
-    if constexpr (FP8) {
-      constexpr int WORDS = C::MT / 2;   // 32-bit words of a row this lane owns: 2 (d = 64) or 4
-      uint32_t r[4][WORDS];
+      for (int nt = 0; nt < NT; ++nt) {
+        float e[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = 2 * t + (i & 1) + 8 * (i >> 1);
-        if constexpr (D == 128) {
-          const uint4 w = lds128(vb + 16 * strip_chunk(key, n, C::CPR));
-          r[i][0] = w.x, r[i][1] = w.y, r[i][2] = w.z, r[i][3] = w.w;
+        for (int c = 0; c < 4; ++c) e[c] = ex2_approx(x[g][nt][c] - mb[nt][c & 1]);
+        l[nt][0] += e[0] + e[2];
+        l[nt][1] += e[1] + e[3];
+        if constexpr (FP8) {
+          pf[g][nt][0] = movmatrix(pack_f16x2(e[0] * vs[g][0], e[1] * vs[g][0]));
+          pf[g][nt][1] = movmatrix(pack_f16x2(e[2] * vs[g][1], e[3] * vs[g][1]));
         } else {
-          const uint2 w = lds64(vb + 16 * strip_chunk(key, n >> 1, C::CPR) + 8 * (n & 1));
-          r[i][0] = w.x, r[i][1] = w.y;
+          const uint32_t h0 = pack_bf16x2(e[0], e[1]), h1 = pack_bf16x2(e[2], e[3]);
+          pf[g][nt][0] = movmatrix(h0);
+          pf[g][nt][1] = movmatrix(h1);
+          pl[g][nt][0] = movmatrix(pack_bf16x2(e[0] - __uint_as_float(h0 << 16), e[1] - __uint_as_float(h0 & 0xffff0000u)));
+          pl[g][nt][1] = movmatrix(pack_bf16x2(e[2] - __uint_as_float(h1 << 16), e[3] - __uint_as_float(h1 & 0xffff0000u)));
         }
       }
+    // out^T += V^T P^T: this lane's four keys 2t, 2t + 1, 2t + 8, 2t + 9 of each group, and its columns
 #pragma unroll
-      for (int i = 0; i < C::MT; ++i) {
-        const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;   // columns 2i, 2i + 1 of two keys, paired by column
-        const uint32_t w0 = __byte_perm(r[0][i / 2], r[1][i / 2], sel), w1 = __byte_perm(r[2][i / 2], r[3][i / 2], sel);
-        const uint32_t a0 = e4m3x2_to_f16x2(w0), a1 = e4m3x2_to_f16x2(w0 >> 16);
-        const uint32_t a2 = e4m3x2_to_f16x2(w1), a3 = e4m3x2_to_f16x2(w1 >> 16);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma<true>(o[nt][i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-      }
-    } else {
-#pragma unroll
-      for (int hh = 0; hh < D / 64; ++hh) {
-        uint32_t r[4][4];
+    for (int g = 0; g < SK; ++g) {
+      const uint32_t vb = sb + g * C::GROUP + C::STRIP;
+      if constexpr (FP8) {
+        constexpr int WORDS = C::MT / 2;   // 32-bit words of a row this lane owns: 2 (d = 64) or 4
+        uint32_t r[4][WORDS];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint4 w = lds128(vb + 16 * strip_chunk(2 * t + (i & 1) + 8 * (i >> 1), n + 8 * hh, C::CPR));
-          r[i][0] = w.x, r[i][1] = w.y, r[i][2] = w.z, r[i][3] = w.w;
+          const int key = 2 * t + (i & 1) + 8 * (i >> 1);
+          if constexpr (D == 128) {
+            const uint4 w = lds128(vb + 16 * strip_chunk(key, n, C::CPR));
+            r[i][0] = w.x, r[i][1] = w.y, r[i][2] = w.z, r[i][3] = w.w;
+          } else {
+            const uint2 w = lds64(vb + 16 * strip_chunk(key, n >> 1, C::CPR) + 8 * (n & 1));
+            r[i][0] = w.x, r[i][1] = w.y;
+          }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t a0 = __byte_perm(r[0][i], r[1][i], 0x5410), a1 = __byte_perm(r[0][i], r[1][i], 0x7632);
-          const uint32_t a2 = __byte_perm(r[2][i], r[3][i], 0x5410), a3 = __byte_perm(r[2][i], r[3][i], 0x7632);
+        for (int i = 0; i < C::MT; ++i) {
+          const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;   // columns 2i, 2i + 1 of two keys, paired by column
+          const uint32_t w0 = __byte_perm(r[0][i / 2], r[1][i / 2], sel), w1 = __byte_perm(r[2][i / 2], r[3][i / 2], sel);
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16x2(w0, a0, a1);
+          e4m3x4_to_f16x2(w1, a2, a3);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma<false>(o[nt][4 * hh + i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-            mma<false>(o[nt][4 * hh + i], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+          for (int nt = 0; nt < NT; ++nt) mma<true>(o[nt][i], a0, a1, a2, a3, pf[g][nt][0], pf[g][nt][1]);
+        }
+      } else {
+#pragma unroll
+        for (int hh = 0; hh < D / 64; ++hh) {
+          uint32_t r[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 w = lds128(vb + 16 * strip_chunk(2 * t + (i & 1) + 8 * (i >> 1), n + 8 * hh, C::CPR));
+            r[i][0] = w.x, r[i][1] = w.y, r[i][2] = w.z, r[i][3] = w.w;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a0 = __byte_perm(r[0][i], r[1][i], 0x5410), a1 = __byte_perm(r[0][i], r[1][i], 0x7632);
+            const uint32_t a2 = __byte_perm(r[2][i], r[3][i], 0x5410), a3 = __byte_perm(r[2][i], r[3][i], 0x7632);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma<false>(o[nt][4 * hh + i], a0, a1, a2, a3, pf[g][nt][0], pf[g][nt][1]);
+              mma<false>(o[nt][4 * hh + i], a0, a1, a2, a3, pl[g][nt][0], pl[g][nt][1]);
+            }
           }
         }
       }
@@ -548,7 +619,8 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
   // results lie in a warp (pair, lane), so that neither side has a bank conflict.
   constexpr int kPairs = NT * C::MT * 2;
   auto end_part = [&](bool whole, int slot) {
-    const float poison = __any_sync(0xffffffffu, bad) ? __int_as_float(0x7fffffff) : 0.f;   // a bad page or length
+    const int h0 = (cur.u / p.subs) * p.group, s0 = (cur.u % p.subs) * NQ;
+    const float poison = cur.bad ? __int_as_float(0x7fffffff) : 0.f;   // a length that its table row cannot hold
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -588,7 +660,13 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
         const float2 v = join_ml[w * NQ + tid];
         sum += v.x == -INFINITY ? v.y : v.y * ex2_approx(v.x - mx);   // v.y is 0 or NaN without a maximum
       }
-      join_ml[kW * NQ + tid] = make_float2(mx, sum);
+      if (whole && s0 + tid < p.group) {
+        const RowEnd r = row_end(p, h0 + s0 + tid, mx, sum, kBias);
+        p.lse[static_cast<int64_t>(h0 + s0 + tid) * p.batch + cur.b] = r.lse;
+        join_ml[kW * NQ + tid].x = r.inv;
+      } else if (!whole) {
+        p.ml[static_cast<int64_t>(slot) * NQ + tid] = make_float2(mx, sum);
+      }
     }
     __syncthreads();
     if (warp < kW / 2) {
@@ -604,11 +682,10 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
           }
     }
     __syncthreads();
-    // what is read from here on (the buffers, the joint (m, l)) is written again only behind the next part's first barrier
-    const int h0 = (cur.u / p.subs) * p.group, s0 = (cur.u % p.subs) * NQ;
+    // what is read from here on (the buffers, the rows' factors) is written again only behind the next part's first barrier
     for (int e = warp; e < kPairs; e += kW) {
       const int i = e / 2 % C::MT, qi = e / (2 * C::MT) * 8 + 2 * t + (e & 1);
-      const int col = FP8 ? (D / 8) * n + 2 * i : (i / 4) * 64 + 8 * n + 2 * (i % 4);
+      const int col = column<D, FP8>(i, n);
       float2 v = make_float2(0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kW / 2; ++w) {
@@ -616,17 +693,37 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
         v.x += a.x, v.y += a.y;
       }
       if (s0 + qi >= p.group) continue;
-      const float2 ml = join_ml[kW * NQ + qi];
-      const int64_t at = static_cast<int64_t>(slot) * NQ + qi;
       if (!whole) {
-        *reinterpret_cast<float2*>(p.part + at * D + col) = v;
-        if (col == 0) *reinterpret_cast<float2*>(p.ml + at * 2) = ml;
+        *reinterpret_cast<float2*>(p.part + (static_cast<int64_t>(slot) * NQ + qi) * D + col) = v;
       } else {
-        const RowEnd r = row_end(p, h0 + s0 + qi, ml.x, ml.y, kBias);
-        *reinterpret_cast<uint32_t*>(p.out + (static_cast<int64_t>(cur.b) * p.hq + h0 + s0 + qi) * D + col) = pack_bf16x2(v.x * r.inv, v.y * r.inv);
-        if (col == 0) p.lse[static_cast<int64_t>(h0 + s0 + qi) * p.batch + cur.b] = r.lse;
+        const float inv = join_ml[kW * NQ + qi].x;
+        *reinterpret_cast<uint32_t*>(p.out + (static_cast<int64_t>(cur.b) * p.hq + h0 + s0 + qi) * D + col) = pack_bf16x2(v.x * inv, v.y * inv);
       }
     }
+  };
+
+  // A unit that was this warp's alone: its rows.
+  auto end_alone = [&]() {
+    const int h0 = (cur.u / p.subs) * p.group, s0 = (cur.u % p.subs) * NQ;
+    const float poison = cur.bad ? __int_as_float(0x7fffffff) : 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float sum = l[nt][c];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const int row = s0 + nt * 8 + 2 * t + c, head = h0 + row;
+        if (row >= p.group) continue;
+        const RowEnd r = row_end(p, head, m[nt][c], sum + poison, kBias);
+        const float f = r.inv * (FP8 ? pow2i(ev_ref - 127) : 1.f);
+        __nv_bfloat16* out = p.out + (static_cast<int64_t>(cur.b) * p.hq + head) * D;
+        if (n == 0) p.lse[static_cast<int64_t>(head) * p.batch + cur.b] = r.lse;
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i)
+          *reinterpret_cast<uint32_t*>(out + column<D, FP8>(i, n)) = pack_bf16x2(o[nt][i][c] * f, o[nt][i][c + 2] * f);
+      }
   };
 
   // ---- the share
@@ -634,11 +731,8 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
   int32_t opened = 0;   // parts of the unit this CTA leaves open to later ones
   int stage = 0, fill = C::STAGES - 1;
 #pragma unroll 1
-  for (int64_t x = t0; x < t1; ++x) {
-    if (ahead < t1) {
-      ++ahead;
-      load_strip(fill, ahead < t1);
-    }
+  for (; todo > 0; --todo) {
+    if (todo > C::STAGES - 1) load_strip(fill, todo > C::STAGES);
     cp_async_commit();
     fill = fill + 1 == C::STAGES ? 0 : fill + 1;
     if (fresh) begin_unit();
@@ -648,15 +742,19 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
     strip(stage);
     __syncwarp();   // the stage has been read by every lane before the next iteration refills it
     stage = stage + 1 == C::STAGES ? 0 : stage + 1;
-    if (cur.left > 1 && x + 1 < t1) {
+    if (cur.left > 1 && todo > 1) {
       cur.step();
       continue;
     }
     const bool last = cur.left == 1;
     const int slot = static_cast<int>(2 * cta) + (first_part ? 0 : 1);
-    end_part(last && from_start, slot);
+    if (last && from_start && cur.end - cur.start / C::KEYS * C::KEYS <= C::KEYS) {   // a unit of one strip: its warp alone
+      if (cur.turn == 0) end_alone();
+    } else {
+      end_part(last && from_start, slot);
+    }
     if (!last && from_start) {
-      opened = static_cast<int32_t>(share_of(total, parts, x + cur.left - 1) - cta + 1);
+      opened = static_cast<int32_t>(share_of(kept[1], kept[2], kept[0] - todo + cur.left - 1) - cta + 1);
       if (tid == 0) {
         JoinDesc d{};
         d.parts = opened;
@@ -668,7 +766,7 @@ __global__ void __launch_bounds__(32 * warps_of(FP8, NT), 1) decode_kernel(Decod
     }
     first_part = false;
     from_start = fresh = true;
-    if (x + 1 < t1) cur.next_unit(p, units, warp);
+    if (todo > 1) cur.next_unit(p, units);
   }
   if (opened == 0 && tid == 0) p.desc[cta].parts = 0;
 }
@@ -703,7 +801,7 @@ __global__ void __launch_bounds__(256) decode_join_kernel(DecodeParams p, float 
       const int k = k0 + i * LANES;
       if (k >= d.parts) continue;
       const int64_t at = (k == 0 ? d.first_slot : 2 * (static_cast<int64_t>(blockIdx.x) + k)) * NQ + qi;
-      ml[i] = *reinterpret_cast<const float2*>(p.ml + at * 2);
+      ml[i] = p.ml[at];
       a[i] = *reinterpret_cast<const float4*>(p.part + at * D + 4 * c);
     }
 #pragma unroll
@@ -797,7 +895,7 @@ ffa_status ffa_fwd_decode(const void* q, int64_t q_stride, const ffa_kv_cache* c
   p.lse = lse;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.desc = reinterpret_cast<JoinDesc*>(ws);
-  p.ml = reinterpret_cast<float*>(ws + kDescBytes);
+  p.ml = reinterpret_cast<float2*>(ws + kDescBytes);
   p.part = reinterpret_cast<float*>(ws + kDescBytes + ml_bytes(nt));
   int device = 0, sms = 0;
   if (cudaGetDevice(&device) != cudaSuccess ||

@@ -201,7 +201,8 @@ ffa_status check_cache(const ffa_kv_cache* c, PageGeom& g) {
   if (c->d != 64 && c->d != 128) return FFA_ERR_UNSUPPORTED;
   if (c->dtype != FFA_KV_BF16 && c->dtype != FFA_KV_E4M3) return FFA_ERR_UNSUPPORTED;
   if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1))) return FFA_ERR_UNSUPPORTED;
-  if (c->hkv > (1 << 16) || c->num_pages > (int64_t{1} << 31)) return FFA_ERR_OVERFLOW;
+  // page numbers are int32; a page's rows, and their bytes, fit 32 bits in the kernels' index arithmetic
+  if (c->num_pages > (int64_t{1} << 31) || static_cast<int64_t>(c->hkv) * c->page_size > (1 << 22)) return FFA_ERR_OVERFLOW;
   if (!c->k || !c->v || !kv_aligned16(c->k) || !kv_aligned16(c->v)) return FFA_ERR_INVALID_ARG;
   if (c->dtype == FFA_KV_E4M3 && (!c->k_exp || !c->v_exp || !kv_aligned16(c->k_exp) || !kv_aligned16(c->v_exp)))
     return FFA_ERR_INVALID_ARG;

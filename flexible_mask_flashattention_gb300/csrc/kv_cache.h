@@ -22,6 +22,11 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
   return r;
 }
+// Four codes of a word as two pairs.
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(codes));
+}
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
   const uint32_t h = e4m3x2_to_f16x2(codes);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));

@@ -46,23 +46,24 @@ FFA_HD KeyRange key_range(int32_t len, int32_t start, int64_t max_pages, int32_t
   return r;
 }
 
-// Blocks of `block` keys (a multiple of 16) that cover the range.  Blocks are counted from the range's first key rounded down to
-// 16, so that 16-key strips never cross a page.  An empty range has one block, which writes its empty row.
-FFA_HD int64_t range_first(const KeyRange& r) { return r.start & ~int64_t{15}; }
-FFA_HD int64_t range_blocks(const KeyRange& r, int32_t block) {
-  const int64_t n = (r.end - range_first(r) + block - 1) / block;
+// Blocks of `block` keys (a multiple of `strip`, itself one of 16) that cover the range.  Blocks are counted from the range's first key
+// rounded down to `strip`, so that a strip's groups of 16 keys never cross a page.  An empty range has one block, which
+// writes its empty row.
+FFA_HD int64_t range_first(const KeyRange& r, int32_t strip) { return r.start / strip * strip; }
+FFA_HD int64_t range_blocks(const KeyRange& r, int32_t block, int32_t strip) {
+  const int64_t n = (r.end - range_first(r, strip) + block - 1) / block;
   return n > 0 ? n : 1;
 }
 
-// `total` blocks are dealt to `parts` (1024 at most) workers in equal contiguous shares: worker c has [share_begin(c),
+// `total` blocks are dealt to `parts` (4096 at most) workers in equal contiguous shares: worker c has [share_begin(c),
 // share_begin(c + 1)).  Few enough blocks take 32-bit divisions, a fifth of the 64-bit ones' time.
 FFA_HD int64_t share_begin(int64_t total, int64_t parts, int64_t c) {
-  if (total < (int64_t{1} << 21)) return static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(parts);
+  if (total < (int64_t{1} << 19)) return static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(parts);
   return total * c / parts;
 }
 // The worker whose share holds block x.
 FFA_HD int64_t share_of(int64_t total, int64_t parts, int64_t x) {
-  if (total < (int64_t{1} << 21)) return ((static_cast<uint32_t>(x) + 1) * static_cast<uint32_t>(parts) - 1) / static_cast<uint32_t>(total);
+  if (total < (int64_t{1} << 19)) return ((static_cast<uint32_t>(x) + 1) * static_cast<uint32_t>(parts) - 1) / static_cast<uint32_t>(total);
   return ((x + 1) * parts - 1) / total;
 }
 
@@ -74,5 +75,9 @@ FFA_HD int32_t strip_chunk(int32_t key, int32_t c, int32_t cpr) {
   const int32_t line = key >> 1;   // 4 chunks a row: two rows a 128-byte line
   return line * 8 + ((((key & 1) << 2) | c) ^ ((line & 3) << 1));
 }
+
+// A lane's chunks lane + 32 i lie 512 bytes apart in a strip as the cache has it, and 512 * period apart, every `period` of them, as
+// shared memory has it: chunk i is at that of chunk i % period plus (i / period) * period * 512 bytes.
+FFA_HD constexpr int32_t strip_period(int32_t cpr) { return cpr == 16 ? 4 : cpr == 8 ? 2 : 1; }
 
 }  // namespace ffa

@@ -442,7 +442,7 @@ typedef enum {
 /* A paged key-value cache (read during the call only).  k and v are
  * [num_pages][hkv][page_size][d] in dtype; k_exp and v_exp (FFA_KV_E4M3 only)
  * [num_pages][hkv][page_size] bytes.  page_size is a power of two in [16, 1024],
- * d in {64, 128}; all pointers 16-byte aligned. */
+ * hkv * page_size at most 2^22, d in {64, 128}; all pointers 16-byte aligned. */
 typedef struct {
   void *k, *v;
   uint8_t *k_exp, *v_exp;

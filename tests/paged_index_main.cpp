@@ -15,36 +15,36 @@ static int fails = 0;
 static uint64_t state = 1;
 static int64_t rnd(int64_t n) { state = state * 6364136223846793005ull + 1442695040888963407ull; return static_cast<int64_t>((state >> 33) % static_cast<uint64_t>(n)); }
 
-// Every row a strip of any block reads lies in the page that its first key names, inside the cache, and in range; every
-// key of the range is read once.
-static void walk(int page_log2, int hkv, int64_t num_pages, int max_pages, int32_t len, int32_t start, int warps) {
+// Every group of 16 keys that a strip of any block reads lies in the page that its first key names, inside the cache, and in
+// range; every key of the range is read once.
+static void walk(int page_log2, int hkv, int64_t num_pages, int max_pages, int32_t len, int32_t start, int warps, int groups) {
   const PageGeom g{num_pages, page_log2, hkv};
-  const int block = 16 * warps;
+  const int strip = 16 * groups, block = strip * warps;
   const KeyRange r = key_range(len, start, max_pages, page_log2);
   const int64_t cap = static_cast<int64_t>(max_pages) << page_log2;
   CHECK(r.bad == (len > cap), "len %d cap %lld", len, static_cast<long long>(cap));
   CHECK(r.start >= 0 && r.start <= r.end && r.end <= cap, "range");
   std::vector<int> seen(static_cast<size_t>(r.end), 0);
-  const int64_t n = range_blocks(r, block);
+  const int64_t n = range_blocks(r, block, strip);
   CHECK(n >= 1, "blocks");
   for (int64_t b = 0; b < n; ++b)
-    for (int w = 0; w < warps; ++w) {
-      const int64_t key0 = range_first(r) + (b * warps + w) * 16, have = r.end - key0;
-      if (have <= 0) continue;
-      const int64_t entry = key0 >> page_log2;
-      CHECK(entry >= 0 && entry < max_pages, "table entry %lld", static_cast<long long>(entry));
-      const int off = static_cast<int>(key0 & ((1 << page_log2) - 1));
-      CHECK(off % 16 == 0 && off + 16 <= (1 << page_log2), "strip crosses its page");
-      const int lo = static_cast<int>(r.start > key0 ? r.start - key0 : 0), hi = static_cast<int>(have < 16 ? have : 16);
-      CHECK(lo < 16, "an empty strip");
-      for (int i = lo; i < hi; ++i) ++seen[static_cast<size_t>(key0 + i)];
-      for (int64_t page : {int64_t{0}, num_pages - 1})
-        for (int h : {0, hkv - 1}) {
-          const int64_t row = cache_row(g, page, h, off);
-          CHECK(page_ok(g, page) && row >= 0 && row + 16 <= (num_pages * hkv << page_log2), "row out of the cache");
-          CHECK(row % 16 == 0, "exponent bytes are read 16 at a time");
-        }
-    }
+    for (int w = 0; w < warps; ++w)
+      for (int i = 0; i < groups; ++i) {
+        const int64_t key0 = range_first(r, strip) + (b * warps + w) * strip + 16 * i, have = r.end - key0;
+        if (have <= 0 || r.start - key0 >= 16) continue;   // no key of the range: nothing is read, its page not looked up
+        const int64_t entry = key0 >> page_log2;
+        CHECK(entry >= (r.start >> page_log2) && entry < max_pages, "table entry %lld", static_cast<long long>(entry));
+        const int off = static_cast<int>(key0 & ((1 << page_log2) - 1));
+        CHECK(off % 16 == 0 && off + 16 <= (1 << page_log2), "a group crosses its page");
+        const int lo = static_cast<int>(r.start > key0 ? r.start - key0 : 0), hi = static_cast<int>(have < 16 ? have : 16);
+        for (int j = lo; j < hi; ++j) ++seen[static_cast<size_t>(key0 + j)];
+        for (int64_t page : {int64_t{0}, num_pages - 1})
+          for (int h : {0, hkv - 1}) {
+            const int64_t row = cache_row(g, page, h, off);
+            CHECK(page_ok(g, page) && row >= 0 && row + 16 <= (num_pages * hkv << page_log2), "row out of the cache");
+            CHECK(row % 16 == 0, "exponent bytes are read 16 at a time");
+          }
+      }
   for (int64_t j = 0; j < r.end; ++j) CHECK(seen[static_cast<size_t>(j)] == (j >= r.start), "key %lld", static_cast<long long>(j));
 }
 
@@ -54,11 +54,11 @@ int main() {
     const int cap = mp << pl;
     const int32_t len = i % 7 == 0 ? cap : static_cast<int32_t>(rnd(cap + 40)) - 10;
     const int32_t start = i % 3 == 0 ? 0 : static_cast<int32_t>(rnd(cap + 40)) - 10;
-    walk(pl, 1 + static_cast<int>(rnd(4)), 1 + rnd(20), mp, len, start, 8);
+    walk(pl, 1 + static_cast<int>(rnd(4)), 1 + rnd(20), mp, len, start, i % 2 ? 8 : 12, 1 << (i / 2 % 3));
   }
-  walk(4, 2, 3, 2, 2147483647, 0, 8);
-  walk(4, 2, 3, 2, -2147483647 - 1, 5, 8);
-  walk(10, 2, 3, 5, 4999, 2147483647, 8);
+  walk(4, 2, 3, 2, 2147483647, 0, 8, 2);
+  walk(4, 2, 3, 2, -2147483647 - 1, 5, 8, 1);
+  walk(10, 2, 3, 5, 4999, 2147483647, 16, 4);
   // pages and slots as a user's arrays may hold them
   const PageGeom g{7, 5, 3};
   for (int64_t p : {int64_t{-1}, int64_t{7}, int64_t{2147483647}, int64_t{-2147483648LL}}) CHECK(!page_ok(g, p), "page %lld", static_cast<long long>(p));
@@ -68,7 +68,7 @@ int main() {
   CHECK(cache_row(PageGeom{int64_t{1} << 27, 6, 8}, (int64_t{1} << 27) - 1, 7, 63) == (int64_t{1} << 36) - 1, "64-bit rows");
   // the shares: contiguous, complete, never empty where parts <= total; share_of is their inverse
   for (int i = 0; i < 3000; ++i) {
-    const int64_t total = 1 + rnd(i % 2 ? 400 : 100000), most = 1 + rnd(512), parts = most < total ? most : total;
+    const int64_t total = 1 + rnd(i % 2 ? 400 : 100000), most = 1 + rnd(4096), parts = most < total ? most : total;
     CHECK(share_begin(total, parts, 0) == 0 && share_begin(total, parts, parts) == total, "ends");
     for (int64_t c = 0; c < parts; ++c) {
       const int64_t a = share_begin(total, parts, c), b = share_begin(total, parts, c + 1);
@@ -77,8 +77,8 @@ int main() {
     }
   }
   for (int i = 0; i < 3000; ++i) {   // around the border of the 32-bit form, and far behind it
-    const int64_t total = i % 2 ? (int64_t{1} << 21) - 3 + rnd(6) : (int64_t{1} << 21) + (rnd(1 << 30) << (i % 13));
-    const int64_t parts = 1 + rnd(1024);
+    const int64_t total = i % 2 ? (int64_t{1} << 19) - 3 + rnd(6) : (int64_t{1} << 19) + (rnd(1 << 30) << (i % 13));
+    const int64_t parts = 1 + rnd(4096);
     for (int64_t c : {int64_t{0}, rnd(parts), parts - 1}) {
       const int64_t a = share_begin(total, parts, c), b = share_begin(total, parts, c + 1);
       CHECK(a == static_cast<int64_t>(static_cast<__int128>(total) * c / parts), "share_begin");
@@ -91,6 +91,13 @@ int main() {
     for (int key = 0; key < 16; ++key)
       for (int c = 0; c < cpr; ++c) all.insert(strip_chunk(key, c, cpr));
     CHECK(static_cast<int>(all.size()) == 16 * cpr && *all.begin() == 0 && *all.rbegin() == 16 * cpr - 1, "cpr %d", cpr);
+    const int period = strip_period(cpr);
+    for (int lane = 0; lane < 32; ++lane)
+      for (int i = 0; i < cpr / 2; ++i) {
+        const int j = i % period;
+        CHECK(strip_chunk((lane + 32 * i) / cpr, (lane + 32 * i) % cpr, cpr) ==
+                  strip_chunk((lane + 32 * j) / cpr, (lane + 32 * j) % cpr, cpr) + i / period * period * 32, "period, cpr %d", cpr);
+      }
     for (int i = 0; i < 8; ++i)
       for (int h = 0; h < cpr / 4; ++h) {   // K: rows 2i, 2i + 1, chunks 4h .. 4h + 3
         std::set<int> banks;

@@ -20,6 +20,27 @@ struct PageGeom {
   int32_t hkv;
 };
 
+// Division of 0 <= n < 2^31 by a constant 1 <= d <= 2^22 as a product: n / d = floor(n m / 2^(31 + s)) with s = ceil(log2 d) and m =
+// floor(2^(31 + s) / d) + 1, which is below 2^32.
+struct FastDiv {
+  uint32_t d, m;
+  int32_t shift;   // s - 1; -1 for d = 1
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f{d, 0, -1};
+  while ((uint64_t{1} << (f.shift + 1)) < d) ++f.shift;
+  f.m = static_cast<uint32_t>((uint64_t{1} << (32 + f.shift)) / d + 1);
+  return f;
+}
+FFA_HD uint32_t divide(const FastDiv& f, uint32_t n) {
+  if (f.shift < 0) return n;
+#ifdef __CUDA_ARCH__
+  return __umulhi(n, f.m) >> f.shift;
+#else
+  return static_cast<uint32_t>((static_cast<uint64_t>(n) * f.m) >> 32 >> f.shift);
+#endif
+}
+
 // Row (page, head, offset) of the cache, counted in rows of d values.
 FFA_HD int64_t cache_row(const PageGeom& g, int64_t page, int32_t head, int32_t off) {
   return ((page * g.hkv + head) << g.page_log2) + off;

@@ -85,6 +85,15 @@ int main() {
       CHECK(a < b && share_of(total, parts, a) == c && share_of(total, parts, b - 1) == c, "share_of, total %lld", static_cast<long long>(total));
     }
   }
+  for (uint32_t d : {1u, 2u, 3u, 5u, 7u, 8u, 31u, 32u, 33u, 96u, 1000u, 4095u, 4096u, 4097u, 65536u, 4194303u, 4194304u}) {
+    const FastDiv f = fast_div(d);
+    for (int i = 0; i < 4000; ++i) {
+      const uint32_t n = i < 1000 ? static_cast<uint32_t>(i) : i < 2000 ? 2147483647u - static_cast<uint32_t>(i - 1000) : static_cast<uint32_t>(rnd(2147483648LL));
+      CHECK(divide(f, n) == n / d, "%u / %u", n, d);
+      const uint32_t k = n / d * d;   // around multiples
+      CHECK(divide(f, k) == k / d && (k == 0 || divide(f, k - 1) == (k - 1) / d), "%u / %u", k, d);
+    }
+  }
   // a strip's chunks: a permutation of its 16-byte places, and no bank conflict in either read pattern
   for (int cpr : {4, 8, 16}) {
     std::set<int> all;

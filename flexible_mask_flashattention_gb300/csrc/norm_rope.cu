@@ -9,11 +9,12 @@
 // r is recomputed in the backward from x, which it reads anyway, so the forward stores nothing for it.
 //
 // Both are bound by HBM: 4 bytes a value forward (x in, out out), 6 backward (x, dout in, dx out).  A lane holds 8
-// consecutive values of a row (16 bytes), d / 8 lanes a row.  The kernels are persistent: a warp walks over units of a
-// token's passes (a pass is the 2 or 4 head rows a warp holds at once), and cp.async keeps the next units' values and
-// table rows on their way to shared memory, where every lane reads back only what it copied itself (the table row is the
-// warp's).  Loads in flight then cost neither registers nor barriers.  Norm statistics, rotation and every
-// gradient sum are fp32, two values an instruction (fma.rn.f32x2); the one rounding to bf16 is the store's.
+// consecutive values of a row (16 bytes), d / 8 lanes a token; a warp takes 2 or 4 neighbouring tokens, one head of each at a
+// time, so that a token's rotation is read once for many heads and no head count leaves lanes empty.  The kernels are
+// persistent: a warp walks over units of up to 10 (backward: 5) heads of its tokens, and cp.async keeps the next unit's
+// values and table rows on their way to shared memory, where a token's lanes read back only what they copied.
+// Loads in flight then cost neither registers nor barriers.  Norm statistics, rotation and every gradient sum are fp32, two
+// values an instruction (fma.rn.f32x2); the one rounding to bf16 is the store's.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -31,7 +32,7 @@ constexpr int kDevices = 64;         // devices whose figures are kept
 constexpr int kMaxBwdCtas = 1024;   // partial weight gradients the workspace holds
 constexpr int kStages = 2;          // units in shared memory: one being used, one on its way
 template <bool BWD>
-constexpr int kUnitPasses = BWD ? 5 : 10;   // passes of a unit at most
+constexpr int kUnitHeads = BWD ? 5 : 10;   // heads of a unit at most
 
 struct NormRopeParams {
   const __nv_bfloat16* x[2];      // q, k
@@ -40,9 +41,9 @@ struct NormRopeParams {
   __nv_bfloat16* out[2];          // forward: outputs; backward: dx; contiguous
   const float* w[2];
   int32_t heads[2];
-  int32_t passes[2];              // a token's passes over its q heads, and over both
-  int32_t unit;                   // passes of a unit
-  int32_t per;                    // units a token
+  int32_t unit;                   // heads of a unit (q's, then k's)
+  int32_t per;                    // units a group of tokens
+  int64_t tokens;
   int64_t units, span;            // all units, and those of a CTA (consecutive ones)
   float eps;
   const float* cos_sin;
@@ -124,90 +125,86 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// Where a warp stands in its units: unit `c` of token `token`, and the position of that token.
+// Where a warp stands in its units: unit `c` of the D / 4 lanes' tokens; this lane's token (behind the last one: has = false) and its
+// position.
+template <int D>
 struct UnitWalk {
+  static constexpr int kGroup = 256 / D;   // tokens a warp
   int64_t token;
   int left;        // units of the CTA's from this one on
   int c, pos;
-  __device__ __forceinline__ void read_pos(const NormRopeParams& p) { pos = left > 0 ? __ldg(p.pos + token) : -1; }
-  __device__ __forceinline__ void init(const NormRopeParams& p, int warp) {
-    const int64_t begin = blockIdx.x * p.span, first = begin + warp;
+  bool has;
+  __device__ __forceinline__ void read_pos(const NormRopeParams& p) {
+    has = left > 0 && token < p.tokens;
+    pos = has ? __ldg(p.pos + token) : -1;
+  }
+  __device__ __forceinline__ void init(const NormRopeParams& p, int warp, int sub) {
+    const int64_t begin = blockIdx.x * p.span, first = begin + warp, group = first / p.per;
     left = static_cast<int>(min(p.span, p.units - begin)) - warp;
-    token = first / p.per;
-    c = static_cast<int>(first - token * p.per);
+    token = group * kGroup + sub;
+    c = static_cast<int>(first - group * p.per);
     read_pos(p);
   }
   __device__ __forceinline__ void next(int per) {   // the warp's next unit: kWarps further
     left -= kWarps;
     c += kWarps;
-    while (c >= per) c -= per, ++token;
+    while (c >= per) c -= per, token += kGroup;
   }
 };
 
-// The stages of a CTA in shared memory, in 16-byte chunks: of every stage a chunk a thread and pass (two in the backward: x
-// and dout), then the warps' table rows (32 chunks at most each).
+// The stages of a CTA in shared memory, in 16-byte chunks: of every stage a chunk a thread and head (two in the backward: x
+// and dout), then two a thread for the table rows, a token's behind each other.
 template <int D, bool BWD>
 struct Stages {
   uint4* base;
   int unit;
   __device__ __forceinline__ uint4* chunk(int stage, int i) const {
-    return base + (stage * (unit * (BWD ? 2 : 1) + 1) + i) * kThreads + threadIdx.x;
+    return base + (stage * (unit * (BWD ? 2 : 1) + 2) + i) * kThreads + threadIdx.x;
   }
-  __device__ __forceinline__ const float* table(int stage) const {
-    return reinterpret_cast<const float*>(chunk(stage, unit * (BWD ? 2 : 1)) - (threadIdx.x & 31));
+  // Chunk i of this lane's token's table row (the lanes l of a token write chunks l and l + D / 8).
+  __device__ __forceinline__ uint4* table(int stage, int i) const {
+    const int lane = threadIdx.x & 31, l = lane & (D / 8 - 1);
+    return base + (stage * (unit * (BWD ? 2 : 1) + 2) + unit * (BWD ? 2 : 1)) * kThreads + 2 * (threadIdx.x - l) + i;
   }
-  static __host__ __device__ constexpr int bytes(int unit) { return kStages * (unit * (BWD ? 2 : 1) + 1) * kThreads * 16; }
+  static __host__ __device__ constexpr int bytes(int unit) { return kStages * (unit * (BWD ? 2 : 1) + 2) * kThreads * 16; }
 };
 
-// The part of a unit in one tensor: a token's heads are contiguous and a pass is 512 bytes of them whatever d is, so pass i of the
-// part is at byte 512 i behind the lane's 16 of the first.  `full`: every lane has a head in every pass.
-constexpr int kPass = 256;   // values a pass
+// The part of a unit in one tensor: `n` heads from `head` on, from place `first` of the unit on.
 struct UnitPart {
-  int n, first, heads_left;   // passes; the first one in the unit's stage; of this lane's head in the first pass, heads from it on
-  int64_t at;                 // of this lane's first value in a token's heads
-  bool full;
+  int n, first, head;
 };
-template <int D>
-__device__ __forceinline__ UnitPart part_of(const NormRopeParams& p, int c, int t, int lane) {
-  const int j0 = c * p.unit, j1 = min(j0 + p.unit, p.passes[1]);
-  const int from = t ? p.passes[0] : 0, a = max(j0, from), b = min(j1, p.passes[t]);
-  UnitPart r;
-  r.n = b - a;
-  r.first = a - j0;
-  r.at = (a - from) * kPass + 8 * lane;
-  r.heads_left = p.heads[t] - (static_cast<int>(r.at) / D);
-  r.full = (b - from) * kPass <= p.heads[t] * D;
-  return r;
+__device__ __forceinline__ UnitPart part_of(const NormRopeParams& p, int c, int t) {
+  const int from = t ? p.heads[0] : 0, j0 = c * p.unit, a = max(j0, from), b = min(j0 + p.unit, from + p.heads[t]);
+  return UnitPart{b - a, a - j0, a - from};
 }
-// Has the lane a head in pass i of the part?
-template <int D>
-__device__ __forceinline__ bool has_head(const UnitPart& r, int i) { return r.full || i * (kPass / D) < r.heads_left; }
 
-// Start the copies of one unit into `stage`.  Rows behind the last head are filled with zeros.
+// Start the copies of one unit into `stage`.  The rows of a token without a valid position, and of none, are filled with zeros:
+// they are not read, so that nothing in them reaches a sum.
 template <int D, bool BWD>
-__device__ __forceinline__ void copy_unit(const NormRopeParams& p, const Stages<D, BWD>& st, int stage, const UnitWalk& w, int lane) {
+__device__ __forceinline__ void copy_unit(const NormRopeParams& p, const Stages<D, BWD>& st, int stage, const UnitWalk<D>& w) {
+  const int l = threadIdx.x & (D / 8 - 1);
+  const bool live = w.pos >= 0 && w.pos < p.max_pos;
+  const int64_t token = live ? w.token : 0;
+  const int bytes = live ? 16 : 0;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const UnitPart r = part_of<D>(p, w.c, t, lane);
+    const UnitPart r = part_of(p, w.c, t);
     if (r.n <= 0) continue;
-    const __nv_bfloat16* x = p.x[t] + w.token * p.x_stride[t] + r.at;
-    const __nv_bfloat16* g = BWD ? p.dout[t] + w.token * p.heads[t] * D + r.at : nullptr;
+    const __nv_bfloat16* x = p.x[t] + token * p.x_stride[t] + r.head * D + 8 * l;
+    const __nv_bfloat16* g = BWD ? p.dout[t] + (token * p.heads[t] + r.head) * D + 8 * l : nullptr;
     const uint32_t to = smem_u32(st.chunk(stage, r.first)), to_g = smem_u32(st.chunk(stage, p.unit + r.first));
 #pragma unroll
-    for (int i = 0; i < kUnitPasses<BWD>; ++i) {
+    for (int i = 0; i < kUnitHeads<BWD>; ++i) {
       if (i >= r.n) break;
-      if (r.full) {
-        cp_async16(to + i * kThreads * 16, x + i * kPass);
-        if constexpr (BWD) cp_async16(to_g + i * kThreads * 16, g + i * kPass);
-      } else {
-        const int bytes = has_head<D>(r, i) ? 16 : 0;
-        cp_async16(to + i * kThreads * 16, bytes ? x + i * kPass : p.x[t], bytes);
-        if constexpr (BWD) cp_async16(to_g + i * kThreads * 16, bytes ? g + i * kPass : p.dout[t], bytes);
-      }
+      cp_async16(to + i * kThreads * 16, x + i * D, bytes);
+      if constexpr (BWD) cp_async16(to_g + i * kThreads * 16, g + i * D, bytes);
     }
   }
-  if (w.pos >= 0 && w.pos < p.max_pos && 4 * lane < p.rot)
-    cp_async16(smem_u32(st.chunk(stage, p.unit * (BWD ? 2 : 1))), p.cos_sin + static_cast<int64_t>(w.pos) * p.rot + 4 * lane);
+  if (live) {
+    const float* row = p.cos_sin + static_cast<int64_t>(w.pos) * p.rot;
+    if (4 * l < p.rot) cp_async16(smem_u32(st.table(stage, l)), row + 4 * l);
+    if (4 * (l + D / 8) < p.rot) cp_async16(smem_u32(st.table(stage, l + D / 8)), row + 4 * (l + D / 8));
+  }
 }
 
 template <int D, bool INTER>
@@ -217,12 +214,12 @@ __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(NormRopeParams 
   float* weights = reinterpret_cast<float*>(smem);   // [2][D]
   const Stages<D, false> st{reinterpret_cast<uint4*>(smem + 2 * D * 4), p.unit};
   const int lane = threadIdx.x & 31, l = lane & (L - 1);
-  UnitWalk cur, ld;
-  cur.init(p, threadIdx.x >> 5);
+  UnitWalk<D> cur, ld;
+  cur.init(p, threadIdx.x >> 5, lane / L);
   ld = cur;
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
-    if (ld.left > 0) copy_unit<D, false>(p, st, s, ld, lane);
+    if (ld.left > 0) copy_unit<D, false>(p, st, s, ld);
     cp_async_commit();
     ld.next(p.per);
     ld.read_pos(p);
@@ -231,27 +228,25 @@ __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(NormRopeParams 
   __syncthreads();
   int stage = 0, fill = kStages - 1;
   for (; cur.left > 0; cur.next(p.per)) {
-    const int pos = __ldg(p.pos + cur.token);
-    if (ld.left > 0) copy_unit<D, false>(p, st, fill, ld, lane);
+    cur.read_pos(p);   // again: from L1
+    const int pos = cur.pos;
+    if (ld.left > 0) copy_unit<D, false>(p, st, fill, ld);
     cp_async_commit();
     ld.next(p.per);
     ld.read_pos(p);   // a unit ahead of its use
     cp_async_wait<kStages - 1>();
     __syncwarp();
     const bool live = pos >= 0 && pos < p.max_pos;
+    // a padded token (negative position) gives zeros, one behind the table NaN
+    const uint32_t fill_bits = pos < 0 ? 0u : 0x7fff7fffu;
+    const uint4 constant = make_uint4(fill_bits, fill_bits, fill_bits, fill_bits);
     Rotation<D, INTER> rot;
-    if (live) rot.load(st.table(stage), p.rot, lane);
+    rot.load(reinterpret_cast<const float*>(st.table(stage, 0)), live ? p.rot : 0, lane);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const UnitPart u = part_of<D>(p, cur.c, t, lane);
+      const UnitPart u = part_of(p, cur.c, t);
       if (u.n <= 0) continue;
-      __nv_bfloat16* out = p.out[t] + cur.token * p.heads[t] * D + u.at;
-      if (!live) {   // a padded token (negative position) gives zeros, one behind the table NaN
-        const uint32_t c = pos < 0 ? 0u : 0x7fff7fffu;
-        for (int i = 0; i < u.n; ++i)
-          if (has_head<D>(u, i)) *reinterpret_cast<uint4*>(out + i * kPass) = make_uint4(c, c, c, c);
-        continue;
-      }
+      __nv_bfloat16* out = p.out[t] + (cur.token * p.heads[t] + u.head) * D + 8 * l;
       const uint4* in = st.chunk(stage, u.first);
       // coefficients with the weights: out_j = r (x_j a_j + partner_j b_j)
       float2 a[4], b[4];
@@ -275,7 +270,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(NormRopeParams 
         rot.partners(v, f, q);
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[j] = mul2(fma2(f[j], a[j], mul2(q[j], b[j])), make_float2(r, r));
-        if (has_head<D>(u, i)) *reinterpret_cast<uint4*>(out + i * kPass) = pack8(f);
+        if (live) *reinterpret_cast<uint4*>(out + i * D) = pack8(f);
+        else if (cur.has) *reinterpret_cast<uint4*>(out + i * D) = constant;
       }
     }
     __syncwarp();   // the stage's table row has been read by every lane before the next iteration refills it
@@ -295,12 +291,12 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NormRopeParams 
   float* red = weights + 2 * D;                      // [kWarps][2][D]
   const Stages<D, true> st{reinterpret_cast<uint4*>(smem + (1 + kWarps) * 2 * D * 4), p.unit};
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (L - 1), sub = lane / L;
-  UnitWalk cur, ld;
-  cur.init(p, warp);
+  UnitWalk<D> cur, ld;
+  cur.init(p, warp, sub);
   ld = cur;
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
-    if (ld.left > 0) copy_unit<D, true>(p, st, s, ld, lane);
+    if (ld.left > 0) copy_unit<D, true>(p, st, s, ld);
     cp_async_commit();
     ld.next(p.per);
     ld.read_pos(p);
@@ -311,30 +307,29 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NormRopeParams 
   float2 acc[2][4] = {};
   int stage = 0, fill = kStages - 1;
   for (; cur.left > 0; cur.next(p.per)) {
-    const int pos = __ldg(p.pos + cur.token);
-    if (ld.left > 0) copy_unit<D, true>(p, st, fill, ld, lane);
+    cur.read_pos(p);   // again: from L1
+    const int pos = cur.pos;
+    if (ld.left > 0) copy_unit<D, true>(p, st, fill, ld);
     cp_async_commit();
     ld.next(p.per);
     ld.read_pos(p);
     cp_async_wait<kStages - 1>();
     __syncwarp();
     const bool live = pos >= 0 && pos < p.max_pos;
+    // a padded token (negative position) gives zeros, one behind the table NaN
+    const uint32_t fill_bits = pos < 0 ? 0u : 0x7fff7fffu;
+    const uint4 constant = make_uint4(fill_bits, fill_bits, fill_bits, fill_bits);
     Rotation<D, INTER> rot;
-    if (live) rot.load(st.table(stage), p.rot, lane);
+    rot.load(reinterpret_cast<const float*>(st.table(stage, 0)), live ? p.rot : 0, lane);
 #pragma unroll
     for (int j = 0; j < 4; ++j) rot.s[j] = make_float2(-rot.s[j].x, -rot.s[j].y);   // R^T turns by the negative angle
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const UnitPart u = part_of<D>(p, cur.c, t, lane);
+      const UnitPart u = part_of(p, cur.c, t);
       if (u.n <= 0) continue;
-      __nv_bfloat16* dx = p.out[t] + cur.token * p.heads[t] * D + u.at;
-      if (!live) {   // padding: no gradient; behind the table: NaN, in the weight's gradient too
-        const uint32_t c = pos < 0 ? 0u : 0x7fff7fffu;
-        for (int i = 0; i < u.n; ++i)
-          if (has_head<D>(u, i)) *reinterpret_cast<uint4*>(dx + i * kPass) = make_uint4(c, c, c, c);
-        if (pos >= 0) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
-        continue;
-      }
+      __nv_bfloat16* dx = p.out[t] + (cur.token * p.heads[t] + u.head) * D + 8 * l;
+      if (!live && pos >= 0)   // a position behind the table makes the weight's gradient NaN too
+        acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
       const uint4 *in = st.chunk(stage, u.first), *in_g = st.chunk(stage, p.unit + u.first);
       float2 w[4];
       load8(weights + t * D + 8 * l, w);
@@ -353,14 +348,16 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NormRopeParams 
           ss = fma2(f[i], f[i], ss);
           hx = fma2(hw[i], f[i], hx);
         }
-        const float r = rsqrtf(row_sum<D>(ss.x + ss.y) * (1.f / D) + p.eps);
+        const float square = row_sum<D>(ss.x + ss.y);   // by all lanes, live or not
+        const float r = live ? rsqrtf(square * (1.f / D) + p.eps) : 0.f;   // 0: adds nothing
         const float c = -row_sum<D>(hx.x + hx.y) * (r * r) * (r * (1.f / D));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           hw[i] = fma2(f[i], make_float2(c, c), mul2(hw[i], make_float2(r, r)));   // dx = r h - x r^3 mean(h x)
           acc[t][i] = fma2(g[i], mul2(f[i], make_float2(r, r)), acc[t][i]);
         }
-        if (has_head<D>(u, k)) *reinterpret_cast<uint4*>(dx + k * kPass) = pack8(hw);
+        if (live) *reinterpret_cast<uint4*>(dx + k * D) = pack8(hw);
+        else if (cur.has) *reinterpret_cast<uint4*>(dx + k * D) = constant;
       }
     }
     __syncwarp();
@@ -451,18 +448,17 @@ ffa_status check_common(const void* q, int64_t q_stride, const void* k, int64_t 
   return FFA_OK;
 }
 
-// Passes and units for `warps` resident warps: a token is cut into units of equal size, kUnitPasses at most, and smaller ones where
-// there would be fewer units than warps.
+// Units for `warps` resident warps: the heads of a group of tokens are cut into units of equal size, kUnitHeads at most, and smaller
+// ones where there would be fewer units than warps.
 template <bool BWD>
 void set_units(NormRopeParams& p, int64_t tokens, int d, int64_t warps) {
-  const int rows = kPass / d;
-  p.passes[0] = (p.heads[0] + rows - 1) / rows;
-  p.passes[1] = p.passes[0] + (p.heads[1] + rows - 1) / rows;
-  const int64_t all = p.passes[1];
-  int64_t per = std::max((all + kUnitPasses<BWD> - 1) / kUnitPasses<BWD>, std::min(all, warps / std::max<int64_t>(tokens, 1)));
+  const int group = 256 / d;
+  const int64_t groups = (tokens + group - 1) / group, all = p.heads[0] + p.heads[1];
+  const int64_t per = std::max((all + kUnitHeads<BWD> - 1) / kUnitHeads<BWD>, std::min(all, warps / std::max<int64_t>(groups, 1)));
+  p.tokens = tokens;
   p.unit = static_cast<int32_t>((all + per - 1) / per);
   p.per = static_cast<int32_t>((all + p.unit - 1) / p.unit);
-  p.units = tokens * p.per;
+  p.units = groups * p.per;
 }
 
 template <int D, bool BWD>
@@ -493,7 +489,7 @@ ffa_status launch(NormRopeParams p, int64_t tokens, cudaStream_t s, int* ctas) {
     else return norm_rope_fwd_kernel<D, INTER>;
   }();
   static std::atomic<int> known[kDevices];
-  constexpr int kMost = smem_bytes<D, BWD>(kUnitPasses<BWD>);
+  constexpr int kMost = smem_bytes<D, BWD>(kUnitHeads<BWD>);
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) return FFA_ERR_CUDA;
   const int held = resident(kernel, kMost, device, known);

@@ -31,6 +31,7 @@
 
 #include "ffa_internal.h"
 #include "kv_cache.h"
+#include "launch.h"
 #include "paged.cuh"
 #include "ptx.cuh"
 
@@ -43,7 +44,7 @@ namespace {
 // keys, 32 heads, d = 64, bf16): 8 x 1 119, 8 x 2 122, 12 x 2 117; (380K keys, 32 + 2 heads, d = 128, e4m3): 8 x 1 46, 8 x 2 43.
 constexpr int warps_of(int d, bool fp8, int nt) { return nt == 2 || d == 128 ? 8 : fp8 ? 16 : 12; }
 constexpr int groups_of(int d, bool fp8) { return d == 128 && !fp8 ? 1 : 2; }
-constexpr int kMaxCtas = 512;          // split parts the workspace holds: two a CTA
+constexpr int kMaxCtas = 160;          // CTAs (one an SM) the workspace holds parts for: two a CTA
 constexpr int kSmemMax = 226 * 1024;   // of 227 KB
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -827,15 +828,13 @@ size_t part_bytes(int nt, int d) { return size_t{2} * kMaxCtas * 8 * nt * d * si
 int tiles_of(int group) { return group > 8 ? 2 : 1; }   // query tiles of 8 a unit
 
 template <int D, bool FP8, int NT>
-ffa_status launch(const DecodeParams& p, int sms, cudaStream_t s) {
+ffa_status launch(const DecodeParams& p, int device, int sms, cudaStream_t s) {
   using C = Cfg<D, FP8, NT>;
   static_assert(C::STAGES >= 2, "ring");
-  auto* kernel = decode_kernel<D, FP8, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (e != cudaSuccess) return FFA_ERR_CUDA;
+  static std::atomic<bool> raised[kDevices];
   const int grid = std::min(sms, kMaxCtas);
-  kernel<<<grid, C::THREADS, C::SMEM, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return FFA_ERR_CUDA;
+  const cudaError_t e = launch_large(decode_kernel<D, FP8, NT>, dim3(grid), C::THREADS, C::SMEM, C::SMEM, s, device, raised, p);
+  if (e != cudaSuccess) return FFA_ERR_CUDA;
   return cuda_status(launch_after(decode_join_kernel<D, NT>, dim3(grid, std::min(8 * NT, p.group)), 256, s, p, FP8 ? 10.f : 0.f));
 }
 
@@ -898,17 +897,15 @@ ffa_status ffa_fwd_decode(const void* q, int64_t q_stride, const ffa_kv_cache* c
   p.ml = reinterpret_cast<float2*>(ws + kDescBytes);
   p.part = reinterpret_cast<float*>(ws + kDescBytes + ml_bytes(nt));
   int device = 0, sms = 0;
-  if (cudaGetDevice(&device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
-    return FFA_ERR_CUDA;
+  if (!current_device(device, sms)) return FFA_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool fp8 = cache->dtype == FFA_KV_E4M3;
   if (d == 128) {
-    if (nt == 1) return fp8 ? launch<128, true, 1>(p, sms, s) : launch<128, false, 1>(p, sms, s);
-    return fp8 ? launch<128, true, 2>(p, sms, s) : launch<128, false, 2>(p, sms, s);
+    if (nt == 1) return fp8 ? launch<128, true, 1>(p, device, sms, s) : launch<128, false, 1>(p, device, sms, s);
+    return fp8 ? launch<128, true, 2>(p, device, sms, s) : launch<128, false, 2>(p, device, sms, s);
   }
-  if (nt == 1) return fp8 ? launch<64, true, 1>(p, sms, s) : launch<64, false, 1>(p, sms, s);
-  return fp8 ? launch<64, true, 2>(p, sms, s) : launch<64, false, 2>(p, sms, s);
+  if (nt == 1) return fp8 ? launch<64, true, 1>(p, device, sms, s) : launch<64, false, 1>(p, device, sms, s);
+  return fp8 ? launch<64, true, 2>(p, device, sms, s) : launch<64, false, 2>(p, device, sms, s);
 }
 
 }  // extern "C"

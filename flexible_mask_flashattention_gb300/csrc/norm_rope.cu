@@ -18,9 +18,9 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "ffa_internal.h"
+#include "launch.h"
 #include "ptx.cuh"
 
 namespace ffa {
@@ -28,7 +28,6 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kDevices = 64;         // devices whose figures are kept
 constexpr int kMaxBwdCtas = 1024;   // partial weight gradients the workspace holds
 constexpr int kStages = 2;          // units in shared memory: one being used, one on its way
 template <bool BWD>
@@ -469,12 +468,11 @@ constexpr int smem_bytes(int unit) {
 // CTAs of `kernel` the whole device holds at its largest shared memory.  The figure depends on the kernel and the device's
 // type alone, so it is asked for once a device (`known`, 0 before; two threads would store the same).
 template <typename K>
-int resident(K* kernel, int smem, int device, std::atomic<int> (&known)[kDevices]) {
+int resident(K* kernel, int smem, int device, int sms, std::atomic<int> (&known)[kDevices]) {
   int n = device < kDevices ? known[device].load(std::memory_order_relaxed) : 0;
   if (n) return n;
-  int sms = 0, per = 0;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+  int per = 0;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
       cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, smem) != cudaSuccess)
     return 0;
   n = per * sms;
@@ -490,9 +488,9 @@ ffa_status launch(NormRopeParams p, int64_t tokens, cudaStream_t s, int* ctas) {
   }();
   static std::atomic<int> known[kDevices];
   constexpr int kMost = smem_bytes<D, BWD>(kUnitHeads<BWD>);
-  int device = 0;
-  if (cudaGetDevice(&device) != cudaSuccess) return FFA_ERR_CUDA;
-  const int held = resident(kernel, kMost, device, known);
+  int device = 0, sms = 0;
+  if (!current_device(device, sms)) return FFA_ERR_CUDA;
+  const int held = resident(kernel, kMost, device, sms, known);
   if (held == 0) return FFA_ERR_CUDA;
   set_units<BWD>(p, tokens, D, static_cast<int64_t>(held) * kWarps);
   // consecutive units to each CTA, all CTAs resident at once (measured at 64K tokens, 16 + 4 heads, d = 128: 112 us forward and
@@ -504,12 +502,8 @@ ffa_status launch(NormRopeParams p, int64_t tokens, cudaStream_t s, int* ctas) {
   const int grid = static_cast<int>((p.units + p.span - 1) / p.span);
   *ctas = grid;
   if (grid == 0) return FFA_OK;
-  const int smem = smem_bytes<D, BWD>(p.unit);
-  // over the default limit, set on every such call: the attribute belongs to the current context's copy of the kernel
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess)
-    return FFA_ERR_CUDA;
-  kernel<<<grid, kThreads, smem, s>>>(p);
-  return cuda_status(cudaGetLastError());
+  static std::atomic<bool> raised[kDevices];
+  return cuda_status(launch_large(kernel, dim3(grid), kThreads, smem_bytes<D, BWD>(p.unit), kMost, s, device, raised, p));
 }
 
 template <bool BWD>

@@ -7,7 +7,6 @@
 
 #include <cstdint>
 #include <cuda.h>
-#include <cuda_runtime.h>
 
 namespace ffa {
 
@@ -468,22 +467,8 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 }
 // Programmatic dependent launch: a kernel launched with launch_after may start while the one before it on the stream still
 // runs, once every CTA of that one has called allow_dependents; it must call wait_for_primary before it touches what
-// that one writes (or reads).
+// that one writes (or reads).  See launch.h.
 __device__ __forceinline__ void allow_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned block, cudaStream_t stream, A... args) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
-}
 
 }  // namespace ffa

@@ -525,6 +525,13 @@ def _check_dense(t, dtype, shape, dev, name):
     raise FFAError(1, f"{name} must be on the device of the other tensors")
 
 
+def _check_workspace(t, dev):
+    """t is a workspace on device dev; its size is checked by the call."""
+    if not isinstance(t, torch.Tensor):
+        raise FFAError(1, "workspace must be a CUDA uint8 tensor")
+    _check_dense(t, torch.uint8, t.shape, dev, "workspace")
+
+
 def _rows_stride(t, name, shape, dev):
     """The token stride of a bf16 tensor of `shape` [tokens, heads, d] whose heads are contiguous within a token."""
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.get_device() != dev:
@@ -629,7 +636,7 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk_ou
     if workspace is None:
         workspace, = _empty(q, context, ((qk_norm_rope_bwd_workspace_size(d),), torch.uint8))
     else:
-        _check_dense(workspace, torch.uint8, workspace.shape, dev, "workspace")
+        _check_workspace(workspace, dev)
     _check(load_library().ffa_qk_norm_rope_bwd(
         q.data_ptr(), qs, k.data_ptr(), ks, tokens, hq, hkv, d, q_weight.data_ptr(), k_weight.data_ptr(), eps,
         cos_sin.data_ptr(), max_pos, rot, interleaved, positions.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(),
@@ -722,7 +729,7 @@ def fwd_decode(q, k_cache, v_cache, page_table, kv_lens, scale: float, k_exp=Non
     if workspace is None:
         workspace, = _empty(q, context, ((fwd_decode_workspace_size(hq, cache.hkv, d),), torch.uint8))
     else:
-        _check_dense(workspace, torch.uint8, workspace.shape, dev, "workspace")
+        _check_workspace(workspace, dev)
     _check(load_library().ffa_fwd_decode(
         q.data_ptr(), qs, ctypes.byref(cache), page_table.data_ptr(), ts, width, b, hq, kv_lens.data_ptr(),
         None if kv_starts is None else kv_starts.data_ptr(), scale, None if sink is None else sink.data_ptr(),

@@ -873,6 +873,13 @@ ffa_status ffa_fwd_decode(const void* q, int64_t q_stride, const ffa_kv_cache* c
   if (q_stride % 8 != 0 || (batch > 1 && q_stride < static_cast<int64_t>(hq) * d)) return FFA_ERR_INVALID_ARG;
   if (workspace_bytes < ffa_fwd_decode_workspace_size(hq, cache->hkv, d)) return FFA_ERR_INVALID_ARG;
   const int group = hq / cache->hkv, nt = tiles_of(group);
+  const CacheSpans at(*cache);
+  Span in[9] = {{q, span_bytes(batch, q_stride, hq, d)}, {page_table, 4 * (static_cast<int64_t>(batch - 1) * table_stride + max_pages)},
+                {kv_lens, 4 * int64_t{batch}}, {kv_starts, kv_starts ? 4 * int64_t{batch} : 0}, {sink, sink ? 4 * hq : 0}};
+  for (int i = 0; i < at.n; ++i) in[5 + i] = at.s[i];
+  const Span outs[] = {{out, 2 * int64_t{batch} * hq * d}, {lse, 4 * int64_t{batch} * hq},
+                       {workspace, static_cast<int64_t>(ffa_fwd_decode_workspace_size(hq, cache->hkv, d))}};
+  if (any_meet(outs, 3, in, 5 + at.n)) return FFA_ERR_INVALID_ARG;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_stride = q_stride;
   p.k = cache->k;

@@ -17,6 +17,7 @@
 
 #include "ffa_internal.h"
 #include "kv_cache.h"
+#include "launch.h"
 #include "paged.cuh"
 #include "ptx.cuh"
 
@@ -245,6 +246,11 @@ ffa_status ffa_kv_cache_write(const void* k, int64_t k_stride, const void* v, in
   const int64_t row = static_cast<int64_t>(cache->hkv) * cache->d;
   if (k_stride % 8 != 0 || v_stride % 8 != 0 || (tokens > 1 && (k_stride < row || v_stride < row)))
     return FFA_ERR_INVALID_ARG;
+  if (tokens > 0x7fffffff / cache->hkv - 256) return FFA_ERR_OVERFLOW;   // rows are counted in 31 bits
+  const CacheSpans at(*cache);
+  const Span in[] = {{k, span_bytes(tokens, k_stride, cache->hkv, cache->d)}, {v, span_bytes(tokens, v_stride, cache->hkv, cache->d)},
+                     {slots, 8 * tokens}};
+  if (any_meet(at.s, at.n, in, 3)) return FFA_ERR_INVALID_ARG;
   p.x[0] = static_cast<const __nv_bfloat16*>(k);
   p.x[1] = static_cast<const __nv_bfloat16*>(v);
   p.stride[0] = k_stride;
@@ -254,7 +260,6 @@ ffa_status ffa_kv_cache_write(const void* k, int64_t k_stride, const void* v, in
   p.exps[0] = cache->k_exp;
   p.exps[1] = cache->v_exp;
   p.slots = slots;
-  if (tokens > 0x7fffffff / cache->hkv - 256) return FFA_ERR_OVERFLOW;   // rows are counted in 31 bits
   p.rows = static_cast<uint32_t>(tokens * cache->hkv);
   p.heads = fast_div(static_cast<uint32_t>(cache->hkv));
   const int per = kWarps * kUnroll * 256 / cache->d;   // rows a CTA
@@ -283,6 +288,12 @@ ffa_status ffa_kv_cache_read(const ffa_kv_cache* cache, const int32_t* page_tabl
   if (max_pages > 0 && (!page_table || (reinterpret_cast<uintptr_t>(page_table) & 3u))) return FFA_ERR_INVALID_ARG;
   if (!k || !v || !kv_aligned16(k) || !kv_aligned16(v)) return FFA_ERR_INVALID_ARG;
   if (total > 0x7fffffff) return FFA_ERR_OVERFLOW;   // cu_seqlens is int32
+  const CacheSpans at(*cache);
+  Span in[6] = {{page_table, 4 * (static_cast<int64_t>(batch - 1) * table_stride + max_pages)}, {cu_seqlens, 4 * (int64_t{batch} + 1)}};
+  for (int i = 0; i < at.n; ++i) in[2 + i] = at.s[i];
+  const int64_t bytes = 2 * total * cache->hkv * cache->d;
+  const Span out[] = {{k, bytes}, {v, bytes}};
+  if (any_meet(out, 2, in, 2 + at.n)) return FFA_ERR_INVALID_ARG;
   p.cache[0] = cache->k;
   p.cache[1] = cache->v;
   p.exps[0] = cache->k_exp;

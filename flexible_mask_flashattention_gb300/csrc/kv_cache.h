@@ -4,6 +4,7 @@
 #include <cuda_fp16.h>
 
 #include "ffa_internal.h"
+#include "launch.h"
 #include "paged.cuh"
 
 namespace ffa {
@@ -12,6 +13,20 @@ inline bool kv_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p)
 
 // Host check of a cache description; fills its geometry.
 ffa_status check_cache(const ffa_kv_cache* c, PageGeom& g);
+
+// The memory of a checked cache.
+struct CacheSpans {
+  Span s[4];
+  int n;
+  explicit CacheSpans(const ffa_kv_cache& c) {
+    const int64_t rows = c.num_pages * c.hkv * c.page_size, bytes = rows * c.d * (c.dtype == FFA_KV_E4M3 ? 1 : 2);
+    s[0] = {c.k, bytes};
+    s[1] = {c.v, bytes};
+    s[2] = {c.k_exp, rows};
+    s[3] = {c.v_exp, rows};
+    n = c.dtype == FFA_KV_E4M3 ? 4 : 2;
+  }
+};
 
 // 2^(byte - 127), the scale an exponent byte stands for (0 for byte 0, which no write stores).
 __device__ __forceinline__ float exp_scale(uint32_t byte) { return __uint_as_float(byte << 23); }

@@ -1,7 +1,9 @@
-// Host helpers of calls that launch small kernels many times a second: what a device is asked for once, and launches.
+// Host helpers of calls that launch small kernels many times a second: what a device is asked for once, launches, and the check
+// that outputs overlap nothing.
 #pragma once
 
 #include <atomic>
+#include <cstdint>
 #include <cuda_runtime.h>
 
 namespace ffa {
@@ -50,6 +52,34 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned block, cudaSt
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+// Do the byte ranges [a, a + na) and [b, b + nb) meet?
+inline bool meet(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na > 0 && nb > 0 && x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
+}
+
+// A range of memory a call reads or writes, in bytes.
+struct Span {
+  const void* p;
+  int64_t n;
+};
+
+// Does an output meet an input or another output?
+inline bool any_meet(const Span* out, int n_out, const Span* in, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      if (meet(out[i].p, out[i].n, in[j].p, in[j].n)) return true;
+    for (int j = i + 1; j < n_out; ++j)
+      if (meet(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+  }
+  return false;
+}
+
+// Bytes from the first to the last value of a strided [tokens][heads][d] bf16 tensor.
+inline int64_t span_bytes(int64_t tokens, int64_t stride, int64_t heads, int64_t d) {
+  return tokens <= 0 ? 0 : 2 * ((tokens - 1) * stride + heads * d);
 }
 
 }  // namespace ffa

@@ -402,17 +402,6 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* partial
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Do the byte ranges [a, a + na) and [b, b + nb) meet?
-bool meet(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return na > 0 && nb > 0 && x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
-}
-
-struct Span {
-  const void* p;
-  int64_t n;
-};
-
 // The checks both directions share; fills what they have in common.
 ffa_status check_common(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int64_t tokens, int32_t hq,
                         int32_t hkv, int32_t d, const float* qw, const float* kw, float eps, const float* cos_sin,
@@ -510,21 +499,6 @@ template <bool BWD>
 ffa_status launch_any(const NormRopeParams& p, int64_t tokens, int d, bool interleaved, cudaStream_t s, int* ctas) {
   if (d == 128) return interleaved ? launch<128, true, BWD>(p, tokens, s, ctas) : launch<128, false, BWD>(p, tokens, s, ctas);
   return interleaved ? launch<64, true, BWD>(p, tokens, s, ctas) : launch<64, false, BWD>(p, tokens, s, ctas);
-}
-
-// Bytes from the first to the last value of a strided [tokens][heads][d] bf16 tensor.
-int64_t span_bytes(int64_t tokens, int64_t stride, int64_t heads, int64_t d) {
-  return tokens <= 0 ? 0 : 2 * ((tokens - 1) * stride + heads * d);
-}
-
-bool any_meet(const Span* out, int n_out, const Span* in, int n_in) {
-  for (int i = 0; i < n_out; ++i) {
-    for (int j = 0; j < n_in; ++j)
-      if (meet(out[i].p, out[i].n, in[j].p, in[j].n)) return true;
-    for (int j = i + 1; j < n_out; ++j)
-      if (meet(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
-  }
-  return false;
 }
 
 }  // namespace

@@ -399,8 +399,11 @@ ffa_status ffa_range_scatter_reduce(const void* src, const int64_t* ranges, int6
  *             padding: its outputs are 0.  One with a position >= max_pos gets
  *             NaN outputs (the table is not read).
  *  q_out, k_out  bf16, contiguous; they must not overlap an input or each other
- * All pointers 16-byte aligned (positions: 4).  Norms and rotation in fp32, one
- * rounding to bf16.  No workspace.
+ * All pointers 16-byte aligned (positions: 4).  Norms and rotation in fp32 (a
+ * row's squares must not pass its range), one rounding to bf16.  No workspace.
+ * As for every call below: device pointers are the current device's, and a call
+ * that is to be captured into a graph is made once before, so that its kernels are
+ * loaded.
  * Errors: FFA_ERR_INVALID_ARG, FFA_ERR_UNSUPPORTED (d, rot_dim),
  * FFA_ERR_OVERFLOW, FFA_ERR_CUDA.
  */
@@ -517,6 +520,7 @@ size_t ffa_fwd_decode_workspace_size(int32_t hq, int32_t hkv, int32_t d);
  *  out, lse    bf16 [batch][hq][d], fp32 [hq][batch]
  *  workspace   at least ffa_fwd_decode_workspace_size() bytes, contents on entry
  *              ignored; calls that run at the same time need one each
+ * out, lse and workspace must not overlap an input or each other.
  * A sequence with a page that is not one of the cache's, or with more keys than
  * its table row holds, gets NaN rows (nothing out of range is read); the other
  * sequences are not affected.

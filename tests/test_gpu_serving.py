@@ -633,6 +633,50 @@ def test_calls_on_another_stream_and_in_a_graph(ffa):
     assert (bits(out) == first[0]).all() and (bits(o2) == first[0]).all()
 
 
+def test_calls_from_several_threads_at_once(ffa):
+    """Threads with a stream of their own, and two on one stream: every call's results are the ones it has alone."""
+    import threading
+    import torch
+    probs = [decode_problem([300 + 40 * i, 17, 90 * i], 8, 2, 128, 32, i % 2 == 0, 200 + i) for i in range(4)]
+    norms = [norm_inputs(257 + i, 6, 2, 64, 32, 300 + i) for i in range(4)]
+    want = [(ffa.fwd_decode(**p, scale=0.09), ffa.qk_norm_rope_bwd(*a)) for p, a in zip(probs, norms)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    streams.append(streams[0])
+    bad = []
+
+    def work(i):
+        with torch.cuda.stream(streams[i]):
+            for _ in range(60):
+                got = (ffa.fwd_decode(**probs[i], scale=0.09), ffa.qk_norm_rope_bwd(*norms[i]))
+                streams[i].synchronize()
+                if not all((bits(a) == bits(b)).all() for x, y in zip(got, want[i]) for a, b in zip(x, y)):
+                    bad.append(i)
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+    assert not bad
+
+
+def test_strided_views(ffa):
+    """A page table that is a part of a wider one, queries that are a part of a projection's output, outputs given."""
+    import torch
+    p = decode_problem([200, 64, 130], 4, 2, 64, 32, True, 111)
+    want = ffa.fwd_decode(**p, scale=0.1)
+    wide = torch.full((3, p["page_table"].shape[1] + 5), -9, dtype=torch.int32, device="cuda")
+    wide[:, 2:-3] = p["page_table"]
+    qkv = torch.randn(3, 8, 64, device="cuda").bfloat16()
+    qkv[:, 2:6] = p["q"]
+    out, lse = torch.zeros(3, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(4, 3, device="cuda")
+    got = ffa.fwd_decode(**{**p, "q": qkv[:, 2:6], "page_table": wide[:, 2:-3]}, scale=0.1, out=out, lse=lse)
+    assert got[0] is out and (bits(out) == bits(want[0])).all() and (bits(lse) == bits(want[1])).all()
+    cu = torch.tensor([0, 200, 264, 394], dtype=torch.int32, device="cuda")
+    a = ffa.kv_cache_read(p["k_cache"], p["v_cache"], p["page_table"], cu, 394, k_exp=p["k_exp"], v_exp=p["v_exp"])
+    b = ffa.kv_cache_read(p["k_cache"], p["v_cache"], wide[:, 2:-3], cu, 394, k_exp=p["k_exp"], v_exp=p["v_exp"])
+    assert all((bits(x) == bits(y)).all() for x, y in zip(a, b))
+
+
 def test_norm_rope_bwd_in_a_graph(ffa):
     import torch
     args = norm_inputs(333, 4, 2, 128, 128, 95)

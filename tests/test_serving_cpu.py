@@ -211,7 +211,8 @@ def test_a_null_cache_and_a_bf16_cache_without_exponents(lib):
 @pytest.mark.parametrize("change,code", [
     (dict(tokens=-1), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(slots=None), INVALID),
     (dict(slots=at(2) + 4), INVALID), (dict(k=at(0) + 8), INVALID), (dict(ks=248), INVALID), (dict(vs=260), INVALID),
-    (dict(tokens=1 << 40), OVERFLOW), (dict(tokens=0, k=None, v=None, slots=None), OK)])
+    (dict(tokens=1 << 40), OVERFLOW), (dict(tokens=0, k=None, v=None, slots=None), OK),
+    (dict(k=at(20) + 512), INVALID), (dict(v=at(21) + 10 * 64 * 2 * 128 - 16), INVALID), (dict(slots=at(22)), INVALID)])
 def test_cache_write_refusals(lib, change, code):
     assert lib.ffa_kv_cache_write(*write_args(cache(), **change)) == code
 
@@ -220,7 +221,8 @@ def test_cache_write_refusals(lib, change, code):
     (dict(total=-1), INVALID), (dict(batch=-1), INVALID), (dict(max_pages=-1), INVALID), (dict(ts=3), INVALID),
     (dict(table=None), INVALID), (dict(table=at(0) + 1), INVALID), (dict(cu=None), INVALID), (dict(cu=at(1) + 2), INVALID),
     (dict(k=None), INVALID), (dict(v=at(3) + 8), INVALID), (dict(total=1 << 31), OVERFLOW),
-    (dict(total=0, k=None, v=None, cu=None, table=None), OK), (dict(batch=0), OK)])
+    (dict(total=0, k=None, v=None, cu=None, table=None), OK), (dict(batch=0), OK),
+    (dict(k=at(3) + 16), INVALID), (dict(v=at(20)), INVALID), (dict(k=at(1) - 16), INVALID), (dict(v=at(0)), INVALID)])
 def test_cache_read_refusals(lib, change, code):
     assert lib.ffa_kv_cache_read(*read_args(cache(), **change)) == code
 
@@ -232,7 +234,9 @@ def test_cache_read_refusals(lib, change, code):
     (dict(lens=None), INVALID), (dict(lens=at(2) + 2), INVALID), (dict(starts=at(9) + 1), INVALID), (dict(sink=at(9) + 2), INVALID),
     (dict(out=None), INVALID), (dict(out=at(3) + 2), INVALID), (dict(lse=None), INVALID), (dict(ws=None), INVALID),
     (dict(ws_bytes=100), INVALID), (dict(hq=1 << 17, qs=1 << 24), OVERFLOW), (dict(batch=(1 << 20) + 1), OVERFLOW),
-    (dict(batch=0, q=None, lens=None, out=None, lse=None, ws=None), OK)])
+    (dict(batch=0, q=None, lens=None, out=None, lse=None, ws=None), OK),
+    (dict(out=at(0)), INVALID), (dict(lse=at(2)), INVALID), (dict(ws=at(3) + 64), INVALID), (dict(out=at(21)), INVALID),
+    (dict(lse=at(23)), INVALID), (dict(ws=at(1) - 4096), INVALID), (dict(sink=at(3)), INVALID), (dict(starts=at(4)), INVALID)])
 def test_decode_refusals(lib, change, code):
     assert lib.ffa_fwd_decode(*decode_args(cache(), **change)) == code
 

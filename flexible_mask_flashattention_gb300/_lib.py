@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from typing import Iterable, Optional, Sequence, Tuple
 
 import numpy as np
@@ -501,6 +502,24 @@ def _empty(like, context, *specs):
         return [like.new_empty(shape, dtype=dtype) for shape, dtype in specs]
 
 
+_workspaces = {}
+
+
+def _workspace(like, context, device: int, handle: int, size: int):
+    """A workspace of at least `size` bytes for a call on that stream.  Calls of one thread on one current stream run in order, so they
+    share one, kept here (a new tensor a call costs a sixth of a small call's host time).  A call that is being captured gets one of
+    its own, since its graph may run beside anything, and so does a call that is given its stream."""
+    if context is not None:
+        return _empty(like, context, ((size,), torch.uint8))[0]
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return like.new_empty((size,), dtype=torch.uint8)
+    key = (device, handle, threading.get_ident())
+    ws = _workspaces.get(key)
+    if ws is None or ws.numel() < size:
+        ws = _workspaces[key] = like.new_empty((size,), dtype=torch.uint8)
+    return ws
+
+
 def _device(t, name) -> int:
     """The device of tensor t, which must be the current one."""
     global torch
@@ -634,7 +653,7 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk_ou
     handle, context = _on(stream, dev)
     dq, dk, dqw, dkw = _empty(q, context, (qshape, bf16), (kshape, bf16), ((d,), f32), ((d,), f32))
     if workspace is None:
-        workspace, = _empty(q, context, ((qk_norm_rope_bwd_workspace_size(d),), torch.uint8))
+        workspace = _workspace(q, context, dev, handle, qk_norm_rope_bwd_workspace_size(d))
     else:
         _check_workspace(workspace, dev)
     _check(load_library().ffa_qk_norm_rope_bwd(
@@ -727,7 +746,7 @@ def fwd_decode(q, k_cache, v_cache, page_table, kv_lens, scale: float, k_exp=Non
     else:
         _check_dense(lse, f32, (hq, b), dev, "lse")
     if workspace is None:
-        workspace, = _empty(q, context, ((fwd_decode_workspace_size(hq, cache.hkv, d),), torch.uint8))
+        workspace = _workspace(q, context, dev, handle, fwd_decode_workspace_size(hq, cache.hkv, d))
     else:
         _check_workspace(workspace, dev)
     _check(load_library().ffa_fwd_decode(

@@ -10,7 +10,8 @@
 //
 // Both kernels are bound by HBM: 2 d bytes a row on the tensors' side, 2 d or d + 1 on the cache's.  A grid's second
 // dimension is k or v; a warp holds 2 or 4 consecutive rows at once (a pass), whatever tokens and heads they are of, 8 values a
-// lane, and starts the loads of kUnroll passes before it uses the first.
+// lane, and starts the loads of kUnroll passes before it uses the first (168K tokens of 8 heads, d = 128, e4m3, written: 147 us so, 194
+// us with 8 passes, 167 us with 2).  Measured: written 153 us, read 157 us, 101 and 97 % of a copy's 6795 GB/s.
 #include <cuda_bf16.h>
 
 #include <algorithm>

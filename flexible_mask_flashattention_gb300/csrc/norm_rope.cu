@@ -14,7 +14,8 @@
 // persistent: a warp walks over units of up to 10 (backward: 5) heads of its tokens, and cp.async keeps the next unit's
 // values and table rows on their way to shared memory, where a token's lanes read back only what they copied.
 // Loads in flight then cost neither registers nor barriers.  Norm statistics, rotation and every gradient sum are fp32, two
-// values an instruction (fma.rn.f32x2); the one rounding to bf16 is the store's.
+// values an instruction (fma.rn.f32x2); the one rounding to bf16 is the store's.  Measured at 64K tokens, 16 + 4 heads, d = 128: forward
+// 114 us, backward 171 us (both 87 % of a copy's 6795 GB/s); two stages beat three (130 and 200 us), which leave fewer warps.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -482,8 +483,8 @@ ffa_status launch(NormRopeParams p, int64_t tokens, cudaStream_t s, int* ctas) {
   const int held = resident(kernel, kMost, device, sms, known);
   if (held == 0) return FFA_ERR_CUDA;
   set_units<BWD>(p, tokens, D, static_cast<int64_t>(held) * kWarps);
-  // consecutive units to each CTA, all CTAs resident at once (measured at 64K tokens, 16 + 4 heads, d = 128: 112 us forward and
-  // 170 us backward, against 120 to 125 and 180 to 184 us with CTAs of 2 to 32 units a warp)
+  // consecutive units to each CTA, all CTAs resident at once (64K tokens, 16 + 4 heads, d = 128, before a warp took several tokens: 112
+  // us forward and 170 us backward, against 120 to 125 and 180 to 184 us with CTAs of 2 to 32 units a warp)
   const int64_t most = std::min(held, kMaxBwdCtas);
   p.span = std::max<int64_t>((p.units + most - 1) / most, 1);
   p.span = (p.span + kWarps - 1) / kWarps * kWarps;

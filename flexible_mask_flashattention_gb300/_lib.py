@@ -8,7 +8,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import threading
 from typing import Iterable, Optional, Sequence, Tuple
 
 import numpy as np
@@ -480,7 +479,20 @@ def bwd(q, k, v, out, lse, dout, plan: Plan, scale: float, dq=None, dk=None, dv=
 # The calls below take a few microseconds on the host and run many times a second in a decode loop, so their checks are
 # single expressions, and what went wrong is worked out only once something did.
 
-torch = None   # imported by the first of these calls, once
+torch = None        # imported by the first of these calls, once
+_new = None         # (size, strides, dtype) -> a new tensor on the current device
+
+
+def _start():
+    """Import torch, and find its quickest way to a new CUDA tensor: the one its compiled programs allocate with, which takes a third of
+    torch.empty's time between launches, where this torch has it."""
+    global torch, _new
+    import torch
+    try:
+        _new = torch._C._dynamo.guards._empty_strided_cuda
+    except AttributeError:
+        def _new(size, strides, dtype):
+            return torch.empty_strided(size, strides, dtype=dtype, device="cuda")
 
 
 def _on(stream, device: int):
@@ -494,37 +506,20 @@ def _on(stream, device: int):
     return handle, torch.cuda.stream(torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream())
 
 
-def _empty(like, context, *specs):
-    """One new tensor a (shape, dtype) of specs, on the device of `like`, for use on the stream of `context`."""
+def _empty(context, size, dtype):
+    """A new tensor of 1 to 3 dimensions for use on the stream of `context`."""
+    n = len(size)
+    strides = (size[1] * size[2], size[2], 1) if n == 3 else (size[1], 1) if n == 2 else (1,)
     if context is None:
-        return [like.new_empty(shape, dtype=dtype) for shape, dtype in specs]
+        return _new(size, strides, dtype)
     with context:
-        return [like.new_empty(shape, dtype=dtype) for shape, dtype in specs]
-
-
-_workspaces = {}
-
-
-def _workspace(like, context, device: int, handle: int, size: int):
-    """A workspace of at least `size` bytes for a call on that stream.  Calls of one thread on one current stream run in order, so they
-    share one, kept here (a new tensor a call costs a sixth of a small call's host time).  A call that is being captured gets one of
-    its own, since its graph may run beside anything, and so does a call that is given its stream."""
-    if context is not None:
-        return _empty(like, context, ((size,), torch.uint8))[0]
-    if torch._C._cuda_isCurrentStreamCapturing():
-        return like.new_empty((size,), dtype=torch.uint8)
-    key = (device, handle, threading.get_ident())
-    ws = _workspaces.get(key)
-    if ws is None or ws.numel() < size:
-        ws = _workspaces[key] = like.new_empty((size,), dtype=torch.uint8)
-    return ws
+        return _new(size, strides, dtype)
 
 
 def _device(t, name) -> int:
     """The device of tensor t, which must be the current one."""
-    global torch
-    if torch is None:
-        import torch
+    if _new is None:
+        _start()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise FFAError(1, f"{name} must be a CUDA tensor")
     dev = t.get_device()
@@ -628,11 +623,11 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6
     handle, context = _on(stream, dev)
     bf16, qshape, kshape = torch.bfloat16, (tokens, hq, d), (tokens, hkv, d)
     if q_out is None:
-        q_out, = _empty(q, context, (qshape, bf16))
+        q_out = _empty(context, qshape, bf16)
     else:
         _check_dense(q_out, bf16, qshape, dev, "q_out")
     if k_out is None:
-        k_out, = _empty(q, context, (kshape, bf16))
+        k_out = _empty(context, kshape, bf16)
     else:
         _check_dense(k_out, bf16, kshape, dev, "k_out")
     _check(load_library().ffa_qk_norm_rope(
@@ -651,9 +646,10 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk_ou
     _check_dense(dq_out, bf16, qshape, dev, "dq_out")
     _check_dense(dk_out, bf16, kshape, dev, "dk_out")
     handle, context = _on(stream, dev)
-    dq, dk, dqw, dkw = _empty(q, context, (qshape, bf16), (kshape, bf16), ((d,), f32), ((d,), f32))
+    dq, dk = _empty(context, qshape, bf16), _empty(context, kshape, bf16)
+    dqw, dkw = _empty(context, (d,), f32), _empty(context, (d,), f32)
     if workspace is None:
-        workspace = _workspace(q, context, dev, handle, qk_norm_rope_bwd_workspace_size(d))
+        workspace = _empty(context, (qk_norm_rope_bwd_workspace_size(d),), torch.uint8)
     else:
         _check_workspace(workspace, dev)
     _check(load_library().ffa_qk_norm_rope_bwd(
@@ -702,11 +698,11 @@ def kv_cache_read(k_cache, v_cache, page_table, cu_seqlens, total: int, k=None, 
         raise FFAError(1, "total must not be negative")
     handle, context = _on(stream, dev)
     if k is None:
-        k, = _empty(k_cache, context, (shape, bf16))
+        k = _empty(context, shape, bf16)
     else:
         _check_dense(k, bf16, shape, dev, "k")
     if v is None:
-        v, = _empty(k_cache, context, (shape, bf16))
+        v = _empty(context, shape, bf16)
     else:
         _check_dense(v, bf16, shape, dev, "v")
     _check(load_library().ffa_kv_cache_read(ctypes.byref(cache), page_table.data_ptr(), ts, width, batch,
@@ -738,15 +734,15 @@ def fwd_decode(q, k_cache, v_cache, page_table, kv_lens, scale: float, k_exp=Non
         _check_dense(sink, f32, (hq,), dev, "sink")
     handle, context = _on(stream, dev)
     if out is None:
-        out, = _empty(q, context, ((b, hq, d), bf16))
+        out = _empty(context, (b, hq, d), bf16)
     else:
         _check_dense(out, bf16, (b, hq, d), dev, "out")
     if lse is None:
-        lse, = _empty(q, context, ((hq, b), f32))
+        lse = _empty(context, (hq, b), f32)
     else:
         _check_dense(lse, f32, (hq, b), dev, "lse")
     if workspace is None:
-        workspace = _workspace(q, context, dev, handle, fwd_decode_workspace_size(hq, cache.hkv, d))
+        workspace = _empty(context, (fwd_decode_workspace_size(hq, cache.hkv, d),), torch.uint8)
     else:
         _check_workspace(workspace, dev)
     _check(load_library().ffa_fwd_decode(

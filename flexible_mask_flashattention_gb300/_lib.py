@@ -495,15 +495,19 @@ def _start():
             return torch.empty_strided(size, strides, dtype=dtype, device="cuda")
 
 
-def _on(stream, device: int):
+def _on(stream, device: int, *tensors):
     """(handle, context): the stream a call launches on, and the context in which tensors are allocated for use on it, or
-    None for the current stream, on which they are anyway."""
+    None for the current stream, on which they are anyway.  On another stream the call's own tensors (None: absent) are marked
+    as used there, so that the allocator does not give their memory away before the work is done."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device), None
-    if isinstance(stream, torch.cuda.Stream):
-        return stream.cuda_stream, torch.cuda.stream(stream)
-    handle = int(_stream_handle(stream))
-    return handle, torch.cuda.stream(torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream())
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(_stream_handle(stream))
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
 
 def _empty(context, size, dtype):
@@ -620,7 +624,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6
     (fp32; the cosines first).  q and k may be views of one projection's output."""
     dev = _device(q, "q")
     qs, ks, tokens, hq, hkv, d, max_pos, rot = _norm_rope_inputs(q, k, q_weight, k_weight, cos_sin, positions, dev)
-    handle, context = _on(stream, dev)
+    handle, context = _on(stream, dev, q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out)
     bf16, qshape, kshape = torch.bfloat16, (tokens, hq, d), (tokens, hkv, d)
     if q_out is None:
         q_out = _empty(context, qshape, bf16)
@@ -645,7 +649,7 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk_ou
     bf16, f32, qshape, kshape = torch.bfloat16, torch.float32, (tokens, hq, d), (tokens, hkv, d)
     _check_dense(dq_out, bf16, qshape, dev, "dq_out")
     _check_dense(dk_out, bf16, kshape, dev, "dk_out")
-    handle, context = _on(stream, dev)
+    handle, context = _on(stream, dev, q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk_out, workspace)
     dq, dk = _empty(context, qshape, bf16), _empty(context, kshape, bf16)
     dqw, dkw = _empty(context, (d,), f32), _empty(context, (d,), f32)
     if workspace is None:
@@ -677,8 +681,9 @@ def kv_cache_write(k, v, k_cache, v_cache, slots, k_exp=None, v_exp=None, stream
     ks = _rows_stride(k, "k", shape, dev)
     vs = _rows_stride(v, "v", shape, dev)
     _check_dense(slots, torch.int64, (tokens,), dev, "slots")
+    handle, _ = _on(stream, dev, k, v, k_cache, v_cache, slots, k_exp, v_exp)
     _check(load_library().ffa_kv_cache_write(k.data_ptr(), ks, v.data_ptr(), vs, tokens, slots.data_ptr(),
-                                             ctypes.byref(cache), _on(stream, dev)[0]), "ffa_kv_cache_write")
+                                             ctypes.byref(cache), handle), "ffa_kv_cache_write")
 
 
 def kv_cache_read(k_cache, v_cache, page_table, cu_seqlens, total: int, k=None, v=None, k_exp=None, v_exp=None,
@@ -696,7 +701,7 @@ def kv_cache_read(k_cache, v_cache, page_table, cu_seqlens, total: int, k=None, 
     shape, bf16 = (int(total), cache.hkv, cache.d), torch.bfloat16
     if shape[0] < 0:
         raise FFAError(1, "total must not be negative")
-    handle, context = _on(stream, dev)
+    handle, context = _on(stream, dev, k_cache, v_cache, page_table, cu_seqlens, k, v, k_exp, v_exp)
     if k is None:
         k = _empty(context, shape, bf16)
     else:
@@ -732,7 +737,8 @@ def fwd_decode(q, k_cache, v_cache, page_table, kv_lens, scale: float, k_exp=Non
         _check_dense(kv_starts, torch.int32, (b,), dev, "kv_starts")
     if sink is not None:
         _check_dense(sink, f32, (hq,), dev, "sink")
-    handle, context = _on(stream, dev)
+    handle, context = _on(stream, dev, q, k_cache, v_cache, page_table, kv_lens, k_exp, v_exp, kv_starts, sink, out, lse,
+                          workspace)
     if out is None:
         out = _empty(context, (b, hq, d), bf16)
     else:

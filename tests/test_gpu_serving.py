@@ -633,6 +633,26 @@ def test_calls_on_another_stream_and_in_a_graph(ffa):
     assert (bits(out) == first[0]).all() and (bits(o2) == first[0]).all()
 
 
+def test_inputs_freed_while_another_stream_still_reads_them(ffa):
+    """A call that is given a busy stream keeps its inputs' memory from being handed out before it has run."""
+    import torch
+    q, k, qw, kw, t, pos, _, _ = norm_inputs(4096, 8, 2, 128, 128, 121)
+    want = [bits(x) for x in ffa.qk_norm_rope(q, k, qw, kw, t, pos)]
+    side, big = torch.cuda.Stream(), torch.randn(4096, 4096, device="cuda")
+    for given in (side, side.cuda_stream):
+        q2, k2 = q.clone(), k.clone()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(40):
+                big @ big                     # some milliseconds of work in front of the call
+        out = ffa.qk_norm_rope(q2, k2, qw, kw, t, pos, stream=given)
+        del q2, k2
+        junk = [torch.full((4096, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+        junk += [torch.full((4096, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all((bits(a) == b).all() for a, b in zip(out, want)) and len(junk) == 8
+
+
 def test_calls_from_several_threads_at_once(ffa):
     """Threads with a stream of their own, and two on one stream: every call's results are the ones it has alone."""
     import threading

@@ -198,9 +198,9 @@ __device__ __forceinline__ RowEnd row_end(const DecodeParams& p, int head, float
     sum = (mx == -INFINITY && sum == 0.f ? 0.f : sum * f) + (s2 == -INFINITY ? 0.f : ex2_approx(s2 - top));
     mx = top;
   }
-  RowEnd r;
-  r.inv = sum == 0.f ? 0.f : f / sum;
-  r.lse = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+  RowEnd r;   // the approximations are off by 2^-22 or two steps, far under the rounding of the output
+  r.inv = sum == 0.f ? 0.f : __fdividef(f, sum);
+  r.lse = sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * kLn2;
   return r;
 }
 
@@ -394,37 +394,43 @@ __global__ void __launch_bounds__(32 * warps_of(D, FP8, NT), 1) decode_kernel(De
   float m[NT][2], l[NT][2];
   float mb[NT][2], thr[NT][2];     // what a score's exponent is taken against, and what raises the maximum
   int ev_ref = 0;                  // e4m3: exponent byte that O's unit stands for
-  auto begin_unit = [&]() {
-    const int h0 = (cur.u / p.subs) * p.group, s0 = (cur.u % p.subs) * NQ;
+  // The query rows of a unit on their way to registers (a warp without a key in the part needs none), and what else begins with it.
+  auto load_q = [&](const Walk<kW, C::KEYS>& w) {
+    const int kvh = w.u / p.subs, s0 = (w.u - kvh * p.subs) * NQ;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int qi = s0 + nt * 8 + n;
-      const bool act = qi < p.group && cur.key < cur.end;   // a warp without a key in this part needs no query
-      const __nv_bfloat16* src = p.q + cur.b * p.q_stride + static_cast<int64_t>(h0 + (act ? qi : 0)) * D;
-      float amax = 0.f;
+      const bool act = qi < p.group && w.key < w.end;
+      const __nv_bfloat16* src = p.q + w.b * p.q_stride + static_cast<int64_t>(kvh * p.group + (act ? qi : 0)) * D;
 #pragma unroll
       for (int ks = 0; ks < C::KSTEPS; ++ks) {
         const int at = FP8 ? (t + 4 * (ks / 4)) * 16 + 4 * (ks % 4) : (t + 4 * (ks / 2)) * 8 + 4 * (ks % 2);
-        const uint2 w = act ? __ldg(reinterpret_cast<const uint2*>(src + at)) : uint2{};
-        qf[nt][ks][0] = w.x;
-        qf[nt][ks][1] = w.y;
-        if constexpr (FP8) {
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w.x << 16)), fabsf(__uint_as_float(w.x & 0xffff0000u))));
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w.y << 16)), fabsf(__uint_as_float(w.y & 0xffff0000u))));
-        }
+        const uint2 x = act ? __ldg(reinterpret_cast<const uint2*>(src + at)) : uint2{};
+        qf[nt][ks][0] = x.x;
+        qf[nt][ks][1] = x.y;
       }
+    }
+  };
+  auto begin_unit = [&]() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
       if constexpr (FP8) {
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        uint32_t top = 0;   // of the magnitudes' bit patterns, which order as integers but for NaN, two at a time
+#pragma unroll
+        for (int ks = 0; ks < C::KSTEPS; ++ks)
+          top = __vmaxu2(top, __vmaxu2(qf[nt][ks][0] & 0x7fff7fffu, qf[nt][ks][1] & 0x7fff7fffu));
+        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // 2^(14 - e) brings the largest to [2^14, 2^15); the exponent kept in range for rows of zeros and of tiny values
-        const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
+        const int e = max(static_cast<int>(max(top & 0xffffu, top >> 16) >> 7) - 127, -100);
         const float f = pow2i(14 - e);
 #pragma unroll
         for (int ks = 0; ks < C::KSTEPS; ++ks)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t w = qf[nt][ks][i];
-            qf[nt][ks][i] = pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
+            const float2 x = mul2(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), make_float2(f, f));
+            qf[nt][ks][i] = pack_f16x2(x.x, x.y);
           }
         // query columns 2t, 2t + 1 of the scores are rows 2t, 2t + 1 here: lanes 4 (2t), 4 (2t + 1)
         const int e0 = __shfl_sync(0xffffffffu, e, 8 * t), e1 = __shfl_sync(0xffffffffu, e, 8 * t + 4);
@@ -656,21 +662,31 @@ __global__ void __launch_bounds__(32 * warps_of(D, FP8, NT), 1) decode_kernel(De
           for (int c = 0; c < 2; ++c)
             join_o[((warp - kW / 2) * kPairs + (nt * C::MT + i) * 2 + c) * 32 + lane] =
                 make_float2(o[nt][i][c] * f[nt][c], o[nt][i][c + 2] * f[nt][c]);
-    } else if (tid < NQ) {
+    } else if (warp < NT) {   // a row's warps are dealt to 4 lanes
+      const int row = warp * 8 + (lane & 7);
+      float2 v[(kW + 3) / 4];
       float mx = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kW; ++w) mx = fmaxf(mx, join_ml[w * NQ + tid].x);
-#pragma unroll
-      for (int w = 0; w < kW; ++w) {
-        const float2 v = join_ml[w * NQ + tid];
-        sum += v.x == -INFINITY ? v.y : v.y * ex2_approx(v.x - mx);   // v.y is 0 or NaN without a maximum
+      for (int i = 0; i < (kW + 3) / 4; ++i) {
+        const int w = (lane >> 3) + 4 * i;
+        v[i] = w < kW ? join_ml[w * NQ + row] : make_float2(-INFINITY, 0.f);
+        mx = fmaxf(mx, v[i].x);
       }
-      if (whole && s0 + tid < p.group) {
-        const RowEnd r = row_end(p, h0 + s0 + tid, mx, sum, kBias);
-        p.lse[static_cast<int64_t>(h0 + s0 + tid) * p.batch + cur.b] = r.lse;
-        join_ml[kW * NQ + tid].x = r.inv;
-      } else if (!whole) {
-        p.ml[static_cast<int64_t>(slot) * NQ + tid] = make_float2(mx, sum);
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+#pragma unroll
+      for (int i = 0; i < (kW + 3) / 4; ++i)
+        sum += v[i].x == -INFINITY ? v[i].y : v[i].y * ex2_approx(v[i].x - mx);   // v.y is 0 or NaN without a maximum
+      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      if (lane < 8) {
+        if (whole && s0 + row < p.group) {
+          const RowEnd r = row_end(p, h0 + s0 + row, mx, sum, kBias);
+          p.lse[static_cast<int64_t>(h0 + s0 + row) * p.batch + cur.b] = r.lse;
+          join_ml[kW * NQ + row].x = r.inv;
+        } else if (!whole) {
+          p.ml[static_cast<int64_t>(slot) * NQ + row] = make_float2(mx, sum);
+        }
       }
     }
     __syncthreads();
@@ -732,31 +748,38 @@ __global__ void __launch_bounds__(32 * warps_of(D, FP8, NT), 1) decode_kernel(De
   };
 
   // ---- the share
-  bool fresh = true, first_part = true, from_start = !opens_mid;
+  load_q(cur);
+  bool first_part = true, from_start = !opens_mid;
   int32_t opened = 0;   // parts of the unit this CTA leaves open to later ones
   int stage = 0, fill = C::STAGES - 1;
 #pragma unroll 1
-  for (; todo > 0; --todo) {
-    if (todo > C::STAGES - 1) load_strip(fill, todo > C::STAGES);
-    cp_async_commit();
-    fill = fill + 1 == C::STAGES ? 0 : fill + 1;
-    if (fresh) begin_unit();
-    fresh = false;
-    cp_async_wait<C::STAGES - 1>();
-    __syncwarp();
-    strip(stage);
-    __syncwarp();   // the stage has been read by every lane before the next iteration refills it
-    stage = stage + 1 == C::STAGES ? 0 : stage + 1;
-    if (cur.left > 1 && todo > 1) {
+  for (;;) {   // a unit's part after the other
+    begin_unit();
+#pragma unroll 1
+    for (;;) {   // its blocks
+      if (todo > C::STAGES - 1) load_strip(fill, todo > C::STAGES);
+      cp_async_commit();
+      fill = fill + 1 == C::STAGES ? 0 : fill + 1;
+      cp_async_wait<C::STAGES - 1>();
+      __syncwarp();
+      strip(stage);
+      __syncwarp();   // the stage has been read by every lane before the next iteration refills it
+      stage = stage + 1 == C::STAGES ? 0 : stage + 1;
+      if (cur.left == 1 || todo == 1) break;
       cur.step();
-      continue;
+      --todo;
     }
-    const bool last = cur.left == 1;
+    const bool last = cur.left == 1, whole = last && from_start;
     const int slot = static_cast<int>(2 * cta) + (first_part ? 0 : 1);
-    if (last && from_start && cur.end - cur.start / C::KEYS * C::KEYS <= C::KEYS) {   // a unit of one strip: its warp alone
+    Walk<kW, C::KEYS> next = cur;
+    if (todo > 1) {   // the next unit's queries travel while this one's part ends
+      next.next_unit(p, units);
+      load_q(next);
+    }
+    if (whole && cur.end - cur.start / C::KEYS * C::KEYS <= C::KEYS) {   // a unit of one strip: its warp alone
       if (cur.turn == 0) end_alone();
     } else {
-      end_part(last && from_start, slot);
+      end_part(whole, slot);
     }
     if (!last && from_start) {
       opened = static_cast<int32_t>(share_of(kept[1], kept[2], kept[0] - todo + cur.left - 1) - cta + 1);
@@ -769,9 +792,10 @@ __global__ void __launch_bounds__(32 * warps_of(D, FP8, NT), 1) decode_kernel(De
         p.desc[cta] = d;
       }
     }
+    if (--todo == 0) break;
     first_part = false;
-    from_start = fresh = true;
-    if (todo > 1) cur.next_unit(p, units);
+    from_start = true;
+    cur = next;
   }
   if (opened == 0 && tid == 0) p.desc[cta].parts = 0;
 }

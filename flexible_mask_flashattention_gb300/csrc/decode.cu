@@ -26,9 +26,10 @@
 //
 // Split parts go to the workspace as (m, l, O) and a second kernel joins them in a fixed order.
 //
-// Measured on the device (of the 6795 GB/s that a copy reaches): 1M keys, 16 + 4 heads, d = 128, e4m3: 171 us (93 %); 64 x 16K keys, 64 + 8
-// heads, e4m3: 229 us (90 %); 24 x 8K keys with a window of 4096, 32 heads, d = 64, bf16: 117 us (90 %); 777 keys, bf16: 6.7 us.  With
-// the products left out the large ones take 161, 219 and 113 us.
+// Measured on the device (of the 6795 GB/s that a copy reaches; the range is that of several GPUs): 1M keys, 16 + 4 heads, d = 128, e4m3:
+// 166 to 172 us (93 to 96 %); 64 x 16K keys, 64 + 8 heads, e4m3: 220 to 226 us (91 to 94 %); 24 x 8K keys with a window of 4096, 32
+// heads, d = 64, bf16: 115 to 119 us (89 to 92 %); 32 x 1K keys: 12 us; 777 keys, bf16: 6.6 us.  With the products left out the large ones take 161,
+// 214 and 113 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -43,7 +44,7 @@ namespace ffa {
 namespace {
 
 // Warps a CTA, and groups of 16 keys a strip.  Warps hide each other's latencies, as far as registers and the ring allow; longer strips
-// spread a strip's fixed instructions over more keys.  Measured (us; 50 x 20K keys, 64 + 8 heads, d = 64, e4m3): 8 warps x 1 group 165,
+// spread a strip's fixed instructions over more keys.  Measured before later steps (us; 50 x 20K keys, 64 + 8 heads, d = 64, e4m3): 8 warps x 1 group 165,
 // 8 x 2 137, 8 x 4 120, 12 x 4 118, 16 x 2 118; (1M keys, 16 + 4 heads, d = 128, e4m3): 8 x 1 181, 12 x 1 170, 8 x 2 169; (24 x 8K
 // keys, 32 heads, d = 64, bf16): 8 x 1 119, 8 x 2 122, 12 x 2 117; (380K keys, 32 + 2 heads, d = 128, e4m3): 8 x 1 46, 8 x 2 43.
 constexpr int warps_of(int d, bool fp8, int nt) { return nt == 2 || d == 128 ? 8 : fp8 ? 16 : 12; }

@@ -33,7 +33,8 @@ def norm_rope(x, weight, cos_sin, positions, eps, interleaved):
 
 
 def norm_rope_grad(x, weight, cos_sin, positions, dout, eps, interleaved):
-    """(dx, dweight, sum of the absolute terms of dweight) of sum(norm_rope(x) * dout)."""
+    """(dx, dweight, sum of the absolute products dweight is made of) of sum(norm_rope(x) * dout).  The last counts the rotation's two
+    products apart, since rounding errors scale with them even where they cancel."""
     x, dout, w = (np.asarray(t, np.float64) for t in (x, dout, weight))
     pos, rot, d = np.asarray(positions), cos_sin.shape[1], x.shape[-1]
     keep = (pos >= 0)[:, None, None]
@@ -42,11 +43,14 @@ def norm_rope_grad(x, weight, cos_sin, positions, dout, eps, interleaved):
     g = dout.copy()
     g[..., a] = dout[..., a] * c + dout[..., b] * s
     g[..., b] = dout[..., b] * c - dout[..., a] * s
+    size = np.abs(dout)
+    size[..., a] = np.abs(dout[..., a] * c) + np.abs(dout[..., b] * s)
+    size[..., b] = np.abs(dout[..., b] * c) + np.abs(dout[..., a] * s)
     rms = np.sqrt((x ** 2).mean(-1, keepdims=True) + eps)
-    terms = np.where(keep, g * x / rms, 0.0)
+    terms, size = np.where(keep, g * x / rms, 0.0), np.where(keep, size * np.abs(x) / rms, 0.0)
     h = g * w
     dx = np.where(keep, h / rms - x * (h * x).sum(-1, keepdims=True) / (d * rms ** 3), 0.0)
-    return dx, terms.sum((0, 1)), np.abs(terms).sum((0, 1))
+    return dx, terms.sum((0, 1)), size.sum((0, 1))
 
 
 def e4m3_values():

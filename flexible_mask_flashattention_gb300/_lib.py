@@ -479,6 +479,7 @@ def bwd(q, k, v, out, lse, dout, plan: Plan, scale: float, dq=None, dk=None, dv=
 # The calls below take a few microseconds on the host and run many times a second in a decode loop, so their checks are
 # single expressions, and what went wrong is worked out only once something did.
 
+_I32_MAX = 0x7fffffff
 torch = None        # imported by the first of these calls, once
 _new = None         # (size, strides, dtype) -> a new tensor on the current device
 
@@ -566,6 +567,8 @@ def _rows_stride(t, name, shape, dev):
 def _dims(t, name, n):
     if t.dim() != n:
         raise FFAError(1, f"{name} must have {n} dimensions")
+    if t.numel() > _I32_MAX and max(t.shape[1:], default=0) > _I32_MAX:   # all but the first are int32 in the C calls
+        raise FFAError(5, f"{name} has a dimension beyond 32 bits")
     return t.shape
 
 
@@ -697,6 +700,8 @@ def kv_cache_read(k_cache, v_cache, page_table, cu_seqlens, total: int, k=None, 
         raise FFAError(1, "cu_seqlens must be an int32 tensor [batch + 1]")
     _check_dense(cu_seqlens, torch.int32, cu_seqlens.shape, dev, "cu_seqlens")
     batch = cu_seqlens.shape[0] - 1
+    if batch > _I32_MAX:
+        raise FFAError(5, "cu_seqlens has more sequences than 32 bits count")
     ts, width = _page_table(page_table, batch, dev)
     shape, bf16 = (int(total), cache.hkv, cache.d), torch.bfloat16
     if shape[0] < 0:

@@ -888,7 +888,7 @@ ffa_status ffa_fwd_decode(const void* q, int64_t q_stride, const ffa_kv_cache* c
   const ffa_status st = check_cache(cache, p.geom);
   if (st != FFA_OK) return st;
   if (batch < 0 || max_pages < 0 || hq <= 0 || hq % cache->hkv != 0) return FFA_ERR_INVALID_ARG;
-  if (!(scale > -INFINITY && scale < INFINITY)) return FFA_ERR_INVALID_ARG;
+  if (!(scale * kLog2e > -INFINITY && scale * kLog2e < INFINITY)) return FFA_ERR_INVALID_ARG;   // the scale in log2 units
   if (batch > 1 && table_stride < max_pages) return FFA_ERR_INVALID_ARG;
   if (hq > (1 << 16) || batch > (1 << 20)) return FFA_ERR_OVERFLOW;
   if (batch == 0) return FFA_OK;

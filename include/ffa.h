@@ -524,7 +524,7 @@ size_t ffa_fwd_decode_workspace_size(int32_t hq, int32_t hkv, int32_t d);
  * A sequence with a page that is not one of the cache's, or with more keys than
  * its table row holds, gets NaN rows (nothing out of range is read); the other
  * sequences are not affected.
- * Scores, maxima and sums are fp32; results do not depend on timing, but
+ * Scores, maxima and sums are fp32 (scale * log2(e) must be finite in it); results do not depend on timing, but
  * where a sequence is split depends on the batch's lengths.
  * Errors: FFA_ERR_INVALID_ARG, FFA_ERR_UNSUPPORTED, FFA_ERR_OVERFLOW,
  * FFA_ERR_CUDA.

@@ -235,6 +235,7 @@ def test_cache_read_refusals(lib, change, code):
     (dict(out=None), INVALID), (dict(out=at(3) + 2), INVALID), (dict(lse=None), INVALID), (dict(ws=None), INVALID),
     (dict(ws_bytes=100), INVALID), (dict(hq=1 << 17, qs=1 << 24), OVERFLOW), (dict(batch=(1 << 20) + 1), OVERFLOW),
     (dict(batch=0, q=None, lens=None, out=None, lse=None, ws=None), OK),
+    (dict(scale=-3e38), INVALID),   # finite, but not in log2 units
     (dict(out=at(0)), INVALID), (dict(lse=at(2)), INVALID), (dict(ws=at(3) + 64), INVALID), (dict(out=at(21)), INVALID),
     (dict(lse=at(23)), INVALID), (dict(ws=at(1) - 4096), INVALID), (dict(sink=at(3)), INVALID), (dict(starts=at(4)), INVALID)])
 def test_decode_refusals(lib, change, code):
@@ -259,3 +260,16 @@ def test_binding_refuses_tensors_that_are_not_on_the_gpu(lib):
                  lambda: ffa.fwd_decode(x, c, c, pt, pos, 1.0)):
         with pytest.raises(ffa.FFAError):
             call()
+
+
+def test_binding_refuses_dimensions_beyond_32_bits():
+    import torch
+    import flexible_mask_flashattention_gb300 as ffa
+    from flexible_mask_flashattention_gb300 import _lib
+    big = 1 << 31
+    for shape in ((2, big), (1, 2, big + 64)):
+        with pytest.raises(ffa.FFAError) as e:
+            _lib._dims(torch.empty(shape, device="meta"), "x", len(shape))
+        assert e.value.code == OVERFLOW
+    assert _lib._dims(torch.empty((big + 1, 2), device="meta"), "x", 2) == (big + 1, 2)
+    assert _lib._dims(torch.empty((big,), device="meta"), "x", 1) == (big,)

@@ -8,17 +8,25 @@
 //   dw = sum over rows of g r x,     dx = r (h - x r^2 mean(h x)).
 // r is recomputed in the backward from x, which it reads anyway, so the forward stores nothing for it.
 //
-// Both are bound by HBM: 4 bytes a value forward (x in, out out), 6 backward (x, dout in, dx out).  A lane holds 8
-// consecutive values of a row (16 bytes), d / 8 lanes a token; a warp takes 2 or 4 neighbouring tokens, one head of each at a
-// time, so that a token's rotation is read once for many heads and no head count leaves lanes empty.  The kernels are
-// persistent: a warp walks over units of up to 10 (backward: 5) heads of its tokens, and cp.async keeps the next unit's
-// values and table rows on their way to shared memory, where a token's lanes read back only what they copied.
-// Loads in flight then cost neither registers nor barriers.  Norm statistics, rotation and every gradient sum are fp32, two
-// values an instruction (fma.rn.f32x2); the one rounding to bf16 is the store's.  Measured at 64K tokens, 16 + 4 heads, d = 128: forward
-// 114 us, backward 171 us (both 87 % of a copy's 6795 GB/s); two stages beat three (130 and 200 us), which leave fewer warps.
+// Both are bound by HBM: 4 bytes a value forward (x in, out out), 6 backward (x, dout in, dx out).  A warp takes 2 or 4
+// neighbouring tokens, d / 8 lanes a token, one head of each at a time, so that a token's rotation is read once for many heads and
+// no head count leaves lanes empty; a lane's 8 columns are two runs of 4 whose values are each other's pair partners, so that the
+// rotation exchanges nothing.  The kernels are persistent: a warp walks over units of up to 5 (backward: 4) heads of its
+// tokens, and cp.async keeps the next unit's values and table rows on their way to shared memory.  A unit's sums are taken for
+// several heads side by side, as one head's exchanges would leave the warp waiting.  Norm statistics, rotation and every gradient sum are
+// fp32, two values an instruction (fma.rn.f32x2); the one rounding to bf16 is the store's.
+//
+// What decides at this bandwidth is how the copies reach memory.  The 8 warps of a CTA take consecutive units and start each round's
+// copies together, behind a barrier: runs of 16 tokens then arrive as one, where warps on their own spread 2.5 KB pieces over the
+// memory.  And more in flight is slower: 57 KB an SM does best.  Measured on one GPU at 64K tokens, 16 + 4 heads, d = 128
+// (forward and backward): 107 and 157 us (94 and 95 % of a copy's 6795 GB/s); CTAs of 4 warps, as many bytes in flight, 109 and 162, with
+// more in flight 127, without the barrier 119 and 176; of 16 warps 110 and 164; units of 4 and 5 heads 110 and 159, of 10 and 7
+// 115 and 185.  Bulk copies (cp.async.bulk) took 110 and 164 where these took 109 and 172, and 0.1 to 0.5 us longer for small
+// batches.
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ffa_internal.h"
 #include "launch.h"
@@ -27,12 +35,16 @@
 namespace ffa {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxBwdCtas = 1024;   // partial weight gradients the workspace holds
 constexpr int kStages = 2;          // units in shared memory: one being used, one on its way
+// Heads of a unit at most, and with so few heads in all that they are one unit (365K tokens of 3 + 3 heads, d = 64: 90 us in one
+// unit, 111 in two; 14K tokens of 64 + 8 heads in units of 6: 87 us, of 5: 82).
 template <bool BWD>
-constexpr int kUnitHeads = BWD ? 5 : 10;   // heads of a unit at most
+constexpr int kUnitHeads = BWD ? 4 : 5;
+template <bool BWD>
+constexpr int kUnitMost = BWD ? 4 : 6;
 
 struct NormRopeParams {
   const __nv_bfloat16* x[2];      // q, k
@@ -43,6 +55,7 @@ struct NormRopeParams {
   int32_t heads[2];
   int32_t unit;                   // heads of a unit (q's, then k's)
   int32_t per;                    // units a group of tokens
+  int32_t step_units, step_tokens;   // kWarps units in whole groups' tokens and units
   int64_t tokens;
   int64_t units, span;            // all units, and those of a CTA (consecutive ones)
   float eps;
@@ -53,6 +66,46 @@ struct NormRopeParams {
   float* partial;                 // backward: [CTAs][2][d]
 };
 
+// The 8 columns of a row that a lane holds, in two runs of 4 such that a rotation's pairs lie in one lane: values 0..3 are columns
+// from `lo` on, 4..7 those from `hi` on.  Pairs (i, i + rot / 2): run l of the rotated columns' first half and run l of the second, then
+// likewise of the columns from rot on; pairs (2i, 2i + 1): 8 neighbouring columns.
+template <int D, bool INTER>
+struct Columns {
+  int lo, hi;
+  __device__ __forceinline__ Columns(int l, int rot) {
+    if constexpr (INTER) {
+      lo = 8 * l, hi = lo + 4;
+    } else {
+      const bool in = 8 * l < rot;
+      lo = in ? 4 * l : rot / 2 + 4 * l;   // rot + 4 (l - rot / 8)
+      hi = lo + (in ? rot : D - rot) / 2;
+    }
+  }
+  __device__ __forceinline__ uint4 load(const uint8_t* row, int swap) const {
+    if constexpr (INTER) return *reinterpret_cast<const uint4*>(row + ((2 * lo) ^ swap));
+    const uint2 a = *reinterpret_cast<const uint2*>(row + ((2 * lo) ^ swap)), b = *reinterpret_cast<const uint2*>(row + ((2 * hi) ^ swap));
+    return make_uint4(a.x, a.y, b.x, b.y);
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* row, const uint4& v) const {
+    if constexpr (INTER) {
+      *reinterpret_cast<uint4*>(row + lo) = v;
+    } else {
+      *reinterpret_cast<uint2*>(row + lo) = make_uint2(v.x, v.y);
+      *reinterpret_cast<uint2*>(row + hi) = make_uint2(v.z, v.w);
+    }
+  }
+  __device__ __forceinline__ void load(const float* row, float2 (&f)[4]) const {
+    const float4 a = *reinterpret_cast<const float4*>(row + lo), b = *reinterpret_cast<const float4*>(row + hi);
+    f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w), f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
+  }
+  __device__ __forceinline__ int column(int j) const { return j < 4 ? lo + j : hi + j - 4; }
+};
+// The pair partners of the two values f[j].
+template <bool INTER>
+__device__ __forceinline__ float2 partner(const float2 (&f)[4], int j) {
+  return INTER ? make_float2(f[j].y, f[j].x) : f[j ^ 2];
+}
+
 __device__ __forceinline__ void unpack8(const uint4& v, float2 (&f)[4]) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -61,68 +114,51 @@ __device__ __forceinline__ void unpack8(const uint4& v, float2 (&f)[4]) {
 __device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
   return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
 }
-__device__ __forceinline__ uint4 shfl4(const uint4& v, int src) {
-  uint4 r;
-  r.x = __shfl_sync(0xffffffffu, v.x, src);
-  r.y = __shfl_sync(0xffffffffu, v.y, src);
-  r.z = __shfl_sync(0xffffffffu, v.z, src);
-  r.w = __shfl_sync(0xffffffffu, v.w, src);
-  return r;
-}
-__device__ __forceinline__ void load8(const float* p, float2 (&f)[4]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
-  f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w), f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
-}
 
-// A lane's part of one token's rotation, for the 8 values it holds of each row: value j becomes
-// c[j] v[j] + s[j] (its pair partner's value).  Columns behind rot_dim have c = 1, s = 0.  `src` is the lane that holds
-// the partners (itself when pairs are interleaved).
-template <int D, bool INTER>
+// A lane's part of one token's rotation, forward or (BACK) by the negative angle: value j becomes c(j) v + s(j) (its partner's
+// value).  Columns behind rot_dim have c = 1, s = 0.
+template <bool INTER, bool BACK>
 struct Rotation {
-  float2 c[4], s[4];
-  int src;
-  __device__ __forceinline__ void load(const float* row, int rot, int lane) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) c[j] = make_float2(1.f, 1.f), s[j] = make_float2(0.f, 0.f);
-    src = lane;
-    const int l = lane & (D / 8 - 1);
-    if (8 * l >= rot) return;
+  float2 cos[INTER ? 4 : 2], up[INTER ? 4 : 2], down[2];   // sines: of values 0..3 (interleaved: of all), of values 4..7
+  __device__ __forceinline__ void load(const float* row, int rot, int l) {
+    float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (8 * l < rot) c = *reinterpret_cast<const float4*>(row + 4 * l), s = *reinterpret_cast<const float4*>(row + rot / 2 + 4 * l);
+    if constexpr (BACK) s = make_float4(-s.x, -s.y, -s.z, -s.w);
     if constexpr (INTER) {
-      const float4 c4 = *reinterpret_cast<const float4*>(row + 4 * l);
-      const float4 s4 = *reinterpret_cast<const float4*>(row + rot / 2 + 4 * l);
-      const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
+      const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = make_float2(cc[i], cc[i]), s[i] = make_float2(-ss[i], ss[i]);
-    } else {   // rot_dim is a multiple of 16, so a lane's values are all in one half
-      const int half = rot >> 4;   // lanes a half
-      const bool lo = l < half;
-      const int i = 8 * (lo ? l : l - half);
-      load8(row + i, c);
-      load8(row + rot / 2 + i, s);
-      if (lo) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[j] = make_float2(-s[j].x, -s[j].y);
-      }
-      src = lo ? lane + half : lane - half;
+      for (int i = 0; i < 4; ++i) cos[i] = make_float2(cc[i], cc[i]), up[i] = make_float2(-ss[i], ss[i]);
+    } else {
+      cos[0] = make_float2(c.x, c.y), cos[1] = make_float2(c.z, c.w);
+      up[0] = make_float2(-s.x, -s.y), up[1] = make_float2(-s.z, -s.w);
+      down[0] = make_float2(s.x, s.y), down[1] = make_float2(s.z, s.w);
     }
   }
-  // The values of f's pair partners; v is f in its packed form.
-  __device__ __forceinline__ void partners(const uint4& v, const float2 (&f)[4], float2 (&p)[4]) const {
-    if constexpr (INTER) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = make_float2(f[j].y, f[j].x);
-    } else {
-      unpack8(shfl4(v, src), p);
-    }
+  __device__ __forceinline__ float2 c(int j) const { return INTER ? cos[j] : cos[j & 1]; }
+  __device__ __forceinline__ float2 s(int j) const {
+    if constexpr (INTER) return up[j];
+    else return j < 2 ? up[j] : down[j & 1];
   }
 };
 
-// Sum over the D / 8 lanes of a row.
-template <int D>
-__device__ __forceinline__ float row_sum(float v) {
+// Sums over the D / 8 lanes of a row, of several rows whose chains of exchanges run side by side.
+template <int D, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N]) {
 #pragma unroll
-  for (int o = D / 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int o = D / 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+}
+// f(count, i) for batches of N = 2 or 3, then fewer, that cover 0 .. n - 1.
+template <int N, typename F>
+__device__ __forceinline__ void in_batches(int n, F& f) {
+  int i = 0;
+#pragma unroll 1
+  for (; i + N <= n; i += N) f(std::integral_constant<int, N>{}, i);
+  if constexpr (N > 2) {
+    if (i + 2 <= n) f(std::integral_constant<int, 2>{}, i), i += 2;
+  }
+  if (i < n) f(std::integral_constant<int, 1>{}, i);
 }
 
 // Where a warp stands in its units: unit `c` of the D / 4 lanes' tokens; this lane's token (behind the last one: has = false) and its
@@ -145,28 +181,31 @@ struct UnitWalk {
     c = static_cast<int>(first - group * p.per);
     read_pos(p);
   }
-  __device__ __forceinline__ void next(int per) {   // the warp's next unit: kWarps further
+  __device__ __forceinline__ void next(const NormRopeParams& p) {   // the warp's next unit: kWarps further
     left -= kWarps;
-    c += kWarps;
-    while (c >= per) c -= per, token += kGroup;
+    c += p.step_units;
+    token += p.step_tokens;
+    if (c >= p.per) c -= p.per, token += kGroup;
   }
 };
 
-// The stages of a CTA in shared memory, in 16-byte chunks: of every stage a chunk a thread and head (two in the backward: x
-// and dout), then two a thread for the table rows, a token's behind each other.
+// A warp's stages in shared memory: of every head of a unit its tokens' rows, x [unit][token][D], in the backward dout likewise, then
+// the table's rows [token][D] (fp32).  At d = 64 odd tokens have their rows' halves swapped, so that two tokens' neighbouring runs
+// of 4 columns lie in different banks.
 template <int D, bool BWD>
 struct Stages {
-  uint4* base;
+  static constexpr int kTokens = 256 / D;
+  uint8_t* base;    // this warp's
   int unit;
-  __device__ __forceinline__ uint4* chunk(int stage, int i) const {
-    return base + (stage * (unit * (BWD ? 2 : 1) + 2) + i) * kThreads + threadIdx.x;
+  static __host__ __device__ constexpr int stage_bytes(int unit) { return kTokens * D * (2 * unit * (BWD ? 2 : 1) + 4); }
+  static __host__ __device__ constexpr int bytes(int unit) { return kWarps * kStages * stage_bytes(unit); }
+  __device__ __forceinline__ uint8_t* rows(int stage, int sub, int tensor) const {   // tensor 0: x, 1: dout; heads 512 bytes apart
+    return base + stage * stage_bytes(unit) + tensor * unit * 512 + sub * (2 * D);
   }
-  // Chunk i of this lane's token's table row (the lanes l of a token write chunks l and l + D / 8).
-  __device__ __forceinline__ uint4* table(int stage, int i) const {
-    const int lane = threadIdx.x & 31, l = lane & (D / 8 - 1);
-    return base + (stage * (unit * (BWD ? 2 : 1) + 2) + unit * (BWD ? 2 : 1)) * kThreads + 2 * (threadIdx.x - l) + i;
+  __device__ __forceinline__ float* table(int stage, int sub) const {
+    return reinterpret_cast<float*>(base + stage * stage_bytes(unit) + (BWD ? 2 : 1) * unit * 512) + sub * D;
   }
-  static __host__ __device__ constexpr int bytes(int unit) { return kStages * (unit * (BWD ? 2 : 1) + 2) * kThreads * 16; }
+  static __device__ __forceinline__ int swap(int sub) { return D == 64 && (sub & 1) ? 64 : 0; }   // XORed to a byte's place in its row
 };
 
 // The part of a unit in one tensor: `n` heads from `head` on, from place `first` of the unit on.
@@ -182,28 +221,29 @@ __device__ __forceinline__ UnitPart part_of(const NormRopeParams& p, int c, int 
 // they are not read, so that nothing in them reaches a sum.
 template <int D, bool BWD>
 __device__ __forceinline__ void copy_unit(const NormRopeParams& p, const Stages<D, BWD>& st, int stage, const UnitWalk<D>& w) {
-  const int l = threadIdx.x & (D / 8 - 1);
+  const int lane = threadIdx.x & 31, l = lane & (D / 8 - 1), sub = lane / (D / 8);
   const bool live = w.pos >= 0 && w.pos < p.max_pos;
   const int64_t token = live ? w.token : 0;
-  const int bytes = live ? 16 : 0;
+  const int bytes = live ? 16 : 0, at = (16 * l) ^ Stages<D, BWD>::swap(sub);
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const UnitPart r = part_of(p, w.c, t);
     if (r.n <= 0) continue;
     const __nv_bfloat16* x = p.x[t] + token * p.x_stride[t] + r.head * D + 8 * l;
     const __nv_bfloat16* g = BWD ? p.dout[t] + (token * p.heads[t] + r.head) * D + 8 * l : nullptr;
-    const uint32_t to = smem_u32(st.chunk(stage, r.first)), to_g = smem_u32(st.chunk(stage, p.unit + r.first));
+    const uint32_t to = smem_u32(st.rows(stage, sub, 0)) + r.first * 512 + at, to_g = smem_u32(st.rows(stage, sub, 1)) + r.first * 512 + at;
 #pragma unroll
-    for (int i = 0; i < kUnitHeads<BWD>; ++i) {
+    for (int i = 0; i < kUnitMost<BWD>; ++i) {
       if (i >= r.n) break;
-      cp_async16(to + i * kThreads * 16, x + i * D, bytes);
-      if constexpr (BWD) cp_async16(to_g + i * kThreads * 16, g + i * D, bytes);
+      cp_async16(to + i * 512, x + i * D, bytes);
+      if constexpr (BWD) cp_async16(to_g + i * 512, g + i * D, bytes);
     }
   }
   if (live) {
     const float* row = p.cos_sin + static_cast<int64_t>(w.pos) * p.rot;
-    if (4 * l < p.rot) cp_async16(smem_u32(st.table(stage, l)), row + 4 * l);
-    if (4 * (l + D / 8) < p.rot) cp_async16(smem_u32(st.table(stage, l + D / 8)), row + 4 * (l + D / 8));
+    const uint32_t to = smem_u32(st.table(stage, sub));
+    if (4 * l < p.rot) cp_async16(to + 16 * l, row + 4 * l);
+    if (4 * (l + D / 8) < p.rot) cp_async16(to + 16 * (l + D / 8), row + 4 * (l + D / 8));
   }
 }
 
@@ -212,67 +252,76 @@ __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(NormRopeParams 
   constexpr int L = D / 8;
   extern __shared__ __align__(128) uint8_t smem[];
   float* weights = reinterpret_cast<float*>(smem);   // [2][D]
-  const Stages<D, false> st{reinterpret_cast<uint4*>(smem + 2 * D * 4), p.unit};
-  const int lane = threadIdx.x & 31, l = lane & (L - 1);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (L - 1), sub = lane / L;
+  const Stages<D, false> st{smem + 2 * D * 4 + warp * kStages * Stages<D, false>::stage_bytes(p.unit), p.unit};
+  const Columns<D, INTER> cols(l, p.rot);
+  const int swap = Stages<D, false>::swap(sub);
   UnitWalk<D> cur, ld;
-  cur.init(p, threadIdx.x >> 5, lane / L);
+  cur.init(p, warp, sub);
   ld = cur;
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
     if (ld.left > 0) copy_unit<D, false>(p, st, s, ld);
     cp_async_commit();
-    ld.next(p.per);
+    ld.next(p);
     ld.read_pos(p);
   }
   for (int i = threadIdx.x; i < 2 * D; i += kThreads) weights[i] = p.w[i / D][i % D];
   __syncthreads();
   int stage = 0, fill = kStages - 1;
-  for (; cur.left > 0; cur.next(p.per)) {
+  for (int todo = cur.left + warp; todo > 0; todo -= kWarps, cur.next(p)) {
+    __syncthreads();   // the warps' copies go out together: one run of memory
+    if (cur.left <= 0) continue;
     cur.read_pos(p);   // again: from L1
-    const int pos = cur.pos;
     if (ld.left > 0) copy_unit<D, false>(p, st, fill, ld);
     cp_async_commit();
-    ld.next(p.per);
+    ld.next(p);
     ld.read_pos(p);   // a unit ahead of its use
     cp_async_wait<kStages - 1>();
-    __syncwarp();
+    __syncwarp();   // lanes read what others copied
+    const int pos = cur.pos;
     const bool live = pos >= 0 && pos < p.max_pos;
     // a padded token (negative position) gives zeros, one behind the table NaN
     const uint32_t fill_bits = pos < 0 ? 0u : 0x7fff7fffu;
     const uint4 constant = make_uint4(fill_bits, fill_bits, fill_bits, fill_bits);
-    Rotation<D, INTER> rot;
-    rot.load(reinterpret_cast<const float*>(st.table(stage, 0)), live ? p.rot : 0, lane);
+    Rotation<INTER, false> rot;
+    rot.load(st.table(stage, sub), live ? p.rot : 0, l);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const UnitPart u = part_of(p, cur.c, t);
       if (u.n <= 0) continue;
-      __nv_bfloat16* out = p.out[t] + (cur.token * p.heads[t] + u.head) * D + 8 * l;
-      const uint4* in = st.chunk(stage, u.first);
+      __nv_bfloat16* out = p.out[t] + (cur.token * p.heads[t] + u.head) * D;
+      const uint8_t* in = st.rows(stage, sub, 0) + u.first * 512;
       // coefficients with the weights: out_j = r (x_j a_j + partner_j b_j)
-      float2 a[4], b[4];
-      load8(weights + t * D + 8 * l, a);
-      if constexpr (INTER) {
+      float2 w[4], a[4], b[4];
+      cols.load(weights + t * D, w);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = make_float2(a[j].y, a[j].x);
-      } else {
-        load8(weights + t * D + 8 * (rot.src & (L - 1)), b);
-      }
+      for (int j = 0; j < 4; ++j) a[j] = mul2(w[j], rot.c(j)), b[j] = mul2(partner<INTER>(w, j), rot.s(j));
+      auto some = [&](auto count, int i) {   // `count` heads from i on, their sums side by side
+        constexpr int N = decltype(count)::value;
+        float2 f[N][4];
+        float r[N];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) a[j] = mul2(a[j], rot.c[j]), b[j] = mul2(b[j], rot.s[j]);
-#pragma unroll 2
-      for (int i = 0; i < u.n; ++i) {
-        const uint4 v = in[i * kThreads];
-        float2 f[4], q[4], ss = make_float2(0.f, 0.f);
-        unpack8(v, f);
+        for (int h = 0; h < N; ++h) {
+          unpack8(cols.load(in + (i + h) * 512, swap), f[h]);
+          float2 ss = mul2(f[h][0], f[h][0]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) ss = fma2(f[j], f[j], ss);
-        const float r = rsqrtf(row_sum<D>(ss.x + ss.y) * (1.f / D) + p.eps);
-        rot.partners(v, f, q);
+          for (int j = 1; j < 4; ++j) ss = fma2(f[h][j], f[h][j], ss);
+          r[h] = ss.x + ss.y;
+        }
+        row_sums<D>(r);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = mul2(fma2(f[j], a[j], mul2(q[j], b[j])), make_float2(r, r));
-        if (live) *reinterpret_cast<uint4*>(out + i * D) = pack8(f);
-        else if (cur.has) *reinterpret_cast<uint4*>(out + i * D) = constant;
-      }
+        for (int h = 0; h < N; ++h) {
+          r[h] = rsqrtf(r[h] * (1.f / D) + p.eps);
+          float2 o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            o[j] = mul2(fma2(f[h][j], a[j], mul2(partner<INTER>(f[h], j), b[j])), make_float2(r[h], r[h]));
+          if (live) cols.store(out + (i + h) * D, pack8(o));
+          else if (cur.has) cols.store(out + (i + h) * D, constant);
+        }
+      };
+      in_batches<3>(u.n, some);
     }
     __syncwarp();   // the stage's table row has been read by every lane before the next iteration refills it
     stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -289,8 +338,10 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NormRopeParams 
   extern __shared__ __align__(128) uint8_t smem[];
   float* weights = reinterpret_cast<float*>(smem);   // [2][D]
   float* red = weights + 2 * D;                      // [kWarps][2][D]
-  const Stages<D, true> st{reinterpret_cast<uint4*>(smem + (1 + kWarps) * 2 * D * 4), p.unit};
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (L - 1), sub = lane / L;
+  const Stages<D, true> st{smem + (1 + kWarps) * 2 * D * 4 + warp * kStages * Stages<D, true>::stage_bytes(p.unit), p.unit};
+  const Columns<D, INTER> cols(l, p.rot);
+  const int swap = Stages<D, true>::swap(sub);
   UnitWalk<D> cur, ld;
   cur.init(p, warp, sub);
   ld = cur;
@@ -298,7 +349,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NormRopeParams 
   for (int s = 0; s < kStages - 1; ++s) {
     if (ld.left > 0) copy_unit<D, true>(p, st, s, ld);
     cp_async_commit();
-    ld.next(p.per);
+    ld.next(p);
     ld.read_pos(p);
   }
   for (int i = threadIdx.x; i < 2 * D; i += kThreads) weights[i] = p.w[i / D][i % D];
@@ -306,59 +357,70 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NormRopeParams 
   allow_dependents();
   float2 acc[2][4] = {};
   int stage = 0, fill = kStages - 1;
-  for (; cur.left > 0; cur.next(p.per)) {
+  for (int todo = cur.left + warp; todo > 0; todo -= kWarps, cur.next(p)) {
+    __syncthreads();   // the warps' copies go out together: one run of memory
+    if (cur.left <= 0) continue;
     cur.read_pos(p);   // again: from L1
-    const int pos = cur.pos;
     if (ld.left > 0) copy_unit<D, true>(p, st, fill, ld);
     cp_async_commit();
-    ld.next(p.per);
+    ld.next(p);
     ld.read_pos(p);
     cp_async_wait<kStages - 1>();
-    __syncwarp();
+    __syncwarp();   // lanes read what others copied
+    const int pos = cur.pos;
     const bool live = pos >= 0 && pos < p.max_pos;
     // a padded token (negative position) gives zeros, one behind the table NaN
     const uint32_t fill_bits = pos < 0 ? 0u : 0x7fff7fffu;
     const uint4 constant = make_uint4(fill_bits, fill_bits, fill_bits, fill_bits);
-    Rotation<D, INTER> rot;
-    rot.load(reinterpret_cast<const float*>(st.table(stage, 0)), live ? p.rot : 0, lane);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) rot.s[j] = make_float2(-rot.s[j].x, -rot.s[j].y);   // R^T turns by the negative angle
+    Rotation<INTER, true> rot;   // R^T turns by the negative angle
+    rot.load(st.table(stage, sub), live ? p.rot : 0, l);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const UnitPart u = part_of(p, cur.c, t);
       if (u.n <= 0) continue;
-      __nv_bfloat16* dx = p.out[t] + (cur.token * p.heads[t] + u.head) * D + 8 * l;
+      __nv_bfloat16* dx = p.out[t] + (cur.token * p.heads[t] + u.head) * D;
       if (!live && pos >= 0)   // a position behind the table makes the weight's gradient NaN too
         acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
-      const uint4 *in = st.chunk(stage, u.first), *in_g = st.chunk(stage, p.unit + u.first);
+      const uint8_t *in = st.rows(stage, sub, 0) + u.first * 512, *in_g = st.rows(stage, sub, 1) + u.first * 512;
       float2 w[4];
-      load8(weights + t * D + 8 * l, w);
-#pragma unroll 2
-      for (int k = 0; k < u.n; ++k) {
-        const uint4 v = in[k * kThreads], gv = in_g[k * kThreads];
-        float2 f[4], g[4], q[4], ss = make_float2(0.f, 0.f), hx = make_float2(0.f, 0.f);
-        unpack8(v, f);
-        unpack8(gv, g);
-        rot.partners(gv, g, q);
-        float2 hw[4];
+      cols.load(weights + t * D, w);
+      auto some = [&](auto count, int k) {
+        constexpr int N = decltype(count)::value;
+        float2 f[N][4], g[N][4];
+        float r[N], c[N];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          g[i] = fma2(g[i], rot.c[i], mul2(q[i], rot.s[i]));
-          hw[i] = mul2(g[i], w[i]);
-          ss = fma2(f[i], f[i], ss);
-          hx = fma2(hw[i], f[i], hx);
-        }
-        const float square = row_sum<D>(ss.x + ss.y);   // by all lanes, live or not
-        const float r = live ? rsqrtf(square * (1.f / D) + p.eps) : 0.f;   // 0: adds nothing
-        const float c = -row_sum<D>(hx.x + hx.y) * (r * r) * (r * (1.f / D));
+        for (int n = 0; n < N; ++n) {
+          const uint4 v = cols.load(in + (k + n) * 512, swap), gv = cols.load(in_g + (k + n) * 512, swap);
+            float2 d[4], ss = make_float2(0.f, 0.f), hx = make_float2(0.f, 0.f);
+          unpack8(v, f[n]);
+          unpack8(gv, d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          hw[i] = fma2(f[i], make_float2(c, c), mul2(hw[i], make_float2(r, r)));   // dx = r h - x r^3 mean(h x)
-          acc[t][i] = fma2(g[i], mul2(f[i], make_float2(r, r)), acc[t][i]);
+          for (int i = 0; i < 4; ++i) {
+            g[n][i] = fma2(d[i], rot.c(i), mul2(partner<INTER>(d, i), rot.s(i)));
+            ss = fma2(f[n][i], f[n][i], ss);
+            hx = fma2(mul2(g[n][i], w[i]), f[n][i], hx);
+          }
+          r[n] = ss.x + ss.y;
+          c[n] = hx.x + hx.y;
         }
-        if (live) *reinterpret_cast<uint4*>(dx + k * D) = pack8(hw);
-        else if (cur.has) *reinterpret_cast<uint4*>(dx + k * D) = constant;
-      }
+        row_sums<D>(r);   // by all lanes, live or not
+        row_sums<D>(c);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          r[n] = live ? rsqrtf(r[n] * (1.f / D) + p.eps) : 0.f;   // 0: adds nothing
+          c[n] = -c[n] * (r[n] * r[n]) * (r[n] * (1.f / D));
+          float2 o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            g[n][i] = mul2(g[n][i], make_float2(r[n], r[n]));
+            o[i] = fma2(f[n][i], make_float2(c[n], c[n]), mul2(g[n][i], w[i]));   // dx = r h - x r^3 mean(h x)
+            acc[t][i] = fma2(g[n][i], f[n][i], acc[t][i]);
+          }
+          if (live) cols.store(dx + (k + n) * D, pack8(o));
+          else if (cur.has) cols.store(dx + (k + n) * D, constant);
+        }
+      };
+      in_batches<2>(u.n, some);
     }
     __syncwarp();
     stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -371,7 +433,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NormRopeParams 
       float s = j & 1 ? acc[t][j / 2].y : acc[t][j / 2].x;
 #pragma unroll
       for (int o = L; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (sub == 0) red[(warp * 2 + t) * D + 8 * l + j] = s;
+      if (sub == 0) red[(warp * 2 + t) * D + cols.column(j)] = s;
     }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
@@ -437,17 +499,20 @@ ffa_status check_common(const void* q, int64_t q_stride, const void* k, int64_t 
   return FFA_OK;
 }
 
-// Units for `warps` resident warps: the heads of a group of tokens are cut into units of equal size, kUnitHeads at most, and smaller
-// ones where there would be fewer units than warps.
+// Units for `warps` resident warps: the heads of a group of tokens are cut into units of equal size, kUnitHeads or kUnitMost at
+// most, and smaller ones where there would be fewer units than warps.
 template <bool BWD>
 void set_units(NormRopeParams& p, int64_t tokens, int d, int64_t warps) {
   const int group = 256 / d;
   const int64_t groups = (tokens + group - 1) / group, all = p.heads[0] + p.heads[1];
-  const int64_t per = std::max((all + kUnitHeads<BWD> - 1) / kUnitHeads<BWD>, std::min(all, warps / std::max<int64_t>(groups, 1)));
+  const int64_t fewest = all <= kUnitMost<BWD> ? 1 : (all + kUnitHeads<BWD> - 1) / kUnitHeads<BWD>;
+  const int64_t per = std::max(fewest, std::min(all, warps / std::max<int64_t>(groups, 1)));
   p.tokens = tokens;
   p.unit = static_cast<int32_t>((all + per - 1) / per);
   p.per = static_cast<int32_t>((all + p.unit - 1) / p.unit);
   p.units = groups * p.per;
+  p.step_units = kWarps % p.per;
+  p.step_tokens = kWarps / p.per * group;
 }
 
 template <int D, bool BWD>
@@ -477,13 +542,13 @@ ffa_status launch(NormRopeParams p, int64_t tokens, cudaStream_t s, int* ctas) {
     else return norm_rope_fwd_kernel<D, INTER>;
   }();
   static std::atomic<int> known[kDevices];
-  constexpr int kMost = smem_bytes<D, BWD>(kUnitHeads<BWD>);
+  constexpr int kMost = smem_bytes<D, BWD>(kUnitMost<BWD>);
   int device = 0, sms = 0;
   if (!current_device(device, sms)) return FFA_ERR_CUDA;
   const int held = resident(kernel, kMost, device, sms, known);
   if (held == 0) return FFA_ERR_CUDA;
   set_units<BWD>(p, tokens, D, static_cast<int64_t>(held) * kWarps);
-  // consecutive units to each CTA, all CTAs resident at once (64K tokens, 16 + 4 heads, d = 128, before a warp took several tokens: 112
+  // consecutive units to each CTA, all CTAs resident at once (64K tokens, 16 + 4 heads, d = 128, measured with CTAs of 4 warps: 112
   // us forward and 170 us backward, against 120 to 125 and 180 to 184 us with CTAs of 2 to 32 units a warp)
   const int64_t most = std::min(held, kMaxBwdCtas);
   p.span = std::max<int64_t>((p.units + most - 1) / most, 1);

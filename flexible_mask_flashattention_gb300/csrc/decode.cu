@@ -45,9 +45,9 @@ namespace {
 
 // Warps a CTA, and groups of 16 keys a strip.  Warps hide each other's latencies, as far as registers and the ring allow; longer strips
 // spread a strip's fixed instructions over more keys.  Measured before later steps (us; 50 x 20K keys, 64 + 8 heads, d = 64, e4m3): 8 warps x 1 group 165,
-// 8 x 2 137, 8 x 4 120, 12 x 4 118, 16 x 2 118; (1M keys, 16 + 4 heads, d = 128, e4m3): 8 x 1 181, 12 x 1 170, 8 x 2 169; (24 x 8K
+// 8 x 2 137, 8 x 4 120, 12 x 4 118, 16 x 2 118, and later 12 x 2 114 and 16 x 2 116; (1M keys, 16 + 4 heads, d = 128, e4m3): 8 x 1 181, 12 x 1 170, 8 x 2 169; (24 x 8K
 // keys, 32 heads, d = 64, bf16): 8 x 1 119, 8 x 2 122, 12 x 2 117; (380K keys, 32 + 2 heads, d = 128, e4m3): 8 x 1 46, 8 x 2 43.
-constexpr int warps_of(int d, bool fp8, int nt) { return nt == 2 || d == 128 ? 8 : fp8 ? 16 : 12; }
+constexpr int warps_of(int d, int nt) { return nt == 2 || d == 128 ? 8 : 12; }
 constexpr int groups_of(int d, bool fp8) { return d == 128 && !fp8 ? 1 : 2; }
 constexpr int kMaxCtas = 160;          // CTAs (one an SM) the workspace holds parts for: two a CTA
 constexpr int kSmemMax = 226 * 1024;   // of 227 KB
@@ -87,7 +87,7 @@ struct DecodeParams {
 
 template <int D, bool FP8, int NT>
 struct Cfg {
-  static constexpr int W = warps_of(D, FP8, NT);
+  static constexpr int W = warps_of(D, NT);
   static constexpr int THREADS = 32 * W;
   static constexpr int SK = groups_of(D, FP8);
   static constexpr int KEYS = 16 * SK;                  // keys of a strip
@@ -100,7 +100,10 @@ struct Cfg {
   static constexpr int STAGE = SK * GROUP;
   static constexpr int JOIN = (W / 2) * 8 * NT * D * 4 + (W + 1) * 8 * NT * 8;   // O buffers; (m, l) of every warp, the rows' factors
   static constexpr int MISC = 1024;
-  static constexpr int STAGES = (kSmemMax - JOIN - MISC) / (W * STAGE) < 8 ? (kSmemMax - JOIN - MISC) / (W * STAGE) : 8;
+  static constexpr int FIT = (kSmemMax - JOIN - MISC) / (W * STAGE);
+  // e4m3 has two stages though three would fit at d = 128: more loads in flight are slower (64 x 16K keys 219 and 224 us, 1M keys 164 and
+  // 169 us).  bf16, with as many bytes in flight at two, takes what fits (3 stages at most; 777 keys 6.6 and 6.8 us).
+  static constexpr int STAGES = FP8 ? 2 : FIT;
   static constexpr int SMEM = MISC + JOIN + W * STAGE * STAGES;
   static constexpr int KSTEPS = D / 16;
   static constexpr int MT = D / 16;                     // 16-column tiles of the output
@@ -206,7 +209,7 @@ __device__ __forceinline__ RowEnd row_end(const DecodeParams& p, int head, float
 }
 
 template <int D, bool FP8, int NT>
-__global__ void __launch_bounds__(32 * warps_of(D, FP8, NT), 1) decode_kernel(DecodeParams p) {
+__global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeParams p) {
   using C = Cfg<D, FP8, NT>;
   constexpr int NQ = 8 * NT, kW = C::W, kThreads = C::THREADS, kBlock = C::BLOCK, SK = C::SK;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -859,7 +862,7 @@ int tiles_of(int group) { return group > 8 ? 2 : 1; }   // query tiles of 8 a un
 template <int D, bool FP8, int NT>
 ffa_status launch(const DecodeParams& p, int device, int sms, cudaStream_t s) {
   using C = Cfg<D, FP8, NT>;
-  static_assert(C::STAGES >= 2, "ring");
+  static_assert(C::FIT >= C::STAGES && C::STAGES >= 2, "ring");
   static std::atomic<bool> raised[kDevices];
   const int grid = std::min(sms, kMaxCtas);
   const cudaError_t e = launch_large(decode_kernel<D, FP8, NT>, dim3(grid), C::THREADS, C::SMEM, C::SMEM, s, device, raised, p);

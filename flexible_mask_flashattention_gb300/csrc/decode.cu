@@ -27,9 +27,8 @@
 // Split parts go to the workspace as (m, l, O) and a second kernel joins them in a fixed order.
 //
 // Measured on the device (of the 6795 GB/s that a copy reaches; the range is that of several GPUs): 1M keys, 16 + 4 heads, d = 128, e4m3:
-// 166 to 172 us (93 to 96 %); 64 x 16K keys, 64 + 8 heads, e4m3: 220 to 226 us (91 to 94 %); 24 x 8K keys with a window of 4096, 32
-// heads, d = 64, bf16: 115 to 119 us (89 to 92 %); 32 x 1K keys: 12 us; 777 keys, bf16: 6.6 us.  With the products left out the large ones take 161,
-// 214 and 113 us.
+// 164 to 168 us (95 to 97 %); 64 x 16K keys, 64 + 8 heads, e4m3: 219 to 223 us (93 to 94 %); 24 x 8K keys with a window of 4096, 32
+// heads, d = 64, bf16: 115 to 119 us (89 to 92 %), 113 with the products left out; 32 x 1K keys: 12 us; 777 keys, bf16: 6.6 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -100,9 +100,10 @@ struct Cfg {
   static constexpr int JOIN = (W / 2) * 8 * NT * D * 4 + (W + 1) * 8 * NT * 8;   // O buffers; (m, l) of every warp, the rows' factors
   static constexpr int MISC = 1024;
   static constexpr int FIT = (kSmemMax - JOIN - MISC) / (W * STAGE);
-  // e4m3 has two stages though three would fit at d = 128: more loads in flight are slower (64 x 16K keys 219 and 224 us, 1M keys 164 and
-  // 169 us).  bf16, with as many bytes in flight at two, takes what fits (3 stages at most; 777 keys 6.6 and 6.8 us).
-  static constexpr int STAGES = FP8 ? 2 : FIT;
+  // Two stages, though three would fit e4m3 at d = 128 and groups over 8 at d = 64: more loads in flight are slower (e4m3, 64 x 16K keys
+  // 219 and 224 us, 1M keys 164 and 169 us; 16 x 32K keys of 16-head groups, d = 64, bf16 37 and 39 us).  bf16 at d = 128 takes what
+  // fits (777 keys 6.6 us with three and 6.8 with two, large batches alike).
+  static constexpr int STAGES = FP8 || D == 64 ? 2 : FIT;
   static constexpr int SMEM = MISC + JOIN + W * STAGE * STAGES;
   static constexpr int KSTEPS = D / 16;
   static constexpr int MT = D / 16;                     // 16-column tiles of the output

@@ -118,6 +118,17 @@ def test_norm_rope_bwd(ffa, tokens, hq, hkv, d, rot, inter):
     assert all((bits(a) == bits(b)).all() for a, b in zip(grads, again))   # a fixed order of sums
 
 
+@pytest.mark.parametrize("tokens,hq,hkv,d,rot", [(12011, 7, 3, 128, 96), (9001, 11, 4, 64, 48)])
+def test_norm_rope_with_several_units_a_warp(ffa, tokens, hq, hkv, d, rot):
+    args = norm_inputs(tokens, hq, hkv, d, rot, tokens)
+    q, k, qw, kw, t, pos = args[:6]
+    pos[::7] = -1
+    qo, ko = ffa.qk_norm_rope(q, k, qw, kw, t, pos, eps=1e-5)
+    check_norm(qo, q, qw, t, pos, 1e-5, False)
+    check_norm(ko, k, kw, t, pos, 1e-5, False)
+    check_norm_bwd(ffa, ffa.qk_norm_rope_bwd(*args, eps=1e-5), *args, 1e-5, False)
+
+
 def test_norm_rope_bwd_equals_differences_of_the_forward(ffa):
     """Along a random direction, against the forward's own fp64 formula at the inputs' values; the backward's dx rounds to bf16
     (2^-8 a value), so the sum's error is 2^-8 of the root of its squared terms, four times that allowed."""

@@ -17,7 +17,7 @@
 // fp32, two values an instruction (fma.rn.f32x2); the one rounding to bf16 is the store's.
 //
 // What decides at this bandwidth is how the copies reach memory.  The 8 warps of a CTA take consecutive units and start each round's
-// copies together, behind a barrier: runs of 16 tokens then arrive as one, where warps on their own spread 2.5 KB pieces over the
+// copies together, behind a barrier: 4 tokens (20 KB) then arrive as one run, where warps on their own spread 2.5 KB pieces over the
 // memory.  And more in flight is slower: 57 KB an SM does best.  Measured on one GPU at 64K tokens, 16 + 4 heads, d = 128
 // (forward and backward): 107 and 157 us (94 and 95 % of a copy's 6795 GB/s); CTAs of 4 warps, as many bytes in flight, 109 and 162, with
 // more in flight 127, without the barrier 119 and 176; of 16 warps 110 and 164; units of 4 and 5 heads 110 and 159, of 10 and 7

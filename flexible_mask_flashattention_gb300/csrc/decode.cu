@@ -20,9 +20,11 @@
 //
 // Types.  bf16 cache: bf16 MMAs; P goes in as a bf16 value plus the bf16 value of its remainder, so that its rounding
 // does not add to the output's.  e4m3 cache: codes are exact in f16; q is scaled by a power of two a row to f16's top range (its bf16
-// mantissa fits; values below 2^-31 of the row's largest round); the scale of a key's row multiplies its score, the scale
-// of a value's row its weight, relative to the largest seen; P is f16 (11 bits).  Scores, maxima, sums and the output
-// accumulate in fp32.
+// mantissa fits; values below 2^-31 of the row's largest round); the scale of a key's row multiplies its score.  The scale 2^n of a
+// value's row goes into its weight, as e^{s_j} 2^{n_j} = 2^{s_j log2(e) + n_j}, which each query has a running reference of its own for: what
+// an f16 weight (11 bits) is relative to is the largest that has counted for this query, not the largest row there is.  Weights
+// from 2^-24 of that on are rounded to 2^-11 of themselves, smaller ones by at most 2^-35 of it.  Scores, maxima, sums and the
+// output accumulate in fp32.
 //
 // Split parts go to the workspace as (m, l, O) and a second kernel joins them in a fixed order.
 //
@@ -187,14 +189,19 @@ __device__ __forceinline__ int column(int i, int n) {
   return FP8 ? (D / 8) * n + 2 * i : (i / 4) * 64 + 8 * n + 2 * (i % 4);
 }
 
-// The end of a row whose sums, times 2^bias, are relative to the maximum mx: the sink, then what its columns are multiplied by
-// (NaN where the sum is) and its lse.
+// 2^x for factors of the output, down to fp32's smallest values (ex2_approx gives 0 under 2^-126).
+__device__ __forceinline__ float ex2_wide(float x) {
+  const bool low = x < -64.f;
+  return ex2_approx(low ? x + 64.f : x) * (low ? 5.421010862427522e-20f : 1.f);   // 2^-64
+}
+
+// The end of a row whose sums are relative to 2^mx: the sink, then what its columns are multiplied by (NaN where the sum is) and
+// its lse.
 struct RowEnd {
   float inv, lse;
 };
-__device__ __forceinline__ RowEnd row_end(const DecodeParams& p, int head, float mx, float sum, float bias) {
+__device__ __forceinline__ RowEnd row_end(const DecodeParams& p, int head, float mx, float sum) {
   float f = 1.f;
-  mx -= bias;
   if (p.sink) {
     const float s2 = p.sink[head] * kLog2e;
     const float top = fmaxf(mx, s2);
@@ -387,17 +394,18 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
     cp_async_commit();
   }
 
-  // A row maximum is raised only when a score passes it by kLazy (log2 units): most strips then cost one vote.
+  // Exponents (log2 units) are taken against references, which are raised only when passed, then to kLazy above the largest: most strips
+  // cost one vote.  l and, for bf16, O are relative to 2^m.  e4m3's O is relative to 2^ub, so that its weights 2^(score + n - ub)
+  // lie under 2^kTop and the largest over 2^(kTop - kLazy): f16 reaches down to 2^-34 of that one.
   constexpr float kLazy = FP8 ? 5.f : 8.f;
-  constexpr float kBias = FP8 ? 10.f : 0.f;   // e4m3: P is held times 2^10, at most 2^15: f16 reaches 2^-34 of the largest
+  constexpr float kTop = 15.f;
+  constexpr float kNone = -3.402823466e38f;   // a reference that no key has raised
 
   // ---- per-unit state
   uint32_t qf[NT][C::KSTEPS][2];   // Q^T fragments in the contraction order of the K loads
   float qs[NT][2];                 // per query column: scale_log2, with the e4m3 path's power of two taken back
   float o[NT][C::MT][4];
-  float m[NT][2], l[NT][2];
-  float mb[NT][2], thr[NT][2];     // what a score's exponent is taken against, and what raises the maximum
-  int ev_ref = 0;                  // e4m3: exponent byte that O's unit stands for
+  float m[NT][2], l[NT][2], ub[NT][2];
   // The query rows of a unit on their way to registers (a warp without a key in the part needs none), and what else begins with it.
   auto load_q = [&](const Walk<kW, C::KEYS>& w) {
     const int kvh = w.u / p.subs, s0 = (w.u - kvh * p.subs) * NQ;
@@ -445,11 +453,9 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
       }
 #pragma unroll
       for (int i = 0; i < C::MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
-      m[nt][0] = m[nt][1] = thr[nt][0] = thr[nt][1] = -INFINITY;
-      mb[nt][0] = mb[nt][1] = -kBias;
+      m[nt][0] = m[nt][1] = ub[nt][0] = ub[nt][1] = kNone;
       l[nt][0] = l[nt][1] = 0.f;
     }
-    ev_ref = 0;
   };
 
   // ---- one strip: all groups' scores, their exponentials, then all groups' values
@@ -488,35 +494,17 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
       }
     // keys n and n + 8 of a group are this lane's; columns 2t, 2t + 1 of each query tile
     auto inside = [&](int key) { return whole || (key >= cur.start - cur.key && key < have); };
-    float ks[SK][2], vs[SK][2];
+    float ks[SK][2], vn[SK][2];   // e4m3: the scale of a key's row, n of its value's (byte 0 stands for a value of 0)
     if constexpr (FP8) {
-      int v[SK][2], top = 0;
 #pragma unroll
       for (int g = 0; g < SK; ++g)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const uint32_t eb = sb + g * C::GROUP + 2 * C::STRIP + n + 8 * r;
           ks[g][r] = exp_scale(lds8(eb));
-          v[g][r] = lds8(eb + 16);
-          if (!whole && !inside(16 * g + n + 8 * r)) v[g][r] = 0;
-          top = max(top, v[g][r]);
+          const uint32_t byte = lds8(eb + 16);
+          vn[g][r] = byte ? static_cast<float>(static_cast<int>(byte) - 127) : -INFINITY;
         }
-      if (__any_sync(0xffffffffu, top > ev_ref)) {
-        const int ref = max(ev_ref, static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(top))));
-        const float f = pow2i(ev_ref - ref);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < C::MT; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) o[nt][i][c] *= f;
-        ev_ref = ref;
-      }
-#pragma unroll
-      for (int g = 0; g < SK; ++g)
-#pragma unroll
-        for (int r = 0; r < 2; ++r)   // 2^(v - ev_ref), 0 below 2^-126
-          vs[g][r] = __uint_as_float(static_cast<uint32_t>(max(v[g][r] - ev_ref + 127, 0)) << 23);
     }
     float x[SK][NT][4];
     bool raise = false;
@@ -531,25 +519,31 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
           v *= FP8 ? qs[nt][c & 1] * ks[g][c >> 1] : qs[nt][c & 1];
           if (!whole && !inside(16 * g + n + 8 * (c >> 1))) v = -INFINITY;
           x[g][nt][c] = v;
-          raise |= v > thr[nt][c & 1];
+          raise |= v > m[nt][c & 1];
+          if constexpr (FP8) raise |= (v + vn[g][c >> 1]) - ub[nt][c & 1] > kTop;
         }
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float mx = -INFINITY;
+          auto largest = [&](auto value) {   // of this query's keys in the strip
+            float mx = -INFINITY;
 #pragma unroll
-          for (int g = 0; g < SK; ++g) mx = fmaxf(mx, fmaxf(x[g][nt][c], x[g][nt][c + 2]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          mx = fmaxf(mx, m[nt][c]);
-          const float f = mx == -INFINITY ? 1.f : ex2_approx(m[nt][c] - mx);
+            for (int g = 0; g < SK; ++g) mx = fmaxf(mx, fmaxf(value(g, c), value(g, c + 2)));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            return fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          };
+          const float mx = fmaxf(largest([&](int g, int e) { return x[g][nt][e]; }) + kLazy, m[nt][c]);
+          float f = ex2_approx(m[nt][c] - mx);
           m[nt][c] = mx;
-          thr[nt][c] = mx + kLazy;
-          mb[nt][c] = mx == -INFINITY ? -kBias : mx - kBias;
           l[nt][c] *= f;
+          if constexpr (FP8) {
+            const float top = fmaxf(largest([&](int g, int e) { return x[g][nt][e] + vn[g][e >> 1]; }) + (kLazy - kTop), ub[nt][c]);
+            f = ex2_approx(ub[nt][c] - top);
+            ub[nt][c] = top;
+          }
 #pragma unroll
           for (int i = 0; i < C::MT; ++i) {
             o[nt][i][c] *= f;
@@ -564,12 +558,14 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
       for (int nt = 0; nt < NT; ++nt) {
         float e[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) e[c] = ex2_approx(x[g][nt][c] - mb[nt][c & 1]);
+        for (int c = 0; c < 4; ++c) e[c] = ex2_approx(x[g][nt][c] - m[nt][c & 1]);
         l[nt][0] += e[0] + e[2];
         l[nt][1] += e[1] + e[3];
         if constexpr (FP8) {
-          pf[g][nt][0] = movmatrix(pack_f16x2(e[0] * vs[g][0], e[1] * vs[g][0]));
-          pf[g][nt][1] = movmatrix(pack_f16x2(e[2] * vs[g][1], e[3] * vs[g][1]));
+#pragma unroll
+          for (int c = 0; c < 4; ++c) e[c] = ex2_approx((x[g][nt][c] + vn[g][c >> 1]) - ub[nt][c & 1]);
+          pf[g][nt][0] = movmatrix(pack_f16x2(e[0], e[1]));
+          pf[g][nt][1] = movmatrix(pack_f16x2(e[2], e[3]));
         } else {
           const uint32_t h0 = pack_bf16x2(e[0], e[1]), h1 = pack_bf16x2(e[2], e[3]);
           pf[g][nt][0] = movmatrix(h0);
@@ -644,6 +640,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
         s += __shfl_xor_sync(0xffffffffu, s, 4);
         s += __shfl_xor_sync(0xffffffffu, s, 8);
         s += __shfl_xor_sync(0xffffffffu, s, 16);
+        m[nt][c] = m[nt][c] == kNone ? -INFINITY : m[nt][c];
         if (n == 0) join_ml[warp * NQ + nt * 8 + 2 * t + c] = make_float2(m[nt][c], s + poison);
       }
     __syncthreads();
@@ -655,7 +652,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
         float mx = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kW; ++w) mx = fmaxf(mx, join_ml[w * NQ + nt * 8 + 2 * t + c].x);
-        f[nt][c] = m[nt][c] == -INFINITY ? 0.f : ex2_approx(m[nt][c] - mx) * (FP8 ? pow2i(ev_ref - 127) : 1.f);
+        f[nt][c] = m[nt][c] == -INFINITY ? 0.f : FP8 ? ex2_wide(ub[nt][c] - mx) : ex2_approx(m[nt][c] - mx);
       }
     if (warp >= kW / 2) {
 #pragma unroll
@@ -685,7 +682,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
       sum += __shfl_xor_sync(0xffffffffu, sum, 16);
       if (lane < 8) {
         if (whole && s0 + row < p.group) {
-          const RowEnd r = row_end(p, h0 + s0 + row, mx, sum, kBias);
+          const RowEnd r = row_end(p, h0 + s0 + row, mx, sum);
           p.lse[static_cast<int64_t>(h0 + s0 + row) * p.batch + cur.b] = r.lse;
           join_ml[kW * NQ + row].x = r.inv;
         } else if (!whole) {
@@ -741,8 +738,9 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         const int row = s0 + nt * 8 + 2 * t + c, head = h0 + row;
         if (row >= p.group) continue;
-        const RowEnd r = row_end(p, head, m[nt][c], sum + poison, kBias);
-        const float f = r.inv * (FP8 ? pow2i(ev_ref - 127) : 1.f);
+        const float mx = m[nt][c] == kNone ? -INFINITY : m[nt][c];
+        const RowEnd r = row_end(p, head, mx, sum + poison);
+        const float f = FP8 && mx != -INFINITY ? r.inv * ex2_wide(ub[nt][c] - mx) : r.inv;
         __nv_bfloat16* out = p.out + (static_cast<int64_t>(cur.b) * p.hq + head) * D;
         if (n == 0) p.lse[static_cast<int64_t>(head) * p.batch + cur.b] = r.lse;
 #pragma unroll
@@ -808,7 +806,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
 // threads to a part and as many parts at once as 256 threads hold, then those by the order of their first part.  Every load
 // of a round is independent, so a unit of 152 parts takes a few memory latencies.
 template <int D, int NT>
-__global__ void __launch_bounds__(256) decode_join_kernel(DecodeParams p, float bias) {
+__global__ void __launch_bounds__(256) decode_join_kernel(DecodeParams p) {
   constexpr int NQ = 8 * NT, COLS = D / 4, LANES = 256 / COLS, UNROLL = 4;
   __shared__ float4 so[LANES][COLS];
   __shared__ float2 sm[LANES];
@@ -848,7 +846,7 @@ __global__ void __launch_bounds__(256) decode_join_kernel(DecodeParams p, float 
 #pragma unroll
   for (int i = 1; i < LANES; ++i) merge(sm[i], so[i][c]);
   const int head = (d.unit / p.subs) * p.group + row;
-  const RowEnd r = row_end(p, head, mx, sum, bias);
+  const RowEnd r = row_end(p, head, mx, sum);
   *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(d.batch) * p.hq + head) * D + 4 * c) =
       make_uint2(pack_bf16x2(v.x * r.inv, v.y * r.inv), pack_bf16x2(v.z * r.inv, v.w * r.inv));
   if (c == 0) p.lse[static_cast<int64_t>(head) * p.batch + d.batch] = r.lse;
@@ -867,7 +865,7 @@ ffa_status launch(const DecodeParams& p, int device, int sms, cudaStream_t s) {
   const int grid = std::min(sms, kMaxCtas);
   const cudaError_t e = launch_large(decode_kernel<D, FP8, NT>, dim3(grid), C::THREADS, C::SMEM, C::SMEM, s, device, raised, p);
   if (e != cudaSuccess) return FFA_ERR_CUDA;
-  return cuda_status(launch_after(decode_join_kernel<D, NT>, dim3(grid, std::min(8 * NT, p.group)), 256, s, p, FP8 ? 10.f : 0.f));
+  return cuda_status(launch_after(decode_join_kernel<D, NT>, dim3(grid, std::min(8 * NT, p.group)), 256, s, p));
 }
 
 }  // namespace

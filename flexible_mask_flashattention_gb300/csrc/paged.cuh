@@ -52,8 +52,8 @@ FFA_HD bool page_ok(const PageGeom& g, int64_t page) { return page >= 0 && page 
 // Is `slot` (page * page_size + offset) one of the cache's?
 FFA_HD bool slot_ok(const PageGeom& g, int64_t slot) { return slot >= 0 && (slot >> g.page_log2) < g.num_pages; }
 
-// The keys [start, end) of one sequence that a one-token attention reads.  A length below 0 counts as 0, a start is
-// clamped into [0, end]; a length that the page table's row cannot hold is marked bad and reads no key.
+// The keys [start, end) of one sequence that a one-token attention reads.  A start below 0 counts as 0; a range without a key is
+// [0, 0), so that nothing is loaded for it; a length that the page table's row cannot hold is marked bad and reads no key.
 struct KeyRange {
   int64_t start, end;
   bool bad;
@@ -62,8 +62,9 @@ FFA_HD KeyRange key_range(int32_t len, int32_t start, int64_t max_pages, int32_t
   KeyRange r;
   const int64_t cap = max_pages << page_log2;
   r.bad = len > cap;
-  r.end = len < 0 || r.bad ? 0 : len;
-  r.start = start < 0 ? 0 : start > r.end ? r.end : start;
+  const bool some = !r.bad && len > 0 && start < len;
+  r.end = some ? len : 0;
+  r.start = some && start > 0 ? start : 0;
   return r;
 }
 

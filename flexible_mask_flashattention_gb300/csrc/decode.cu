@@ -631,7 +631,6 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
   constexpr int kPairs = NT * C::MT * 2;
   auto end_part = [&](bool whole, int slot) {
     const int h0 = (cur.u / p.subs) * p.group, s0 = (cur.u % p.subs) * NQ;
-    const float poison = cur.bad ? __int_as_float(0x7fffffff) : 0.f;   // a length that its table row cannot hold
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -641,7 +640,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
         s += __shfl_xor_sync(0xffffffffu, s, 8);
         s += __shfl_xor_sync(0xffffffffu, s, 16);
         m[nt][c] = m[nt][c] == kNone ? -INFINITY : m[nt][c];
-        if (n == 0) join_ml[warp * NQ + nt * 8 + 2 * t + c] = make_float2(m[nt][c], s + poison);
+        if (n == 0) join_ml[warp * NQ + nt * 8 + 2 * t + c] = make_float2(m[nt][c], s);
       }
     __syncthreads();
     float f[NT][2];
@@ -724,10 +723,10 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
     }
   };
 
-  // A unit that was this warp's alone: its rows.
+  // A unit that was this warp's alone: its rows.  A sequence with a length that its table row cannot hold reads no key and ends here too.
   auto end_alone = [&]() {
     const int h0 = (cur.u / p.subs) * p.group, s0 = (cur.u % p.subs) * NQ;
-    const float poison = cur.bad ? __int_as_float(0x7fffffff) : 0.f;
+    const float poison = cur.bad ? __int_as_float(0x7fffffff) : 0.f;   // makes its rows NaN
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

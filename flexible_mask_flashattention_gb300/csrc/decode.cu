@@ -3,8 +3,10 @@
 // For sequence b, q head h (kv head h / (hq / hkv)) and the keys j in [start_b, len_b):
 //   s_j = scale q . k_j,  lse = ln(sum_j e^{s_j} [+ e^{sink_h}]),  out = sum_j e^{s_j - lse} v_j.
 //
-// Bound by HBM: every stored key and value is read once, 4 hq / hkv FLOPs a byte (e4m3) or half that (bf16), far under what the tensor cores need
-// to be busy.  So the design is about keeping loads in flight:
+// Bound by HBM for groups (hq / hkv) of up to 8: every stored key and value is read once, 4 hq / hkv FLOPs a byte (e4m3) or half that (bf16),
+// far under what the tensor cores need to be busy.  Groups above 8 take two query tiles a warp, whose MMAs and
+// registers bound them, and groups above 16 walk over the cache once for every 16 of their heads.  The design is about keeping
+// loads in flight:
 //   - The batch's keys are counted in blocks of a strip (16 or 32 keys) a warp; all (sequence, kv head) units' blocks form
 //     one list, dealt to the CTAs, one an SM, in equal contiguous shares (paged.cuh: share_begin).  Ragged lengths and few
 //     long sequences balance the same way, and no length has to be known on the host.

@@ -896,7 +896,7 @@ ffa_status ffa_fwd_decode(const void* q, int64_t q_stride, const ffa_kv_cache* c
   if (batch == 0) return FFA_OK;
   const int32_t d = cache->d;
   if (!q || !out || !lse || !kv_lens || !workspace) return FFA_ERR_INVALID_ARG;
-  if (!kv_aligned16(q) || !kv_aligned16(out) || !kv_aligned16(lse) || !kv_aligned16(workspace)) return FFA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || !aligned16(workspace)) return FFA_ERR_INVALID_ARG;
   if (max_pages > 0 && !page_table) return FFA_ERR_INVALID_ARG;
   for (const void* a : {static_cast<const void*>(page_table), static_cast<const void*>(kv_lens),
                         static_cast<const void*>(kv_starts), static_cast<const void*>(sink)})

@@ -219,8 +219,8 @@ ffa_status check_cache(const ffa_kv_cache* c, PageGeom& g) {
   if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1))) return FFA_ERR_UNSUPPORTED;
   // page numbers are int32; a page's rows, and their bytes, fit 32 bits in the kernels' index arithmetic
   if (c->num_pages > (int64_t{1} << 31) || static_cast<int64_t>(c->hkv) * c->page_size > (1 << 22)) return FFA_ERR_OVERFLOW;
-  if (!c->k || !c->v || !kv_aligned16(c->k) || !kv_aligned16(c->v)) return FFA_ERR_INVALID_ARG;
-  if (c->dtype == FFA_KV_E4M3 && (!c->k_exp || !c->v_exp || !kv_aligned16(c->k_exp) || !kv_aligned16(c->v_exp)))
+  if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return FFA_ERR_INVALID_ARG;
+  if (c->dtype == FFA_KV_E4M3 && (!c->k_exp || !c->v_exp || !aligned16(c->k_exp) || !aligned16(c->v_exp)))
     return FFA_ERR_INVALID_ARG;
   g.num_pages = c->num_pages;
   g.hkv = c->hkv;
@@ -242,7 +242,7 @@ ffa_status ffa_kv_cache_write(const void* k, int64_t k_stride, const void* v, in
   if (st != FFA_OK) return st;
   if (tokens < 0) return FFA_ERR_INVALID_ARG;
   if (tokens == 0) return FFA_OK;
-  if (!k || !v || !slots || !kv_aligned16(k) || !kv_aligned16(v) || (reinterpret_cast<uintptr_t>(slots) & 7u))
+  if (!k || !v || !slots || !aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(slots) & 7u))
     return FFA_ERR_INVALID_ARG;
   const int64_t row = static_cast<int64_t>(cache->hkv) * cache->d;
   if (k_stride % 8 != 0 || v_stride % 8 != 0 || (tokens > 1 && (k_stride < row || v_stride < row)))
@@ -287,7 +287,7 @@ ffa_status ffa_kv_cache_read(const ffa_kv_cache* cache, const int32_t* page_tabl
   if (total == 0 || batch == 0) return FFA_OK;
   if (!cu_seqlens || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u)) return FFA_ERR_INVALID_ARG;
   if (max_pages > 0 && (!page_table || (reinterpret_cast<uintptr_t>(page_table) & 3u))) return FFA_ERR_INVALID_ARG;
-  if (!k || !v || !kv_aligned16(k) || !kv_aligned16(v)) return FFA_ERR_INVALID_ARG;
+  if (!k || !v || !aligned16(k) || !aligned16(v)) return FFA_ERR_INVALID_ARG;
   if (total > 0x7fffffff) return FFA_ERR_OVERFLOW;   // cu_seqlens is int32
   const CacheSpans at(*cache);
   Span in[6] = {{page_table, 4 * (static_cast<int64_t>(batch - 1) * table_stride + max_pages)}, {cu_seqlens, 4 * (int64_t{batch} + 1)}};

@@ -9,8 +9,6 @@
 
 namespace ffa {
 
-inline bool kv_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // Host check of a cache description; fills its geometry.
 ffa_status check_cache(const ffa_kv_cache* c, PageGeom& g);
 

@@ -1,5 +1,5 @@
-// Host helpers of calls that launch small kernels many times a second: what a device is asked for once, launches, and the check
-// that outputs overlap nothing.
+// Host helpers of calls that launch small kernels many times a second: what a device is asked for once, launches, and the checks
+// of alignment and that outputs overlap nothing.
 #pragma once
 
 #include <atomic>
@@ -53,6 +53,8 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned block, cudaSt
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Do the byte ranges [a, a + na) and [b, b + nb) meet?
 inline bool meet(const void* a, int64_t na, const void* b, int64_t nb) {

@@ -161,7 +161,7 @@ __device__ __forceinline__ void in_batches(int n, F& f) {
   if (i < n) f(std::integral_constant<int, 1>{}, i);
 }
 
-// Where a warp stands in its units: unit `c` of the D / 4 lanes' tokens; this lane's token (behind the last one: has = false) and its
+// Where a warp stands in its units: unit `c` of its 256 / D tokens' units; this lane's token (behind the last one: has = false) and its
 // position.
 template <int D>
 struct UnitWalk {
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NormRopeParams 
 #pragma unroll
         for (int n = 0; n < N; ++n) {
           const uint4 v = cols.load(in + (k + n) * 512, swap), gv = cols.load(in_g + (k + n) * 512, swap);
-            float2 d[4], ss = make_float2(0.f, 0.f), hx = make_float2(0.f, 0.f);
+          float2 d[4], ss = make_float2(0.f, 0.f), hx = make_float2(0.f, 0.f);
           unpack8(v, f[n]);
           unpack8(gv, d);
 #pragma unroll
@@ -462,8 +462,6 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* partial
     (col < D ? dqw : dkw)[col % D] = s;
   }
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // The checks both directions share; fills what they have in common.
 ffa_status check_common(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int64_t tokens, int32_t hq,

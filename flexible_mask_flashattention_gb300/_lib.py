@@ -482,18 +482,47 @@ def bwd(q, k, v, out, lse, dout, plan: Plan, scale: float, dq=None, dk=None, dv=
 _I32_MAX = 0x7fffffff
 torch = None        # imported by the first of these calls, once
 _new = None         # (size, strides, dtype) -> a new tensor on the current device
+_raw_stream = None  # device -> handle of its current stream
+
+
+def _new_plain(size, strides, dtype):
+    return torch.empty_strided(size, strides, dtype=dtype, device="cuda")
+
+
+def _raw_stream_plain(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _gives_tensors(make, device_type: str) -> bool:
+    """Does make(size, strides, dtype) give the tensor that torch.empty_strided gives on such a device?"""
+    import torch
+    try:
+        t = make((2, 3), (3, 1), torch.bfloat16)
+        return (t.shape, t.stride(), t.dtype, t.device.type) == ((2, 3), (3, 1), torch.bfloat16, device_type)
+    except Exception:   # whatever a call of another signature, or none, answers with
+        return False
+
+
+def _gives_streams(get) -> bool:
+    """Does get(device) give the current stream's handle?"""
+    import torch
+    try:
+        device = torch.cuda.current_device()
+        return get(device) == torch.cuda.current_stream(device).cuda_stream
+    except Exception:
+        return False
 
 
 def _start():
-    """Import torch, and find its quickest way to a new CUDA tensor: the one its compiled programs allocate with, which takes a third of
-    torch.empty's time between launches, where this torch has it."""
-    global torch, _new
+    """Import torch, and find its quickest ways to a new CUDA tensor (the call its compiled programs allocate with, a third of torch.empty's
+    time between launches) and to the current stream's handle.  Neither is public, so each is taken only if it answers as the public
+    call does."""
+    global torch, _new, _raw_stream
     import torch
-    try:
-        _new = torch._C._dynamo.guards._empty_strided_cuda
-    except AttributeError:
-        def _new(size, strides, dtype):
-            return torch.empty_strided(size, strides, dtype=dtype, device="cuda")
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _raw_stream = get if _gives_streams(get) else _raw_stream_plain
+    quick = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+    _new = quick if _gives_tensors(quick, "cuda") else _new_plain
 
 
 def _on(stream, device: int, *tensors):
@@ -501,7 +530,7 @@ def _on(stream, device: int, *tensors):
     None for the current stream, on which they are anyway.  On another stream the call's own tensors (None: absent) are marked
     as used there, so that the allocator does not give their memory away before the work is done."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device), None
+        return _raw_stream(device), None
     if not isinstance(stream, torch.cuda.Stream):
         handle = int(_stream_handle(stream))
         stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
@@ -515,10 +544,11 @@ def _empty(context, size, dtype):
     """A new tensor of 1 to 3 dimensions for use on the stream of `context`."""
     n = len(size)
     strides = (size[1] * size[2], size[2], 1) if n == 3 else (size[1], 1) if n == 2 else (1,)
+    new = _new_plain if torch.are_deterministic_algorithms_enabled() else _new   # torch.empty fills its tensors then
     if context is None:
-        return _new(size, strides, dtype)
+        return new(size, strides, dtype)
     with context:
-        return _new(size, strides, dtype)
+        return new(size, strides, dtype)
 
 
 def _device(t, name) -> int:

@@ -91,3 +91,20 @@ def test_steps_against_the_causal_forward_by_what_each_row_weighs(ffa, fp8):
         assert (np.abs(a - b) <= tol).all(), (i, (np.abs(a - b) / tol).max())
         tol = 2 * ((d + 16) * 2.0 ** -24 * size + 2.0 ** -20 + 4 * 2.0 ** -24 * np.abs(rl))
         assert (np.abs(f64(l)[:, 0] - f64(lse)[:, i]) <= tol).all()
+
+
+def test_new_tensors_are_filled_in_deterministic_mode(ffa):
+    """torch fills what it allocates in this mode; so are the rows of a read behind the last sequence, which nothing writes."""
+    import torch
+    kc, vc, _, _ = new_cache(2, 2, 16, 64, False)
+    args = kc, vc, torch.zeros(1, 1, dtype=torch.int32).cuda(), torch.tensor([0, 3], dtype=torch.int32).cuda()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        torch.full((400, 2, 64), 5.0, dtype=torch.bfloat16, device="cuda")   # memory that the next tensors may get
+    torch.use_deterministic_algorithms(True)
+    try:
+        k, v = ffa.kv_cache_read(*args, 400)
+    finally:
+        torch.use_deterministic_algorithms(False)
+    for x in (k, v):
+        assert (x[:3] == 0).all() and x[3:].isnan().all()

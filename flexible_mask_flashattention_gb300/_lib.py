@@ -669,7 +669,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6
         _check_dense(k_out, bf16, kshape, dev, "k_out")
     _check(load_library().ffa_qk_norm_rope(
         q.data_ptr(), qs, k.data_ptr(), ks, tokens, hq, hkv, d, q_weight.data_ptr(), k_weight.data_ptr(), eps,
-        cos_sin.data_ptr(), max_pos, rot, interleaved, positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
+        cos_sin.data_ptr(), max_pos, rot, bool(interleaved), positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
         handle), "ffa_qk_norm_rope")
     return q_out, k_out
 
@@ -691,7 +691,7 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk_ou
         _check_workspace(workspace, dev)
     _check(load_library().ffa_qk_norm_rope_bwd(
         q.data_ptr(), qs, k.data_ptr(), ks, tokens, hq, hkv, d, q_weight.data_ptr(), k_weight.data_ptr(), eps,
-        cos_sin.data_ptr(), max_pos, rot, interleaved, positions.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(),
+        cos_sin.data_ptr(), max_pos, rot, bool(interleaved), positions.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(),
         dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), workspace.data_ptr(), workspace.numel(), handle),
         "ffa_qk_norm_rope_bwd")
     return dq, dk, dqw, dkw

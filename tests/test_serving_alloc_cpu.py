@@ -61,3 +61,34 @@ def test_deterministic_mode_allocates_with_torchs_own_call(monkeypatch):
         assert _lib._empty(None, (2, 3, 4), torch.float32) == "plain"
     finally:
         torch.use_deterministic_algorithms(was)
+
+
+def test_interleaved_may_be_any_truth_value(monkeypatch):
+    import ctypes
+    import numpy as np
+    import torch
+    from flexible_mask_flashattention_gb300 import _lib
+    got = []
+
+    class Library:
+        def ffa_qk_norm_rope(self, *args):
+            got.append(ctypes.c_int32(args[14]).value)
+            return 0
+
+        def ffa_qk_norm_rope_bwd(self, *args):
+            got.append(ctypes.c_int32(args[14]).value)
+            return 0
+
+        def ffa_qk_norm_rope_bwd_workspace_size(self, d):
+            return 16
+
+    monkeypatch.setattr(_lib, "torch", torch)
+    monkeypatch.setattr(_lib, "load_library", Library)
+    monkeypatch.setattr(_lib, "_device", lambda t, name: -1)
+    monkeypatch.setattr(_lib, "_on", lambda *a: (0, None))
+    monkeypatch.setattr(_lib, "_empty", lambda context, size, dtype: torch.empty(size, dtype=dtype))
+    x, w, t, pos = torch.zeros(2, 2, 64, dtype=torch.bfloat16), torch.zeros(64), torch.zeros(4, 64), torch.zeros(2, dtype=torch.int32)
+    for value in (True, np.bool_(True), torch.tensor(True), 2):
+        _lib.qk_norm_rope(x, x, w, w, t, pos, interleaved=value)
+        _lib.qk_norm_rope_bwd(x, x, w, w, t, pos, x, x, interleaved=value)
+    assert got == [1] * 8

@@ -703,7 +703,7 @@ def qk_norm_rope_bwd_workspace_size(d: int) -> int:
 
 def kv_cache_write(k, v, k_cache, v_cache, slots, k_exp=None, v_exp=None, stream=None):
     """Write the rows of k, v [T, Hkv, d] into the cache [pages, Hkv, page_size, d] at slots (int64 [T]: page *
-    page_size + offset; negative or outside: not written).  A float8_e4m3fn cache holds codes and, in k_exp / v_exp
+    page_size + offset, all different; negative or outside: not written).  A float8_e4m3fn cache holds codes and, in k_exp / v_exp
     [pages, Hkv, page_size] uint8, each row's exponent: value = code * 2^(byte - 127)."""
     dev = _device(k_cache, "k_cache")
     cache = _kv_cache(k_cache, v_cache, k_exp, v_exp, dev)

@@ -466,8 +466,9 @@ typedef struct {
  *         ffa_qk_norm_rope; 16-byte aligned, not overlapping the cache
  *  slots  int64 device array [tokens]: page * page_size + offset.  A token
  *         whose slot is negative (padding) or outside the cache is not written.
- *         Slots of one call must differ: of two tokens with one slot, each 16
- *         bytes of the slot's rows may be either's.
+ *         Slots of one call must differ: a slot that two tokens have is left
+ *         undefined (FFA_KV_E4M3: with codes of either and the other's scale),
+ *         all others are not affected.
  * Errors: FFA_ERR_INVALID_ARG, FFA_ERR_UNSUPPORTED, FFA_ERR_OVERFLOW,
  * FFA_ERR_CUDA.
  */

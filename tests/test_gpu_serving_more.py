@@ -108,3 +108,21 @@ def test_new_tensors_are_filled_in_deterministic_mode(ffa):
         torch.use_deterministic_algorithms(False)
     for x in (k, v):
         assert (x[:3] == 0).all() and x[3:].isnan().all()
+
+
+@pytest.mark.parametrize("hkv", [2, 8])
+def test_a_slot_given_twice_leaves_the_others_as_they_should_be(ffa, hkv):
+    import torch
+    d, page, n = 128, 16, 60
+    g = torch.Generator().manual_seed(hkv)
+    x = torch.randn(n, hkv, d, generator=g).bfloat16().cuda()
+    slots = torch.randperm(5 * page, generator=g)[:n].cuda()
+    one, two = new_cache(5, hkv, page, d, True), new_cache(5, hkv, page, d, True)
+    ffa.kv_cache_write(x, x, one[0], one[1], slots, one[2], one[3])
+    again = torch.cat([slots, slots[:3], slots[:3]])
+    ffa.kv_cache_write(torch.cat([x, 3 * x[7:10], -x[20:23]]), torch.cat([x, x[:6]]), two[0], two[1], again, two[2], two[3])
+    twice = np.zeros((5, page), bool)
+    twice[(slots[:3] // page).cpu().numpy(), (slots[:3] % page).cpu().numpy()] = True
+    for a, b in zip(one, two):
+        a, b = (bits(t).reshape(5, hkv, page, -1).transpose(0, 2, 1, 3) for t in (a, b))
+        assert np.array_equal(a[~twice], b[~twice])

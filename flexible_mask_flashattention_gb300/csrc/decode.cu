@@ -4,9 +4,9 @@
 //   s_j = scale q . k_j,  lse = ln(sum_j e^{s_j} [+ e^{sink_h}]),  out = sum_j e^{s_j - lse} v_j.
 //
 // Bound by HBM for groups (hq / hkv) of up to 8: every stored key and value is read once, 4 hq / hkv FLOPs a byte (e4m3) or half that (bf16),
-// far under what the tensor cores need to be busy.  Groups above 8 take two query tiles a warp, whose MMAs and
-// registers bound them, and groups above 16 walk over the cache once for every 16 of their heads.  The design is about keeping
-// loads in flight:
+// far under what the tensor cores need to be busy.  Groups above 8 take two query tiles a warp, whose registers leave two warps a
+// scheduler, and a strip's chain of dependent instructions bounds them (no pipe is above 45 %); groups above 16 walk over the
+// cache once for every 16 of their heads.  The design is about keeping loads in flight:
 //   - The batch's keys are counted in blocks of a strip (16 or 32 keys) a warp; all (sequence, kv head) units' blocks form
 //     one list, dealt to the CTAs, one an SM, in equal contiguous shares (paged.cuh: share_begin).  Ragged lengths and few
 //     long sequences balance the same way, and no length has to be known on the host.
@@ -25,14 +25,18 @@
 // mantissa fits; values below 2^-31 of the row's largest round); the scale of a key's row multiplies its score.  The scale 2^n of a
 // value's row goes into its weight, as e^{s_j} 2^{n_j} = 2^{s_j log2(e) + n_j}, which each query has a running reference of its own for: what
 // an f16 weight (11 bits) is relative to is the largest that has counted for this query, not the largest row there is.  Weights
-// from 2^-24 of that on are rounded to 2^-11 of themselves, smaller ones by at most 2^-35 of it.  Scores, maxima, sums and the
-// output accumulate in fp32.
+// from 2^-24 of that on are rounded to 2^-11 of themselves, smaller ones by at most 2^-35 of it.  11 bits are enough here: the output's error
+// against 64 bits is 1.673e-3 of its norm, and 1.661e-3 with a pair of f16 values, which the output's own rounding makes; the
+// pair costs nothing at 64 x 16K keys, but 3 % at 32 x 1K, 4 to 5 % at d = 64 and 4 to 12 % in groups above 8.  Scores, maxima,
+// sums and the output accumulate in fp32.
 //
 // Split parts go to the workspace as (m, l, O) and a second kernel joins them in a fixed order.
 //
 // Measured on the device (of the 6795 GB/s that a copy reaches; the range is that of several GPUs): 1M keys, 16 + 4 heads, d = 128, e4m3:
 // 164 to 168 us (95 to 97 %); 64 x 16K keys, 64 + 8 heads, e4m3: 219 to 223 us (93 to 94 %); 24 x 8K keys with a window of 4096, 32
-// heads, d = 64, bf16: 115 to 119 us (89 to 92 %), 113 with the products left out; 32 x 1K keys: 12 us; 777 keys, bf16: 6.6 us.
+// heads, d = 64, bf16: 115 to 119 us (89 to 92 %), 113 with the products left out; 777 keys, bf16: 6.6 us.  Far from HBM's bound: groups of 16
+// (380K keys, e4m3: 41.5 us, 70 %; 32 x 4K keys, d = 64, bf16: 18.6 us, 35 %), 48 heads over one kv head (1M keys, e4m3: 128 us,
+// 31 %), and short sequences (32 x 1K keys, e4m3: 11.8 us, 26 %).
 #include <cuda_bf16.h>
 
 #include <algorithm>

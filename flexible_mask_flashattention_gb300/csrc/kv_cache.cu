@@ -10,8 +10,9 @@
 //
 // Both kernels are bound by HBM: 2 d bytes a row on the tensors' side, 2 d or d + 1 on the cache's.  A grid's second
 // dimension is k or v; a warp holds 2 or 4 consecutive rows at once (a pass), whatever tokens and heads they are of, 8 values a
-// lane, and starts the loads of kUnroll passes before it uses the first (168K tokens of 8 heads, d = 128, e4m3, written: 147 us so, 194
-// us with 8 passes, 167 us with 2).  Measured: written 153 us, read 157 us, 101 and 97 % of a copy's 6795 GB/s.
+// lane, and starts the loads of kUnroll passes before it uses the first (168K tokens of 8 heads, d = 128, e4m3, written, all on one GPU: 147
+// us so, 194 us with 8 passes, 167 us with 2).  Measured on another GPU, the same tokens: e4m3 written in 153 us and read in 157 us,
+// 101 and 97 % of a copy's 6795 GB/s; bf16 in 199 and 203 us, 102 and 100 %.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -53,7 +54,7 @@ __device__ __forceinline__ uint32_t e4m3x2(float2 f) {
 }
 
 // FILLED: a token's rows fill the passes of a whole number of warps (hkv a multiple of kUnroll * RW), so that token and page are the
-// warp's and addresses a step apart.  Measured (168K tokens of 8 heads, d = 128, e4m3): 147 us, and 172 us without; with
+// warp's and addresses a step apart.  Measured (168K tokens of 8 heads, d = 128, e4m3, on the first GPU above): 147 us, and 172 us without; with
 // 3 heads of d = 64, which leave most of such a warp empty, 21.6 us for 30K tokens, and 11.8 us without.
 template <int D, bool FP8, bool FILLED>
 __global__ void __launch_bounds__(kThreads) kv_cache_write_kernel(WriteParams p) {

@@ -528,7 +528,7 @@ size_t ffa_fwd_decode_workspace_size(int32_t hq, int32_t hkv, int32_t d);
  * Scores, maxima and sums are fp32 (scale * log2(e) must be finite in it); results do not depend on timing, but
  * where a sequence is split depends on the batch's lengths.  A weight e^(s_j - lse) enters the products as a pair of bf16 values
  * (FFA_KV_BF16), or times its value row's scale as one f16 value (FFA_KV_E4M3): 2^-11 of itself, or 2^-35 of the largest that
- * its query has met, whichever is more.
+ * its query has met, whichever is more.  Over an FFA_KV_E4M3 cache, values of q below 2^-31 of their row's largest are rounded.
  * Errors: FFA_ERR_INVALID_ARG, FFA_ERR_UNSUPPORTED, FFA_ERR_OVERFLOW,
  * FFA_ERR_CUDA.
  */

@@ -23,8 +23,8 @@
 // Types.  bf16 cache: bf16 MMAs; P goes in as a bf16 value plus the bf16 value of its remainder, so that its rounding
 // does not add to the output's.  e4m3 cache: codes are exact in f16; q is scaled by a power of two a row to f16's top range (its bf16
 // mantissa fits; values below 2^-31 of the row's largest round); the scale of a key's row multiplies its score.  The scale 2^n of a
-// value's row goes into its weight, as e^{s_j} 2^{n_j} = 2^{s_j log2(e) + n_j}, which each query has a running reference of its own for: what
-// an f16 weight (11 bits) is relative to is the largest that has counted for this query, not the largest row there is.  Weights
+// value's row goes into its weight, as e^{s_j} 2^{n_j}, which each query has a running reference of its own for: what an f16 weight
+// (11 bits) is relative to is the largest that has counted for this query, not the largest row there is.  Weights
 // from 2^-24 of that on are rounded to 2^-11 of themselves, smaller ones by at most 2^-35 of it.  11 bits are enough here: the output's error
 // against 64 bits is 1.673e-3 of its norm, and 1.661e-3 with a pair of f16 values, which the output's own rounding makes; the
 // pair costs nothing at 64 x 16K keys, but 3 % at 32 x 1K, 4 to 5 % at d = 64 and 4 to 12 % in groups above 8.  Scores, maxima,
@@ -154,6 +154,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ float2 ex2(float2 v) { return make_float2(ex2_approx(v.x), ex2_approx(v.y)); }
 __device__ __forceinline__ float pow2i(int e) {   // 2^e, 0 below the normal range; e <= 127
   return e < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
@@ -401,8 +402,9 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
   }
 
   // Exponents (log2 units) are taken against references, which are raised only when passed, then to kLazy above the largest: most strips
-  // cost one vote.  l and, for bf16, O are relative to 2^m.  e4m3's O is relative to 2^ub, so that its weights 2^(score + n - ub)
-  // lie under 2^kTop and the largest over 2^(kTop - kLazy): f16 reaches down to 2^-34 of that one.
+  // cost one vote.  l and, for bf16, O are relative to 2^m.  e4m3's O is relative to 2^(m + vr), so that its weights
+  // 2^((score - m) + (n - vr)) lie under 2^kTop and the largest over 2^(kTop - kLazy): f16 reaches down to 2^-34 of that one.  vr is
+  // counted from m so that a score's own rounding, in the first bracket, is the same in a weight and in l.
   constexpr float kLazy = FP8 ? 5.f : 8.f;
   constexpr float kTop = 15.f;
   constexpr float kNone = -3.402823466e38f;   // a reference that no key has raised
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
   uint32_t qf[NT][C::KSTEPS][2];   // Q^T fragments in the contraction order of the K loads
   float qs[NT][2];                 // per query column: scale_log2, with the e4m3 path's power of two taken back
   float o[NT][C::MT][4];
-  float m[NT][2], l[NT][2], ub[NT][2];
+  float m[NT][2], l[NT][2], vr[NT][2];
   // The query rows of a unit on their way to registers (a warp without a key in the part needs none), and what else begins with it.
   auto load_q = [&](const Walk<kW, C::KEYS>& w) {
     const int kvh = w.u / p.subs, s0 = (w.u - kvh * p.subs) * NQ;
@@ -459,8 +461,8 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
       }
 #pragma unroll
       for (int i = 0; i < C::MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
-      m[nt][0] = m[nt][1] = ub[nt][0] = ub[nt][1] = kNone;
-      l[nt][0] = l[nt][1] = 0.f;
+      m[nt][0] = m[nt][1] = kNone;
+      l[nt][0] = l[nt][1] = vr[nt][0] = vr[nt][1] = 0.f;
     }
   };
 
@@ -512,43 +514,54 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
           vn[g][r] = byte ? static_cast<float>(static_cast<int>(byte) - 127) : -INFINITY;
         }
     }
-    float x[SK][NT][4];
+    // scores of a key (n, n + 8 of a group) and the two queries, two an instruction; exponents of the weights: of l (and bf16's O), of e4m3's O
+    float2 x[SK][NT][2];
+    auto less_m = [&](int g, int nt, int r) { return add2(x[g][nt][r], make_float2(-m[nt][0], -m[nt][1])); };
+    auto less_vr = [&](int g, int nt, int r) {
+      return add2(less_m(g, nt, r), add2(make_float2(vn[g][r], vn[g][r]), make_float2(-vr[nt][0], -vr[nt][1])));
+    };
     bool raise = false;
 #pragma unroll
     for (int g = 0; g < SK; ++g)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v = s[g][nt][0][c];
-          if constexpr (CH == 2) v += s[g][nt][1][c];
-          v *= FP8 ? qs[nt][c & 1] * ks[g][c >> 1] : qs[nt][c & 1];
-          if (!whole && !inside(16 * g + n + 8 * (c >> 1))) v = -INFINITY;
-          x[g][nt][c] = v;
-          raise |= v > m[nt][c & 1];
-          if constexpr (FP8) raise |= (v + vn[g][c >> 1]) - ub[nt][c & 1] > kTop;
+        for (int r = 0; r < 2; ++r) {
+          const float2 q2 = make_float2(qs[nt][0], qs[nt][1]);
+          float2 v = make_float2(s[g][nt][0][2 * r], s[g][nt][0][2 * r + 1]);
+          if constexpr (CH == 2) v = add2(v, make_float2(s[g][nt][1][2 * r], s[g][nt][1][2 * r + 1]));
+          v = mul2(v, FP8 ? mul2(q2, make_float2(ks[g][r], ks[g][r])) : q2);
+          if (!whole && !inside(16 * g + n + 8 * r)) v = make_float2(-INFINITY, -INFINITY);
+          x[g][nt][r] = v;
+          raise |= v.x > m[nt][0] || v.y > m[nt][1];
+          if constexpr (FP8) {
+            const float2 y = less_vr(g, nt, r);
+            raise |= y.x > kTop || y.y > kTop;
+          }
         }
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
+          auto score = [&](int g, int r) { return c ? x[g][nt][r].y : x[g][nt][r].x; };
           auto largest = [&](auto value) {   // of this query's keys in the strip
             float mx = -INFINITY;
 #pragma unroll
-            for (int g = 0; g < SK; ++g) mx = fmaxf(mx, fmaxf(value(g, c), value(g, c + 2)));
+            for (int g = 0; g < SK; ++g) mx = fmaxf(mx, fmaxf(value(g, 0), value(g, 1)));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             return fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
           };
-          const float mx = fmaxf(largest([&](int g, int e) { return x[g][nt][e]; }) + kLazy, m[nt][c]);
-          float f = ex2_approx(m[nt][c] - mx);
+          const float mx = fmaxf(largest(score) + kLazy, m[nt][c]);
+          const float up = m[nt][c] - mx;
+          float f = ex2_approx(up);
           m[nt][c] = mx;
           l[nt][c] *= f;
           if constexpr (FP8) {
-            const float top = fmaxf(largest([&](int g, int e) { return x[g][nt][e] + vn[g][e >> 1]; }) + (kLazy - kTop), ub[nt][c]);
-            f = ex2_approx(ub[nt][c] - top);
-            ub[nt][c] = top;
+            const float top = fmaxf(largest([&](int g, int r) { return (score(g, r) - mx) + vn[g][r]; }) + (kLazy - kTop), vr[nt][c] + up);
+            f = ex2_approx(up + (vr[nt][c] - top));
+            vr[nt][c] = top;
           }
 #pragma unroll
           for (int i = 0; i < C::MT; ++i) {
@@ -562,22 +575,19 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
     for (int g = 0; g < SK; ++g)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float e[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) e[c] = ex2_approx(x[g][nt][c] - m[nt][c & 1]);
-        l[nt][0] += e[0] + e[2];
-        l[nt][1] += e[1] + e[3];
+        float2 e0 = ex2(less_m(g, nt, 0)), e1 = ex2(less_m(g, nt, 1));
+        const float2 sum = add2(make_float2(l[nt][0], l[nt][1]), add2(e0, e1));
+        l[nt][0] = sum.x, l[nt][1] = sum.y;
         if constexpr (FP8) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) e[c] = ex2_approx((x[g][nt][c] + vn[g][c >> 1]) - ub[nt][c & 1]);
-          pf[g][nt][0] = movmatrix(pack_f16x2(e[0], e[1]));
-          pf[g][nt][1] = movmatrix(pack_f16x2(e[2], e[3]));
+          e0 = ex2(less_vr(g, nt, 0)), e1 = ex2(less_vr(g, nt, 1));
+          pf[g][nt][0] = movmatrix(pack_f16x2(e0.x, e0.y));
+          pf[g][nt][1] = movmatrix(pack_f16x2(e1.x, e1.y));
         } else {
-          const uint32_t h0 = pack_bf16x2(e[0], e[1]), h1 = pack_bf16x2(e[2], e[3]);
+          const uint32_t h0 = pack_bf16x2(e0.x, e0.y), h1 = pack_bf16x2(e1.x, e1.y);
           pf[g][nt][0] = movmatrix(h0);
           pf[g][nt][1] = movmatrix(h1);
-          pl[g][nt][0] = movmatrix(pack_bf16x2(e[0] - __uint_as_float(h0 << 16), e[1] - __uint_as_float(h0 & 0xffff0000u)));
-          pl[g][nt][1] = movmatrix(pack_bf16x2(e[2] - __uint_as_float(h1 << 16), e[3] - __uint_as_float(h1 & 0xffff0000u)));
+          pl[g][nt][0] = movmatrix(pack_bf16x2(e0.x - __uint_as_float(h0 << 16), e0.y - __uint_as_float(h0 & 0xffff0000u)));
+          pl[g][nt][1] = movmatrix(pack_bf16x2(e1.x - __uint_as_float(h1 << 16), e1.y - __uint_as_float(h1 & 0xffff0000u)));
         }
       }
     // out^T += V^T P^T: this lane's four keys 2t, 2t + 1, 2t + 8, 2t + 9 of each group, and its columns
@@ -657,7 +667,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
         float mx = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kW; ++w) mx = fmaxf(mx, join_ml[w * NQ + nt * 8 + 2 * t + c].x);
-        f[nt][c] = m[nt][c] == -INFINITY ? 0.f : FP8 ? ex2_wide(ub[nt][c] - mx) : ex2_approx(m[nt][c] - mx);
+        f[nt][c] = m[nt][c] == -INFINITY ? 0.f : FP8 ? ex2_wide(m[nt][c] - mx + vr[nt][c]) : ex2_approx(m[nt][c] - mx);
       }
     if (warp >= kW / 2) {
 #pragma unroll
@@ -745,7 +755,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
         if (row >= p.group) continue;
         const float mx = m[nt][c] == kNone ? -INFINITY : m[nt][c];
         const RowEnd r = row_end(p, head, mx, sum + poison);
-        const float f = FP8 && mx != -INFINITY ? r.inv * ex2_wide(ub[nt][c] - mx) : r.inv;
+        const float f = FP8 && mx != -INFINITY ? r.inv * ex2_wide(vr[nt][c]) : r.inv;
         __nv_bfloat16* out = p.out + (static_cast<int64_t>(cur.b) * p.hq + head) * D;
         if (n == 0) p.lse[static_cast<int64_t>(head) * p.batch + cur.b] = r.lse;
 #pragma unroll

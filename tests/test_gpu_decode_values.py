@@ -83,3 +83,27 @@ def test_values_at_both_ends_of_the_range(ffa):
     p["v_exp"][:] = 0
     out, lse = ffa.fwd_decode(**p, scale=0.1)
     assert (out == 0).all() and lse.isfinite().all()
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("power", [4, 10, 14, 17, 20, 23])
+def test_one_key_with_a_large_score(ffa, power, sign):
+    """A row of one key is its value, whatever its score: the scores lie next to a power of two (in log2 units), where the value's
+    exponent, added to them, changes their rounding.  f16 weight and its exponent's additions, bf16 output."""
+    import torch
+    d, n = 64, 64
+    g = torch.Generator().manual_seed(power)
+    k, q = torch.zeros(n * 16, 1, d), torch.zeros(n, 3, d)
+    k[:, 0, 0], q[:, :, 0] = 1.0, 1.0
+    v = torch.randn(n * 16, 1, d, generator=g) * 2.0 ** torch.linspace(-70, 70, n).repeat_interleave(16)[:, None, None]
+    kc, vc, ke, ve = new_cache(n, 1, 16, d, True)
+    ffa_write(k.bfloat16().cuda(), v.bfloat16().cuda(), kc, vc, ke, ve)
+    p = dict(q=q.bfloat16().cuda(), k_cache=kc, v_cache=vc, page_table=torch.arange(n, dtype=torch.int32).cuda()[:, None],
+             kv_lens=torch.ones(n, dtype=torch.int32).cuda(), k_exp=ke, v_exp=ve)
+    for off in (-40.3, -3.7, 0.4, 33.9):
+        score = sign * (2.0 ** power + off)
+        out, lse = ffa.fwd_decode(**p, scale=score * float(np.log(2.0)))
+        want = cache_values(p)[1][:, :, 0]
+        assert (np.abs(f64(out) - want) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -15) * np.abs(want)).all()
+        ref = score * np.log(2.0)
+        assert (np.abs(f64(lse) - ref) <= 2.0 ** -20 + 8 * U * abs(ref)).all()

@@ -35,8 +35,8 @@
 // Measured on the device (of the 6795 GB/s that a copy reaches; the range is that of several GPUs): 1M keys, 16 + 4 heads, d = 128, e4m3:
 // 164 to 168 us (95 to 97 %); 64 x 16K keys, 64 + 8 heads, e4m3: 219 to 223 us (93 to 94 %); 24 x 8K keys with a window of 4096, 32
 // heads, d = 64, bf16: 115 to 119 us (89 to 92 %), 113 with the products left out; 777 keys, bf16: 6.6 us.  Far from HBM's bound: groups of 16
-// (380K keys, e4m3: 41.5 us, 70 %; 32 x 4K keys, d = 64, bf16: 18.6 us, 35 %), 48 heads over one kv head (1M keys, e4m3: 128 us,
-// 31 %), and short sequences (32 x 1K keys, e4m3: 11.8 us, 26 %).
+// (380K keys, e4m3: 41.9 us, 69 %; 32 x 4K keys, d = 64, bf16: 18.7 us, 35 %), 48 heads over one kv head (1M keys, e4m3: 129 us,
+// 31 %), and short sequences (32 x 1K keys, e4m3: 12.0 us, 25 %).
 #include <cuda_bf16.h>
 
 #include <algorithm>

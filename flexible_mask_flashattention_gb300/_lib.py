@@ -52,7 +52,8 @@ class PlanInfoC(ctypes.Structure):
 class KVCacheC(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
                 ("v_exp", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
-                ("hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+                ("hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
 
 
 _lib = None
@@ -132,6 +133,9 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.ffa_fwd_decode.restype = ctypes.c_int
     lib.ffa_fwd_decode.argtypes = [_vp, _i64, cache, _vp, _i64, _i32, _i32, _i32, _vp, _vp, ctypes.c_float, _vp, _vp,
                                    _vp, _vp, ctypes.c_size_t, _vp]
+    lib.ffa_fwd_decode_window.restype = ctypes.c_int
+    lib.ffa_fwd_decode_window.argtypes = [_vp, _i64, cache, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp, ctypes.c_float, _vp,
+                                          _vp, _vp, _vp, ctypes.c_size_t, _vp]
     lib.ffa_selftest_bounded_wait.restype = ctypes.c_int
     lib.ffa_selftest_bounded_wait.argtypes = [_vp, ctypes.POINTER(ctypes.c_uint32), ctypes.POINTER(ctypes.c_uint32)]
     lib.ffa_plan_enable_cta_trace.restype = ctypes.c_int
@@ -602,22 +606,32 @@ def _dims(t, name, n):
     return t.shape
 
 
-def _kv_cache(k_cache, v_cache, k_exp, v_exp, dev) -> KVCacheC:
-    """The C description of a cache: k, v [pages, hkv, page_size, d] bf16, or float8_e4m3fn with exponent bytes."""
+def _kv_cache(k_cache, v_cache, k_exp, v_exp, k_scale, v_scale, dev) -> KVCacheC:
+    """The C description of a cache: k, v [pages, hkv, page_size, d] bf16, or float8_e4m3fn with exponent bytes, or
+    [pages, hkv, page_size, d / 2] uint8 (two e2m1 codes a byte) with exponent bytes and float8_e4m3fn scales."""
     dtype = k_cache.dtype
-    quantised = dtype is torch.float8_e4m3fn
-    if not quantised and dtype is not torch.bfloat16:
-        raise FFAError(1, "k_cache must be a bfloat16 or float8_e4m3fn tensor")
+    if dtype is not torch.bfloat16 and dtype is not torch.float8_e4m3fn and dtype is not torch.uint8:
+        raise FFAError(1, "k_cache must be a bfloat16, float8_e4m3fn or uint8 tensor")
     shape = pages, hkv, page_size, d = _dims(k_cache, "k_cache", 4)
     _check_dense(k_cache, dtype, shape, dev, "k_cache")
     _check_dense(v_cache, dtype, shape, dev, "v_cache")
-    if not quantised:
+    if dtype is not torch.uint8 and (k_scale is not None or v_scale is not None):
+        raise FFAError(1, "only a cache in 4 bits (uint8) has scales")
+    if dtype is torch.bfloat16:
         if k_exp is not None or v_exp is not None:
             raise FFAError(1, "a bfloat16 cache has no exponent bytes")
         return KVCacheC(k_cache.data_ptr(), v_cache.data_ptr(), None, None, pages, page_size, hkv, d, 0)
     _check_dense(k_exp, torch.uint8, shape[:3], dev, "k_exp")
     _check_dense(v_exp, torch.uint8, shape[:3], dev, "v_exp")
-    return KVCacheC(k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), pages, page_size, hkv, d, 1)
+    if dtype is torch.float8_e4m3fn:
+        return KVCacheC(k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), pages, page_size, hkv, d, 1)
+    if d != 32 and d != 64:
+        raise FFAError(4, f"k_cache holds rows of {2 * d} values in 4 bits")
+    scales = (pages, hkv, page_size, d // 8)
+    _check_dense(k_scale, torch.float8_e4m3fn, scales, dev, "k_scale")
+    _check_dense(v_scale, torch.float8_e4m3fn, scales, dev, "v_scale")
+    return KVCacheC(k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), pages, page_size, hkv, 2 * d, 4,
+                    k_scale.data_ptr(), v_scale.data_ptr())
 
 
 def _page_table(t, batch: int, dev):
@@ -701,12 +715,14 @@ def qk_norm_rope_bwd_workspace_size(d: int) -> int:
     return load_library().ffa_qk_norm_rope_bwd_workspace_size(d)
 
 
-def kv_cache_write(k, v, k_cache, v_cache, slots, k_exp=None, v_exp=None, stream=None):
+def kv_cache_write(k, v, k_cache, v_cache, slots, k_exp=None, v_exp=None, stream=None, k_scale=None, v_scale=None):
     """Write the rows of k, v [T, Hkv, d] into the cache [pages, Hkv, page_size, d] at slots (int64 [T]: page *
     page_size + offset, all different; negative or outside: not written).  A float8_e4m3fn cache holds codes and, in k_exp / v_exp
-    [pages, Hkv, page_size] uint8, each row's exponent: value = code * 2^(byte - 127)."""
+    [pages, Hkv, page_size] uint8, each row's exponent: value = code * 2^(byte - 127).  A uint8 cache [pages, Hkv, page_size,
+    d / 2] holds e2m1 codes, two a byte (the lower half first), such exponents and, in k_scale / v_scale [pages, Hkv, page_size,
+    d / 16] float8_e4m3fn, a scale every 16 values: value = code * scale * 2^(byte - 127)."""
     dev = _device(k_cache, "k_cache")
-    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp, dev)
+    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp, k_scale, v_scale, dev)
     if not isinstance(slots, torch.Tensor):
         raise FFAError(1, "slots must be a CUDA tensor")
     tokens, = _dims(slots, "slots", 1)
@@ -714,18 +730,18 @@ def kv_cache_write(k, v, k_cache, v_cache, slots, k_exp=None, v_exp=None, stream
     ks = _rows_stride(k, "k", shape, dev)
     vs = _rows_stride(v, "v", shape, dev)
     _check_dense(slots, torch.int64, (tokens,), dev, "slots")
-    handle, _ = _on(stream, dev, k, v, k_cache, v_cache, slots, k_exp, v_exp)
+    handle, _ = _on(stream, dev, k, v, k_cache, v_cache, slots, k_exp, v_exp, k_scale, v_scale)
     _check(load_library().ffa_kv_cache_write(k.data_ptr(), ks, v.data_ptr(), vs, tokens, slots.data_ptr(),
                                              ctypes.byref(cache), handle), "ffa_kv_cache_write")
 
 
 def kv_cache_read(k_cache, v_cache, page_table, cu_seqlens, total: int, k=None, v=None, k_exp=None, v_exp=None,
-                  stream=None):
+                  stream=None, k_scale=None, v_scale=None):
     """k, v [total, Hkv, d] bf16: the first cu_seqlens[b + 1] - cu_seqlens[b] (int32 [B + 1]) keys and values of
     every sequence, back to back; page_table [B, max_pages] int32.  Rows behind the last sequence are left as they
-    were (undefined where k and v are allocated here)."""
+    were (undefined where k and v are allocated here).  Caches as in kv_cache_write."""
     dev = _device(k_cache, "k_cache")
-    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp, dev)
+    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp, k_scale, v_scale, dev)
     if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise FFAError(1, "cu_seqlens must be an int32 tensor [batch + 1]")
     _check_dense(cu_seqlens, torch.int32, cu_seqlens.shape, dev, "cu_seqlens")
@@ -736,7 +752,7 @@ def kv_cache_read(k_cache, v_cache, page_table, cu_seqlens, total: int, k=None, 
     shape, bf16 = (int(total), cache.hkv, cache.d), torch.bfloat16
     if shape[0] < 0:
         raise FFAError(1, "total must not be negative")
-    handle, context = _on(stream, dev, k_cache, v_cache, page_table, cu_seqlens, k, v, k_exp, v_exp)
+    handle, context = _on(stream, dev, k_cache, v_cache, page_table, cu_seqlens, k, v, k_exp, v_exp, k_scale, v_scale)
     if k is None:
         k = _empty(context, shape, bf16)
     else:
@@ -756,13 +772,14 @@ def fwd_decode_workspace_size(hq: int, hkv: int, d: int) -> int:
 
 
 def fwd_decode(q, k_cache, v_cache, page_table, kv_lens, scale: float, k_exp=None, v_exp=None, kv_starts=None,
-               sink=None, out=None, lse=None, workspace=None, stream=None):
+               sink=None, out=None, lse=None, workspace=None, stream=None, k_scale=None, v_scale=None, kv_firsts=None):
     """out [B, Hq, d] bf16 and lse [Hq, B] fp32 of one new token a sequence, q [B, Hq, d], over the keys
-    [kv_starts[b], kv_lens[b]) (int32 [B]) of the paged cache; sink [Hq] fp32 as in fwd_sink."""
+    [kv_starts[b], kv_lens[b]) (int32 [B]) of the paged cache, and [0, kv_firsts[b]) beside them; sink [Hq] fp32 as in
+    fwd_sink; caches as in kv_cache_write."""
     dev = _device(q, "q")
     if not isinstance(k_cache, torch.Tensor):
         raise FFAError(1, "k_cache must be a CUDA tensor")
-    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp, dev)
+    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp, k_scale, v_scale, dev)
     b, hq, d = _dims(q, "q", 3)
     qs = _rows_stride(q, "q", (b, hq, cache.d), dev)
     ts, width = _page_table(page_table, b, dev)
@@ -770,10 +787,12 @@ def fwd_decode(q, k_cache, v_cache, page_table, kv_lens, scale: float, k_exp=Non
     _check_dense(kv_lens, torch.int32, (b,), dev, "kv_lens")
     if kv_starts is not None:
         _check_dense(kv_starts, torch.int32, (b,), dev, "kv_starts")
+    if kv_firsts is not None:
+        _check_dense(kv_firsts, torch.int32, (b,), dev, "kv_firsts")
     if sink is not None:
         _check_dense(sink, f32, (hq,), dev, "sink")
     handle, context = _on(stream, dev, q, k_cache, v_cache, page_table, kv_lens, k_exp, v_exp, kv_starts, sink, out, lse,
-                          workspace)
+                          workspace, k_scale, v_scale, kv_firsts)
     if out is None:
         out = _empty(context, (b, hq, d), bf16)
     else:
@@ -786,8 +805,9 @@ def fwd_decode(q, k_cache, v_cache, page_table, kv_lens, scale: float, k_exp=Non
         workspace = _empty(context, (fwd_decode_workspace_size(hq, cache.hkv, d),), torch.uint8)
     else:
         _check_workspace(workspace, dev)
-    _check(load_library().ffa_fwd_decode(
+    _check(load_library().ffa_fwd_decode_window(
         q.data_ptr(), qs, ctypes.byref(cache), page_table.data_ptr(), ts, width, b, hq, kv_lens.data_ptr(),
-        None if kv_starts is None else kv_starts.data_ptr(), scale, None if sink is None else sink.data_ptr(),
-        out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), handle), "ffa_fwd_decode")
+        None if kv_starts is None else kv_starts.data_ptr(), None if kv_firsts is None else kv_firsts.data_ptr(), scale,
+        None if sink is None else sink.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        handle), "ffa_fwd_decode")
     return out, lse

@@ -55,7 +55,7 @@ namespace {
 // 8 x 2 137, 8 x 4 120, 12 x 4 118, 16 x 2 118, and later 12 x 2 114 and 16 x 2 116; (1M keys, 16 + 4 heads, d = 128, e4m3): 8 x 1 181, 12 x 1 170, 8 x 2 169; (24 x 8K
 // keys, 32 heads, d = 64, bf16): 8 x 1 119, 8 x 2 122, 12 x 2 117; (380K keys, 32 + 2 heads, d = 128, e4m3): 8 x 1 46, 8 x 2 43.
 constexpr int warps_of(int d, int nt) { return nt == 2 || d == 128 ? 8 : 12; }
-constexpr int groups_of(int d, bool fp8) { return d == 128 && !fp8 ? 1 : 2; }
+constexpr int groups_of(int d, int type) { return d == 128 && type == kBf16 ? 1 : type == kE2m1 && d == 64 ? 4 : 2; }
 constexpr int kMaxCtas = 160;          // CTAs (one an SM) the workspace holds parts for: two a CTA
 constexpr int kSmemMax = 226 * 1024;   // of 227 KB
 constexpr float kLog2e = 1.4426950408889634f;
@@ -76,6 +76,8 @@ struct DecodeParams {
   const void* v;
   const uint8_t* k_exp;
   const uint8_t* v_exp;
+  const uint8_t* k_scale;
+  const uint8_t* v_scale;
   PageGeom geom;
   const int32_t* table;
   int64_t table_stride;
@@ -83,6 +85,7 @@ struct DecodeParams {
   int32_t batch, hq, group, subs;   // group = hq / hkv; subs = units a kv head (group / (8 NT) rounded up)
   const int32_t* lens;
   const int32_t* starts;
+  const int32_t* firsts;
   float scale_log2;
   const float* sink;
   __nv_bfloat16* out;
@@ -92,18 +95,20 @@ struct DecodeParams {
   float* part;        // [2 kMaxCtas][8 NT][D]
 };
 
-template <int D, bool FP8, int NT>
+template <int D, int T, int NT>
 struct Cfg {
+  static constexpr bool QUANT = T != kBf16;
   static constexpr int W = warps_of(D, NT);
   static constexpr int THREADS = 32 * W;
-  static constexpr int SK = groups_of(D, FP8);
+  static constexpr int SK = groups_of(D, T);
   static constexpr int KEYS = 16 * SK;                  // keys of a strip
   static constexpr int BLOCK = KEYS * W;                // keys of a block
-  static constexpr int ES = FP8 ? 1 : 2;
-  static constexpr int ROW = D * ES;                    // bytes a stored row
+  static constexpr int ROW = value_bytes(T, D);         // bytes a stored row
   static constexpr int CPR = ROW / 16;                  // 16-byte chunks a row
   static constexpr int STRIP = 16 * ROW;                // bytes of 16 rows
-  static constexpr int GROUP = 2 * STRIP + (FP8 ? 32 : 0);   // of 16 keys: K, V, exponents
+  static constexpr int SCALES = 16 * scale_bytes(T, D); // bytes of 16 rows' scales
+  static constexpr int GROUP = 2 * (STRIP + SCALES) + (QUANT ? 32 : 0);   // of 16 keys: K, V, their scales, their exponents
+  [[maybe_unused]] static constexpr int SIDE = (2 * SCALES + (QUANT ? 32 : 0)) / 16;       // 16-byte chunks behind K and V
   static constexpr int STAGE = SK * GROUP;
   static constexpr int JOIN = (W / 2) * 8 * NT * D * 4 + (W + 1) * 8 * NT * 8;   // O buffers; (m, l) of every warp, the rows' factors
   static constexpr int MISC = 1024;
@@ -111,7 +116,7 @@ struct Cfg {
   // Two stages, though three would fit e4m3 at d = 128 and groups over 8 at d = 64: more loads in flight are slower (e4m3, 64 x 16K keys
   // 219 and 224 us, 1M keys 164 and 169 us; 16 x 32K keys of 16-head groups, d = 64, bf16 37 and 39 us).  bf16 at d = 128 takes what
   // fits (777 keys 6.6 us with three and 6.8 with two, large batches alike).
-  static constexpr int STAGES = FP8 || D == 64 ? 2 : FIT;
+  static constexpr int STAGES = T == kE2m1 ? 3 : T == kE4m3 || D == 64 ? 2 : FIT;
   static constexpr int SMEM = MISC + JOIN + W * STAGE * STAGES;
   static constexpr int KSTEPS = D / 16;
   static constexpr int MT = D / 16;                     // 16-column tiles of the output
@@ -125,6 +130,16 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 r;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(r) : "r"(a) : "memory");
   return r;
 }
 __device__ __forceinline__ uint32_t lds8(uint32_t a) {
@@ -159,6 +174,10 @@ __device__ __forceinline__ float pow2i(int e) {   // 2^e, 0 below the normal ran
   return e < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+__device__ __forceinline__ KeyRange range_of(const DecodeParams& p, int seq, int strip) {
+  return key_range(p.lens[seq], p.starts ? p.starts[seq] : 0, p.firsts ? p.firsts[seq] : 0, p.max_pages, p.geom.page_log2, strip);
+}
+
 // Where a walk over the CTA's share of the block list stands: unit (b, u) with u = kv head * subs + sub, `left` blocks of it from
 // the current one on, and the first key of this warp's strip in the current block.  Which of a block's strips is a warp's turns with
 // every unit, so that units of one strip keep all warps busy.
@@ -166,6 +185,7 @@ template <int W, int KEYS>
 struct Walk {
   static constexpr int kBlock = KEYS * W;
   int b, u, left, key, start, end, turn;   // turn: of the block's strips, the one that is this warp's
+  int first, gap;                          // as in the KeyRange: keys are counted without the gap
   bool bad;
   // The first of the unit's blocks that is walked is `blk`.
   __device__ __forceinline__ void set(const KeyRange& r, int seq, int unit, int64_t blk) {
@@ -173,6 +193,8 @@ struct Walk {
     u = unit;
     start = static_cast<int>(r.start);
     end = static_cast<int>(r.end);
+    first = r.first;
+    gap = static_cast<int>(r.gap);
     bad = r.bad;
     left = static_cast<int>(range_blocks(r, kBlock, KEYS) - blk);
     const int64_t k = range_first(r, KEYS) + (blk * W + turn) * KEYS;
@@ -186,14 +208,20 @@ struct Walk {
     turn = turn == 0 ? W - 1 : turn - 1;
     const bool wrap = u + 1 == units;
     const int seq = wrap ? b + 1 : b;
-    set(key_range(p.lens[seq], p.starts ? p.starts[seq] : 0, p.max_pages, p.geom.page_log2), seq, wrap ? 0 : u + 1, 0);
+    set(range_of(p, seq, KEYS), seq, wrap ? 0 : u + 1, 0);
   }
+  // Of this warp's strip: all its keys count; one of its keys, `key - key of the strip` = i, does; one of those from i on, 16 of them.
+  __device__ __forceinline__ bool whole() const { return end - key >= KEYS && (key >= start || key + KEYS <= first); }
+  __device__ __forceinline__ bool counts(int i) const { return i < end - key && (i >= start - key || i < first - key); }
+  __device__ __forceinline__ bool some(int i) const { return end - key > i && (start - key < i + 16 || first - key > i); }
+  // The unit is one strip.
+  __device__ __forceinline__ bool single() const { return end - (first > 0 ? 0 : start / KEYS * KEYS) <= KEYS; }
 };
 
 // The first of the two neighbouring columns that a lane's MMA results of tile i are.
-template <int D, bool FP8>
+template <int D, bool QUANT>
 __device__ __forceinline__ int column(int i, int n) {
-  return FP8 ? (D / 8) * n + 2 * i : (i / 4) * 64 + 8 * n + 2 * (i % 4);
+  return QUANT ? (D / 8) * n + 2 * i : (i / 4) * 64 + 8 * n + 2 * (i % 4);
 }
 
 // 2^x for factors of the output, down to fp32's smallest values (ex2_approx gives 0 under 2^-126).
@@ -222,9 +250,10 @@ __device__ __forceinline__ RowEnd row_end(const DecodeParams& p, int head, float
   return r;
 }
 
-template <int D, bool FP8, int NT>
+template <int D, int T, int NT>
 __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeParams p) {
-  using C = Cfg<D, FP8, NT>;
+  using C = Cfg<D, T, NT>;
+  constexpr bool QUANT = C::QUANT;
   constexpr int NQ = 8 * NT, kW = C::W, kThreads = C::THREADS, kBlock = C::BLOCK, SK = C::SK;
   extern __shared__ __align__(128) uint8_t smem[];
   float2* join_o = reinterpret_cast<float2*>(smem + C::MISC);   // [kW / 2][an MMA's result registers in pairs][32 lanes]
@@ -240,15 +269,14 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
   const int units = p.geom.hkv * p.subs;
 
   // ---- this CTA's share of the block list
-  auto range_of = [&](int seq) { return key_range(p.lens[seq], p.starts ? p.starts[seq] : 0, p.max_pages, p.geom.page_log2); };
-  auto blocks_of = [&](int seq) { return range_blocks(range_of(seq), kBlock, C::KEYS); };
+  auto blocks_of = [&](int seq) { return range_blocks(range_of(p, seq, C::KEYS), kBlock, C::KEYS); };
   int64_t total, t0, t1, parts, off;   // off: of the share's first block in its sequence b
   int b;
   KeyRange range;
   const int64_t cta = blockIdx.x;
   if (p.batch <= 32) {   // a sequence a lane, every warp for itself
     KeyRange r{0, 0, false};
-    if (lane < p.batch) r = range_of(lane);
+    if (lane < p.batch) r = range_of(p, lane, C::KEYS);
     const int64_t mine = lane < p.batch ? range_blocks(r, kBlock, C::KEYS) : 0;
     int64_t incl = mine;
 #pragma unroll
@@ -269,6 +297,8 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
     range.start = __shfl_sync(0xffffffffu, static_cast<int>(r.start), b);
     range.end = __shfl_sync(0xffffffffu, static_cast<int>(r.end), b);
     range.bad = __shfl_sync(0xffffffffu, static_cast<int>(r.bad), b) != 0;
+    range.first = __shfl_sync(0xffffffffu, r.first, b);
+    range.gap = __shfl_sync(0xffffffffu, static_cast<int>(r.gap), b);
   } else {
     const int per = (p.batch + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
@@ -311,7 +341,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
     __syncthreads();
     b = begin->b;
     off = begin->off;
-    range = range_of(b);
+    range = range_of(p, b, C::KEYS);
   }
   Walk<kW, C::KEYS> cur;
   bool opens_mid;
@@ -328,15 +358,14 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
   const uint32_t ring = smem_u32(smem + C::MISC + C::JOIN) + warp * (C::STAGE * C::STAGES);
   Walk<kW, C::KEYS> ld = cur;
   const int page_rows = p.geom.hkv << p.geom.page_log2, page_mask = (1 << p.geom.page_log2) - 1;
+  int real;               // the next strip's first key, the gap counted
   int head_row;           // the loading unit's head's first row in a page
   int page[SK];           // of the next strip's groups of 16 keys, read a strip ahead; -1 for a group outside the range
   auto read_pages = [&]() {
     const int32_t* row = p.table + ld.b * p.table_stride;
+    real = ld.key < ld.first ? ld.key : ld.key + ld.gap;
 #pragma unroll
-    for (int g = 0; g < SK; ++g) {
-      const bool in = ld.end - ld.key > 16 * g && ld.start - ld.key < 16 * (g + 1);
-      page[g] = in ? __ldg(row + ((ld.key + 16 * g) >> p.geom.page_log2)) : -1;
-    }
+    for (int g = 0; g < SK; ++g) page[g] = ld.some(16 * g) ? __ldg(row + ((real + 16 * g) >> p.geom.page_log2)) : -1;
   };
   auto open_unit = [&]() {
     head_row = (p.subs == 1 ? ld.u : ld.u / p.subs) << p.geom.page_log2;
@@ -347,14 +376,22 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
   uint32_t dst_of[kPeriod];
 #pragma unroll
   for (int i = 0; i < kPeriod; ++i) dst_of[i] = ring + 16 * strip_chunk((lane + 32 * i) / C::CPR, (lane + 32 * i) % C::CPR, C::CPR);
+  // the chunk behind K and V that this lane copies: of K's scales, V's scales, K's exponents, V's exponents
+  const uint8_t* side = nullptr;
+  if constexpr (T == kE2m1) {
+    constexpr int N = C::SCALES / 16;
+    side = lane < N ? p.k_scale + 16 * lane : lane < 2 * N ? p.v_scale + 16 * (lane - N) : lane == 2 * N ? p.k_exp : p.v_exp;
+  } else if constexpr (T == kE4m3) {
+    side = lane ? p.v_exp : p.k_exp;
+  }
   auto load_strip = [&](int stage, bool more) {
     const int have = ld.end - ld.key;
     if (have > 0) {
-      const bool full = have >= C::KEYS && ld.key >= ld.start;
+      const bool full = ld.whole();
 #pragma unroll
       for (int g = 0; g < SK; ++g) {
         const bool ok = static_cast<uint32_t>(page[g]) < static_cast<uint32_t>(p.geom.num_pages);   // as page_ok, for pages of 32 bits
-        const int64_t row = static_cast<int64_t>(ok ? page[g] : 0) * page_rows + (head_row + ((ld.key + 16 * g) & page_mask));
+        const int64_t row = static_cast<int64_t>(ok ? page[g] : 0) * page_rows + (head_row + ((real + 16 * g) & page_mask));
         const int64_t at = row * C::ROW + lane * 16;
         const uint8_t *k = static_cast<const uint8_t*>(p.k) + at, *v = static_cast<const uint8_t*>(p.v) + at;
         const uint32_t base = stage * C::STAGE + g * C::GROUP;
@@ -366,19 +403,20 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
             cp_async16(to + C::STRIP, v + 512 * i);
           }
         } else {   // rows outside the range are filled with zeros, not read
-          const int lo = ld.start - ld.key - 16 * g, hi = min(have - 16 * g, 16);
-          const bool none = lo >= 16 || hi <= 0;
+          const bool none = !ld.some(16 * g);
 #pragma unroll
           for (int i = 0; i < C::CPR / 2; ++i) {
             const uint32_t to = base + dst_of[i % kPeriod] + i / kPeriod * (kPeriod * 512);
-            const int key = (lane + 32 * i) / C::CPR, bytes = ok && key >= lo && key < hi ? 16 : 0;
+            const int key = (lane + 32 * i) / C::CPR, bytes = ok && ld.counts(key + 16 * g) ? 16 : 0;
             if (ok || none) cp_async16(to, k + 512 * i, bytes);
-            else sts128(to, 0x7fff7fffu);   // no such page: keys of NaN, which make the row NaN
+            else sts128(to, 0x7fff7fffu);   // no such page: keys of NaN, which make the row NaN (e2m1: below)
             cp_async16(to + C::STRIP, v + 512 * i, bytes);
           }
         }
-        if constexpr (FP8) {
-          if (lane < 2) cp_async16(ring + base + 2 * C::STRIP + 16 * lane, (lane ? p.v_exp : p.k_exp) + row);
+        if constexpr (QUANT) {
+          const uint32_t to = ring + base + 2 * C::STRIP + 16 * lane;
+          if (T == kE2m1 && !ok && lane < C::SCALES / 16) sts128(to, 0x7f7f7f7fu);   // no such page: scales of NaN
+          else if (lane < C::SIDE) cp_async16(to, side + (lane < C::SIDE - 2 ? row * (D / 16) : row));
         }
       }
     }
@@ -405,7 +443,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
   // cost one vote.  l and, for bf16, O are relative to 2^m.  e4m3's O is relative to 2^(m + vr), so that its weights
   // 2^((score - m) + (n - vr)) lie under 2^kTop and the largest over 2^(kTop - kLazy): f16 reaches down to 2^-34 of that one.  vr is
   // counted from m so that a score's own rounding, in the first bracket, is the same in a weight and in l.
-  constexpr float kLazy = FP8 ? 5.f : 8.f;
+  constexpr float kLazy = QUANT ? 5.f : 8.f;
   constexpr float kTop = 15.f;
   constexpr float kNone = -3.402823466e38f;   // a reference that no key has raised
 
@@ -424,7 +462,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
       const __nv_bfloat16* src = p.q + w.b * p.q_stride + static_cast<int64_t>(kvh * p.group + (act ? qi : 0)) * D;
 #pragma unroll
       for (int ks = 0; ks < C::KSTEPS; ++ks) {
-        const int at = FP8 ? (t + 4 * (ks / 4)) * 16 + 4 * (ks % 4) : (t + 4 * (ks / 2)) * 8 + 4 * (ks % 2);
+        const int at = T == kE2m1 ? (D / 4) * t + 4 * ks : T == kE4m3 ? (t + 4 * (ks / 4)) * 16 + 4 * (ks % 4) : (t + 4 * (ks / 2)) * 8 + 4 * (ks % 2);
         const uint2 x = act ? __ldg(reinterpret_cast<const uint2*>(src + at)) : uint2{};
         qf[nt][ks][0] = x.x;
         qf[nt][ks][1] = x.y;
@@ -434,7 +472,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
   auto begin_unit = [&]() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      if constexpr (FP8) {
+      if constexpr (QUANT) {
         uint32_t top = 0;   // of the magnitudes' bit patterns, which order as integers but for NaN, two at a time
 #pragma unroll
         for (int ks = 0; ks < C::KSTEPS; ++ks)
@@ -470,19 +508,55 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
   auto strip = [&](int stage) {
     const int have = cur.end - cur.key;
     if (have <= 0) return;
-    const bool whole = have >= C::KEYS && cur.key >= cur.start;
+    const bool whole = cur.whole();
     const uint32_t sb = ring + stage * C::STAGE;
     constexpr int CH = SK == 1 ? 2 : 1;   // accumulators a score tile: one group alone would be one long chain of MMAs
     float s[SK][NT][CH][4] = {};
+    if constexpr (T == kE2m1) {
 #pragma unroll
-    for (int h = 0; h < C::CPR / 4; ++h)
+      for (int g = 0; g < SK; ++g) {
+        constexpr int WORDS = D / 32;   // of a row that are this lane's: columns D / 4 * t on, one scale (d = 64) or two
+        const uint32_t kb = sb + g * C::GROUP, cb = kb + 2 * C::STRIP;
+        uint32_t w[2][WORDS], sc[2][WORDS / 2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int key = n + 8 * r;
+          if constexpr (D == 128) {
+            const uint4 x = lds128(kb + 16 * strip_chunk(key, t, C::CPR));
+            w[r][0] = x.x, w[r][1] = x.y, w[r][2] = x.z, w[r][3] = x.w;
+            const uint32_t two = e4m3x2_to_f16x2(lds16(cb + key * 8 + 2 * t));
+            sc[r][0] = __byte_perm(two, 0, 0x1010), sc[r][1] = __byte_perm(two, 0, 0x3232);
+          } else {
+            const uint2 x = lds64(kb + 16 * strip_chunk(key, t >> 1, C::CPR) + 8 * (t & 1));
+            w[r][0] = x.x, w[r][1] = x.y;
+            const uint32_t one = lds8(cb + key * 4 + t);
+            sc[r][0] = e4m3x2_to_f16x2(one | one << 8);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < WORDS; ++j) {
+          uint32_t x[4], y[4];
+          e2m1x8_to_f16x2(w[0][j], x);
+          e2m1x8_to_f16x2(w[1][j], y);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = mul_f16x2(x[i], sc[0][j / 2]), y[i] = mul_f16x2(y[i], sc[1][j / 2]);   // exact
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma<true>(s[g][nt][i % CH], x[2 * i], y[2 * i], x[2 * i + 1], y[2 * i + 1], qf[nt][2 * j + i][0], qf[nt][2 * j + i][1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < (T == kE2m1 ? 0 : C::CPR / 4); ++h)
 #pragma unroll
       for (int g = 0; g < SK; ++g) {
         const uint32_t kb = sb + g * C::GROUP;
         const uint4 x = lds128(kb + 16 * strip_chunk(n, t + 4 * h, C::CPR));
         const uint4 y = lds128(kb + 16 * strip_chunk(n + 8, t + 4 * h, C::CPR));
         const uint32_t xa[4] = {x.x, x.y, x.z, x.w}, ya[4] = {y.x, y.y, y.z, y.w};
-        if constexpr (FP8) {
+        if constexpr (T == kE4m3) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t a0, a1, a2, a3;
@@ -501,14 +575,13 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
         }
       }
     // keys n and n + 8 of a group are this lane's; columns 2t, 2t + 1 of each query tile
-    auto inside = [&](int key) { return whole || (key >= cur.start - cur.key && key < have); };
     float ks[SK][2], vn[SK][2];   // e4m3: the scale of a key's row, n of its value's (byte 0 stands for a value of 0)
-    if constexpr (FP8) {
+    if constexpr (QUANT) {
 #pragma unroll
       for (int g = 0; g < SK; ++g)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const uint32_t eb = sb + g * C::GROUP + 2 * C::STRIP + n + 8 * r;
+          const uint32_t eb = sb + g * C::GROUP + 2 * (C::STRIP + C::SCALES) + n + 8 * r;
           ks[g][r] = exp_scale(lds8(eb));
           const uint32_t byte = lds8(eb + 16);
           vn[g][r] = byte ? static_cast<float>(static_cast<int>(byte) - 127) : -INFINITY;
@@ -530,11 +603,11 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
           const float2 q2 = make_float2(qs[nt][0], qs[nt][1]);
           float2 v = make_float2(s[g][nt][0][2 * r], s[g][nt][0][2 * r + 1]);
           if constexpr (CH == 2) v = add2(v, make_float2(s[g][nt][1][2 * r], s[g][nt][1][2 * r + 1]));
-          v = mul2(v, FP8 ? mul2(q2, make_float2(ks[g][r], ks[g][r])) : q2);
-          if (!whole && !inside(16 * g + n + 8 * r)) v = make_float2(-INFINITY, -INFINITY);
+          v = mul2(v, QUANT ? mul2(q2, make_float2(ks[g][r], ks[g][r])) : q2);
+          if (!whole && !cur.counts(16 * g + n + 8 * r)) v = make_float2(-INFINITY, -INFINITY);
           x[g][nt][r] = v;
           raise |= v.x > m[nt][0] || v.y > m[nt][1];
-          if constexpr (FP8) {
+          if constexpr (QUANT) {
             const float2 y = less_vr(g, nt, r);
             raise |= y.x > kTop || y.y > kTop;
           }
@@ -558,7 +631,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
           float f = ex2_approx(up);
           m[nt][c] = mx;
           l[nt][c] *= f;
-          if constexpr (FP8) {
+          if constexpr (QUANT) {
             const float top = fmaxf(largest([&](int g, int r) { return (score(g, r) - mx) + vn[g][r]; }) + (kLazy - kTop), vr[nt][c] + up);
             f = ex2_approx(up + (vr[nt][c] - top));
             vr[nt][c] = top;
@@ -578,7 +651,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
         float2 e0 = ex2(less_m(g, nt, 0)), e1 = ex2(less_m(g, nt, 1));
         const float2 sum = add2(make_float2(l[nt][0], l[nt][1]), add2(e0, e1));
         l[nt][0] = sum.x, l[nt][1] = sum.y;
-        if constexpr (FP8) {
+        if constexpr (QUANT) {
           e0 = ex2(less_vr(g, nt, 0)), e1 = ex2(less_vr(g, nt, 1));
           pf[g][nt][0] = movmatrix(pack_f16x2(e0.x, e0.y));
           pf[g][nt][1] = movmatrix(pack_f16x2(e1.x, e1.y));
@@ -594,7 +667,39 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
 #pragma unroll
     for (int g = 0; g < SK; ++g) {
       const uint32_t vb = sb + g * C::GROUP + C::STRIP;
-      if constexpr (FP8) {
+      if constexpr (T == kE2m1) {
+        constexpr int WORDS = D / 64;   // of a row that are this lane's: columns D / 8 * n on, of one scale
+        const uint32_t cb = vb + C::STRIP + C::SCALES + (D == 128 ? n : n >> 1);
+        uint32_t w[4][WORDS], sc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = 2 * t + (i & 1) + 8 * (i >> 1);
+          if constexpr (D == 128) {
+            const uint2 x = lds64(vb + 16 * strip_chunk(key, n >> 1, C::CPR) + 8 * (n & 1));
+            w[i][0] = x.x, w[i][1] = x.y;
+          } else {
+            w[i][0] = lds32(vb + 16 * strip_chunk(key, n >> 2, C::CPR) + 4 * (n & 3));
+          }
+          sc[i] = lds8(cb + key * (D / 16));
+          if (!whole && !cur.counts(16 * g + key)) sc[i] = 0;   // a row that was not written may have any scale
+        }
+        const uint32_t s0 = e4m3x2_to_f16x2(sc[0] | sc[1] << 8), s1 = e4m3x2_to_f16x2(sc[2] | sc[3] << 8);
+#pragma unroll
+        for (int j = 0; j < WORDS; ++j) {
+          // columns 2i (a0, a2) and 2i + 1 (a1, a3), two keys' codes to a byte
+          uint32_t a[4][4];
+          e2m1x8_to_f16x2((w[0][j] & 0x0f0f0f0fu) | (w[1][j] << 4 & 0xf0f0f0f0u), a[0]);
+          e2m1x8_to_f16x2((w[0][j] >> 4 & 0x0f0f0f0fu) | (w[1][j] & 0xf0f0f0f0u), a[1]);
+          e2m1x8_to_f16x2((w[2][j] & 0x0f0f0f0fu) | (w[3][j] << 4 & 0xf0f0f0f0u), a[2]);
+          e2m1x8_to_f16x2((w[2][j] >> 4 & 0x0f0f0f0fu) | (w[3][j] & 0xf0f0f0f0u), a[3]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a0 = mul_f16x2(a[0][i], s0), a1 = mul_f16x2(a[1][i], s0), a2 = mul_f16x2(a[2][i], s1), a3 = mul_f16x2(a[3][i], s1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma<true>(o[nt][4 * j + i], a0, a1, a2, a3, pf[g][nt][0], pf[g][nt][1]);
+          }
+        }
+      } else if constexpr (T == kE4m3) {
         constexpr int WORDS = C::MT / 2;   // 32-bit words of a row this lane owns: 2 (d = 64) or 4
         uint32_t r[4][WORDS];
 #pragma unroll
@@ -667,7 +772,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
         float mx = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kW; ++w) mx = fmaxf(mx, join_ml[w * NQ + nt * 8 + 2 * t + c].x);
-        f[nt][c] = m[nt][c] == -INFINITY ? 0.f : FP8 ? ex2_wide(m[nt][c] - mx + vr[nt][c]) : ex2_approx(m[nt][c] - mx);
+        f[nt][c] = m[nt][c] == -INFINITY ? 0.f : QUANT ? ex2_wide(m[nt][c] - mx + vr[nt][c]) : ex2_approx(m[nt][c] - mx);
       }
     if (warp >= kW / 2) {
 #pragma unroll
@@ -722,7 +827,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
     // what is read from here on (the buffers, the rows' factors) is written again only behind the next part's first barrier
     for (int e = warp; e < kPairs; e += kW) {
       const int i = e / 2 % C::MT, qi = e / (2 * C::MT) * 8 + 2 * t + (e & 1);
-      const int col = column<D, FP8>(i, n);
+      const int col = column<D, QUANT>(i, n);
       float2 v = make_float2(0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kW / 2; ++w) {
@@ -755,12 +860,12 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
         if (row >= p.group) continue;
         const float mx = m[nt][c] == kNone ? -INFINITY : m[nt][c];
         const RowEnd r = row_end(p, head, mx, sum + poison);
-        const float f = FP8 && mx != -INFINITY ? r.inv * ex2_wide(vr[nt][c]) : r.inv;
+        const float f = QUANT && mx != -INFINITY ? r.inv * ex2_wide(vr[nt][c]) : r.inv;
         __nv_bfloat16* out = p.out + (static_cast<int64_t>(cur.b) * p.hq + head) * D;
         if (n == 0) p.lse[static_cast<int64_t>(head) * p.batch + cur.b] = r.lse;
 #pragma unroll
         for (int i = 0; i < C::MT; ++i)
-          *reinterpret_cast<uint32_t*>(out + column<D, FP8>(i, n)) = pack_bf16x2(o[nt][i][c] * f, o[nt][i][c + 2] * f);
+          *reinterpret_cast<uint32_t*>(out + column<D, QUANT>(i, n)) = pack_bf16x2(o[nt][i][c] * f, o[nt][i][c + 2] * f);
       }
   };
 
@@ -793,7 +898,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT), 1) decode_kernel(DecodeP
       next.next_unit(p, units);
       load_q(next);
     }
-    if (whole && cur.end - cur.start / C::KEYS * C::KEYS <= C::KEYS) {   // a unit of one strip: its warp alone
+    if (whole && cur.single()) {   // a unit of one strip: its warp alone
       if (cur.turn == 0) end_alone();
     } else {
       end_part(whole, slot);
@@ -872,15 +977,22 @@ size_t ml_bytes(int nt) { return size_t{2} * kMaxCtas * 8 * nt * 2 * sizeof(floa
 size_t part_bytes(int nt, int d) { return size_t{2} * kMaxCtas * 8 * nt * d * sizeof(float); }
 int tiles_of(int group) { return group > 8 ? 2 : 1; }   // query tiles of 8 a unit
 
-template <int D, bool FP8, int NT>
+template <int D, int T, int NT>
 ffa_status launch(const DecodeParams& p, int device, int sms, cudaStream_t s) {
-  using C = Cfg<D, FP8, NT>;
+  using C = Cfg<D, T, NT>;
   static_assert(C::FIT >= C::STAGES && C::STAGES >= 2, "ring");
   static std::atomic<bool> raised[kDevices];
   const int grid = std::min(sms, kMaxCtas);
-  const cudaError_t e = launch_large(decode_kernel<D, FP8, NT>, dim3(grid), C::THREADS, C::SMEM, C::SMEM, s, device, raised, p);
+  const cudaError_t e = launch_large(decode_kernel<D, T, NT>, dim3(grid), C::THREADS, C::SMEM, C::SMEM, s, device, raised, p);
   if (e != cudaSuccess) return FFA_ERR_CUDA;
   return cuda_status(launch_after(decode_join_kernel<D, NT>, dim3(grid, std::min(8 * NT, p.group)), 256, s, p));
+}
+
+template <int D>
+ffa_status launch_any(int type, int nt, const DecodeParams& p, int device, int sms, cudaStream_t s) {
+  if (type == kE2m1) return nt == 1 ? launch<D, kE2m1, 1>(p, device, sms, s) : launch<D, kE2m1, 2>(p, device, sms, s);
+  if (type == kE4m3) return nt == 1 ? launch<D, kE4m3, 1>(p, device, sms, s) : launch<D, kE4m3, 2>(p, device, sms, s);
+  return nt == 1 ? launch<D, kBf16, 1>(p, device, sms, s) : launch<D, kBf16, 2>(p, device, sms, s);
 }
 
 }  // namespace
@@ -896,10 +1008,10 @@ size_t ffa_fwd_decode_workspace_size(int32_t hq, int32_t hkv, int32_t d) {
   return kDescBytes + ml_bytes(nt) + part_bytes(nt, d);
 }
 
-ffa_status ffa_fwd_decode(const void* q, int64_t q_stride, const ffa_kv_cache* cache, const int32_t* page_table,
-                          int64_t table_stride, int32_t max_pages, int32_t batch, int32_t hq, const int32_t* kv_lens,
-                          const int32_t* kv_starts, float scale, const float* sink, void* out, float* lse,
-                          void* workspace, size_t workspace_bytes, void* stream) {
+ffa_status ffa_fwd_decode_window(const void* q, int64_t q_stride, const ffa_kv_cache* cache, const int32_t* page_table,
+                                 int64_t table_stride, int32_t max_pages, int32_t batch, int32_t hq, const int32_t* kv_lens,
+                                 const int32_t* kv_starts, const int32_t* kv_firsts, float scale, const float* sink, void* out,
+                                 float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   DecodeParams p{};
   const ffa_status st = check_cache(cache, p.geom);
   if (st != FFA_OK) return st;
@@ -913,24 +1025,27 @@ ffa_status ffa_fwd_decode(const void* q, int64_t q_stride, const ffa_kv_cache* c
   if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || !aligned16(workspace)) return FFA_ERR_INVALID_ARG;
   if (max_pages > 0 && !page_table) return FFA_ERR_INVALID_ARG;
   for (const void* a : {static_cast<const void*>(page_table), static_cast<const void*>(kv_lens),
-                        static_cast<const void*>(kv_starts), static_cast<const void*>(sink)})
+                        static_cast<const void*>(kv_starts), static_cast<const void*>(kv_firsts), static_cast<const void*>(sink)})
     if (reinterpret_cast<uintptr_t>(a) & 3u) return FFA_ERR_INVALID_ARG;
   if (q_stride % 8 != 0 || (batch > 1 && q_stride < static_cast<int64_t>(hq) * d)) return FFA_ERR_INVALID_ARG;
   if (workspace_bytes < ffa_fwd_decode_workspace_size(hq, cache->hkv, d)) return FFA_ERR_INVALID_ARG;
   const int group = hq / cache->hkv, nt = tiles_of(group);
   const CacheSpans at(*cache);
-  Span in[9] = {{q, span_bytes(batch, q_stride, hq, d)}, {page_table, 4 * (static_cast<int64_t>(batch - 1) * table_stride + max_pages)},
-                {kv_lens, 4 * int64_t{batch}}, {kv_starts, kv_starts ? 4 * int64_t{batch} : 0}, {sink, sink ? 4 * hq : 0}};
-  for (int i = 0; i < at.n; ++i) in[5 + i] = at.s[i];
+  Span in[12] = {{q, span_bytes(batch, q_stride, hq, d)}, {page_table, 4 * (static_cast<int64_t>(batch - 1) * table_stride + max_pages)},
+                {kv_lens, 4 * int64_t{batch}}, {kv_starts, kv_starts ? 4 * int64_t{batch} : 0}, {sink, sink ? 4 * hq : 0},
+                 {kv_firsts, kv_firsts ? 4 * int64_t{batch} : 0}};
+  for (int i = 0; i < at.n; ++i) in[6 + i] = at.s[i];
   const Span outs[] = {{out, 2 * int64_t{batch} * hq * d}, {lse, 4 * int64_t{batch} * hq},
                        {workspace, static_cast<int64_t>(ffa_fwd_decode_workspace_size(hq, cache->hkv, d))}};
-  if (any_meet(outs, 3, in, 5 + at.n)) return FFA_ERR_INVALID_ARG;
+  if (any_meet(outs, 3, in, 6 + at.n)) return FFA_ERR_INVALID_ARG;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_stride = q_stride;
   p.k = cache->k;
   p.v = cache->v;
   p.k_exp = cache->k_exp;
   p.v_exp = cache->v_exp;
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
   p.table = page_table;
   p.table_stride = table_stride;
   p.max_pages = max_pages;
@@ -940,6 +1055,7 @@ ffa_status ffa_fwd_decode(const void* q, int64_t q_stride, const ffa_kv_cache* c
   p.subs = (group + 8 * nt - 1) / (8 * nt);
   p.lens = kv_lens;
   p.starts = kv_starts;
+  p.firsts = kv_firsts;
   p.scale_log2 = scale * kLog2e;
   p.sink = sink;
   p.out = static_cast<__nv_bfloat16*>(out);
@@ -951,13 +1067,15 @@ ffa_status ffa_fwd_decode(const void* q, int64_t q_stride, const ffa_kv_cache* c
   int device = 0, sms = 0;
   if (!current_device(device, sms)) return FFA_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool fp8 = cache->dtype == FFA_KV_E4M3;
-  if (d == 128) {
-    if (nt == 1) return fp8 ? launch<128, true, 1>(p, device, sms, s) : launch<128, false, 1>(p, device, sms, s);
-    return fp8 ? launch<128, true, 2>(p, device, sms, s) : launch<128, false, 2>(p, device, sms, s);
-  }
-  if (nt == 1) return fp8 ? launch<64, true, 1>(p, device, sms, s) : launch<64, false, 1>(p, device, sms, s);
-  return fp8 ? launch<64, true, 2>(p, device, sms, s) : launch<64, false, 2>(p, device, sms, s);
+  return d == 128 ? launch_any<128>(cache->dtype, nt, p, device, sms, s) : launch_any<64>(cache->dtype, nt, p, device, sms, s);
+}
+
+ffa_status ffa_fwd_decode(const void* q, int64_t q_stride, const ffa_kv_cache* cache, const int32_t* page_table,
+                          int64_t table_stride, int32_t max_pages, int32_t batch, int32_t hq, const int32_t* kv_lens,
+                          const int32_t* kv_starts, float scale, const float* sink, void* out, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  return ffa_fwd_decode_window(q, q_stride, cache, page_table, table_stride, max_pages, batch, hq, kv_lens, kv_starts, nullptr, scale,
+                               sink, out, lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

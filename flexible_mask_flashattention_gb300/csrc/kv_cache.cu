@@ -6,9 +6,12 @@
 //         two for which max|x| <= 448 * 2^n.  A power of two rather than max|x| / 448: codes have an exponent of
 //         their own, so the scale's rounding up costs no mantissa bit, the division by it is exact (each value is rounded once),
 //         and every stored value is exact in bf16 down to bf16's smallest, so that reading back does not round again.
-//         A row that holds a NaN or an infinity is stored as NaN throughout (byte 127).
+//         A row that holds a NaN or an infinity is stored as NaN throughout (byte 127);
+//   e2m1  4-bit codes, an e4m3 scale every 16 columns and one exponent byte a row: value = code * scale * 2^(byte - 127).  The byte takes
+//         the row's range, so that scales need no calibration and no fp32 factor beside the cache; code times scale has 6 bits,
+//         exact in f16 and in bf16.  d / 2 + d / 16 + 1 bytes: 4.6 bits a value at d = 128.
 //
-// Both kernels are bound by HBM: 2 d bytes a row on the tensors' side, 2 d or d + 1 on the cache's.  A grid's second
+// Both kernels are bound by HBM: 2 d bytes a row on the tensors' side, 2 d, d + 1 or 9 d / 16 + 1 on the cache's.  A grid's second
 // dimension is k or v; a warp holds 2 or 4 consecutive rows at once (a pass), whatever tokens and heads they are of, 8 values a
 // lane, and starts the loads of kUnroll passes before it uses the first (168K tokens of 8 heads, d = 128, e4m3, written, all on one GPU: 147
 // us so, 194 us with 8 passes, 167 us with 2).  Measured on another GPU, the same tokens: e4m3 written in 153 us and read in 157 us,
@@ -39,24 +42,17 @@ __device__ __forceinline__ T pick(T const (&pair)[2], int i) {
 struct WriteParams {
   const __nv_bfloat16* x[2];   // k, v
   int64_t stride[2];
-  void* cache[2];
-  uint8_t* exps[2];
+  CacheRows cache[2];
   const int64_t* slots;
   PageGeom geom;
   FastDiv heads;
   uint32_t rows;               // tokens * hkv
 };
 
-__device__ __forceinline__ uint32_t e4m3x2(float2 f) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(f.y), "f"(f.x));
-  return r;
-}
-
 // FILLED: a token's rows fill the passes of a whole number of warps (hkv a multiple of kUnroll * RW), so that token and page are the
 // warp's and addresses a step apart.  Measured (168K tokens of 8 heads, d = 128, e4m3, on the first GPU above): 147 us, and 172 us without; with
 // 3 heads of d = 64, which leave most of such a warp empty, 21.6 us for 30K tokens, and 11.8 us without.
-template <int D, bool FP8, bool FILLED>
+template <int D, int T, bool FILLED>
 __global__ void __launch_bounds__(kThreads) kv_cache_write_kernel(WriteParams p) {
   constexpr int L = D / 8, RW = 32 / L;
   const int lane = threadIdx.x & 31, l = lane & (L - 1), sub = lane / L, which = blockIdx.y;
@@ -90,39 +86,13 @@ __global__ void __launch_bounds__(kThreads) kv_cache_write_kernel(WriteParams p)
       }
     }
   }
+  const CacheRows cache = pick(p.cache, which);
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
-    const bool act = FILLED || dst[i] >= 0;
-    if constexpr (!FP8) {
-      if (act) reinterpret_cast<uint4*>(pick(p.cache, which))[dst[i] * (D / 8) + l] = v[i];
-    } else {
-      // bf16 magnitudes order as 15-bit integers: the row's largest, two at a time
-      uint32_t m = __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu), __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
-#pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-      m = max(m & 0xffffu, m >> 16);
-      // max|x| = 1.f * 2^(e - 127), 448 = 1.75 * 2^8: the scale's byte is e - 8, one more where 1.f > 1.75 (mantissa 0x60)
-      const bool finite = m < 0x7f80u;
-      const int byte = finite ? max(static_cast<int>((m + 0x1fu) >> 7) - 8, 1) : 127;
-      const float inv = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);   // 2^-(byte - 127), exact
-      const uint32_t u4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      uint32_t c[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        c[j] = e4m3x2(mul2(make_float2(__uint_as_float(u4[j] << 16), __uint_as_float(u4[j] & 0xffff0000u)), make_float2(inv, inv)));
-      uint2 codes = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-      if (!finite) codes = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-      if (act) {
-        reinterpret_cast<uint2*>(pick(p.cache, which))[dst[i] * (D / 8) + l] = codes;
-        if (l == 0) pick(p.exps, which)[dst[i]] = static_cast<uint8_t>(byte);
-      }
-    }
-  }
+  for (int i = 0; i < kUnroll; ++i) store_row<D, T>(v[i], FILLED || dst[i] >= 0, dst[i], l, cache);
 }
 
 struct ReadParams {
-  const void* cache[2];
-  const uint8_t* exps[2];
+  CacheRows cache[2];
   __nv_bfloat16* out[2];
   const int32_t* table;
   int64_t table_stride;
@@ -137,7 +107,7 @@ struct ReadParams {
 constexpr int kReadRows = 256;   // rows a CTA, or those of 8 tokens: so many tokens that a thread each finds their places
 
 // A CTA takes `tile` consecutive tokens of the output; a thread a token finds its sequence and page.
-template <int D, bool FP8>
+template <int D, int T>
 __global__ void __launch_bounds__(kThreads) kv_cache_read_kernel(ReadParams p) {
   constexpr int L = D / 8, RW = 32 / L;
   __shared__ int64_t src[kReadRows];   // row of head 0 in the cache; -1: outside the batch, -2: no page of this cache
@@ -167,6 +137,7 @@ __global__ void __launch_bounds__(kThreads) kv_cache_read_kernel(ReadParams p) {
   __syncthreads();
   const int lane = threadIdx.x & 31, l = lane & (L - 1), sub = lane / L, which = blockIdx.y;
   const uint32_t rows = p.tile * p.geom.hkv;
+  const CacheRows cache = pick(p.cache, which);
   __nv_bfloat16* out = pick(p.out, which) + t0 * p.geom.hkv * D + 8 * l;
   for (uint32_t r0 = (threadIdx.x >> 5) * (kUnroll * RW) + sub; r0 - sub < rows; r0 += kWarps * kUnroll * RW) {
     uint4 v[kUnroll];
@@ -180,12 +151,16 @@ __global__ void __launch_bounds__(kThreads) kv_cache_read_kernel(ReadParams p) {
       at[i] = src[token];
       if (at[i] < 0) continue;
       const int64_t row = at[i] + (static_cast<int64_t>(r - token * p.heads.d) << p.geom.page_log2);
-      if constexpr (FP8) {
-        const uint2 c = __ldg(reinterpret_cast<const uint2*>(pick(p.cache, which)) + row * (D / 8) + l);
+      if constexpr (T == kE2m1) {
+        v[i].x = __ldg(static_cast<const uint32_t*>(cache.rows) + row * L + l);
+        v[i].y = __ldg(cache.scales + row * (L / 2) + (l >> 1));
+        e[i] = __ldg(cache.exps + row);
+      } else if constexpr (T == kE4m3) {
+        const uint2 c = __ldg(static_cast<const uint2*>(cache.rows) + row * L + l);
         v[i].x = c.x, v[i].y = c.y;
-        e[i] = __ldg(pick(p.exps, which) + row);
+        e[i] = __ldg(cache.exps + row);
       } else {
-        v[i] = __ldg(reinterpret_cast<const uint4*>(pick(p.cache, which)) + row * (D / 8) + l);
+        v[i] = __ldg(static_cast<const uint4*>(cache.rows) + row * L + l);
       }
     }
 #pragma unroll
@@ -194,7 +169,19 @@ __global__ void __launch_bounds__(kThreads) kv_cache_read_kernel(ReadParams p) {
       uint4 o = v[i];
       if (at[i] == -2) {
         o = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-      } else if constexpr (FP8) {
+      } else if constexpr (T == kE2m1) {
+        const float s = exp_scale(e[i]);
+        const uint32_t scale = e4m3x2_to_f16x2(v[i].y | v[i].y << 8);
+        uint32_t c[4], w[4];
+        e2m1x8_to_f16x2(v[i].x, c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {   // code times scale is exact in f16
+          const uint32_t h = mul_f16x2(c[j], scale);
+          const float2 f = mul2(__half22float2(*reinterpret_cast<const __half2*>(&h)), make_float2(s, s));
+          w[j] = pack_bf16x2(f.x, f.y);
+        }
+        o = make_uint4(w[0], w[1], w[2], w[3]);
+      } else if constexpr (T == kE4m3) {
         const float s = exp_scale(e[i]);
         const uint32_t c[4] = {v[i].x & 0xffffu, v[i].x >> 16, v[i].y & 0xffffu, v[i].y >> 16};
         uint32_t w[4];
@@ -210,18 +197,33 @@ __global__ void __launch_bounds__(kThreads) kv_cache_read_kernel(ReadParams p) {
   }
 }
 
+template <int D, int T>
+auto* write_kernel_of(bool filled) {
+  return filled ? kv_cache_write_kernel<D, T, true> : kv_cache_write_kernel<D, T, false>;
+}
+template <int D>
+auto* write_kernel(int type, bool filled) {
+  return type == kE2m1 ? write_kernel_of<D, kE2m1>(filled) : type == kE4m3 ? write_kernel_of<D, kE4m3>(filled) : write_kernel_of<D, kBf16>(filled);
+}
+template <int D>
+auto* read_kernel(int type) {
+  return type == kE2m1 ? kv_cache_read_kernel<D, kE2m1> : type == kE4m3 ? kv_cache_read_kernel<D, kE4m3> : kv_cache_read_kernel<D, kBf16>;
+}
+
 }  // namespace
 
 ffa_status check_cache(const ffa_kv_cache* c, PageGeom& g) {
   if (!c) return FFA_ERR_INVALID_ARG;
   if (c->num_pages <= 0 || c->hkv <= 0 || c->page_size <= 0) return FFA_ERR_INVALID_ARG;
   if (c->d != 64 && c->d != 128) return FFA_ERR_UNSUPPORTED;
-  if (c->dtype != FFA_KV_BF16 && c->dtype != FFA_KV_E4M3) return FFA_ERR_UNSUPPORTED;
+  if (c->dtype != FFA_KV_BF16 && c->dtype != FFA_KV_E4M3 && c->dtype != FFA_KV_E2M1) return FFA_ERR_UNSUPPORTED;
   if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1))) return FFA_ERR_UNSUPPORTED;
   // page numbers are int32; a page's rows, and their bytes, fit 32 bits in the kernels' index arithmetic
   if (c->num_pages > (int64_t{1} << 31) || static_cast<int64_t>(c->hkv) * c->page_size > (1 << 22)) return FFA_ERR_OVERFLOW;
   if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return FFA_ERR_INVALID_ARG;
-  if (c->dtype == FFA_KV_E4M3 && (!c->k_exp || !c->v_exp || !aligned16(c->k_exp) || !aligned16(c->v_exp)))
+  if (c->dtype != FFA_KV_BF16 && (!c->k_exp || !c->v_exp || !aligned16(c->k_exp) || !aligned16(c->v_exp)))
+    return FFA_ERR_INVALID_ARG;
+  if (c->dtype == FFA_KV_E2M1 && (!c->k_scale || !c->v_scale || !aligned16(c->k_scale) || !aligned16(c->v_scale)))
     return FFA_ERR_INVALID_ARG;
   g.num_pages = c->num_pages;
   g.hkv = c->hkv;
@@ -257,23 +259,17 @@ ffa_status ffa_kv_cache_write(const void* k, int64_t k_stride, const void* v, in
   p.x[1] = static_cast<const __nv_bfloat16*>(v);
   p.stride[0] = k_stride;
   p.stride[1] = v_stride;
-  p.cache[0] = cache->k;
-  p.cache[1] = cache->v;
-  p.exps[0] = cache->k_exp;
-  p.exps[1] = cache->v_exp;
+  p.cache[0] = {cache->k, cache->k_exp, cache->k_scale};
+  p.cache[1] = {cache->v, cache->v_exp, cache->v_scale};
   p.slots = slots;
   p.rows = static_cast<uint32_t>(tokens * cache->hkv);
   p.heads = fast_div(static_cast<uint32_t>(cache->hkv));
   const int per = kWarps * kUnroll * 256 / cache->d;   // rows a CTA
   const unsigned blocks = (p.rows + per - 1) / per;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool fp8 = cache->dtype == FFA_KV_E4M3;
   const dim3 grid(blocks, 2);
   const bool filled = cache->hkv % (kUnroll * 256 / cache->d) == 0;
-  auto* kernel = cache->d == 128 ? fp8 ? filled ? kv_cache_write_kernel<128, true, true> : kv_cache_write_kernel<128, true, false>
-                                       : filled ? kv_cache_write_kernel<128, false, true> : kv_cache_write_kernel<128, false, false>
-                                 : fp8 ? filled ? kv_cache_write_kernel<64, true, true> : kv_cache_write_kernel<64, true, false>
-                                       : filled ? kv_cache_write_kernel<64, false, true> : kv_cache_write_kernel<64, false, false>;
+  auto* kernel = cache->d == 128 ? write_kernel<128>(cache->dtype, filled) : write_kernel<64>(cache->dtype, filled);
   kernel<<<grid, kThreads, 0, s>>>(p);
   return cuda_status(cudaGetLastError());
 }
@@ -291,15 +287,13 @@ ffa_status ffa_kv_cache_read(const ffa_kv_cache* cache, const int32_t* page_tabl
   if (!k || !v || !aligned16(k) || !aligned16(v)) return FFA_ERR_INVALID_ARG;
   if (total > 0x7fffffff) return FFA_ERR_OVERFLOW;   // cu_seqlens is int32
   const CacheSpans at(*cache);
-  Span in[6] = {{page_table, 4 * (static_cast<int64_t>(batch - 1) * table_stride + max_pages)}, {cu_seqlens, 4 * (int64_t{batch} + 1)}};
+  Span in[8] = {{page_table, 4 * (static_cast<int64_t>(batch - 1) * table_stride + max_pages)}, {cu_seqlens, 4 * (int64_t{batch} + 1)}};
   for (int i = 0; i < at.n; ++i) in[2 + i] = at.s[i];
   const int64_t bytes = 2 * total * cache->hkv * cache->d;
   const Span out[] = {{k, bytes}, {v, bytes}};
   if (any_meet(out, 2, in, 2 + at.n)) return FFA_ERR_INVALID_ARG;
-  p.cache[0] = cache->k;
-  p.cache[1] = cache->v;
-  p.exps[0] = cache->k_exp;
-  p.exps[1] = cache->v_exp;
+  p.cache[0] = {cache->k, cache->k_exp, cache->k_scale};
+  p.cache[1] = {cache->v, cache->v_exp, cache->v_scale};
   p.out[0] = static_cast<__nv_bfloat16*>(k);
   p.out[1] = static_cast<__nv_bfloat16*>(v);
   p.table = page_table;
@@ -311,12 +305,9 @@ ffa_status ffa_kv_cache_read(const ffa_kv_cache* cache, const int32_t* page_tabl
   p.heads = fast_div(static_cast<uint32_t>(cache->hkv));
   p.tile = std::max(8, kReadRows / cache->hkv);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool fp8 = cache->dtype == FFA_KV_E4M3;
   const dim3 grid(static_cast<unsigned>((total + p.tile - 1) / p.tile), 2);
-  if (cache->d == 128)
-    (fp8 ? kv_cache_read_kernel<128, true> : kv_cache_read_kernel<128, false>)<<<grid, kThreads, 0, s>>>(p);
-  else
-    (fp8 ? kv_cache_read_kernel<64, true> : kv_cache_read_kernel<64, false>)<<<grid, kThreads, 0, s>>>(p);
+  auto* kernel = cache->d == 128 ? read_kernel<128>(cache->dtype) : read_kernel<64>(cache->dtype);
+  kernel<<<grid, kThreads, 0, s>>>(p);
   return cuda_status(cudaGetLastError());
 }
 

@@ -52,11 +52,16 @@ FFA_HD bool page_ok(const PageGeom& g, int64_t page) { return page >= 0 && page 
 // Is `slot` (page * page_size + offset) one of the cache's?
 FFA_HD bool slot_ok(const PageGeom& g, int64_t slot) { return slot >= 0 && (slot >> g.page_log2) < g.num_pages; }
 
-// The keys [start, end) of one sequence that a one-token attention reads.  A start below 0 counts as 0; a range without a key is
-// [0, 0), so that nothing is loaded for it; a length that the page table's row cannot hold is marked bad and reads no key.
+// The keys [start, end) of one sequence that a one-token attention reads, and [0, first) beside them.  A start below 0 counts as 0; a
+// range without a key is [0, 0), so that nothing is loaded for it; a length that the page table's row cannot hold is marked bad and
+// reads no key.  Where first keys and a later range both have keys, the whole strips between them are left out: keys are then
+// counted without those `gap` keys, start and end among them, and key k of that count is key k + gap from `first` rounded up to a
+// strip on (key_of).  Otherwise first and gap are 0.
 struct KeyRange {
   int64_t start, end;
   bool bad;
+  int32_t first = 0;
+  int64_t gap = 0;
 };
 FFA_HD KeyRange key_range(int32_t len, int32_t start, int64_t max_pages, int32_t page_log2) {
   KeyRange r;
@@ -67,11 +72,30 @@ FFA_HD KeyRange key_range(int32_t len, int32_t start, int64_t max_pages, int32_t
   r.start = some && start > 0 ? start : 0;
   return r;
 }
+FFA_HD KeyRange key_range(int32_t len, int32_t start, int32_t first, int64_t max_pages, int32_t page_log2, int32_t strip) {
+  KeyRange r = key_range(len, start, max_pages, page_log2);
+  if (r.bad || first <= 0 || len <= 0) return r;
+  if (r.end == 0) {   // no key in the range: the first ones alone
+    r.end = first < len ? first : len;
+  } else if (first >= r.start) {
+    r.start = 0;
+  } else {
+    const int64_t hop = (static_cast<int64_t>(first) + strip - 1) / strip * strip, lo = r.start / strip * strip;
+    r.first = first;
+    r.gap = lo > hop ? lo - hop : 0;
+    r.start -= r.gap;
+    r.end -= r.gap;
+  }
+  return r;
+}
+
+// The key that the first of a strip's counted keys is (`key` a multiple of the strip).
+FFA_HD int64_t key_of(const KeyRange& r, int64_t key) { return key < r.first ? key : key + r.gap; }
 
 // Blocks of `block` keys (a multiple of `strip`, itself one of 16) that cover the range.  Blocks are counted from the range's first key
 // rounded down to `strip`, so that a strip's groups of 16 keys never cross a page.  An empty range has one block, which
 // writes its empty row.
-FFA_HD int64_t range_first(const KeyRange& r, int32_t strip) { return r.start / strip * strip; }
+FFA_HD int64_t range_first(const KeyRange& r, int32_t strip) { return r.first > 0 ? 0 : r.start / strip * strip; }
 FFA_HD int64_t range_blocks(const KeyRange& r, int32_t block, int32_t strip) {
   const int64_t n = (r.end - range_first(r, strip) + block - 1) / block;
   return n > 0 ? n : 1;
@@ -94,6 +118,7 @@ FFA_HD int64_t share_of(int64_t total, int64_t parts, int64_t x) {
 // rows), and 8 lanes reading chunks 2i, 2i + 1 of rows 0, 2, 4, 6 or 1, 3, 5, 7 (keys as the contraction).
 FFA_HD int32_t strip_chunk(int32_t key, int32_t c, int32_t cpr) {
   if (cpr >= 8) return key * cpr + (c ^ ((((key >> 1) & 3) ^ ((key & 1) << 1)) << 1));
+  if (cpr == 2) return (key >> 2) * 8 + (((key ^ (key >> 2)) & 3) << 1) + c;   // four rows a line, read in 8- and 4-byte pieces
   const int32_t line = key >> 1;   // 4 chunks a row: two rows a 128-byte line
   return line * 8 + ((((key & 1) << 2) | c) ^ ((line & 3) << 1));
 }

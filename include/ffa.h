@@ -439,35 +439,46 @@ ffa_status ffa_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, 
 /* Types a key-value cache stores. */
 typedef enum {
   FFA_KV_BF16 = 0,
-  FFA_KV_E4M3 = 1 /* 8-bit codes and one exponent byte a row: value = code * 2^(byte - 127), 0 where byte = 0 */
+  FFA_KV_E4M3 = 1, /* 8-bit codes and one exponent byte a row: value = code * 2^(byte - 127), 0 where byte = 0 */
+  FFA_KV_E2M1 = 4  /* 4-bit codes, an e4m3 scale every 16 columns and one exponent byte a row:
+                      value = code * scale * 2^(byte - 127), 0 where byte = 0 */
 } ffa_kv_dtype;
 
 /* A paged key-value cache (read during the call only).  k and v are
- * [num_pages][hkv][page_size][d] in dtype; k_exp and v_exp (FFA_KV_E4M3 only)
- * [num_pages][hkv][page_size] bytes.  page_size is a power of two in [16, 1024],
- * hkv * page_size at most 2^22, d in {64, 128}; all pointers 16-byte aligned. */
+ * [num_pages][hkv][page_size][d] in dtype; k_exp and v_exp (quantised types)
+ * [num_pages][hkv][page_size] bytes; k_scale and v_scale (FFA_KV_E2M1 only, not
+ * read otherwise) [num_pages][hkv][page_size][d / 16] e4m3 bytes.  An FFA_KV_E2M1
+ * row is d / 2 bytes, column 2i in the low half of byte i and 2i + 1 in the high
+ * one.  page_size is a power of two in [16, 1024], hkv * page_size at most 2^22,
+ * d in {64, 128}; all pointers 16-byte aligned. */
 typedef struct {
   void *k, *v;
   uint8_t *k_exp, *v_exp;
   int64_t num_pages;
   int32_t page_size, hkv, d;
   int32_t dtype; /* ffa_kv_dtype */
+  uint8_t *k_scale, *v_scale;
 } ffa_kv_cache;
 
 /*
  * Write rows of k and v into a paged cache, quantising them where the cache is
- * FFA_KV_E4M3 (no counterpart on the pages).  A row (token, kv head) with
- * largest magnitude a is stored with n the smallest integer >= -126 for which
- * a <= 448 * 2^n: codes e4m3(x / 2^n), exact division and one rounding to
- * nearest even, and the byte n + 127.  A row that holds a NaN or an infinity is
- * stored as NaN throughout.
+ * FFA_KV_E4M3 or FFA_KV_E2M1 (no counterpart on the pages).  A row (token, kv
+ * head) with largest magnitude a is stored as
+ *   FFA_KV_E4M3  n the smallest integer >= -126 for which a <= 448 * 2^n: codes
+ *                e4m3(x / 2^n), exact division and one rounding, and the byte n + 127;
+ *   FFA_KV_E2M1  n the smallest integer >= -126 for which a <= 6 * 448 * 2^n, the
+ *                byte n + 127; every 16 columns with largest magnitude g a scale
+ *                s = e4m3(g / (6 * 2^n)) and codes e2m1(x / (s * 2^n)), those
+ *                beyond 6 as 6, and 0 where s = 0;
+ * every rounding of the exact quotient, to nearest even.  A row that holds a NaN
+ * or an infinity is stored as NaN throughout.
  *
  *  k, v   bf16 [tokens][hkv][d] with token strides k_stride / v_stride as in
  *         ffa_qk_norm_rope; 16-byte aligned, not overlapping the cache
  *  slots  int64 device array [tokens]: page * page_size + offset.  A token
  *         whose slot is negative (padding) or outside the cache is not written.
  *         Slots of one call must differ: a slot that two tokens have is left
- *         undefined (FFA_KV_E4M3: with codes of either and the other's scale),
+ *         undefined (quantised types: with codes of either and the other's scale),
  *         all others are not affected.
  * Errors: FFA_ERR_INVALID_ARG, FFA_ERR_UNSUPPORTED, FFA_ERR_OVERFLOW,
  * FFA_ERR_CUDA.
@@ -478,8 +489,8 @@ ffa_status ffa_kv_cache_write(const void* k, int64_t k_stride, const void* v, in
 /*
  * Read the first cu_seqlens[b + 1] - cu_seqlens[b] keys and values of every
  * sequence back to back, as ffa_fwd takes them (e.g. to prefill a next chunk
- * over a cached prefix with bottom-right CAUSAL slices).  Stored e4m3 values
- * are exact in bf16 (down to bf16's smallest).
+ * over a cached prefix with bottom-right CAUSAL slices).  Stored e4m3 and e2m1
+ * values are exact in bf16 (down to bf16's smallest).
  *
  *  page_table  int32 device array, row b (table_stride apart) the pages of
  *              sequence b in order, max_pages of them
@@ -527,8 +538,8 @@ size_t ffa_fwd_decode_workspace_size(int32_t hq, int32_t hkv, int32_t d);
  * sequences are not affected.
  * Scores, maxima and sums are fp32 (scale * log2(e) must be finite in it); results do not depend on timing, but
  * where a sequence is split depends on the batch's lengths.  A weight e^(s_j - lse) enters the products as a pair of bf16 values
- * (FFA_KV_BF16), or times its value row's scale as one f16 value (FFA_KV_E4M3): 2^-11 of itself, or 2^-35 of the largest that
- * its query has met, whichever is more.  Over an FFA_KV_E4M3 cache, values of q below 2^-31 of their row's largest are rounded.
+ * (FFA_KV_BF16), or times its value row's 2^(byte - 127) as one f16 value (quantised types): 2^-11 of itself, or 2^-35 of the largest
+ * that its query has met, whichever is more.  Over a quantised cache, values of q below 2^-31 of their row's largest are rounded.
  * Errors: FFA_ERR_INVALID_ARG, FFA_ERR_UNSUPPORTED, FFA_ERR_OVERFLOW,
  * FFA_ERR_CUDA.
  */
@@ -536,6 +547,21 @@ ffa_status ffa_fwd_decode(const void* q, int64_t q_stride, const ffa_kv_cache* c
                           int64_t table_stride, int32_t max_pages, int32_t batch, int32_t hq, const int32_t* kv_lens,
                           const int32_t* kv_starts, float scale, const float* sink, void* out, float* lse,
                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ffa_fwd_decode with first keys that stay visible beside the range: the keys of
+ * sequence b are [0, kv_firsts[b]) and [kv_starts[b], kv_lens[b]), each once
+ * where they overlap (no counterpart on the pages; the mask of a new token under
+ * a causal window with first tokens).  Only the pages of those keys are read.
+ *  kv_firsts   int32 device array [batch] or NULL (0); <= 0 counts as 0, and
+ *              kv_lens[b] where it is more
+ * Everything else, and errors, as ffa_fwd_decode (which is this call without it).
+ */
+ffa_status ffa_fwd_decode_window(const void* q, int64_t q_stride, const ffa_kv_cache* cache, const int32_t* page_table,
+                                 int64_t table_stride, int32_t max_pages, int32_t batch, int32_t hq,
+                                 const int32_t* kv_lens, const int32_t* kv_starts, const int32_t* kv_firsts, float scale,
+                                 const float* sink, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                 void* stream);
 
 /* Synchronize `stream`, read and clear the plan's device status word.
  * Returns FFA_ERR_DEVICE_CHECK (and the word in *status_out, if not NULL)

@@ -87,6 +87,60 @@ def stored_values(codes, byte):
     return np.where(codes & 0x80, -mag, mag) * np.where(np.asarray(byte) == 0, 0.0, 2.0 ** (np.asarray(byte, np.float64) - 127))[..., None]
 
 
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def _nearest(grid, z):
+    """Index of the grid value nearest to each z >= 0, ties to the even index, beyond the last the last."""
+    z = np.minimum(np.asarray(z, np.float64), grid[-1])
+    hi = np.clip(np.searchsorted(grid, z), 1, len(grid) - 1)
+    lo = hi - 1
+    dl, dh = z - grid[lo], grid[hi] - z
+    return np.where((dh < dl) | ((dh == dl) & (hi % 2 == 0)), hi, lo)
+
+
+def quantise_row4(row):
+    """(codes uint8 [d], one a byte, scale codes uint8 [d / 16], byte) of one row in 4 bits: the smallest n >= -126 with max|x| <=
+    6 * 448 * 2^n; every 16 values the nearest e4m3 scale to max|x| / (6 * 2^n); the nearest e2m1 codes, all ties to even."""
+    row = np.asarray(row, np.float64)
+    groups = row.reshape(-1, 16)
+    if not np.isfinite(row).all():
+        return np.zeros(row.shape, np.uint8), np.full(len(groups), 0x7f, np.uint8), 127
+    top, n = np.abs(row).max(), -126
+    while top > 2688.0 * 2.0 ** n:
+        n += 1
+    grid = e4m3_values()
+    scales = _nearest(grid, np.abs(groups).max(1) / 6.0 / 2.0 ** n)
+    s = grid[scales][:, None]
+    codes = np.where(s > 0, _nearest(E2M1, np.abs(groups) / 2.0 ** n / np.where(s > 0, s, 1.0)), 0)
+    return (codes + 8 * np.signbit(groups)).astype(np.uint8).reshape(-1), scales.astype(np.uint8), n + 127
+
+
+def packed_codes(codes):
+    """Codes [..., d] as the bytes [..., d / 2] a cache holds: the even columns in the lower halves."""
+    return codes[..., 0::2] | codes[..., 1::2] << 4
+
+
+def stored_values4(packed, scales, byte):
+    """What 4-bit rows [..., d / 2] with scale codes [..., d / 16] and exponent bytes [...] stand for; byte 0 stands for 0."""
+    packed = np.asarray(packed)
+    codes = np.stack([packed & 15, packed >> 4], -1).reshape(packed.shape[:-1] + (-1,))
+    mag = E2M1[codes & 7] * np.repeat(stored_values(scales, np.full(np.shape(byte), 127)), 16, -1)
+    return np.where(codes & 8, -mag, mag) * np.where(np.asarray(byte) == 0, 0.0, 2.0 ** (np.asarray(byte, np.float64) - 127))[..., None]
+
+
+def visible_keys(length, start=0, first=0):
+    """The keys of one sequence that a new token sees: [0, first) and [start, length), each once."""
+    return [j for j in range(max(0, length)) if j >= start or j < first]
+
+
+def gather_keys(values, page_table_row, keys):
+    """Those rows of one sequence, [n, hkv, d], of values [pages, hkv, page, d]."""
+    page = values.shape[2]
+    rows = [values[page_table_row[j // page], :, j % page] for j in keys]
+    return np.stack(rows) if rows else np.zeros((0, values.shape[1], values.shape[3]))
+
+
 def gather_rows(values, page_table_row, start, end):
     """Rows [start, end) of one sequence, [n, hkv, d], of values [pages, hkv, page, d]."""
     page = values.shape[2]

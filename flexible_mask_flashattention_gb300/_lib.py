@@ -123,7 +123,15 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.ffa_qk_norm_rope_bwd_workspace_size.argtypes = [_i32]
     lib.ffa_qk_norm_rope_bwd.restype = ctypes.c_int
     lib.ffa_qk_norm_rope_bwd.argtypes = norm_args + [_vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    axes_args = norm_args + [_i32, _vp]
+    lib.ffa_qk_norm_rope_axes.restype = ctypes.c_int
+    lib.ffa_qk_norm_rope_axes.argtypes = axes_args + [_vp, _vp, _vp]
+    lib.ffa_qk_norm_rope_axes_bwd.restype = ctypes.c_int
+    lib.ffa_qk_norm_rope_axes_bwd.argtypes = axes_args + [_vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
     cache = ctypes.POINTER(KVCacheC)
+    lib.ffa_kv_cache_append.restype = ctypes.c_int
+    lib.ffa_kv_cache_append.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i32, _vp, _vp, ctypes.c_float, _vp, _i64, _i32,
+                                        _i32, _vp, _i32, _vp, _vp, cache, _vp, _vp]
     lib.ffa_kv_cache_write.restype = ctypes.c_int
     lib.ffa_kv_cache_write.argtypes = [_vp, _i64, _vp, _i64, _i64, _vp, cache, _vp]
     lib.ffa_kv_cache_read.restype = ctypes.c_int
@@ -647,30 +655,56 @@ def _page_table(t, batch: int, dev):
     return s[0] if batch > 1 else width, width
 
 
-def _norm_rope_inputs(q, k, q_weight, k_weight, cos_sin, positions, dev):
-    """Checked (q's stride, k's stride, tokens, hq, hkv, d, max_pos, rot_dim) of the inputs both directions share."""
-    if not isinstance(k, torch.Tensor) or not isinstance(cos_sin, torch.Tensor):
-        raise FFAError(1, "k and cos_sin must be CUDA tensors")
-    tokens, hq, d = _dims(q, "q", 3)
-    hkv = _dims(k, "k", 3)[1]
+def _rotation_inputs(q_weight, k_weight, cos_sin, positions, axes, tokens, d, dev):
+    """Checked (q_weight, k_weight pointers, max_pos, rot_dim, number of axes, bytes of the pairs' axes); 0 axes: one position a token,
+    and weights."""
+    if not isinstance(cos_sin, torch.Tensor):
+        raise FFAError(1, "cos_sin must be a CUDA tensor")
     table = _dims(cos_sin, "cos_sin", 2)
     f32 = torch.float32
+    bare = q_weight is None and k_weight is None
+    if not bare:
+        _check_dense(q_weight, f32, (d,), dev, "q_weight")
+        _check_dense(k_weight, f32, (d,), dev, "k_weight")
+    n, pairs = 1 if bare else 0, None
+    if axes is None:
+        _check_dense(positions, torch.int32, (tokens,), dev, "positions")
+    else:
+        if not isinstance(positions, torch.Tensor):
+            raise FFAError(1, "positions must be a CUDA tensor")
+        n = _dims(positions, "positions", 2)[0]
+        _check_dense(positions, torch.int32, (n, tokens), dev, "positions")
+        try:
+            pairs = bytes(axes)
+        except (TypeError, ValueError):
+            raise FFAError(1, "axes must be a sequence of small numbers")
+        if n < 1 or len(pairs) * 2 != table[1]:
+            raise FFAError(1, f"axes must hold one of {n} axes for each of {table[1] // 2} pairs")
+    _check_dense(cos_sin, f32, table, dev, "cos_sin")
+    return None if bare else q_weight.data_ptr(), None if bare else k_weight.data_ptr(), table[0], table[1], n, pairs
+
+
+def _norm_rope_inputs(q, k, q_weight, k_weight, cos_sin, positions, axes, dev):
+    """Checked (q's stride, k's stride, tokens, hq, hkv, d, and those of the rotation) of the inputs both directions share."""
+    if not isinstance(k, torch.Tensor):
+        raise FFAError(1, "k must be a CUDA tensor")
+    tokens, hq, d = _dims(q, "q", 3)
+    hkv = _dims(k, "k", 3)[1]
     qs = _rows_stride(q, "q", (tokens, hq, d), dev)
     ks = _rows_stride(k, "k", (tokens, hkv, d), dev)
-    _check_dense(q_weight, f32, (d,), dev, "q_weight")
-    _check_dense(k_weight, f32, (d,), dev, "k_weight")
-    _check_dense(positions, torch.int32, (tokens,), dev, "positions")
-    _check_dense(cos_sin, f32, table, dev, "cos_sin")
-    return qs, ks, tokens, hq, hkv, d, table[0], table[1]
+    return (qs, ks, tokens, hq, hkv, d) + _rotation_inputs(q_weight, k_weight, cos_sin, positions, axes, tokens, d, dev)
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6, interleaved: bool = False,
-                 q_out=None, k_out=None, stream=None):
+                 q_out=None, k_out=None, stream=None, axes=None):
     """(q_out, k_out): every head row of q [S, Hq, d] and k [S, Hkv, d] divided by its RMS, times its
     weight [d] (fp32), and rotated by its token's position (int32 [S]) with cos_sin [max_pos, rot_dim]
-    (fp32; the cosines first).  q and k may be views of one projection's output."""
+    (fp32; the cosines first).  q and k may be views of one projection's output.  Both weights None: no norm, the rotation
+    alone.  axes, rot_dim / 2 numbers under A <= 4: positions are [A, S], and rotation pair i goes by positions[axes[i]]
+    (sections such as 16 * [0] + 24 * [1] + 24 * [2], axes in turns, or any other order)."""
     dev = _device(q, "q")
-    qs, ks, tokens, hq, hkv, d, max_pos, rot = _norm_rope_inputs(q, k, q_weight, k_weight, cos_sin, positions, dev)
+    qs, ks, tokens, hq, hkv, d, qw, kw, max_pos, rot, n, pairs = _norm_rope_inputs(q, k, q_weight, k_weight, cos_sin, positions,
+                                                                                   axes, dev)
     handle, context = _on(stream, dev, q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out)
     bf16, qshape, kshape = torch.bfloat16, (tokens, hq, d), (tokens, hkv, d)
     if q_out is None:
@@ -681,33 +715,50 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6
         k_out = _empty(context, kshape, bf16)
     else:
         _check_dense(k_out, bf16, kshape, dev, "k_out")
-    _check(load_library().ffa_qk_norm_rope(
-        q.data_ptr(), qs, k.data_ptr(), ks, tokens, hq, hkv, d, q_weight.data_ptr(), k_weight.data_ptr(), eps,
-        cos_sin.data_ptr(), max_pos, rot, bool(interleaved), positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
-        handle), "ffa_qk_norm_rope")
+    if n:
+        _check(load_library().ffa_qk_norm_rope_axes(
+            q.data_ptr(), qs, k.data_ptr(), ks, tokens, hq, hkv, d, qw, kw, eps, cos_sin.data_ptr(), max_pos, rot, bool(interleaved),
+            positions.data_ptr(), n, pairs, q_out.data_ptr(), k_out.data_ptr(), handle), "ffa_qk_norm_rope_axes")
+    else:
+        _check(load_library().ffa_qk_norm_rope(
+            q.data_ptr(), qs, k.data_ptr(), ks, tokens, hq, hkv, d, qw, kw, eps, cos_sin.data_ptr(), max_pos, rot, bool(interleaved),
+            positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), handle), "ffa_qk_norm_rope")
     return q_out, k_out
 
 
 def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk_out, eps: float = 1e-6,
-                     interleaved: bool = False, workspace=None, stream=None):
-    """dq, dk (bf16) and dq_weight, dk_weight (fp32 [d]) of qk_norm_rope, from the gradients of its outputs."""
+                     interleaved: bool = False, workspace=None, stream=None, axes=None):
+    """dq, dk (bf16) and dq_weight, dk_weight (fp32 [d]; None without weights) of qk_norm_rope, from the gradients of its
+    outputs."""
     dev = _device(q, "q")
-    qs, ks, tokens, hq, hkv, d, max_pos, rot = _norm_rope_inputs(q, k, q_weight, k_weight, cos_sin, positions, dev)
+    qs, ks, tokens, hq, hkv, d, qw, kw, max_pos, rot, n, pairs = _norm_rope_inputs(q, k, q_weight, k_weight, cos_sin, positions,
+                                                                                   axes, dev)
     bf16, f32, qshape, kshape = torch.bfloat16, torch.float32, (tokens, hq, d), (tokens, hkv, d)
     _check_dense(dq_out, bf16, qshape, dev, "dq_out")
     _check_dense(dk_out, bf16, kshape, dev, "dk_out")
     handle, context = _on(stream, dev, q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk_out, workspace)
-    dq, dk = _empty(context, qshape, bf16), _empty(context, kshape, bf16)
+    dq, dk, dqw, dkw = _empty(context, qshape, bf16), _empty(context, kshape, bf16), None, None
+    if workspace is not None:
+        _check_workspace(workspace, dev)
+    if qw is None:
+        _check(load_library().ffa_qk_norm_rope_axes_bwd(
+            q.data_ptr(), qs, k.data_ptr(), ks, tokens, hq, hkv, d, None, None, eps, cos_sin.data_ptr(), max_pos, rot,
+            bool(interleaved), positions.data_ptr(), n, pairs, dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+            None, None, None, 0, handle), "ffa_qk_norm_rope_axes_bwd")
+        return dq, dk, None, None
     dqw, dkw = _empty(context, (d,), f32), _empty(context, (d,), f32)
     if workspace is None:
         workspace = _empty(context, (qk_norm_rope_bwd_workspace_size(d),), torch.uint8)
+    if n:
+        _check(load_library().ffa_qk_norm_rope_axes_bwd(
+            q.data_ptr(), qs, k.data_ptr(), ks, tokens, hq, hkv, d, qw, kw, eps, cos_sin.data_ptr(), max_pos, rot, bool(interleaved),
+            positions.data_ptr(), n, pairs, dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(),
+            dkw.data_ptr(), workspace.data_ptr(), workspace.numel(), handle), "ffa_qk_norm_rope_axes_bwd")
     else:
-        _check_workspace(workspace, dev)
-    _check(load_library().ffa_qk_norm_rope_bwd(
-        q.data_ptr(), qs, k.data_ptr(), ks, tokens, hq, hkv, d, q_weight.data_ptr(), k_weight.data_ptr(), eps,
-        cos_sin.data_ptr(), max_pos, rot, bool(interleaved), positions.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(),
-        dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), workspace.data_ptr(), workspace.numel(), handle),
-        "ffa_qk_norm_rope_bwd")
+        _check(load_library().ffa_qk_norm_rope_bwd(
+            q.data_ptr(), qs, k.data_ptr(), ks, tokens, hq, hkv, d, qw, kw, eps, cos_sin.data_ptr(), max_pos, rot, bool(interleaved),
+            positions.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(),
+            workspace.data_ptr(), workspace.numel(), handle), "ffa_qk_norm_rope_bwd")
     return dq, dk, dqw, dkw
 
 
@@ -733,6 +784,36 @@ def kv_cache_write(k, v, k_cache, v_cache, slots, k_exp=None, v_exp=None, stream
     handle, _ = _on(stream, dev, k, v, k_cache, v_cache, slots, k_exp, v_exp, k_scale, v_scale)
     _check(load_library().ffa_kv_cache_write(k.data_ptr(), ks, v.data_ptr(), vs, tokens, slots.data_ptr(),
                                              ctypes.byref(cache), handle), "ffa_kv_cache_write")
+
+
+def kv_cache_append(q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_cache, slots, eps: float = 1e-6,
+                    interleaved: bool = False, k_exp=None, v_exp=None, k_scale=None, v_scale=None, axes=None, q_out=None,
+                    stream=None):
+    """q_out [T, Hq, d]: what qk_norm_rope gives for q, with the keys it gives for k and the values v [T, Hkv, d] written into the
+    cache as kv_cache_write does, in one pass and to the same bits.  Weights, positions and axes as in qk_norm_rope; slots and
+    caches as in kv_cache_write."""
+    dev = _device(k_cache, "k_cache")
+    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp, k_scale, v_scale, dev)
+    if not isinstance(q, torch.Tensor) or not isinstance(slots, torch.Tensor):
+        raise FFAError(1, "q and slots must be CUDA tensors")
+    tokens, hq, d = _dims(q, "q", 3)
+    shape = (tokens, cache.hkv, cache.d)
+    qs = _rows_stride(q, "q", (tokens, hq, cache.d), dev)
+    ks = _rows_stride(k, "k", shape, dev)
+    vs = _rows_stride(v, "v", shape, dev)
+    qw, kw, max_pos, rot, n, pairs = _rotation_inputs(q_weight, k_weight, cos_sin, positions, axes, tokens, d, dev)
+    _check_dense(slots, torch.int64, (tokens,), dev, "slots")
+    handle, context = _on(stream, dev, q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_cache, slots, k_exp, v_exp,
+                          k_scale, v_scale, q_out)
+    if q_out is None:
+        q_out = _empty(context, (tokens, hq, d), torch.bfloat16)
+    else:
+        _check_dense(q_out, torch.bfloat16, (tokens, hq, d), dev, "q_out")
+    _check(load_library().ffa_kv_cache_append(
+        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, tokens, hq, qw, kw, eps, cos_sin.data_ptr(), max_pos, rot,
+        bool(interleaved), positions.data_ptr(), n or 1, pairs, slots.data_ptr(), ctypes.byref(cache), q_out.data_ptr(), handle),
+        "ffa_kv_cache_append")
+    return q_out
 
 
 def kv_cache_read(k_cache, v_cache, page_table, cu_seqlens, total: int, k=None, v=None, k_exp=None, v_exp=None,

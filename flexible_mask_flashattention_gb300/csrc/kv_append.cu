@@ -1,0 +1,198 @@
+// Norm and rotation of new tokens' q and k, and their keys and values into the paged key-value cache, in one pass.
+//
+// What qk_norm_rope (without weights: the rotation alone) and then kv_cache_write compute, rounding for rounding: a key is rounded to bf16
+// and then, where the cache is quantised, to its type; the rows in the cache are the same bits as the two calls leave, so that a prompt
+// written one way and steps written the other agree.
+//
+// Bound by HBM: q in and out, k and v in, their stored rows out; the two calls also write k and read it again, 4 d bytes a k row, and are
+// two launches and 15 us of host time to one's.  The walk over tokens and heads, the copies to shared memory and the rotation are norm_rope.cu's, with v
+// as a third tensor behind q and k.  A normalised key's columns lie in its lanes as rotation partners; it goes back to its place in
+// shared memory and is read from there in the order that kv_cache.h's rows want, 8 neighbouring columns a lane.
+#include "kv_cache.h"
+#include "norm_rope.cuh"
+
+namespace ffa {
+namespace {
+
+struct AppendParams : NormRopeParams {
+  CacheRows cache[2];
+  const int64_t* slots;
+  PageGeom geom;
+};
+
+template <int D, bool INTER, int T>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendParams p) {
+  constexpr int L = D / 8;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* weights = reinterpret_cast<float*>(smem);   // [2][D]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (L - 1), sub = lane / L;
+  const Stages<D, false> st{smem + 2 * D * 4 + warp * kStages * Stages<D, false>::stage_bytes(p.unit), p.unit};
+  const Columns<D, INTER> cols(l, p.rot);
+  const int swap = Stages<D, false>::swap(sub), natural = (16 * l) ^ swap;
+  auto copy = [&](int stage, const UnitWalk<D, true>& w) {
+    copy_unit<D, false, true>(p, st, stage, w);
+    const UnitPart v = part_of(p, w.c, 2);   // a value goes into the cache whatever its token's positions
+    if (v.n > 0)
+      copy_rows<D, false>(smem_u32(st.rows(stage, sub, 0)) + v.first * 512 + natural,
+                          p.x[2] + (w.has ? w.token : 0) * p.x_stride[2] + v.head * D + 8 * l, v.n, w.has ? 16 : 0);
+  };
+  UnitWalk<D, true> cur, ld;
+  cur.init(p, warp, sub);
+  ld = cur;
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) {
+    if (ld.left > 0) copy(s, ld);
+    cp_async_commit();
+    ld.next(p);
+    ld.read_pos(p);
+  }
+  for (int i = threadIdx.x; i < 2 * D; i += kThreads) weights[i] = p.w[0] ? p.w[i / D][i % D] : 1.f;
+  __syncthreads();
+  const int page_rows = p.geom.hkv << p.geom.page_log2, page_mask = (1 << p.geom.page_log2) - 1;
+  int stage = 0, fill = kStages - 1;
+  for (int todo = cur.left + warp; todo > 0; todo -= kWarps, cur.next(p)) {
+    __syncthreads();   // the warps' copies go out together: one run of memory
+    if (cur.left <= 0) continue;
+    cur.read_pos(p);   // again: from L1
+    const int64_t slot = cur.has ? __ldg(p.slots + cur.token) : -1;
+    if (ld.left > 0) copy(fill, ld);
+    cp_async_commit();
+    ld.next(p);
+    ld.read_pos(p);   // a unit ahead of its use
+    cp_async_wait<kStages - 1>();
+    __syncwarp();   // lanes read what others copied
+    const int pos = cur.pos;
+    const bool live = pos >= 0 && pos < p.max_pos, keep = slot_ok(p.geom, slot);
+    const int64_t base = keep ? (slot >> p.geom.page_log2) * page_rows + (slot & page_mask) : 0;   // head 0's row
+    // a padded token (negative position) gives zeros, one behind the table NaN
+    const uint32_t fill_bits = pos < 0 ? 0u : 0x7fff7fffu;
+    const uint4 constant = make_uint4(fill_bits, fill_bits, fill_bits, fill_bits);
+    Rotation<INTER, false> rot;
+    rot.load(st.table(stage, sub), live ? p.rot : 0, l);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const UnitPart u = part_of(p, cur.c, t);
+      if (u.n <= 0) continue;
+      __nv_bfloat16* out = p.out[0] + (cur.token * p.heads[0] + u.head) * D;   // q's
+      uint8_t* in = st.rows(stage, sub, 0) + u.first * 512;
+      // coefficients with the weights: out_j = r (x_j a_j + partner_j b_j)
+      float2 w[4], a[4], b[4];
+      cols.load(weights + t * D, w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a[j] = mul2(w[j], rot.c(j)), b[j] = mul2(partner<INTER>(w, j), rot.s(j));
+      auto some = [&](auto count, int i) {   // `count` heads from i on, their sums side by side
+        constexpr int N = decltype(count)::value;
+        float2 f[N][4];
+        float r[N];
+        uint4 v[N];
+#pragma unroll
+        for (int h = 0; h < N; ++h) {
+          unpack8(cols.load(in + (i + h) * 512, swap), f[h]);
+          float2 ss = mul2(f[h][0], f[h][0]);
+#pragma unroll
+          for (int j = 1; j < 4; ++j) ss = fma2(f[h][j], f[h][j], ss);
+          r[h] = ss.x + ss.y;
+        }
+        row_sums<D>(r);
+#pragma unroll
+        for (int h = 0; h < N; ++h) {
+          r[h] = p.w[0] ? rsqrtf(r[h] * (1.f / D) + p.eps) : 1.f;
+          float2 o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            o[j] = mul2(fma2(f[h][j], a[j], mul2(partner<INTER>(f[h], j), b[j])), make_float2(r[h], r[h]));
+          v[h] = live ? pack8(o) : constant;
+          if (t == 0 && cur.has) cols.store(out + (i + h) * D, v[h]);
+          if (t == 1 && !INTER) cols.store(in + (i + h) * 512, swap, v[h]);
+        }
+        if (t == 1) {
+          if constexpr (!INTER) {
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < N; ++h) v[h] = *reinterpret_cast<const uint4*>(in + (i + h) * 512 + natural);
+          }
+          StoredRow row[N];
+#pragma unroll
+          for (int h = 0; h < N; ++h) row[h] = make_row<D, T>(v[h]);
+#pragma unroll
+          for (int h = 0; h < N; ++h)
+            if (keep) put_row<D, T>(row[h], base + (static_cast<int64_t>(u.head + i + h) << p.geom.page_log2), l, p.cache[0]);
+        }
+      };
+      in_batches<3>(u.n, some);
+    }
+    const UnitPart u = part_of(p, cur.c, 2);
+    if (u.n > 0) {
+      const uint8_t* in = st.rows(stage, sub, 0) + u.first * 512 + natural;
+      auto some = [&](auto count, int i) {
+        constexpr int N = decltype(count)::value;
+        StoredRow row[N];
+#pragma unroll
+        for (int h = 0; h < N; ++h) row[h] = make_row<D, T>(*reinterpret_cast<const uint4*>(in + (i + h) * 512));
+#pragma unroll
+        for (int h = 0; h < N; ++h)
+          if (keep) put_row<D, T>(row[h], base + (static_cast<int64_t>(u.head + i + h) << p.geom.page_log2), l, p.cache[1]);
+      };
+      in_batches<3>(u.n, some);
+    }
+    __syncwarp();   // the stage has been read by every lane before the next iteration refills it
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    fill = fill + 1 == kStages ? 0 : fill + 1;
+  }
+}
+
+template <int D, bool INTER, int T>
+ffa_status launch(const AppendParams& p, int64_t tokens, cudaStream_t s) {
+  static std::atomic<int> known[kDevices];
+  static std::atomic<bool> raised[kDevices];
+  int ctas = 0;
+  return launch_units<D, false>(kv_append_kernel<D, INTER, T>, p, tokens, s, &ctas, known, raised);
+}
+template <int D, bool INTER>
+ffa_status launch_type(const AppendParams& p, int type, int64_t tokens, cudaStream_t s) {
+  return type == kE2m1 ? launch<D, INTER, kE2m1>(p, tokens, s) : type == kE4m3 ? launch<D, INTER, kE4m3>(p, tokens, s) : launch<D, INTER, kBf16>(p, tokens, s);
+}
+
+}  // namespace
+}  // namespace ffa
+
+using namespace ffa;
+
+extern "C" {
+
+ffa_status ffa_kv_cache_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                               int64_t tokens, int32_t hq, const float* q_weight, const float* k_weight, float eps,
+                               const float* cos_sin, int64_t max_pos, int32_t rot_dim, int32_t interleaved,
+                               const int32_t* positions, int32_t n_axes, const uint8_t* pair_axis, const int64_t* slots,
+                               const ffa_kv_cache* cache, void* q_out, void* stream) {
+  AppendParams p{};
+  ffa_status st = check_cache(cache, p.geom);
+  if (st != FFA_OK) return st;
+  if (n_axes <= 0) return FFA_ERR_INVALID_ARG;
+  const int32_t d = cache->d, hkv = cache->hkv;
+  st = check_common(q, q_stride, k, k_stride, tokens, hq, hkv, d, q_weight, k_weight, eps, cos_sin, max_pos, rot_dim, positions, n_axes,
+                    pair_axis, p);
+  if (st != FFA_OK) return st;
+  if (tokens == 0) return FFA_OK;
+  if (!v || !slots || !q_out || !aligned16(v) || !aligned16(q_out) || (reinterpret_cast<uintptr_t>(slots) & 7u)) return FFA_ERR_INVALID_ARG;
+  if (v_stride % 8 != 0 || (tokens > 1 && v_stride < static_cast<int64_t>(hkv) * d)) return FFA_ERR_INVALID_ARG;
+  const CacheSpans at(*cache);
+  Span outs[7] = {{q_out, 2 * tokens * hq * d}};
+  for (int i = 0; i < at.n; ++i) outs[1 + i] = at.s[i];
+  const Span in[] = {{q, span_bytes(tokens, q_stride, hq, d)}, {k, span_bytes(tokens, k_stride, hkv, d)}, {v, span_bytes(tokens, v_stride, hkv, d)},
+                     {q_weight, q_weight ? 4 * d : 0}, {k_weight, k_weight ? 4 * d : 0}, {cos_sin, 4 * max_pos * rot_dim},
+                     {positions, 4 * tokens * n_axes}, {slots, 8 * tokens}};
+  if (any_meet(outs, 1 + at.n, in, 8)) return FFA_ERR_INVALID_ARG;
+  p.x[2] = static_cast<const __nv_bfloat16*>(v);
+  p.x_stride[2] = v_stride;
+  p.heads[2] = hkv;
+  p.out[0] = static_cast<__nv_bfloat16*>(q_out);
+  p.cache[0] = {cache->k, cache->k_exp, cache->k_scale};
+  p.cache[1] = {cache->v, cache->v_exp, cache->v_scale};
+  p.slots = slots;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d == 128) return interleaved ? launch_type<128, true>(p, cache->dtype, tokens, s) : launch_type<128, false>(p, cache->dtype, tokens, s);
+  return interleaved ? launch_type<64, true>(p, cache->dtype, tokens, s) : launch_type<64, false>(p, cache->dtype, tokens, s);
+}
+
+}  // extern "C"

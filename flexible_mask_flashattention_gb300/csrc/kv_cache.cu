@@ -88,7 +88,10 @@ __global__ void __launch_bounds__(kThreads) kv_cache_write_kernel(WriteParams p)
   }
   const CacheRows cache = pick(p.cache, which);
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) store_row<D, T>(v[i], FILLED || dst[i] >= 0, dst[i], l, cache);
+  for (int i = 0; i < kUnroll; ++i) {
+    const StoredRow r = make_row<D, T>(v[i]);
+    if (FILLED || dst[i] >= 0) put_row<D, T>(r, dst[i], l, cache);
+  }
 }
 
 struct ReadParams {

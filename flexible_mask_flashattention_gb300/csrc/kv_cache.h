@@ -98,26 +98,33 @@ struct CacheRows {
   uint8_t* scales;
 };
 
-// Store one row of bf16 values, 8 a lane (lane `l` of the D / 8 that hold it has columns 8l .. 8l + 7), at `row` of the cache if `act`.
-// All lanes of the warp take part.
+// A row as a cache stores it, 8 values a lane: lane `l` of the D / 8 that hold the row has columns 8l .. 8l + 7.
+struct StoredRow {
+  uint4 codes;      // e4m3: x, y; e2m1: x
+  uint32_t scale;   // e2m1: of this lane's 16 columns (lanes 2i and 2i + 1 alike)
+  int byte;
+};
+
+// One row of bf16 values in its stored form.  All lanes of the warp take part.
 template <int D, int T>
-__device__ __forceinline__ void store_row(const uint4& v, bool act, int64_t row, int l, const CacheRows& c) {
+__device__ __forceinline__ StoredRow make_row(const uint4& v) {
   constexpr int L = D / 8;
+  StoredRow r{};
   if constexpr (T == kBf16) {
-    if (act) reinterpret_cast<uint4*>(c.rows)[row * L + l] = v;
+    r.codes = v;
   } else {
     // bf16 magnitudes order as 15-bit integers: the row's largest, two at a time
     uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
     m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    uint32_t g = max(m & 0xffffu, m >> 16);   // of 16 columns
+    const uint32_t g = max(m & 0xffffu, m >> 16);   // of 16 columns
 #pragma unroll
     for (int o = L / 2; o > 1; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
     m = max(m & 0xffffu, m >> 16);
     const bool finite = m < 0x7f80u;
     // max|x| = 1.f * 2^(e - 127).  448 = 1.75 * 2^8: the scale's byte is e - 8, one more where 1.f > 1.75 (mantissa 0x60).
     // 6 * 448 = 1.3125 * 2^11: e - 11, one more where 1.f > 1.3125 (mantissa 0x28).
-    const int byte = !finite ? 127 : T == kE4m3 ? max(static_cast<int>((m + 0x1fu) >> 7) - 8, 1) : max(static_cast<int>((m + 0x57u) >> 7) - 11, 1);
-    const float inv = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);   // 2^-(byte - 127), exact
+    r.byte = !finite ? 127 : T == kE4m3 ? max(static_cast<int>((m + 0x1fu) >> 7) - 8, 1) : max(static_cast<int>((m + 0x57u) >> 7) - 11, 1);
+    const float inv = __uint_as_float(static_cast<uint32_t>(254 - r.byte) << 23);   // 2^-(byte - 127), exact
     const uint32_t u4[4] = {v.x, v.y, v.z, v.w};
     float2 y[4];
 #pragma unroll
@@ -127,22 +134,35 @@ __device__ __forceinline__ void store_row(const uint4& v, bool act, int64_t row,
       uint32_t x[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) x[j] = e4m3x2(y[j]);
-      uint2 codes = make_uint2(x[0] | x[1] << 16, x[2] | x[3] << 16);
-      if (!finite) codes = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-      if (act) reinterpret_cast<uint2*>(c.rows)[row * L + l] = codes;
+      r.codes.x = finite ? x[0] | x[1] << 16 : 0x7f7f7f7fu;
+      r.codes.y = finite ? x[2] | x[3] << 16 : 0x7f7f7f7fu;
     } else {
       const float sixth = __uint_as_float(g << 16) * inv * (1.f / 6.f);
       const uint32_t code = e4m3x2(round12(make_float2(sixth, 0.f))) & 0xffu;
-      const float s = e4m3x2_to_float2(code).x, r = s > 0.f ? __fdividef(1.f, s) : 0.f;
+      const float s = e4m3x2_to_float2(code).x, over = s > 0.f ? __fdividef(1.f, s) : 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = round12(mul2(y[j], make_float2(r, r)));
-      const uint32_t codes = finite ? e2m1x8(y) : 0u;
-      if (act) {
-        reinterpret_cast<uint32_t*>(c.rows)[row * L + l] = codes;
-        if (!(l & 1)) c.scales[row * (L / 2) + (l >> 1)] = static_cast<uint8_t>(finite ? code : 0x7fu);
-      }
+      for (int j = 0; j < 4; ++j) y[j] = round12(mul2(y[j], make_float2(over, over)));
+      r.codes.x = finite ? e2m1x8(y) : 0u;
+      r.scale = finite ? code : 0x7fu;
     }
-    if (act && l == 0) c.exps[row] = static_cast<uint8_t>(byte);
+  }
+  return r;
+}
+
+// Write it at `row` of the cache.
+template <int D, int T>
+__device__ __forceinline__ void put_row(const StoredRow& r, int64_t row, int l, const CacheRows& c) {
+  constexpr int L = D / 8;
+  if constexpr (T == kBf16) {
+    reinterpret_cast<uint4*>(c.rows)[row * L + l] = r.codes;
+  } else {
+    if constexpr (T == kE4m3) {
+      reinterpret_cast<uint2*>(c.rows)[row * L + l] = make_uint2(r.codes.x, r.codes.y);
+    } else {
+      reinterpret_cast<uint32_t*>(c.rows)[row * L + l] = r.codes.x;
+      if (!(l & 1)) c.scales[row * (L / 2) + (l >> 1)] = static_cast<uint8_t>(r.scale);
+    }
+    if (l == 0) c.exps[row] = static_cast<uint8_t>(r.byte);
   }
 }
 

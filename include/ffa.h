@@ -436,6 +436,37 @@ ffa_status ffa_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, 
                                 float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
                                 void* stream);
 
+/*
+ * ffa_qk_norm_rope with positions of several axes (e.g. time, height and width of
+ * a video's patches; no counterpart on the pages): rotation pair i turns by the
+ * angle of position positions[pair_axis[i]][token].
+ *
+ *  positions  int32 device array [n_axes][tokens]; n_axes in [1, 4].  A token with
+ *             a negative position on any axis is padding; otherwise one with a
+ *             position >= max_pos on any axis gets NaN outputs.
+ *  pair_axis  host array [rot_dim / 2] of axes in [0, n_axes), read during the
+ *             call: sections of neighbouring pairs, axes in turns, or any other
+ *             order.  NULL for n_axes = 1.
+ *  q_weight, k_weight  both NULL: no norm, the rotation alone
+ * Everything else as ffa_qk_norm_rope (n_axes > 4: FFA_ERR_UNSUPPORTED).
+ */
+ffa_status ffa_qk_norm_rope_axes(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int64_t tokens,
+                                 int32_t hq, int32_t hkv, int32_t d, const float* q_weight, const float* k_weight,
+                                 float eps, const float* cos_sin, int64_t max_pos, int32_t rot_dim, int32_t interleaved,
+                                 const int32_t* positions, int32_t n_axes, const uint8_t* pair_axis, void* q_out,
+                                 void* k_out, void* stream);
+
+/* Backward pass of ffa_qk_norm_rope_axes, as ffa_qk_norm_rope_bwd.  Without weights
+ * q, k, dq_weight, dk_weight and workspace are not used and may be NULL, and a
+ * position >= max_pos makes its rows' gradients NaN. */
+ffa_status ffa_qk_norm_rope_axes_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int64_t tokens,
+                                     int32_t hq, int32_t hkv, int32_t d, const float* q_weight, const float* k_weight,
+                                     float eps, const float* cos_sin, int64_t max_pos, int32_t rot_dim,
+                                     int32_t interleaved, const int32_t* positions, int32_t n_axes,
+                                     const uint8_t* pair_axis, const void* dq_out, const void* dk_out, void* dq,
+                                     void* dk, float* dq_weight, float* dk_weight, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
 /* Types a key-value cache stores. */
 typedef enum {
   FFA_KV_BF16 = 0,
@@ -485,6 +516,29 @@ typedef struct {
  */
 ffa_status ffa_kv_cache_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t tokens,
                               const int64_t* slots, const ffa_kv_cache* cache, void* stream);
+
+/*
+ * Norm and rotation of new tokens' q and k (ffa_qk_norm_rope_axes), with the
+ * rotated keys and the values written into a paged cache (ffa_kv_cache_write), in
+ * one pass (no counterpart on the pages).  q_out and the cache get the same bits
+ * as from those two calls: keys are rounded to bf16, then to the cache's type.
+ *
+ *  q, k, v    bf16 [tokens][hq or hkv][d] with token strides as in
+ *             ffa_qk_norm_rope; hkv and d are the cache's
+ *  positions, n_axes, pair_axis, weights  as in ffa_qk_norm_rope_axes.  A padding
+ *             token's q_out row and key are 0, one behind the table has NaN; its
+ *             value is its value.
+ *  slots      as in ffa_kv_cache_write: a token whose slot is negative or outside
+ *             the cache is not written, and has its q_out row
+ *  q_out      bf16 [tokens][hq][d], contiguous
+ * q_out and the cache must not overlap an input or each other.  Errors as those
+ * two calls.
+ */
+ffa_status ffa_kv_cache_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                               int64_t v_stride, int64_t tokens, int32_t hq, const float* q_weight,
+                               const float* k_weight, float eps, const float* cos_sin, int64_t max_pos, int32_t rot_dim,
+                               int32_t interleaved, const int32_t* positions, int32_t n_axes, const uint8_t* pair_axis,
+                               const int64_t* slots, const ffa_kv_cache* cache, void* q_out, void* stream);
 
 /*
  * Read the first cu_seqlens[b + 1] - cu_seqlens[b] keys and values of every

@@ -16,12 +16,24 @@ def _pair_index(rot, interleaved):
     return (2 * i, 2 * i + 1) if interleaved else (i, i + rot // 2)
 
 
+def rows_of_axes(cos_sin, positions, axes):
+    """(a table [tokens, rot] with a row for each token, positions in it) that stand for positions [A, tokens] of which pair i
+    goes by positions[axes[i]]: what the functions below take."""
+    table, pos, axes = np.asarray(cos_sin, np.float64), np.asarray(positions, np.int64), np.asarray(axes)
+    half, inside = table.shape[1] // 2, (pos >= 0) & (pos < len(table))
+    at = np.where(inside, pos, 0)[axes].T                       # [tokens, pairs]
+    rows = np.concatenate([table[at, np.arange(half)], table[at, half + np.arange(half)]], 1)
+    n = pos.shape[1]
+    return rows, np.where((pos < 0).any(0), -1, np.where((pos >= len(table)).any(0), n, np.arange(n)))
+
+
 def norm_rope(x, weight, cos_sin, positions, eps, interleaved):
-    """R(pos) diag(weight) x / rms(x) for x [tokens, heads, d]; padding (pos < 0) gives 0, pos >= max_pos NaN."""
+    """R(pos) diag(weight) x / rms(x) for x [tokens, heads, d], or R(pos) x where weight is None; padding (pos < 0) gives 0, pos >=
+    max_pos NaN."""
     x = np.asarray(x, np.float64)
     pos, rot = np.asarray(positions), cos_sin.shape[1]
     inside = (pos >= 0) & (pos < cos_sin.shape[0])
-    y = x / np.sqrt((x ** 2).mean(-1, keepdims=True) + eps) * np.asarray(weight, np.float64)
+    y = x if weight is None else x / np.sqrt((x ** 2).mean(-1, keepdims=True) + eps) * np.asarray(weight, np.float64)
     c, s = _angles(cos_sin, np.where(inside, pos, 0), rot)
     a, b = _pair_index(rot, interleaved)
     out = y.copy()
@@ -51,6 +63,17 @@ def norm_rope_grad(x, weight, cos_sin, positions, dout, eps, interleaved):
     h = g * w
     dx = np.where(keep, h / rms - x * (h * x).sum(-1, keepdims=True) / (d * rms ** 3), 0.0)
     return dx, terms.sum((0, 1)), size.sum((0, 1))
+
+
+def rope_grad(cos_sin, positions, dout, interleaved):
+    """dx of sum(norm_rope(x, None) * dout): dout turned back; 0 for padding."""
+    dout, pos, rot = np.asarray(dout, np.float64), np.asarray(positions), cos_sin.shape[1]
+    c, s = _angles(cos_sin, np.maximum(pos, 0), rot)
+    a, b = _pair_index(rot, interleaved)
+    g = dout.copy()
+    g[..., a] = dout[..., a] * c + dout[..., b] * s
+    g[..., b] = dout[..., b] * c - dout[..., a] * s
+    return np.where((pos >= 0)[:, None, None], g, 0.0)
 
 
 def e4m3_values():

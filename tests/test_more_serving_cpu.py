@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 
 from oracle import serving as S
-from test_serving_cpu import INVALID, OK, OVERFLOW, UNSUPPORTED, at, cache, decode_args, lib, read_args, write_args  # noqa: F401
+from test_serving_cpu import BWD, INVALID, NORM, NORM_BAD, OK, OVERFLOW, UNSUPPORTED, at, cache, decode_args, lib, read_args, table, write_args  # noqa: F401
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -171,3 +171,92 @@ def test_decode_window_is_taken(lib):  # noqa: F811
     for c in (cache(), cache4(), cache(dtype=0, k_exp=None, v_exp=None)):
         for firsts in (None, at(9)):
             assert lib.ffa_fwd_decode_window(*window_args(c, firsts=firsts)) not in (OK, INVALID, UNSUPPORTED, OVERFLOW)
+
+
+# ---- positions of several axes, the rotation alone, and the append
+
+def test_oracle_rows_of_axes():
+    t, r = table(9, 16), np.random.default_rng(0)
+    pos = np.array([[0, 8, -1, 9, 3], [5, 2, 4, 4, 3], [1, 1, 1, -7, 3]])
+    axes = [0, 0, 1, 2, 1, 0, 2, 2]
+    rows, at_ = S.rows_of_axes(t, pos, axes)
+    x = r.normal(size=(5, 2, 16))
+    out = S.norm_rope(x, None, rows, at_, 0.0, False)
+    assert (out[2] == 0).all() and (out[3] == 0).all()          # padding, even beside a position behind the table
+    for i in (0, 1, 4):
+        for pair in range(8):
+            z = (x[i, :, pair] + 1j * x[i, :, pair + 8]) * np.exp(1j * pos[axes[pair], i] * 100.0 ** (-2 * pair / 16))
+            assert np.allclose(out[i, :, pair], z.real) and np.allclose(out[i, :, pair + 8], z.imag)
+    pos[2, 3] = 0
+    assert np.isnan(S.norm_rope(x, None, *S.rows_of_axes(t, pos, axes), 0.0, False)[3]).all()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_oracle_rope_grad_is_the_transpose(interleaved):
+    r = np.random.default_rng(1)
+    x, g, t, pos = r.normal(size=(4, 3, 8)), r.normal(size=(4, 3, 8)), table(6, 4), np.array([5, -1, 2, 0])
+    assert np.isclose((S.norm_rope(x, None, t, pos, 0.0, interleaved) * g).sum(), (x * S.rope_grad(t, pos, g, interleaved)).sum())
+
+
+PAIRS = (ctypes.c_uint8 * 64)(*([0] * 16 + [1] * 24 + [2] * 24))
+BAD_PAIRS = (ctypes.c_uint8 * 64)(*([0] * 63 + [3]))
+AXES = dict(list(NORM.items())[:16], n=3, pairs=ctypes.cast(PAIRS, ctypes.c_void_p), qo=at(6), ko=at(7), stream=None)
+AXES_BWD = dict(list(BWD.items())[:16], n=3, pairs=ctypes.cast(PAIRS, ctypes.c_void_p), **dict(list(BWD.items())[16:]))
+AXES_BAD = [(dict(n=0), INVALID), (dict(n=-1), INVALID), (dict(n=5), UNSUPPORTED), (dict(n=2), INVALID), (dict(pairs=None), INVALID),
+            (dict(pairs=ctypes.cast(BAD_PAIRS, ctypes.c_void_p)), INVALID), (dict(qw=None), INVALID), (dict(kw=None), INVALID)]
+
+
+@pytest.mark.parametrize("change,code", [c for c in NORM_BAD if not set(c[0]) & {"hq"}] + AXES_BAD)
+def test_norm_rope_axes_refusals(lib, change, code):  # noqa: F811
+    assert lib.ffa_qk_norm_rope_axes(*{**AXES, **change}.values()) == code
+    if not set(change) & {"qo", "ko"}:
+        assert lib.ffa_qk_norm_rope_axes_bwd(*{**AXES_BWD, **change}.values()) == code
+
+
+def test_norm_rope_axes_is_taken(lib):  # noqa: F811
+    good = (OK, INVALID, UNSUPPORTED, OVERFLOW)
+    bare = dict(qw=None, kw=None)
+    for change in (dict(), bare, dict(n=4), dict(n=1, pairs=None), dict(n=1, pairs=None, **bare)):
+        assert lib.ffa_qk_norm_rope_axes(*{**AXES, **change}.values()) not in good
+        assert lib.ffa_qk_norm_rope_axes_bwd(*{**AXES_BWD, **change}.values()) not in good
+    none = dict(q=None, k=None, dqw=None, dkw=None, ws=None, ws_bytes=0)
+    assert lib.ffa_qk_norm_rope_axes_bwd(*{**AXES_BWD, **bare, **none}.values()) not in good
+    assert lib.ffa_qk_norm_rope_axes_bwd(*{**AXES_BWD, **none}.values()) == INVALID
+    # positions of all three axes are what outputs must not overlap
+    assert lib.ffa_qk_norm_rope_axes(*{**AXES, "pos": at(6) - 32}.values()) == INVALID
+    assert lib.ffa_qk_norm_rope_axes(*{**AXES, "pos": at(6) - 48}.values()) not in good
+
+
+APPEND = dict(q=at(0), qs=512, k=at(1), ks=256, v=at(2), vs=256, tokens=4, hq=4, qw=at(3), kw=at(4), eps=1e-6, table=at(5), max_pos=16, rot=128,
+              inter=0, pos=at(6), n=1, pairs=None, slots=at(7), cache=None, qo=at(8), stream=None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(tokens=-1), INVALID), (dict(hq=0), INVALID), (dict(rot=8), UNSUPPORTED), (dict(max_pos=0), INVALID), (dict(eps=float("nan")), INVALID),
+    (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(table=None), INVALID), (dict(pos=None), INVALID),
+    (dict(slots=None), INVALID), (dict(qo=None), INVALID), (dict(slots=at(7) + 4), INVALID), (dict(v=at(2) + 8), INVALID), (dict(vs=248), INVALID),
+    (dict(vs=260), INVALID), (dict(qs=504), INVALID), (dict(n=0), INVALID), (dict(n=2), INVALID), (dict(n=5, pairs=ctypes.cast(PAIRS, ctypes.c_void_p)), UNSUPPORTED),
+    (dict(qw=None), INVALID), (dict(qo=at(0)), INVALID), (dict(qo=at(2) + 64), INVALID), (dict(qo=at(20)), INVALID), (dict(v=at(21)), INVALID),
+    (dict(slots=at(23)), INVALID), (dict(pos=at(24)), INVALID), (dict(qo=at(25)), INVALID), (dict(tokens=0, q=None, k=None, v=None, slots=None, qo=None, pos=None), OK),
+    (dict(tokens=1 << 37), OVERFLOW)])
+def test_append_refusals(lib, change, code):  # noqa: F811
+    assert lib.ffa_kv_cache_append(*{**APPEND, "cache": ctypes.byref(cache4()), **change}.values()) == code
+
+
+def test_append_is_taken_over_every_cache(lib):  # noqa: F811
+    good = (OK, INVALID, UNSUPPORTED, OVERFLOW)
+    for c in (cache(), cache4(), cache(dtype=0, k_exp=None, v_exp=None)):
+        for change in (dict(), dict(qw=None, kw=None), dict(n=3, pairs=ctypes.cast(PAIRS, ctypes.c_void_p)), dict(inter=1)):
+            assert lib.ffa_kv_cache_append(*{**APPEND, "cache": ctypes.byref(c), **change}.values()) not in good
+    for c in (cache(dtype=2), cache(page_size=48)):
+        assert lib.ffa_kv_cache_append(*{**APPEND, "cache": ctypes.byref(c)}.values()) == UNSUPPORTED
+    assert lib.ffa_kv_cache_append(*{**APPEND, "cache": None}.values()) == INVALID
+
+
+def test_binding_refuses_tensors_that_are_not_on_the_gpu(lib):  # noqa: F811
+    import torch
+    import flexible_mask_flashattention_gb300 as ffa
+    x, w, t = torch.zeros(2, 2, 64, dtype=torch.bfloat16), torch.zeros(64), torch.zeros(4, 64)
+    pos, c = torch.zeros(2, dtype=torch.int32), torch.zeros(3, 2, 16, 64, dtype=torch.bfloat16)
+    with pytest.raises(ffa.FFAError):
+        ffa.kv_cache_append(x, x, x, w, w, t, pos, c, c, pos.long())

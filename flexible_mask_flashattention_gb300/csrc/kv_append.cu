@@ -37,12 +37,16 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendParams p) {
                           p.x[2] + (w.has ? w.token : 0) * p.x_stride[2] + v.head * D + 8 * l, v.n, w.has ? 16 : 0);
   };
   UnitWalk<D, true> cur, ld;
+  int pos_ahead = -1;   // what the copies one unit ahead have found of its positions
+  static_assert(kStages == 2, "one unit ahead");
   cur.init(p, warp, sub);
   ld = cur;
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
+    ld.settle(p);
     if (ld.left > 0) copy(s, ld);
     cp_async_commit();
+    pos_ahead = ld.pos;
     ld.next(p);
     ld.read_pos(p);
   }
@@ -53,7 +57,10 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendParams p) {
   for (int todo = cur.left + warp; todo > 0; todo -= kWarps, cur.next(p)) {
     __syncthreads();   // the warps' copies go out together: one run of memory
     if (cur.left <= 0) continue;
-    cur.read_pos(p);   // again: from L1
+    cur.pos = pos_ahead;
+    cur.has = cur.token < p.tokens;
+    ld.settle(p);
+    pos_ahead = ld.pos;
     const int64_t slot = cur.has ? __ldg(p.slots + cur.token) : -1;
     if (ld.left > 0) copy(fill, ld);
     cp_async_commit();

@@ -38,12 +38,16 @@ __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(NormRopeParams 
   const Columns<D, INTER> cols(l, p.rot);
   const int swap = Stages<D, false>::swap(sub);
   UnitWalk<D, AXES> cur, ld;
+  [[maybe_unused]] int pos_ahead = -1;   // several axes: what the copies one unit ahead have found of its positions
+  static_assert(kStages == 2, "one unit ahead");
   cur.init(p, warp, sub);
   ld = cur;
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
+    if constexpr (AXES) ld.settle(p);
     if (ld.left > 0) copy_unit<D, false, AXES>(p, st, s, ld);
     cp_async_commit();
+    if constexpr (AXES) pos_ahead = ld.pos;
     ld.next(p);
     ld.read_pos(p);
   }
@@ -53,7 +57,14 @@ __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(NormRopeParams 
   for (int todo = cur.left + warp; todo > 0; todo -= kWarps, cur.next(p)) {
     __syncthreads();   // the warps' copies go out together: one run of memory
     if (cur.left <= 0) continue;
-    cur.read_pos(p);   // again: from L1
+    if constexpr (AXES) {
+      cur.pos = pos_ahead;
+      cur.has = cur.token < p.tokens;
+      ld.settle(p);
+      pos_ahead = ld.pos;
+    } else {
+      cur.read_pos(p);   // again: from L1
+    }
     if (ld.left > 0) copy_unit<D, false, AXES>(p, st, fill, ld);
     cp_async_commit();
     ld.next(p);
@@ -124,12 +135,16 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NormRopeParams 
   const Columns<D, INTER> cols(l, p.rot);
   const int swap = Stages<D, true>::swap(sub);
   UnitWalk<D, AXES> cur, ld;
+  [[maybe_unused]] int pos_ahead = -1;   // several axes: what the copies one unit ahead have found of its positions
+  static_assert(kStages == 2, "one unit ahead");
   cur.init(p, warp, sub);
   ld = cur;
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
+    if constexpr (AXES) ld.settle(p);
     if (ld.left > 0) copy_unit<D, true, AXES>(p, st, s, ld);
     cp_async_commit();
+    if constexpr (AXES) pos_ahead = ld.pos;
     ld.next(p);
     ld.read_pos(p);
   }
@@ -141,7 +156,14 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NormRopeParams 
   for (int todo = cur.left + warp; todo > 0; todo -= kWarps, cur.next(p)) {
     __syncthreads();   // the warps' copies go out together: one run of memory
     if (cur.left <= 0) continue;
-    cur.read_pos(p);   // again: from L1
+    if constexpr (AXES) {
+      cur.pos = pos_ahead;
+      cur.has = cur.token < p.tokens;
+      ld.settle(p);
+      pos_ahead = ld.pos;
+    } else {
+      cur.read_pos(p);   // again: from L1
+    }
     if (ld.left > 0) copy_unit<D, true, AXES>(p, st, fill, ld);
     cp_async_commit();
     ld.next(p);

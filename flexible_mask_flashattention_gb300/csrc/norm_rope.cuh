@@ -45,15 +45,9 @@ struct NormRopeParams {
   float* partial;                 // backward: [CTAs][2][d]
   int32_t axes;                   // several axes: how many, and which one each pair of columns goes by, 2 bits a pair
   uint32_t pair_axis[4];
+  bool chunks;                    // the 4 pairs of every 16-byte chunk of a table row go by one axis
   float turn;                     // several axes, forward: 1, or -1 for the rotation back
 };
-
-// Of several axes: axes of the 4 pairs whose cosines (or sines) are 16-byte chunk `c` of a table row, 2 bits each.
-__device__ __forceinline__ uint32_t chunk_axes(const NormRopeParams& p, int c) {
-  const int half = p.rot / 8, i = c < half ? c : c - half;
-  const uint32_t lo = i & 4 ? p.pair_axis[1] : p.pair_axis[0], hi = i & 4 ? p.pair_axis[3] : p.pair_axis[2];
-  return ((i & 8 ? hi : lo) >> (8 * (i & 3))) & 0xffu;
-}
 
 // The 8 columns of a row that a lane holds, in two runs of 4 such that a rotation's pairs lie in one lane: values 0..3 are columns
 // from `lo` on, 4..7 those from `hi` on.  Pairs (i, i + rot / 2): run l of the rotated columns' first half and run l of the second, then
@@ -160,29 +154,25 @@ __device__ __forceinline__ void in_batches(int n, F& f) {
 }
 
 // Where a warp stands in its units: unit `c` of its 256 / D tokens' units; this lane's token (behind the last one: has = false) and its
-// position.  Of several axes `pos` says whether all of the token's positions are good: a negative one if one is, else the largest.
+// position.  Of several axes lane l of a token's D / 8 reads the position on axis l % 4, and `pos` says, once all have come (settle), whether
+// they are good: negative if one is, behind the table if one is, else any good one.
 template <int D, bool AXES = false>
 struct UnitWalk {
   static constexpr int kGroup = 256 / D;   // tokens a warp
   int64_t token;
   int left;        // units of the CTA's from this one on
   int c, pos;
-  int at[AXES ? 4 : 1];   // the position on each axis
+  int mine;        // several axes: the position this lane has read
   bool has;
   __device__ __forceinline__ void read_pos(const NormRopeParams& p) {
     has = left > 0 && token < p.tokens;
-    if constexpr (AXES) {
-#pragma unroll
-      for (int a = 0; a < 4; ++a) at[a] = has && a < p.axes ? __ldg(p.pos + a * p.tokens + token) : 0;
-      const int least = min(min(at[0], at[1]), min(at[2], at[3]));
-      pos = !has || least < 0 ? -1 : max(max(at[0], at[1]), max(at[2], at[3]));
-    } else {
-      pos = has ? __ldg(p.pos + token) : -1;
-    }
+    if constexpr (AXES) mine = has ? __ldg(p.pos + min(static_cast<int>(threadIdx.x) & 3, p.axes - 1) * p.tokens + token) : -1;
+    else pos = has ? __ldg(p.pos + token) : -1;
   }
-  __device__ __forceinline__ int on(uint32_t axis) const {
-    const int lo = axis & 1 ? at[1] : at[0], hi = axis & 1 ? at[3] : at[2];
-    return axis & 2 ? hi : lo;
+  __device__ __forceinline__ void settle(const NormRopeParams& p) {   // by all lanes of the warp
+    const uint32_t token_lanes = (D == 128 ? 0xffffu : 0xffu) << (threadIdx.x & 31 & -(D / 8));
+    const uint32_t low = __ballot_sync(0xffffffffu, mine < 0), far = __ballot_sync(0xffffffffu, mine >= p.max_pos);
+    pos = low & token_lanes ? -1 : far & token_lanes ? 0x7fffffff : 0;
   }
   __device__ __forceinline__ void init(const NormRopeParams& p, int warp, int sub) {
     const int64_t begin = blockIdx.x * p.span, first = begin + warp, group = first / p.per;
@@ -237,23 +227,41 @@ __device__ __forceinline__ void copy_rows(uint32_t to, const __nv_bfloat16* x, i
   }
 }
 
-// Copy what lane l has of the token's table row, chunks l and l + D / 8: where the pairs of a chunk go by different axes, value by value.
+// Copy a token's table row, with the lanes of the token: 16-byte chunks l and l + D / 8 of it.  Of several axes lane l takes the cosines
+// and the sines of pairs 4l .. 4l + 3, if every such chunk goes by one axis, or of pairs l, l + D / 8, ...: neighbouring lanes then copy
+// neighbouring values, as far as they are of one row.
 template <int D, bool AXES>
-__device__ __forceinline__ void copy_table(const NormRopeParams& p, uint32_t to, const UnitWalk<D, AXES>& w, int l) {
-  const float* row = p.cos_sin + static_cast<int64_t>(w.pos) * p.rot;
-#pragma unroll
-  for (int c = l; c < D / 4; c += D / 8) {
-    if (4 * c >= p.rot) break;
-    if constexpr (!AXES) {
-      cp_async16(to + 16 * c, row + 4 * c);
+__device__ __forceinline__ void copy_table(const NormRopeParams& p, uint32_t to, const UnitWalk<D, AXES>& w, int l, bool live) {
+  constexpr int L = D / 8;
+  if constexpr (!AXES) {
+    if (!live) return;
+    const float* row = p.cos_sin + static_cast<int64_t>(w.pos) * p.rot;
+    if (4 * l < p.rot) cp_async16(to + 16 * l, row + 4 * l);
+    if (4 * (l + L) < p.rot) cp_async16(to + 16 * (l + L), row + 4 * (l + L));
+  } else {
+    const int half = p.rot / 2;
+    auto axis_of = [&](int pair) {
+      const uint32_t lo = pair & 16 ? p.pair_axis[1] : p.pair_axis[0], hi = pair & 16 ? p.pair_axis[3] : p.pair_axis[2];
+      return static_cast<int>((pair & 32 ? hi : lo) >> (2 * (pair & 15)) & 3u);
+    };
+    auto row_of = [&](int pair) {   // of the axis that the pair goes by; shuffled by all lanes
+      return p.cos_sin + static_cast<int64_t>(__shfl_sync(0xffffffffu, w.mine, axis_of(pair), L)) * p.rot;
+    };
+    if (p.chunks) {
+      const float* row = row_of(4 * l);
+      if (live && 4 * l < half) {
+        cp_async16(to + 16 * l, row + 4 * l);
+        cp_async16(to + 16 * l + 4 * half, row + half + 4 * l);
+      }
     } else {
-      const uint32_t axes = chunk_axes(p, c);
-      if (axes == (axes & 3u) * 0x55u) {
-        cp_async16(to + 16 * c, p.cos_sin + static_cast<int64_t>(w.on(axes & 3u)) * p.rot + 4 * c);
-      } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          cp_async4(to + 16 * c + 4 * i, p.cos_sin + static_cast<int64_t>(w.on(axes >> (2 * i) & 3u)) * p.rot + 4 * c + i);
+      for (int i = 0; i < 4; ++i) {
+        const int pair = l + L * i;
+        const float* row = row_of(pair) + pair;
+        if (live && pair < half) {
+          cp_async4(to + 4 * pair, row);
+          cp_async4(to + 4 * (half + pair), row + half);
+        }
       }
     }
   }
@@ -281,7 +289,7 @@ __device__ __forceinline__ void copy_unit(const NormRopeParams& p, const Stages<
       if constexpr (BWD) cp_async16(to_g + i * 512, g + i * D, bytes);
     }
   }
-  if (live) copy_table<D, AXES>(p, smem_u32(st.table(stage, sub)), w, l);
+  copy_table<D, AXES>(p, smem_u32(st.table(stage, sub)), w, l, live);
 }
 
 // Several axes (0: one position a token): how many, and the axis of every pair (null: one axis).
@@ -290,9 +298,11 @@ inline ffa_status check_axes(int32_t axes, const uint8_t* pair_axis, int32_t rot
   if (axes > 4) return FFA_ERR_UNSUPPORTED;
   p.axes = axes;
   p.turn = 1.f;
+  p.chunks = true;
   for (int i = 0; axes && pair_axis && i < rot / 2; ++i) {
     if (pair_axis[i] >= axes) return FFA_ERR_INVALID_ARG;
     p.pair_axis[i / 16] |= static_cast<uint32_t>(pair_axis[i]) << (2 * (i % 16));
+    p.chunks &= pair_axis[i] == pair_axis[i / 4 * 4];
   }
   return FFA_OK;
 }

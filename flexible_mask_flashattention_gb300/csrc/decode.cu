@@ -54,7 +54,7 @@ namespace {
 // spread a strip's fixed instructions over more keys.  Measured before later steps (us; 50 x 20K keys, 64 + 8 heads, d = 64, e4m3): 8 warps x 1 group 165,
 // 8 x 2 137, 8 x 4 120, 12 x 4 118, 16 x 2 118, and later 12 x 2 114 and 16 x 2 116; (1M keys, 16 + 4 heads, d = 128, e4m3): 8 x 1 181, 12 x 1 170, 8 x 2 169; (24 x 8K
 // keys, 32 heads, d = 64, bf16): 8 x 1 119, 8 x 2 122, 12 x 2 117; (380K keys, 32 + 2 heads, d = 128, e4m3): 8 x 1 46, 8 x 2 43.
-constexpr int warps_of(int d, int nt, int type) { return nt == 2 || d == 128 ? 8 : 12; }
+constexpr int warps_of(int d, int nt, int type) { return nt == 2 || (d == 128 && type != kE2m1) ? 8 : 12; }
 constexpr int groups_of(int d, int type) { return d == 128 && type == kBf16 ? 1 : type == kE2m1 ? (d == 64 ? 4 : 2) : 2; }
 constexpr int kMaxCtas = 160;          // CTAs (one an SM) the workspace holds parts for: two a CTA
 constexpr int kSmemMax = 226 * 1024;   // of 227 KB
@@ -211,9 +211,9 @@ struct Walk {
     set(range_of(p, seq, KEYS), seq, wrap ? 0 : u + 1, 0);
   }
   // Of this warp's strip: all its keys count; one of its keys, `key - key of the strip` = i, does; one of those from i on, 16 of them.
-  __device__ __forceinline__ bool whole() const { return end - key >= KEYS && (key >= start || key + KEYS <= first); }
-  __device__ __forceinline__ bool counts(int i) const { return i < end - key && (i >= start - key || i < first - key); }
-  __device__ __forceinline__ bool some(int i) const { return end - key > i && (start - key < i + 16 || first - key > i); }
+  __device__ __forceinline__ bool whole() const { return (end - key >= KEYS) & ((key >= start) | (key + KEYS <= first)); }
+  __device__ __forceinline__ bool counts(int i) const { return (i < end - key) & ((i >= start - key) | (i < first - key)); }
+  __device__ __forceinline__ bool some(int i) const { return (end - key > i) & ((start - key < i + 16) | (first - key > i)); }
   // The unit is one strip.
   __device__ __forceinline__ bool single() const { return end - (first > 0 ? 0 : start / KEYS * KEYS) <= KEYS; }
 };
@@ -358,14 +358,21 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
   const uint32_t ring = smem_u32(smem + C::MISC + C::JOIN) + warp * (C::STAGE * C::STAGES);
   Walk<kW, C::KEYS> ld = cur;
   const int page_rows = p.geom.hkv << p.geom.page_log2, page_mask = (1 << p.geom.page_log2) - 1;
+  const bool one_page = page_mask + 1 >= C::KEYS && (C::KEYS & (C::KEYS - 1)) == 0;   // strips start at multiples of their length
   int real;               // the next strip's first key, the gap counted
   int head_row;           // the loading unit's head's first row in a page
   int page[SK];           // of the next strip's groups of 16 keys, read a strip ahead; -1 for a group outside the range
   auto read_pages = [&]() {
     const int32_t* row = p.table + ld.b * p.table_stride;
     real = ld.key < ld.first ? ld.key : ld.key + ld.gap;
+    if (SK > 1 && one_page) {   // its groups are all of the page that its first key is
+      page[0] = ld.end > ld.key ? __ldg(row + (real >> p.geom.page_log2)) : -1;
 #pragma unroll
-    for (int g = 0; g < SK; ++g) page[g] = ld.some(16 * g) ? __ldg(row + ((real + 16 * g) >> p.geom.page_log2)) : -1;
+      for (int g = 1; g < SK; ++g) page[g] = page[0];
+    } else {
+#pragma unroll
+      for (int g = 0; g < SK; ++g) page[g] = ld.some(16 * g) ? __ldg(row + ((real + 16 * g) >> p.geom.page_log2)) : -1;
+    }
   };
   auto open_unit = [&]() {
     head_row = (p.subs == 1 ? ld.u : ld.u / p.subs) << p.geom.page_log2;
@@ -376,7 +383,10 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
   uint32_t dst_of[kPeriod];
 #pragma unroll
   for (int i = 0; i < kPeriod; ++i) dst_of[i] = ring + 16 * strip_chunk((lane + 32 * i) / C::CPR, (lane + 32 * i) % C::CPR, C::CPR);
-  // the chunk behind K and V that this lane copies: of K's scales, V's scales, K's exponents, V's exponents
+  const uint8_t* k_lane = static_cast<const uint8_t*>(p.k) + lane * 16;
+  const int64_t v_from_k = static_cast<const uint8_t*>(p.v) - static_cast<const uint8_t*>(p.k);
+  // the chunk behind K and V that this lane copies: of K's scales, V's scales, K's exponents, V's exponents; and its bytes a row
+  [[maybe_unused]] const uint32_t side_row = lane < C::SIDE - 2 ? D / 16 : 1;
   const uint8_t* side = nullptr;
   if constexpr (T == kE2m1) {
     constexpr int N = C::SCALES / 16;
@@ -386,8 +396,26 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
   }
   auto load_strip = [&](int stage, bool more) {
     const int have = ld.end - ld.key;
-    if (have > 0) {
-      const bool full = ld.whole();
+    const bool full = ld.whole();
+    if (have > 0 && full && (SK == 1 || one_page) && static_cast<uint32_t>(page[0]) < static_cast<uint32_t>(p.geom.num_pages)) {
+      const uint32_t off = head_row + (real & page_mask), base = stage * C::STAGE;   // one run of rows
+      const uint8_t* k = k_lane + static_cast<uint64_t>(static_cast<uint32_t>(page[0])) * static_cast<uint32_t>(page_rows * C::ROW) + off * C::ROW;
+      const uint8_t* v = k + v_from_k;
+      const uint8_t* s = nullptr;
+      if constexpr (QUANT) s = side + static_cast<uint64_t>(static_cast<uint32_t>(page[0])) * (static_cast<uint32_t>(page_rows) * side_row) + off * side_row;
+#pragma unroll
+      for (int g = 0; g < SK; ++g) {
+#pragma unroll
+        for (int i = 0; i < C::CPR / 2; ++i) {
+          const uint32_t to = base + g * C::GROUP + dst_of[i % kPeriod] + i / kPeriod * (kPeriod * 512);
+          cp_async16(to, k + g * C::STRIP + 512 * i);
+          cp_async16(to + C::STRIP, v + g * C::STRIP + 512 * i);
+        }
+        if constexpr (QUANT) {
+          if (lane < C::SIDE) cp_async16(ring + base + g * C::GROUP + 2 * C::STRIP + 16 * lane, s + g * 16 * side_row);
+        }
+      }
+    } else if (have > 0) {
 #pragma unroll
       for (int g = 0; g < SK; ++g) {
         const bool ok = static_cast<uint32_t>(page[g]) < static_cast<uint32_t>(p.geom.num_pages);   // as page_ok, for pages of 32 bits
@@ -416,7 +444,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
         if constexpr (QUANT) {
           const uint32_t to = ring + base + 2 * C::STRIP + 16 * lane;
           if (T == kE2m1 && !ok && lane < C::SCALES / 16) sts128(to, 0x7f7f7f7fu);   // no such page: scales of NaN
-          else if (lane < C::SIDE) cp_async16(to, side + (lane < C::SIDE - 2 ? row * (D / 16) : row));
+          else if (lane < C::SIDE) cp_async16(to, side + row * side_row);
         }
       }
     }
@@ -504,32 +532,44 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
     }
   };
 
+  // e2m1: this lane's places in 16 keys: its columns' codes and scales of row n (K) and of rows 2t, 2t + 1 (V)
+  [[maybe_unused]] uint32_t at_k = 0, s_k = 0, at_v[2] = {}, s_v = 0;
+  if constexpr (T == kE2m1) {
+    at_k = D == 128 ? 16 * strip_chunk(n, t, C::CPR) : 16 * strip_chunk(n, t >> 1, C::CPR) + 8 * (t & 1);
+    s_k = 2 * C::STRIP + n * (D / 16) + (D == 128 ? 2 * t : t);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      at_v[i] = C::STRIP + (D == 128 ? 16 * strip_chunk(2 * t + i, n >> 1, C::CPR) + 8 * (n & 1) : 16 * strip_chunk(2 * t + i, n >> 2, C::CPR) + 4 * (n & 3));
+    s_v = 2 * C::STRIP + C::SCALES + 2 * t * (D / 16) + (D == 128 ? n : n >> 1);
+  }
+
   // ---- one strip: all groups' scores, their exponentials, then all groups' values
   auto strip = [&](int stage) {
     const int have = cur.end - cur.key;
     if (have <= 0) return;
     const bool whole = cur.whole();
     const uint32_t sb = ring + stage * C::STAGE;
+    // this lane's places in a strip; rows 8 further on are half a strip further on
+    constexpr uint32_t kHalf = C::STRIP / 2, kScales = 2 * C::STRIP, kExps = kScales + 2 * C::SCALES;
     constexpr int CH = SK == 1 ? 2 : 1;   // accumulators a score tile: one group alone would be one long chain of MMAs
     float s[SK][NT][CH][4] = {};
     if constexpr (T == kE2m1) {
 #pragma unroll
       for (int g = 0; g < SK; ++g) {
         constexpr int WORDS = D / 32;   // of a row that are this lane's: columns D / 4 * t on, one scale (d = 64) or two
-        const uint32_t kb = sb + g * C::GROUP, cb = kb + 2 * C::STRIP;
         uint32_t w[2][WORDS], sc[2][WORDS / 2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int key = n + 8 * r;
+          const uint32_t at = g * C::GROUP + r * kHalf, sat = sb + s_k + g * C::GROUP + r * (C::SCALES / 2);
           if constexpr (D == 128) {
-            const uint4 x = lds128(kb + 16 * strip_chunk(key, t, C::CPR));
+            const uint4 x = lds128(sb + at_k + at);
             w[r][0] = x.x, w[r][1] = x.y, w[r][2] = x.z, w[r][3] = x.w;
-            const uint32_t two = e4m3x2_to_f16x2(lds16(cb + key * 8 + 2 * t));
+            const uint32_t two = e4m3x2_to_f16x2(lds16(sat));
             sc[r][0] = __byte_perm(two, 0, 0x1010), sc[r][1] = __byte_perm(two, 0, 0x3232);
           } else {
-            const uint2 x = lds64(kb + 16 * strip_chunk(key, t >> 1, C::CPR) + 8 * (t & 1));
+            const uint2 x = lds64(sb + at_k + at);
             w[r][0] = x.x, w[r][1] = x.y;
-            const uint32_t one = lds8(cb + key * 4 + t);
+            const uint32_t one = lds8(sat);
             sc[r][0] = e4m3x2_to_f16x2(one | one << 8);
           }
         }
@@ -581,19 +621,18 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
       for (int g = 0; g < SK; ++g)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const uint32_t eb = sb + g * C::GROUP + 2 * (C::STRIP + C::SCALES) + n + 8 * r;
+          const uint32_t eb = sb + n + kExps + g * C::GROUP + 8 * r;
           ks[g][r] = exp_scale(lds8(eb));
           const uint32_t byte = lds8(eb + 16);
-          vn[g][r] = byte ? static_cast<float>(static_cast<int>(byte) - 127) : -INFINITY;
+          vn[g][r] = byte ? __uint_as_float(0x4b000000u | byte) - (8388608.f + 127.f) : -INFINITY;   // byte - 127, exactly
         }
     }
     // scores of a key (n, n + 8 of a group) and the two queries, two an instruction; exponents of the weights: of l (and bf16's O), of e4m3's O
-    float2 x[SK][NT][2];
-    auto less_m = [&](int g, int nt, int r) { return add2(x[g][nt][r], make_float2(-m[nt][0], -m[nt][1])); };
-    auto less_vr = [&](int g, int nt, int r) {
-      return add2(less_m(g, nt, r), add2(make_float2(vn[g][r], vn[g][r]), make_float2(-vr[nt][0], -vr[nt][1])));
+    float2 x[SK][NT][2], xm[SK][NT][2], xv[SK][NT][2];
+    auto exponents = [&](int g, int nt, int r) {
+      xm[g][nt][r] = add2(x[g][nt][r], make_float2(-m[nt][0], -m[nt][1]));
+      if constexpr (QUANT) xv[g][nt][r] = add2(xm[g][nt][r], make_float2(vn[g][r] - vr[nt][0], vn[g][r] - vr[nt][1]));
     };
-    bool raise = false;
 #pragma unroll
     for (int g = 0; g < SK; ++g)
 #pragma unroll
@@ -603,15 +642,30 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
           const float2 q2 = make_float2(qs[nt][0], qs[nt][1]);
           float2 v = make_float2(s[g][nt][0][2 * r], s[g][nt][0][2 * r + 1]);
           if constexpr (CH == 2) v = add2(v, make_float2(s[g][nt][1][2 * r], s[g][nt][1][2 * r + 1]));
-          v = mul2(v, QUANT ? mul2(q2, make_float2(ks[g][r], ks[g][r])) : q2);
-          if (!whole && !cur.counts(16 * g + n + 8 * r)) v = make_float2(-INFINITY, -INFINITY);
-          x[g][nt][r] = v;
-          raise |= v.x > m[nt][0] || v.y > m[nt][1];
-          if constexpr (QUANT) {
-            const float2 y = less_vr(g, nt, r);
-            raise |= y.x > kTop || y.y > kTop;
-          }
+          x[g][nt][r] = mul2(v, QUANT ? make_float2(q2.x * ks[g][r], q2.y * ks[g][r]) : q2);
         }
+    if (!whole) {
+#pragma unroll
+      for (int g = 0; g < SK; ++g)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const bool in = cur.counts(16 * g + n + 8 * r);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) x[g][nt][r] = in ? x[g][nt][r] : make_float2(-INFINITY, -INFINITY);
+        }
+    }
+    float over_m = -1.f, over_v = -1.f;   // the largest of each
+#pragma unroll
+    for (int g = 0; g < SK; ++g)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          exponents(g, nt, r);
+          over_m = fmax3(over_m, xm[g][nt][r].x, xm[g][nt][r].y);
+          if constexpr (QUANT) over_v = fmax3(over_v, xv[g][nt][r].x, xv[g][nt][r].y);
+        }
+    const bool raise = over_m > 0.f || over_v > kTop;
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -642,17 +696,21 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
             o[nt][i][c + 2] *= f;
           }
         }
+#pragma unroll
+      for (int g = 0; g < SK; ++g)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) exponents(g, nt, 0), exponents(g, nt, 1);
     }
     uint32_t pf[SK][NT][2], pl[SK][NT][2];
 #pragma unroll
     for (int g = 0; g < SK; ++g)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float2 e0 = ex2(less_m(g, nt, 0)), e1 = ex2(less_m(g, nt, 1));
+        float2 e0 = ex2(xm[g][nt][0]), e1 = ex2(xm[g][nt][1]);
         const float2 sum = add2(make_float2(l[nt][0], l[nt][1]), add2(e0, e1));
         l[nt][0] = sum.x, l[nt][1] = sum.y;
         if constexpr (QUANT) {
-          e0 = ex2(less_vr(g, nt, 0)), e1 = ex2(less_vr(g, nt, 1));
+          e0 = ex2(xv[g][nt][0]), e1 = ex2(xv[g][nt][1]);
           pf[g][nt][0] = movmatrix(pack_f16x2(e0.x, e0.y));
           pf[g][nt][1] = movmatrix(pack_f16x2(e1.x, e1.y));
         } else {
@@ -669,19 +727,21 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
       const uint32_t vb = sb + g * C::GROUP + C::STRIP;
       if constexpr (T == kE2m1) {
         constexpr int WORDS = D / 64;   // of a row that are this lane's: columns D / 8 * n on, of one scale
-        const uint32_t cb = vb + C::STRIP + C::SCALES + (D == 128 ? n : n >> 1);
         uint32_t w[4][WORDS], sc[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = 2 * t + (i & 1) + 8 * (i >> 1);
+        for (int i = 0; i < 4; ++i) {   // keys 2t, 2t + 1, 2t + 8, 2t + 9
+          const uint32_t at = sb + at_v[i & 1] + g * C::GROUP + (i >> 1) * kHalf;
           if constexpr (D == 128) {
-            const uint2 x = lds64(vb + 16 * strip_chunk(key, n >> 1, C::CPR) + 8 * (n & 1));
+            const uint2 x = lds64(at);
             w[i][0] = x.x, w[i][1] = x.y;
           } else {
-            w[i][0] = lds32(vb + 16 * strip_chunk(key, n >> 2, C::CPR) + 4 * (n & 3));
+            w[i][0] = lds32(at);
           }
-          sc[i] = lds8(cb + key * (D / 16));
-          if (!whole && !cur.counts(16 * g + key)) sc[i] = 0;   // a row that was not written may have any scale
+          sc[i] = lds8(sb + s_v + g * C::GROUP + (i >> 1) * (C::SCALES / 2) + (i & 1) * (D / 16));
+        }
+        if (!whole) {   // a row that was not written may have any scale
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[i] = cur.counts(16 * g + 2 * t + (i & 1) + 8 * (i >> 1)) ? sc[i] : 0;
         }
         const uint32_t s0 = e4m3x2_to_f16x2(sc[0] | sc[1] << 8), s1 = e4m3x2_to_f16x2(sc[2] | sc[3] << 8);
 #pragma unroll

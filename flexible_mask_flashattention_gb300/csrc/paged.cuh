@@ -118,7 +118,7 @@ FFA_HD int64_t share_of(int64_t total, int64_t parts, int64_t x) {
 // rows), and 8 lanes reading chunks 2i, 2i + 1 of rows 0, 2, 4, 6 or 1, 3, 5, 7 (keys as the contraction).
 FFA_HD int32_t strip_chunk(int32_t key, int32_t c, int32_t cpr) {
   if (cpr >= 8) return key * cpr + (c ^ ((((key >> 1) & 3) ^ ((key & 1) << 1)) << 1));
-  if (cpr == 2) return (key >> 2) * 8 + (((key ^ (key >> 2)) & 3) << 1) + c;   // four rows a line, read in 8- and 4-byte pieces
+  if (cpr == 2) return (key >> 2) * 8 + (((key ^ (key >> 2 & 1)) & 3) << 1) + c;   // four rows a line, read in 8- and 4-byte pieces
   const int32_t line = key >> 1;   // 4 chunks a row: two rows a 128-byte line
   return line * 8 + ((((key & 1) << 2) | c) ^ ((line & 3) << 1));
 }

@@ -5,9 +5,13 @@
 // written one way and steps written the other agree.
 //
 // Bound by HBM: q in and out, k and v in, their stored rows out; the two calls also write k and read it again, 4 d bytes a k row, and are
-// two launches and 15 us of host time to one's.  The walk over tokens and heads, the copies to shared memory and the rotation are norm_rope.cu's, with v
-// as a third tensor behind q and k.  A normalised key's columns lie in its lanes as rotation partners; it goes back to its place in
-// shared memory and is read from there in the order that kv_cache.h's rows want, 8 neighbouring columns a lane.
+// two launches.  The walk over tokens and heads, the copies to shared memory and the rotation are norm_rope.cu's, with v as a third tensor
+// behind q and k.  A normalised key's columns lie in its lanes as rotation partners; it goes back to its place in shared memory and is
+// read from there in the order that kv_cache.h's rows want.
+//
+// Unlike there, the warps of a CTA do not start their copies together: units of q's, k's and v's heads take different times (78K tokens
+// of 16 + 4 heads, d = 128, into 4 bits: 169 us with a barrier a round, 140 without), nor are units cut across tensors (155) or made of
+// equal shares of each (206).
 #include "kv_cache.h"
 #include "norm_rope.cuh"
 
@@ -18,7 +22,30 @@ struct AppendParams : NormRopeParams {
   CacheRows cache[2];
   const int64_t* slots;
   PageGeom geom;
+  int32_t first[4];   // q's, k's and v's first unit, and behind the last
+  int32_t size[3];    // heads of such a unit
 };
+
+// Unit c's heads of tensor t.
+__device__ __forceinline__ UnitPart part_of(const AppendParams& p, int c, int t) {
+  const int head = (c - p.first[t]) * p.size[t];
+  return UnitPart{c < p.first[t] || c >= p.first[t + 1] ? 0 : min(p.size[t], p.heads[t] - head), 0, head};
+}
+
+// Units of q's, of k's and of v's heads: what a unit begins with (its rotation, coefficients, places) is then of one tensor.  As many as
+// fit, since that costs as much as three heads; smaller ones where there would be fewer units than warps.
+constexpr int kAppendMost = kUnitMost<false>;
+template <bool BWD>
+void set_units(AppendParams& p, int64_t tokens, int d, int64_t warps) {
+  const int group = 256 / d;
+  const int64_t groups = std::max<int64_t>((tokens + group - 1) / group, 1), heads = p.heads[0] + p.heads[1] + p.heads[2];
+  for (int t = 0; t < 3; ++t) {
+    const int64_t all = p.heads[t], per = std::max((all + kAppendMost - 1) / kAppendMost, std::min(all, warps / groups * all / heads));
+    p.size[t] = static_cast<int32_t>((all + per - 1) / per);
+    p.first[t + 1] = p.first[t] + static_cast<int32_t>((all + p.size[t] - 1) / p.size[t]);
+  }
+  cut_units(p, tokens, d, p.first[3], std::max({p.size[0], p.size[1], p.size[2]}));
+}
 
 template <int D, bool INTER, int T>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendParams p) {
@@ -30,11 +57,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendParams p) {
   const Columns<D, INTER> cols(l, p.rot);
   const int swap = Stages<D, false>::swap(sub), natural = (16 * l) ^ swap;
   auto copy = [&](int stage, const UnitWalk<D, true>& w) {
-    copy_unit<D, false, true>(p, st, stage, w);
-    const UnitPart v = part_of(p, w.c, 2);   // a value goes into the cache whatever its token's positions
-    if (v.n > 0)
-      copy_rows<D, false>(smem_u32(st.rows(stage, sub, 0)) + v.first * 512 + natural,
-                          p.x[2] + (w.has ? w.token : 0) * p.x_stride[2] + v.head * D + 8 * l, v.n, w.has ? 16 : 0);
+    if (w.c < p.first[2]) {
+      copy_unit<D, false, true>(p, st, stage, w);
+    } else {   // a value goes into the cache whatever its token's positions
+      const UnitPart v = part_of(p, w.c, 2);
+      copy_rows<D, false>(smem_u32(st.rows(stage, sub, 0)) + natural, p.x[2] + (w.has ? w.token : 0) * p.x_stride[2] + v.head * D + 8 * l, v.n,
+                          w.has ? 16 : 0);
+    }
   };
   UnitWalk<D, true> cur, ld;
   int pos_ahead = -1;   // what the copies one unit ahead have found of its positions
@@ -55,8 +84,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendParams p) {
   const int page_rows = p.geom.hkv << p.geom.page_log2, page_mask = (1 << p.geom.page_log2) - 1;
   int stage = 0, fill = kStages - 1;
   for (int todo = cur.left + warp; todo > 0; todo -= kWarps, cur.next(p)) {
-    __syncthreads();   // the warps' copies go out together: one run of memory
-    if (cur.left <= 0) continue;
+    if (cur.left <= 0) break;
     cur.pos = pos_ahead;
     cur.has = cur.token < p.tokens;
     ld.settle(p);
@@ -74,73 +102,77 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendParams p) {
     // a padded token (negative position) gives zeros, one behind the table NaN
     const uint32_t fill_bits = pos < 0 ? 0u : 0x7fff7fffu;
     const uint4 constant = make_uint4(fill_bits, fill_bits, fill_bits, fill_bits);
-    Rotation<INTER, false> rot;
-    rot.load(st.table(stage, sub), live ? p.rot : 0, l);
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const UnitPart u = part_of(p, cur.c, t);
-      if (u.n <= 0) continue;
-      __nv_bfloat16* out = p.out[0] + (cur.token * p.heads[0] + u.head) * D;   // q's
-      uint8_t* in = st.rows(stage, sub, 0) + u.first * 512;
-      // coefficients with the weights: out_j = r (x_j a_j + partner_j b_j)
-      float2 w[4], a[4], b[4];
-      cols.load(weights + t * D, w);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) a[j] = mul2(w[j], rot.c(j)), b[j] = mul2(partner<INTER>(w, j), rot.s(j));
-      auto some = [&](auto count, int i) {   // `count` heads from i on, their sums side by side
-        constexpr int N = decltype(count)::value;
-        float2 f[N][4];
-        float r[N];
-        uint4 v[N];
-#pragma unroll
-        for (int h = 0; h < N; ++h) {
-          unpack8(cols.load(in + (i + h) * 512, swap), f[h]);
-          float2 ss = mul2(f[h][0], f[h][0]);
-#pragma unroll
-          for (int j = 1; j < 4; ++j) ss = fma2(f[h][j], f[h][j], ss);
-          r[h] = ss.x + ss.y;
-        }
-        row_sums<D>(r);
-#pragma unroll
-        for (int h = 0; h < N; ++h) {
-          r[h] = p.w[0] ? rsqrtf(r[h] * (1.f / D) + p.eps) : 1.f;
-          float2 o[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            o[j] = mul2(fma2(f[h][j], a[j], mul2(partner<INTER>(f[h], j), b[j])), make_float2(r[h], r[h]));
-          v[h] = live ? pack8(o) : constant;
-          if (t == 0 && cur.has) cols.store(out + (i + h) * D, v[h]);
-          if (t == 1 && !INTER) cols.store(in + (i + h) * 512, swap, v[h]);
-        }
-        if (t == 1) {
-          if constexpr (!INTER) {
-            __syncwarp();
-#pragma unroll
-            for (int h = 0; h < N; ++h) v[h] = *reinterpret_cast<const uint4*>(in + (i + h) * 512 + natural);
-          }
-          StoredRow row[N];
-#pragma unroll
-          for (int h = 0; h < N; ++h) row[h] = make_row<D, T>(v[h]);
-#pragma unroll
-          for (int h = 0; h < N; ++h)
-            if (keep) put_row<D, T>(row[h], base + (static_cast<int64_t>(u.head + i + h) << p.geom.page_log2), l, p.cache[0]);
-        }
-      };
-      in_batches<3>(u.n, some);
-    }
-    const UnitPart u = part_of(p, cur.c, 2);
-    if (u.n > 0) {
-      const uint8_t* in = st.rows(stage, sub, 0) + u.first * 512 + natural;
+    // the rows of a part's heads into the cache: D / V lanes a row, so that a token's lanes have one head's at once, or (e2m1) two heads'
+    auto store_heads = [&](const uint8_t* in, const UnitPart& u, int which) {
+      constexpr int V = kLaneValues<T>, kRows = V / 8;
+      const int rl = l % (D / V), rh = l / (D / V);
       auto some = [&](auto count, int i) {
         constexpr int N = decltype(count)::value;
         StoredRow row[N];
 #pragma unroll
-        for (int h = 0; h < N; ++h) row[h] = make_row<D, T>(*reinterpret_cast<const uint4*>(in + (i + h) * 512));
+        for (int h = 0; h < N; ++h) {
+          const uint8_t* at = in + min((i + h) * kRows + rh, u.n - 1) * 512;
+          LaneValues<T> v;
 #pragma unroll
-        for (int h = 0; h < N; ++h)
-          if (keep) put_row<D, T>(row[h], base + (static_cast<int64_t>(u.head + i + h) << p.geom.page_log2), l, p.cache[1]);
+          for (int j = 0; j < V / 8; ++j) v[j] = *reinterpret_cast<const uint4*>(at + ((2 * V * rl + 16 * j) ^ swap));
+          row[h] = make_row<D, T>(v);
+        }
+#pragma unroll
+        for (int h = 0; h < N; ++h) {
+          const int head = (i + h) * kRows + rh;
+          if (keep && head < u.n)
+            put_row<D, T>(row[h], base + (static_cast<int64_t>(u.head + head) << p.geom.page_log2), rl, which ? p.cache[1] : p.cache[0]);
+        }
       };
-      in_batches<3>(u.n, some);
+      in_batches<2>((u.n + kRows - 1) / kRows, some);
+    };
+    if (cur.c >= p.first[2]) {
+      store_heads(st.rows(stage, sub, 0), part_of(p, cur.c, 2), 1);
+    } else {
+      Rotation<INTER, false> rot;
+      rot.load(st.table(stage, sub), live ? p.rot : 0, l);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const UnitPart u = part_of(p, cur.c, t);
+        if (u.n <= 0) continue;
+        __nv_bfloat16* out = p.out[0] + (cur.token * p.heads[0] + u.head) * D;   // q's
+        uint8_t* in = st.rows(stage, sub, 0) + u.first * 512;
+        // coefficients with the weights: out_j = r (x_j a_j + partner_j b_j)
+        float2 w[4], a[4], b[4];
+        cols.load(weights + t * D, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j] = mul2(w[j], rot.c(j)), b[j] = mul2(partner<INTER>(w, j), rot.s(j));
+        auto some = [&](auto count, int i) {   // `count` heads from i on, their sums side by side
+          constexpr int N = decltype(count)::value;
+          float2 f[N][4];
+          float r[N];
+#pragma unroll
+          for (int h = 0; h < N; ++h) {
+            unpack8(cols.load(in + (i + h) * 512, swap), f[h]);
+            float2 ss = mul2(f[h][0], f[h][0]);
+#pragma unroll
+            for (int j = 1; j < 4; ++j) ss = fma2(f[h][j], f[h][j], ss);
+            r[h] = ss.x + ss.y;
+          }
+          row_sums<D>(r);
+#pragma unroll
+          for (int h = 0; h < N; ++h) {
+            r[h] = p.w[0] ? rsqrtf(r[h] * (1.f / D) + p.eps) : 1.f;
+            float2 o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              o[j] = mul2(fma2(f[h][j], a[j], mul2(partner<INTER>(f[h], j), b[j])), make_float2(r[h], r[h]));
+            const uint4 v = live ? pack8(o) : constant;
+            if (t == 1) cols.store(in + (i + h) * 512, swap, v);   // a key's row goes back to its place
+            else if (cur.has) cols.store(out + (i + h) * D, v);
+          }
+        };
+        in_batches<2>(u.n, some);
+        if (t == 1) {
+          __syncwarp();
+          store_heads(in, u, 0);
+        }
+      }
     }
     __syncwarp();   // the stage has been read by every lane before the next iteration refills it
     stage = stage + 1 == kStages ? 0 : stage + 1;

@@ -54,33 +54,38 @@ struct WriteParams {
 // 3 heads of d = 64, which leave most of such a warp empty, 21.6 us for 30K tokens, and 11.8 us without.
 template <int D, int T, bool FILLED>
 __global__ void __launch_bounds__(kThreads) kv_cache_write_kernel(WriteParams p) {
-  constexpr int L = D / 8, RW = 32 / L;
+  constexpr int V = kLaneValues<T>, L = D / V, RW = 32 / L, U = kUnroll * 8 / V;   // passes of RW rows
   const int lane = threadIdx.x & 31, l = lane & (L - 1), sub = lane / L, which = blockIdx.y;
-  const uint32_t row0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * (kUnroll * RW) + sub;
+  const uint32_t row0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * (U * RW) + sub;
   if (row0 - sub >= p.rows) return;
   const int page_rows = p.geom.hkv << p.geom.page_log2, page_mask = (1 << p.geom.page_log2) - 1;
-  uint4 v[kUnroll];
-  int64_t dst[kUnroll];   // cache row; -1: not written
+  LaneValues<T> v[U];
+  int64_t dst[U];   // cache row; -1: not written
   if constexpr (FILLED) {
     const uint32_t token = divide(p.heads, row0 - sub);
     const int h = static_cast<int>(row0 - token * p.heads.d);
     const int64_t slot = __ldg(p.slots + token);
-    const __nv_bfloat16* x = pick(p.x, which) + token * pick(p.stride, which) + h * D + 8 * l;
+    const __nv_bfloat16* x = pick(p.x, which) + token * pick(p.stride, which) + h * D + V * l;
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(x + i * (RW * D)));
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int j = 0; j < V / 8; ++j) v[i][j] = __ldg(reinterpret_cast<const uint4*>(x + i * (RW * D)) + j);
     if (!slot_ok(p.geom, slot)) return;   // padding, or no slot of this cache
     dst[0] = (slot >> p.geom.page_log2) * page_rows + (h << p.geom.page_log2) + (slot & page_mask);
 #pragma unroll
-    for (int i = 1; i < kUnroll; ++i) dst[i] = dst[i - 1] + (RW << p.geom.page_log2);
+    for (int i = 1; i < U; ++i) dst[i] = dst[i - 1] + (RW << p.geom.page_log2);
   } else {
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
+    for (int i = 0; i < U; ++i) {
       const uint32_t row = row0 + i * RW, token = divide(p.heads, row);
       const int h = static_cast<int>(row - token * p.heads.d);
-      v[i] = uint4{};
+#pragma unroll
+      for (int j = 0; j < V / 8; ++j) v[i][j] = uint4{};
       dst[i] = -1;
       if (row < p.rows) {
-        v[i] = __ldg(reinterpret_cast<const uint4*>(pick(p.x, which) + token * pick(p.stride, which) + h * D + 8 * l));
+#pragma unroll
+        for (int j = 0; j < V / 8; ++j)
+          v[i][j] = __ldg(reinterpret_cast<const uint4*>(pick(p.x, which) + token * pick(p.stride, which) + h * D + V * l) + j);
         const int64_t slot = __ldg(p.slots + token);
         if (slot_ok(p.geom, slot)) dst[i] = (slot >> p.geom.page_log2) * page_rows + (h << p.geom.page_log2) + (slot & page_mask);
       }
@@ -88,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) kv_cache_write_kernel(WriteParams p)
   }
   const CacheRows cache = pick(p.cache, which);
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
+  for (int i = 0; i < U; ++i) {
     const StoredRow r = make_row<D, T>(v[i]);
     if (FILLED || dst[i] >= 0) put_row<D, T>(r, dst[i], l, cache);
   }

@@ -74,21 +74,21 @@ __device__ __forceinline__ uint32_t e4m3x2(float2 f) {
   return r;
 }
 // The nearest e2m1 codes of 8 values, ties to even, beyond 6 as 6: value i in bits 4i .. 4i + 3.
-__device__ __forceinline__ uint32_t e2m1x8(const float2 (&f)[4]) {
+__device__ __forceinline__ uint32_t e2m1x8(float2 f0, float2 f1, float2 f2, float2 f3) {
   uint32_t r;
   asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
-      : "=r"(r) : "f"(f[0].x), "f"(f[0].y), "f"(f[1].x), "f"(f[1].y), "f"(f[2].x), "f"(f[2].y), "f"(f[3].x), "f"(f[3].y));
+      : "=r"(r) : "f"(f0.x), "f"(f0.y), "f"(f1.x), "f"(f1.y), "f"(f2.x), "f"(f2.y), "f"(f3.x), "f"(f3.y));
   return r;
 }
 
-// Values rounded to 12 bits (z (2^12 + 1) split in two).  A quotient of an 8-bit value by a 4-bit one (or by 6) that is not halfway between
-// two codes is off it by 2^-8 of itself, far over 12 bits, so a quotient from an approximate reciprocal, rounded so, lies on the same
-// side of, or exactly on, every border between codes as the exact one.
-__device__ __forceinline__ float2 round12(float2 z) {
-  const float2 c = mul2(z, make_float2(4097.f, 4097.f));
-  const float2 low = fma2(z, make_float2(-1.f, -1.f), c);
-  return fma2(low, make_float2(-1.f, -1.f), c);
+// Quotients y / s of an 8-bit value by a 4-bit one (or by 6), given an approximate 1 / s: corrected by what is left of y, so that one that
+// is halfway between two codes is exactly so.  Any other is off every such point by 2^-8 of itself, so that both rounded to codes are the
+// exact quotient's.  (y * (1 / s) alone misses 18 % of the halfway points.)  Zeros keep their signs.
+__device__ __forceinline__ float2 quotient(float2 y, float s, float over) {
+  const float2 z = mul2(y, make_float2(over, over));
+  const float2 e = fma2(z, make_float2(s, s), make_float2(-y.x, -y.y));
+  return fma2(e, make_float2(-over, -over), z);
 }
 
 // A cache's arrays, of k or of v.
@@ -98,51 +98,61 @@ struct CacheRows {
   uint8_t* scales;
 };
 
-// A row as a cache stores it, 8 values a lane: lane `l` of the D / 8 that hold the row has columns 8l .. 8l + 7.
+// A row as a cache stores it, spread over lanes: lane `l` of the D / V that hold it has columns V l .. V l + V - 1.  V is 8, or 16 for e2m1: a
+// lane then has all of what one scale is of (168K tokens of 8 heads, d = 128, into 4 bits: WRITE16 us, WRITE8 with 8 a lane).
+template <int T>
+constexpr int kLaneValues = T == kE2m1 ? 16 : 8;
+template <int T>
+using LaneValues = uint4[kLaneValues<T> / 8];   // bf16
 struct StoredRow {
-  uint4 codes;      // e4m3: x, y; e2m1: x
-  uint32_t scale;   // e2m1: of this lane's 16 columns (lanes 2i and 2i + 1 alike)
+  uint4 codes;      // e4m3, e2m1: x, y
+  uint32_t scale;   // e2m1
   int byte;
 };
 
 // One row of bf16 values in its stored form.  All lanes of the warp take part.
 template <int D, int T>
-__device__ __forceinline__ StoredRow make_row(const uint4& v) {
-  constexpr int L = D / 8;
+__device__ __forceinline__ StoredRow make_row(const LaneValues<T>& v) {
   StoredRow r{};
   if constexpr (T == kBf16) {
-    r.codes = v;
+    r.codes = v[0];
   } else {
-    // bf16 magnitudes order as 15-bit integers: the row's largest, two at a time
-    uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    const uint32_t g = max(m & 0xffffu, m >> 16);   // of 16 columns
+    // bf16 magnitudes order as 15-bit integers: the lane's largest, then the row's, two at a time
+    constexpr int N = kLaneValues<T> / 2;
+    uint32_t u[N];
 #pragma unroll
-    for (int o = L / 2; o > 1; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int j = 0; j < N / 4; ++j) u[4 * j] = v[j].x, u[4 * j + 1] = v[j].y, u[4 * j + 2] = v[j].z, u[4 * j + 3] = v[j].w;
+    uint32_t g = u[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int j = 1; j < N; ++j) g = __vmaxu2(g, u[j] & 0x7fff7fffu);
+    uint32_t m = g;
+#pragma unroll
+    for (int o = D / kLaneValues<T> / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
     m = max(m & 0xffffu, m >> 16);
     const bool finite = m < 0x7f80u;
     // max|x| = 1.f * 2^(e - 127).  448 = 1.75 * 2^8: the scale's byte is e - 8, one more where 1.f > 1.75 (mantissa 0x60).
     // 6 * 448 = 1.3125 * 2^11: e - 11, one more where 1.f > 1.3125 (mantissa 0x28).
     r.byte = !finite ? 127 : T == kE4m3 ? max(static_cast<int>((m + 0x1fu) >> 7) - 8, 1) : max(static_cast<int>((m + 0x57u) >> 7) - 11, 1);
     const float inv = __uint_as_float(static_cast<uint32_t>(254 - r.byte) << 23);   // 2^-(byte - 127), exact
-    const uint32_t u4[4] = {v.x, v.y, v.z, v.w};
-    float2 y[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      y[j] = mul2(make_float2(__uint_as_float(u4[j] << 16), __uint_as_float(u4[j] & 0xffff0000u)), make_float2(inv, inv));
+    auto scaled = [&](int j) {
+      return mul2(make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u)), make_float2(inv, inv));
+    };
     if constexpr (T == kE4m3) {
       uint32_t x[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = e4m3x2(y[j]);
+      for (int j = 0; j < 4; ++j) x[j] = e4m3x2(scaled(j));
       r.codes.x = finite ? x[0] | x[1] << 16 : 0x7f7f7f7fu;
       r.codes.y = finite ? x[2] | x[3] << 16 : 0x7f7f7f7fu;
     } else {
-      const float sixth = __uint_as_float(g << 16) * inv * (1.f / 6.f);
-      const uint32_t code = e4m3x2(round12(make_float2(sixth, 0.f))) & 0xffu;
+      g = max(g & 0xffffu, g >> 16);
+      const float top = __uint_as_float(g << 16) * inv;
+      const uint32_t code = e4m3x2(quotient(make_float2(top, 0.f), 6.f, 1.f / 6.f)) & 0xffu;
       const float s = e4m3x2_to_float2(code).x, over = s > 0.f ? __fdividef(1.f, s) : 0.f;
+      float2 z[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = round12(mul2(y[j], make_float2(over, over)));
-      r.codes.x = finite ? e2m1x8(y) : 0u;
+      for (int j = 0; j < 8; ++j) z[j] = quotient(scaled(j), s, over);
+      r.codes.x = finite ? e2m1x8(z[0], z[1], z[2], z[3]) : 0u;
+      r.codes.y = finite ? e2m1x8(z[4], z[5], z[6], z[7]) : 0u;
       r.scale = finite ? code : 0x7fu;
     }
   }
@@ -152,16 +162,12 @@ __device__ __forceinline__ StoredRow make_row(const uint4& v) {
 // Write it at `row` of the cache.
 template <int D, int T>
 __device__ __forceinline__ void put_row(const StoredRow& r, int64_t row, int l, const CacheRows& c) {
-  constexpr int L = D / 8;
+  constexpr int L = D / kLaneValues<T>;
   if constexpr (T == kBf16) {
     reinterpret_cast<uint4*>(c.rows)[row * L + l] = r.codes;
   } else {
-    if constexpr (T == kE4m3) {
-      reinterpret_cast<uint2*>(c.rows)[row * L + l] = make_uint2(r.codes.x, r.codes.y);
-    } else {
-      reinterpret_cast<uint32_t*>(c.rows)[row * L + l] = r.codes.x;
-      if (!(l & 1)) c.scales[row * (L / 2) + (l >> 1)] = static_cast<uint8_t>(r.scale);
-    }
+    reinterpret_cast<uint2*>(c.rows)[row * L + l] = make_uint2(r.codes.x, r.codes.y);
+    if constexpr (T == kE2m1) c.scales[row * L + l] = static_cast<uint8_t>(r.scale);
     if (l == 0) c.exps[row] = static_cast<uint8_t>(r.byte);
   }
 }

@@ -170,7 +170,7 @@ struct UnitWalk {
     else pos = has ? __ldg(p.pos + token) : -1;
   }
   __device__ __forceinline__ void settle(const NormRopeParams& p) {   // by all lanes of the warp
-    const uint32_t token_lanes = (D == 128 ? 0xffffu : 0xffu) << (threadIdx.x & 31 & -(D / 8));
+    const uint32_t token_lanes = (D == 128 ? 0xffffu : 0xffu) << (threadIdx.x & (32 - D / 8));
     const uint32_t low = __ballot_sync(0xffffffffu, mine < 0), far = __ballot_sync(0xffffffffu, mine >= p.max_pos);
     pos = low & token_lanes ? -1 : far & token_lanes ? 0x7fffffff : 0;
   }
@@ -269,8 +269,8 @@ __device__ __forceinline__ void copy_table(const NormRopeParams& p, uint32_t to,
 
 // Start the copies of one unit into `stage`.  The rows of a token without a valid position, and of none, are filled with zeros:
 // they are not read, so that nothing in them reaches a sum.
-template <int D, bool BWD, bool AXES>
-__device__ __forceinline__ void copy_unit(const NormRopeParams& p, const Stages<D, BWD>& st, int stage, const UnitWalk<D, AXES>& w) {
+template <int D, bool BWD, bool AXES, typename P>
+__device__ __forceinline__ void copy_unit(const P& p, const Stages<D, BWD>& st, int stage, const UnitWalk<D, AXES>& w) {
   const int lane = threadIdx.x & 31, l = lane & (D / 8 - 1), sub = lane / (D / 8);
   const bool live = w.pos >= 0 && w.pos < p.max_pos;
   const int64_t token = live ? w.token : 0;
@@ -342,20 +342,27 @@ inline ffa_status check_common(const void* q, int64_t q_stride, const void* k, i
   return check_axes(axes, pair_axis, rot, p);
 }
 
-// Units for `warps` resident warps: the heads of a group of tokens are cut into units of equal size, kUnitHeads or kUnitMost at
-// most, and smaller ones where there would be fewer units than warps.
+// Cut the heads of a group of tokens into `per` units of `unit` heads at most.
+inline void cut_units(NormRopeParams& p, int64_t tokens, int d, int64_t per, int64_t unit) {
+  const int group = 256 / d;
+  p.tokens = tokens;
+  p.unit = static_cast<int32_t>(unit);
+  p.per = static_cast<int32_t>(per);
+  p.units = (tokens + group - 1) / group * per;
+  p.step_units = kWarps % p.per;
+  p.step_tokens = kWarps / p.per * group;
+}
+
+// Units for `warps` resident warps: equal sizes, kUnitHeads or kUnitMost at most, and smaller ones where there would be fewer units than
+// warps.
 template <bool BWD>
 void set_units(NormRopeParams& p, int64_t tokens, int d, int64_t warps) {
   const int group = 256 / d;
-  const int64_t groups = (tokens + group - 1) / group, all = p.heads[0] + p.heads[1] + p.heads[2];
+  const int64_t groups = (tokens + group - 1) / group, all = p.heads[0] + p.heads[1];
   const int64_t fewest = all <= kUnitMost<BWD> ? 1 : (all + kUnitHeads<BWD> - 1) / kUnitHeads<BWD>;
   const int64_t per = std::max(fewest, std::min(all, warps / std::max<int64_t>(groups, 1)));
-  p.tokens = tokens;
-  p.unit = static_cast<int32_t>((all + per - 1) / per);
-  p.per = static_cast<int32_t>((all + p.unit - 1) / p.unit);
-  p.units = groups * p.per;
-  p.step_units = kWarps % p.per;
-  p.step_tokens = kWarps / p.per * group;
+  const int64_t unit = (all + per - 1) / per;
+  cut_units(p, tokens, d, (all + unit - 1) / unit, unit);
 }
 
 template <int D, bool BWD>

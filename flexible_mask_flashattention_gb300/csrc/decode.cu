@@ -174,18 +174,21 @@ __device__ __forceinline__ float pow2i(int e) {   // 2^e, 0 below the normal ran
   return e < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+template <bool FIRSTS>   // first keys beside the range
 __device__ __forceinline__ KeyRange range_of(const DecodeParams& p, int seq, int strip) {
-  return key_range(p.lens[seq], p.starts ? p.starts[seq] : 0, p.firsts ? p.firsts[seq] : 0, p.max_pages, p.geom.page_log2, strip);
+  const int len = p.lens[seq], start = p.starts ? p.starts[seq] : 0;
+  if constexpr (FIRSTS) return key_range(len, start, p.firsts[seq], p.max_pages, p.geom.page_log2, strip);
+  else return key_range(len, start, p.max_pages, p.geom.page_log2);
 }
 
 // Where a walk over the CTA's share of the block list stands: unit (b, u) with u = kv head * subs + sub, `left` blocks of it from
 // the current one on, and the first key of this warp's strip in the current block.  Which of a block's strips is a warp's turns with
 // every unit, so that units of one strip keep all warps busy.
-template <int W, int KEYS>
+template <int W, int KEYS, bool FIRSTS>
 struct Walk {
   static constexpr int kBlock = KEYS * W;
   int b, u, left, key, start, end, turn;   // turn: of the block's strips, the one that is this warp's
-  int first, gap;                          // as in the KeyRange: keys are counted without the gap
+  int first, gap;                          // as in the KeyRange: keys are counted without the gap (0 without first keys)
   bool bad;
   // The first of the unit's blocks that is walked is `blk`.
   __device__ __forceinline__ void set(const KeyRange& r, int seq, int unit, int64_t blk) {
@@ -193,8 +196,8 @@ struct Walk {
     u = unit;
     start = static_cast<int>(r.start);
     end = static_cast<int>(r.end);
-    first = r.first;
-    gap = static_cast<int>(r.gap);
+    first = FIRSTS ? r.first : 0;
+    gap = FIRSTS ? static_cast<int>(r.gap) : 0;
     bad = r.bad;
     left = static_cast<int>(range_blocks(r, kBlock, KEYS) - blk);
     const int64_t k = range_first(r, KEYS) + (blk * W + turn) * KEYS;
@@ -208,14 +211,14 @@ struct Walk {
     turn = turn == 0 ? W - 1 : turn - 1;
     const bool wrap = u + 1 == units;
     const int seq = wrap ? b + 1 : b;
-    set(range_of(p, seq, KEYS), seq, wrap ? 0 : u + 1, 0);
+    set(range_of<FIRSTS>(p, seq, KEYS), seq, wrap ? 0 : u + 1, 0);
   }
   // Of this warp's strip: all its keys count; one of its keys, `key - key of the strip` = i, does; one of those from i on, 16 of them.
-  __device__ __forceinline__ bool whole() const { return (end - key >= KEYS) & ((key >= start) | (key + KEYS <= first)); }
-  __device__ __forceinline__ bool counts(int i) const { return (i < end - key) & ((i >= start - key) | (i < first - key)); }
-  __device__ __forceinline__ bool some(int i) const { return (end - key > i) & ((start - key < i + 16) | (first - key > i)); }
+  __device__ __forceinline__ bool whole() const { return (end - key >= KEYS) & ((key >= start) | (FIRSTS && key + KEYS <= first)); }
+  __device__ __forceinline__ bool counts(int i) const { return (i < end - key) & ((i >= start - key) | (FIRSTS && i < first - key)); }
+  __device__ __forceinline__ bool some(int i) const { return (end - key > i) & ((start - key < i + 16) | (FIRSTS && first - key > i)); }
   // The unit is one strip.
-  __device__ __forceinline__ bool single() const { return end - (first > 0 ? 0 : start / KEYS * KEYS) <= KEYS; }
+  __device__ __forceinline__ bool single() const { return end - (FIRSTS && first > 0 ? 0 : start / KEYS * KEYS) <= KEYS; }
 };
 
 // The first of the two neighbouring columns that a lane's MMA results of tile i are.
@@ -250,7 +253,7 @@ __device__ __forceinline__ RowEnd row_end(const DecodeParams& p, int head, float
   return r;
 }
 
-template <int D, int T, int NT>
+template <int D, int T, int NT, bool FIRSTS>
 __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(DecodeParams p) {
   using C = Cfg<D, T, NT>;
   constexpr bool QUANT = C::QUANT;
@@ -269,14 +272,14 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
   const int units = p.geom.hkv * p.subs;
 
   // ---- this CTA's share of the block list
-  auto blocks_of = [&](int seq) { return range_blocks(range_of(p, seq, C::KEYS), kBlock, C::KEYS); };
+  auto blocks_of = [&](int seq) { return range_blocks(range_of<FIRSTS>(p, seq, C::KEYS), kBlock, C::KEYS); };
   int64_t total, t0, t1, parts, off;   // off: of the share's first block in its sequence b
   int b;
   KeyRange range;
   const int64_t cta = blockIdx.x;
   if (p.batch <= 32) {   // a sequence a lane, every warp for itself
     KeyRange r{0, 0, false};
-    if (lane < p.batch) r = range_of(p, lane, C::KEYS);
+    if (lane < p.batch) r = range_of<FIRSTS>(p, lane, C::KEYS);
     const int64_t mine = lane < p.batch ? range_blocks(r, kBlock, C::KEYS) : 0;
     int64_t incl = mine;
 #pragma unroll
@@ -297,8 +300,10 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
     range.start = __shfl_sync(0xffffffffu, static_cast<int>(r.start), b);
     range.end = __shfl_sync(0xffffffffu, static_cast<int>(r.end), b);
     range.bad = __shfl_sync(0xffffffffu, static_cast<int>(r.bad), b) != 0;
-    range.first = __shfl_sync(0xffffffffu, r.first, b);
-    range.gap = __shfl_sync(0xffffffffu, static_cast<int>(r.gap), b);
+    if constexpr (FIRSTS) {
+      range.first = __shfl_sync(0xffffffffu, r.first, b);
+      range.gap = __shfl_sync(0xffffffffu, static_cast<int>(r.gap), b);
+    }
   } else {
     const int per = (p.batch + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
@@ -341,9 +346,9 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
     __syncthreads();
     b = begin->b;
     off = begin->off;
-    range = range_of(p, b, C::KEYS);
+    range = range_of<FIRSTS>(p, b, C::KEYS);
   }
-  Walk<kW, C::KEYS> cur;
+  Walk<kW, C::KEYS, FIRSTS> cur;
   bool opens_mid;
   {
     const int64_t nb = range_blocks(range, kBlock, C::KEYS);
@@ -356,26 +361,30 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
 
   // ---- loading one strip of this warp; the loads' walk runs ahead of the products'
   const uint32_t ring = smem_u32(smem + C::MISC + C::JOIN) + warp * (C::STAGE * C::STAGES);
-  Walk<kW, C::KEYS> ld = cur;
+  Walk<kW, C::KEYS, FIRSTS> ld = cur;
   const int page_rows = p.geom.hkv << p.geom.page_log2, page_mask = (1 << p.geom.page_log2) - 1;
+  // Strips that are one run of rows have a way of their own where issue slots bound the work.  Elsewhere its code costs small calls more than it
+  // gives large ones (e4m3, 32 x 1K keys 14.4 and 15.7 us, 1M keys 170 and 167).
+  constexpr bool kRuns = T == kE2m1;
   const bool one_page = page_mask + 1 >= C::KEYS && (C::KEYS & (C::KEYS - 1)) == 0;   // strips start at multiples of their length
   int real;               // the next strip's first key, the gap counted
   int head_row;           // the loading unit's head's first row in a page
   int page[SK];           // of the next strip's groups of 16 keys, read a strip ahead; -1 for a group outside the range
+  const int32_t* table_row;   // the loading unit's sequence's
   auto read_pages = [&]() {
-    const int32_t* row = p.table + ld.b * p.table_stride;
     real = ld.key < ld.first ? ld.key : ld.key + ld.gap;
-    if (SK > 1 && one_page) {   // its groups are all of the page that its first key is
-      page[0] = ld.end > ld.key ? __ldg(row + (real >> p.geom.page_log2)) : -1;
+    if (kRuns && one_page) {   // its groups are all of the page that its first key is
+      page[0] = ld.end > ld.key ? __ldg(table_row + (real >> p.geom.page_log2)) : -1;
 #pragma unroll
       for (int g = 1; g < SK; ++g) page[g] = page[0];
     } else {
 #pragma unroll
-      for (int g = 0; g < SK; ++g) page[g] = ld.some(16 * g) ? __ldg(row + ((real + 16 * g) >> p.geom.page_log2)) : -1;
+      for (int g = 0; g < SK; ++g) page[g] = ld.some(16 * g) ? __ldg(table_row + ((real + 16 * g) >> p.geom.page_log2)) : -1;
     }
   };
   auto open_unit = [&]() {
     head_row = (p.subs == 1 ? ld.u : ld.u / p.subs) << p.geom.page_log2;
+    table_row = p.table + ld.b * p.table_stride;
     read_pages();
   };
   // this lane's chunks of a strip: chunk lane + 32 i, 512 bytes apart in the cache; their places repeat every kPeriod of them
@@ -394,27 +403,31 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
   } else if constexpr (T == kE4m3) {
     side = lane ? p.v_exp : p.k_exp;
   }
+  auto page_good = [&]() { return static_cast<uint32_t>(page[0]) < static_cast<uint32_t>(p.geom.num_pages); };   // as page_ok, for pages of 32 bits
+  auto load_run = [&](int stage) {   // a strip that is one run of rows in a good page
+    const uint32_t off = head_row + (real & page_mask), base = stage * C::STAGE;
+    const uint8_t* k = k_lane + static_cast<uint64_t>(static_cast<uint32_t>(page[0])) * static_cast<uint32_t>(page_rows * C::ROW) + off * C::ROW;
+    const uint8_t* v = k + v_from_k;
+    const uint8_t* s = nullptr;
+    if constexpr (QUANT) s = side + static_cast<uint64_t>(static_cast<uint32_t>(page[0])) * (static_cast<uint32_t>(page_rows) * side_row) + off * side_row;
+#pragma unroll
+    for (int g = 0; g < SK; ++g) {
+#pragma unroll
+      for (int i = 0; i < C::CPR / 2; ++i) {
+        const uint32_t to = base + g * C::GROUP + dst_of[i % kPeriod] + i / kPeriod * (kPeriod * 512);
+        cp_async16(to, k + g * C::STRIP + 512 * i);
+        cp_async16(to + C::STRIP, v + g * C::STRIP + 512 * i);
+      }
+      if constexpr (QUANT) {
+        if (lane < C::SIDE) cp_async16(ring + base + g * C::GROUP + 2 * C::STRIP + 16 * lane, s + g * 16 * side_row);
+      }
+    }
+  };
   auto load_strip = [&](int stage, bool more) {
     const int have = ld.end - ld.key;
     const bool full = ld.whole();
-    if (have > 0 && full && (SK == 1 || one_page) && static_cast<uint32_t>(page[0]) < static_cast<uint32_t>(p.geom.num_pages)) {
-      const uint32_t off = head_row + (real & page_mask), base = stage * C::STAGE;   // one run of rows
-      const uint8_t* k = k_lane + static_cast<uint64_t>(static_cast<uint32_t>(page[0])) * static_cast<uint32_t>(page_rows * C::ROW) + off * C::ROW;
-      const uint8_t* v = k + v_from_k;
-      const uint8_t* s = nullptr;
-      if constexpr (QUANT) s = side + static_cast<uint64_t>(static_cast<uint32_t>(page[0])) * (static_cast<uint32_t>(page_rows) * side_row) + off * side_row;
-#pragma unroll
-      for (int g = 0; g < SK; ++g) {
-#pragma unroll
-        for (int i = 0; i < C::CPR / 2; ++i) {
-          const uint32_t to = base + g * C::GROUP + dst_of[i % kPeriod] + i / kPeriod * (kPeriod * 512);
-          cp_async16(to, k + g * C::STRIP + 512 * i);
-          cp_async16(to + C::STRIP, v + g * C::STRIP + 512 * i);
-        }
-        if constexpr (QUANT) {
-          if (lane < C::SIDE) cp_async16(ring + base + g * C::GROUP + 2 * C::STRIP + 16 * lane, s + g * 16 * side_row);
-        }
-      }
+    if (kRuns && have > 0 && full && one_page && page_good()) {
+      load_run(stage);
     } else if (have > 0) {
 #pragma unroll
       for (int g = 0; g < SK; ++g) {
@@ -481,7 +494,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
   float o[NT][C::MT][4];
   float m[NT][2], l[NT][2], vr[NT][2];
   // The query rows of a unit on their way to registers (a warp without a key in the part needs none), and what else begins with it.
-  auto load_q = [&](const Walk<kW, C::KEYS>& w) {
+  auto load_q = [&](const Walk<kW, C::KEYS, FIRSTS>& w) {
     const int kvh = w.u / p.subs, s0 = (w.u - kvh * p.subs) * NQ;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -544,10 +557,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
   }
 
   // ---- one strip: all groups' scores, their exponentials, then all groups' values
-  auto strip = [&](int stage) {
-    const int have = cur.end - cur.key;
-    if (have <= 0) return;
-    const bool whole = cur.whole();
+  auto strip = [&](int stage, bool whole) {
     const uint32_t sb = ring + stage * C::STAGE;
     // this lane's places in a strip; rows 8 further on are half a strip further on
     constexpr uint32_t kHalf = C::STRIP / 2, kScales = 2 * C::STRIP, kExps = kScales + 2 * C::SCALES;
@@ -654,6 +664,16 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
           for (int nt = 0; nt < NT; ++nt) x[g][nt][r] = in ? x[g][nt][r] : make_float2(-INFINITY, -INFINITY);
         }
     }
+    auto all_exponents = [&]() {
+#pragma unroll
+      for (int g = 0; g < SK; ++g)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) exponents(g, nt, 0), exponents(g, nt, 1);
+    };
+    // Where issue slots bound the work the exponents of most strips, whose references stay, are taken once, here; elsewhere behind the
+    // raise, which short units meet in every strip.
+    constexpr bool kOnce = T == kE2m1;
+    bool raise = false;
     float over_m = -1.f, over_v = -1.f;   // the largest of each
 #pragma unroll
     for (int g = 0; g < SK; ++g)
@@ -661,11 +681,16 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          exponents(g, nt, r);
-          over_m = fmax3(over_m, xm[g][nt][r].x, xm[g][nt][r].y);
-          if constexpr (QUANT) over_v = fmax3(over_v, xv[g][nt][r].x, xv[g][nt][r].y);
+          if constexpr (kOnce || QUANT) exponents(g, nt, r);
+          if constexpr (kOnce) {
+            over_m = fmax3(over_m, xm[g][nt][r].x, xm[g][nt][r].y);
+            over_v = fmax3(over_v, xv[g][nt][r].x, xv[g][nt][r].y);
+          } else {
+            raise |= x[g][nt][r].x > m[nt][0] || x[g][nt][r].y > m[nt][1];
+            if constexpr (QUANT) raise |= xv[g][nt][r].x > kTop || xv[g][nt][r].y > kTop;
+          }
         }
-    const bool raise = over_m > 0.f || over_v > kTop;
+    if constexpr (kOnce) raise = over_m > 0.f || over_v > kTop;
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -696,11 +721,9 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
             o[nt][i][c + 2] *= f;
           }
         }
-#pragma unroll
-      for (int g = 0; g < SK; ++g)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) exponents(g, nt, 0), exponents(g, nt, 1);
+      if constexpr (kOnce) all_exponents();
     }
+    if constexpr (!kOnce) all_exponents();
     uint32_t pf[SK][NT][2], pl[SK][NT][2];
 #pragma unroll
     for (int g = 0; g < SK; ++g)
@@ -934,26 +957,52 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
   bool first_part = true, from_start = !opens_mid;
   int32_t opened = 0;   // parts of the unit this CTA leaves open to later ones
   int stage = 0, fill = C::STAGES - 1;
+  // Blocks from here on whose strips, this warp's and the one to be loaded, are whole ones of the unit, none of them the unit's last, nor the
+  // share's: their walks need no more than a counter.
+  int run = 0, ran = 0;
+  auto runs = [&]() {
+    if (!one_page || ld.b != cur.b || ld.u != cur.u || cur.key < cur.start) return 0;
+    // ld's key is not before cur's; its strip behind the last of the run is a whole one too, so that its page may be looked up
+    const int most = min(min(cur.left, ld.left) - 1, (cur.end - ld.key - C::KEYS) / kBlock);
+    return static_cast<int>(min(static_cast<int64_t>(most), todo - C::STAGES));
+  };
 #pragma unroll 1
   for (;;) {   // a unit's part after the other
     begin_unit();
 #pragma unroll 1
     for (;;) {   // its blocks
-      if (todo > C::STAGES - 1) load_strip(fill, todo > C::STAGES);
+      const bool plain = run > 0 && page_good();
+      if (plain) {
+        load_run(fill);
+        --ld.left;
+        ld.key += kBlock;
+        real += kBlock;
+        page[0] = __ldg(table_row + (real >> p.geom.page_log2));
+      } else if (todo > C::STAGES - 1) {
+        load_strip(fill, todo > C::STAGES);
+      }
       cp_async_commit();
       fill = fill + 1 == C::STAGES ? 0 : fill + 1;
       cp_async_wait<C::STAGES - 1>();
       __syncwarp();
-      strip(stage);
+      if (run > 0 || cur.end > cur.key) strip(stage, run > 0 || cur.whole());
       __syncwarp();   // the stage has been read by every lane before the next iteration refills it
       stage = stage + 1 == C::STAGES ? 0 : stage + 1;
+      if (run > 0) {
+        if (--run > 0) continue;
+        cur.left -= ran;
+        cur.key += ran * kBlock;
+        todo -= ran;
+        continue;
+      }
       if (cur.left == 1 || todo == 1) break;
       cur.step();
       --todo;
+      if (kRuns && cur.left > 2) ran = run = runs();
     }
     const bool last = cur.left == 1, whole = last && from_start;
     const int slot = static_cast<int>(2 * cta) + (first_part ? 0 : 1);
-    Walk<kW, C::KEYS> next = cur;
+    Walk<kW, C::KEYS, FIRSTS> next = cur;
     if (todo > 1) {   // the next unit's queries travel while this one's part ends
       next.next_unit(p, units);
       load_q(next);
@@ -1037,22 +1086,25 @@ size_t ml_bytes(int nt) { return size_t{2} * kMaxCtas * 8 * nt * 2 * sizeof(floa
 size_t part_bytes(int nt, int d) { return size_t{2} * kMaxCtas * 8 * nt * d * sizeof(float); }
 int tiles_of(int group) { return group > 8 ? 2 : 1; }   // query tiles of 8 a unit
 
-template <int D, int T, int NT>
+template <int D, int T, int NT, bool FIRSTS>
 ffa_status launch(const DecodeParams& p, int device, int sms, cudaStream_t s) {
   using C = Cfg<D, T, NT>;
   static_assert(C::FIT >= C::STAGES && C::STAGES >= 2, "ring");
   static std::atomic<bool> raised[kDevices];
   const int grid = std::min(sms, kMaxCtas);
-  const cudaError_t e = launch_large(decode_kernel<D, T, NT>, dim3(grid), C::THREADS, C::SMEM, C::SMEM, s, device, raised, p);
+  const cudaError_t e = launch_large(decode_kernel<D, T, NT, FIRSTS>, dim3(grid), C::THREADS, C::SMEM, C::SMEM, s, device, raised, p);
   if (e != cudaSuccess) return FFA_ERR_CUDA;
   return cuda_status(launch_after(decode_join_kernel<D, NT>, dim3(grid, std::min(8 * NT, p.group)), 256, s, p));
 }
 
+template <int D, int T>
+ffa_status launch_type(int nt, const DecodeParams& p, int device, int sms, cudaStream_t s) {
+  if (p.firsts) return nt == 1 ? launch<D, T, 1, true>(p, device, sms, s) : launch<D, T, 2, true>(p, device, sms, s);
+  return nt == 1 ? launch<D, T, 1, false>(p, device, sms, s) : launch<D, T, 2, false>(p, device, sms, s);
+}
 template <int D>
 ffa_status launch_any(int type, int nt, const DecodeParams& p, int device, int sms, cudaStream_t s) {
-  if (type == kE2m1) return nt == 1 ? launch<D, kE2m1, 1>(p, device, sms, s) : launch<D, kE2m1, 2>(p, device, sms, s);
-  if (type == kE4m3) return nt == 1 ? launch<D, kE4m3, 1>(p, device, sms, s) : launch<D, kE4m3, 2>(p, device, sms, s);
-  return nt == 1 ? launch<D, kBf16, 1>(p, device, sms, s) : launch<D, kBf16, 2>(p, device, sms, s);
+  return type == kE2m1 ? launch_type<D, kE2m1>(nt, p, device, sms, s) : type == kE4m3 ? launch_type<D, kE4m3>(nt, p, device, sms, s) : launch_type<D, kBf16>(nt, p, device, sms, s);
 }
 
 }  // namespace

@@ -54,8 +54,8 @@ namespace {
 // spread a strip's fixed instructions over more keys.  Measured before later steps (us; 50 x 20K keys, 64 + 8 heads, d = 64, e4m3): 8 warps x 1 group 165,
 // 8 x 2 137, 8 x 4 120, 12 x 4 118, 16 x 2 118, and later 12 x 2 114 and 16 x 2 116; (1M keys, 16 + 4 heads, d = 128, e4m3): 8 x 1 181, 12 x 1 170, 8 x 2 169; (24 x 8K
 // keys, 32 heads, d = 64, bf16): 8 x 1 119, 8 x 2 122, 12 x 2 117; (380K keys, 32 + 2 heads, d = 128, e4m3): 8 x 1 46, 8 x 2 43.
-constexpr int warps_of(int d, int nt, int type) { return nt == 2 || (d == 128 && type != kE2m1) ? 8 : 12; }
-constexpr int groups_of(int d, int type) { return d == 128 && type == kBf16 ? 1 : type == kE2m1 ? (d == 64 ? 4 : 2) : 2; }
+constexpr int warps_of(int d, int nt, int type) { return nt == 2 ? 8 : d == 64 ? (type == kE2m1 ? 16 : 12) : type == kE2m1 ? 12 : 8; }
+constexpr int groups_of(int d, int type) { return d == 128 && type == kBf16 ? 1 : 2; }
 constexpr int kMaxCtas = 160;          // CTAs (one an SM) the workspace holds parts for: two a CTA
 constexpr int kSmemMax = 226 * 1024;   // of 227 KB
 constexpr float kLog2e = 1.4426950408889634f;
@@ -116,7 +116,7 @@ struct Cfg {
   // Two stages, though three would fit e4m3 at d = 128 and groups over 8 at d = 64: more loads in flight are slower (e4m3, 64 x 16K keys
   // 219 and 224 us, 1M keys 164 and 169 us; 16 x 32K keys of 16-head groups, d = 64, bf16 37 and 39 us).  bf16 at d = 128 takes what
   // fits (777 keys 6.6 us with three and 6.8 with two, large batches alike).
-  static constexpr int STAGES = T == kE2m1 ? (D == 64 ? 3 : 3) : T == kE4m3 || D == 64 ? 2 : FIT;
+  static constexpr int STAGES = T != kBf16 || D == 64 ? 2 : FIT;
   static constexpr int SMEM = MISC + JOIN + W * STAGE * STAGES;
   static constexpr int KSTEPS = D / 16;
   static constexpr int MT = D / 16;                     // 16-column tiles of the output

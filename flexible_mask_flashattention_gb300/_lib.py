@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Iterable, Optional, Sequence, Tuple
 
 import numpy as np
@@ -128,7 +129,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.ffa_qk_norm_rope_axes.argtypes = axes_args + [_vp, _vp, _vp]
     lib.ffa_qk_norm_rope_axes_bwd.restype = ctypes.c_int
     lib.ffa_qk_norm_rope_axes_bwd.argtypes = axes_args + [_vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
-    cache = ctypes.POINTER(KVCacheC)
+    cache = _vp   # a KVCacheC, or its bytes
     lib.ffa_kv_cache_append.restype = ctypes.c_int
     lib.ffa_kv_cache_append.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i32, _vp, _vp, ctypes.c_float, _vp, _i64, _i32,
                                         _i32, _vp, _i32, _vp, _vp, cache, _vp, _vp]
@@ -614,12 +615,13 @@ def _dims(t, name, n):
     return t.shape
 
 
-def _kv_cache(k_cache, v_cache, k_exp, v_exp, k_scale, v_scale, dev) -> KVCacheC:
-    """The C description of a cache: k, v [pages, hkv, page_size, d] bf16, or float8_e4m3fn with exponent bytes, or
+_pack_cache = struct.Struct("@4Pq4i2P").pack   # a KVCacheC's bytes, in half the time
+
+
+def _kv_cache(k_cache, v_cache, k_exp, v_exp, k_scale, v_scale, dev):
+    """(bytes of the C description, hkv, d) of a cache: k, v [pages, hkv, page_size, d] bf16, or float8_e4m3fn with exponent bytes, or
     [pages, hkv, page_size, d / 2] uint8 (two e2m1 codes a byte) with exponent bytes and float8_e4m3fn scales."""
     dtype = k_cache.dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.float8_e4m3fn and dtype is not torch.uint8:
-        raise FFAError(1, "k_cache must be a bfloat16, float8_e4m3fn or uint8 tensor")
     shape = pages, hkv, page_size, d = _dims(k_cache, "k_cache", 4)
     _check_dense(k_cache, dtype, shape, dev, "k_cache")
     _check_dense(v_cache, dtype, shape, dev, "v_cache")
@@ -628,18 +630,21 @@ def _kv_cache(k_cache, v_cache, k_exp, v_exp, k_scale, v_scale, dev) -> KVCacheC
     if dtype is torch.bfloat16:
         if k_exp is not None or v_exp is not None:
             raise FFAError(1, "a bfloat16 cache has no exponent bytes")
-        return KVCacheC(k_cache.data_ptr(), v_cache.data_ptr(), None, None, pages, page_size, hkv, d, 0)
+        return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), 0, 0, pages, page_size, hkv, d, 0, 0, 0), hkv, d
+    if dtype is not torch.float8_e4m3fn and dtype is not torch.uint8:
+        raise FFAError(1, "k_cache must be a bfloat16, float8_e4m3fn or uint8 tensor")
     _check_dense(k_exp, torch.uint8, shape[:3], dev, "k_exp")
     _check_dense(v_exp, torch.uint8, shape[:3], dev, "v_exp")
     if dtype is torch.float8_e4m3fn:
-        return KVCacheC(k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), pages, page_size, hkv, d, 1)
+        return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), pages, page_size, hkv, d, 1,
+                           0, 0), hkv, d
     if d != 32 and d != 64:
         raise FFAError(4, f"k_cache holds rows of {2 * d} values in 4 bits")
     scales = (pages, hkv, page_size, d // 8)
     _check_dense(k_scale, torch.float8_e4m3fn, scales, dev, "k_scale")
     _check_dense(v_scale, torch.float8_e4m3fn, scales, dev, "v_scale")
-    return KVCacheC(k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), pages, page_size, hkv, 2 * d, 4,
-                    k_scale.data_ptr(), v_scale.data_ptr())
+    return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), pages, page_size, hkv, 2 * d, 4,
+                       k_scale.data_ptr(), v_scale.data_ptr()), hkv, 2 * d
 
 
 def _page_table(t, batch: int, dev):
@@ -773,17 +778,17 @@ def kv_cache_write(k, v, k_cache, v_cache, slots, k_exp=None, v_exp=None, stream
     d / 2] holds e2m1 codes, two a byte (the lower half first), such exponents and, in k_scale / v_scale [pages, Hkv, page_size,
     d / 16] float8_e4m3fn, a scale every 16 values: value = code * scale * 2^(byte - 127)."""
     dev = _device(k_cache, "k_cache")
-    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp, k_scale, v_scale, dev)
+    cache, hkv, cd = _kv_cache(k_cache, v_cache, k_exp, v_exp, k_scale, v_scale, dev)
     if not isinstance(slots, torch.Tensor):
         raise FFAError(1, "slots must be a CUDA tensor")
     tokens, = _dims(slots, "slots", 1)
-    shape = (tokens, cache.hkv, cache.d)
+    shape = (tokens, hkv, cd)
     ks = _rows_stride(k, "k", shape, dev)
     vs = _rows_stride(v, "v", shape, dev)
     _check_dense(slots, torch.int64, (tokens,), dev, "slots")
     handle, _ = _on(stream, dev, k, v, k_cache, v_cache, slots, k_exp, v_exp, k_scale, v_scale)
     _check(load_library().ffa_kv_cache_write(k.data_ptr(), ks, v.data_ptr(), vs, tokens, slots.data_ptr(),
-                                             ctypes.byref(cache), handle), "ffa_kv_cache_write")
+                                             cache, handle), "ffa_kv_cache_write")
 
 
 def kv_cache_append(q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_cache, slots, eps: float = 1e-6,
@@ -793,12 +798,12 @@ def kv_cache_append(q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_
     cache as kv_cache_write does, in one pass and to the same bits.  Weights, positions and axes as in qk_norm_rope; slots and
     caches as in kv_cache_write."""
     dev = _device(k_cache, "k_cache")
-    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp, k_scale, v_scale, dev)
+    cache, hkv, cd = _kv_cache(k_cache, v_cache, k_exp, v_exp, k_scale, v_scale, dev)
     if not isinstance(q, torch.Tensor) or not isinstance(slots, torch.Tensor):
         raise FFAError(1, "q and slots must be CUDA tensors")
     tokens, hq, d = _dims(q, "q", 3)
-    shape = (tokens, cache.hkv, cache.d)
-    qs = _rows_stride(q, "q", (tokens, hq, cache.d), dev)
+    shape = (tokens, hkv, cd)
+    qs = _rows_stride(q, "q", (tokens, hq, cd), dev)
     ks = _rows_stride(k, "k", shape, dev)
     vs = _rows_stride(v, "v", shape, dev)
     qw, kw, max_pos, rot, n, pairs = _rotation_inputs(q_weight, k_weight, cos_sin, positions, axes, tokens, d, dev)
@@ -811,7 +816,7 @@ def kv_cache_append(q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_
         _check_dense(q_out, torch.bfloat16, (tokens, hq, d), dev, "q_out")
     _check(load_library().ffa_kv_cache_append(
         q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, tokens, hq, qw, kw, eps, cos_sin.data_ptr(), max_pos, rot,
-        bool(interleaved), positions.data_ptr(), n or 1, pairs, slots.data_ptr(), ctypes.byref(cache), q_out.data_ptr(), handle),
+        bool(interleaved), positions.data_ptr(), n or 1, pairs, slots.data_ptr(), cache, q_out.data_ptr(), handle),
         "ffa_kv_cache_append")
     return q_out
 
@@ -822,7 +827,7 @@ def kv_cache_read(k_cache, v_cache, page_table, cu_seqlens, total: int, k=None, 
     every sequence, back to back; page_table [B, max_pages] int32.  Rows behind the last sequence are left as they
     were (undefined where k and v are allocated here).  Caches as in kv_cache_write."""
     dev = _device(k_cache, "k_cache")
-    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp, k_scale, v_scale, dev)
+    cache, hkv, cd = _kv_cache(k_cache, v_cache, k_exp, v_exp, k_scale, v_scale, dev)
     if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise FFAError(1, "cu_seqlens must be an int32 tensor [batch + 1]")
     _check_dense(cu_seqlens, torch.int32, cu_seqlens.shape, dev, "cu_seqlens")
@@ -830,7 +835,7 @@ def kv_cache_read(k_cache, v_cache, page_table, cu_seqlens, total: int, k=None, 
     if batch > _I32_MAX:
         raise FFAError(5, "cu_seqlens has more sequences than 32 bits count")
     ts, width = _page_table(page_table, batch, dev)
-    shape, bf16 = (int(total), cache.hkv, cache.d), torch.bfloat16
+    shape, bf16 = (int(total), hkv, cd), torch.bfloat16
     if shape[0] < 0:
         raise FFAError(1, "total must not be negative")
     handle, context = _on(stream, dev, k_cache, v_cache, page_table, cu_seqlens, k, v, k_exp, v_exp, k_scale, v_scale)
@@ -842,7 +847,7 @@ def kv_cache_read(k_cache, v_cache, page_table, cu_seqlens, total: int, k=None, 
         v = _empty(context, shape, bf16)
     else:
         _check_dense(v, bf16, shape, dev, "v")
-    _check(load_library().ffa_kv_cache_read(ctypes.byref(cache), page_table.data_ptr(), ts, width, batch,
+    _check(load_library().ffa_kv_cache_read(cache, page_table.data_ptr(), ts, width, batch,
                                             cu_seqlens.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(), handle),
            "ffa_kv_cache_read")
     return k, v
@@ -850,6 +855,9 @@ def kv_cache_read(k_cache, v_cache, page_table, cu_seqlens, total: int, k=None, 
 
 def fwd_decode_workspace_size(hq: int, hkv: int, d: int) -> int:
     return load_library().ffa_fwd_decode_workspace_size(hq, hkv, d)
+
+
+_decode_sizes = {}   # workspace sizes by head counts and head dim
 
 
 def fwd_decode(q, k_cache, v_cache, page_table, kv_lens, scale: float, k_exp=None, v_exp=None, kv_starts=None,
@@ -860,9 +868,9 @@ def fwd_decode(q, k_cache, v_cache, page_table, kv_lens, scale: float, k_exp=Non
     dev = _device(q, "q")
     if not isinstance(k_cache, torch.Tensor):
         raise FFAError(1, "k_cache must be a CUDA tensor")
-    cache = _kv_cache(k_cache, v_cache, k_exp, v_exp, k_scale, v_scale, dev)
+    cache, hkv, cd = _kv_cache(k_cache, v_cache, k_exp, v_exp, k_scale, v_scale, dev)
     b, hq, d = _dims(q, "q", 3)
-    qs = _rows_stride(q, "q", (b, hq, cache.d), dev)
+    qs = _rows_stride(q, "q", (b, hq, cd), dev)
     ts, width = _page_table(page_table, b, dev)
     bf16, f32 = torch.bfloat16, torch.float32
     _check_dense(kv_lens, torch.int32, (b,), dev, "kv_lens")
@@ -883,11 +891,14 @@ def fwd_decode(q, k_cache, v_cache, page_table, kv_lens, scale: float, k_exp=Non
     else:
         _check_dense(lse, f32, (hq, b), dev, "lse")
     if workspace is None:
-        workspace = _empty(context, (fwd_decode_workspace_size(hq, cache.hkv, d),), torch.uint8)
+        size = _decode_sizes.get((hq, hkv, d))
+        if size is None:
+            size = _decode_sizes[hq, hkv, d] = fwd_decode_workspace_size(hq, hkv, d)
+        workspace = _empty(context, (size,), torch.uint8)
     else:
         _check_workspace(workspace, dev)
     _check(load_library().ffa_fwd_decode_window(
-        q.data_ptr(), qs, ctypes.byref(cache), page_table.data_ptr(), ts, width, b, hq, kv_lens.data_ptr(),
+        q.data_ptr(), qs, cache, page_table.data_ptr(), ts, width, b, hq, kv_lens.data_ptr(),
         None if kv_starts is None else kv_starts.data_ptr(), None if kv_firsts is None else kv_firsts.data_ptr(), scale,
         None if sink is None else sink.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
         handle), "ffa_fwd_decode")

@@ -47,6 +47,7 @@ struct WriteParams {
   PageGeom geom;
   FastDiv heads;
   uint32_t rows;               // tokens * hkv
+  bool wide;                   // every row of k and v at a multiple of 32 bytes
 };
 
 // FILLED: a token's rows fill the passes of a whole number of warps (hkv a multiple of kUnroll * RW), so that token and page are the
@@ -59,6 +60,14 @@ __global__ void __launch_bounds__(kThreads) kv_cache_write_kernel(WriteParams p)
   const uint32_t row0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * (U * RW) + sub;
   if (row0 - sub >= p.rows) return;
   const int page_rows = p.geom.hkv << p.geom.page_log2, page_mask = (1 << p.geom.page_log2) - 1;
+  auto read = [&](const __nv_bfloat16* x, LaneValues<T>& to) {
+    if (FILLED && V == 16 && p.wide) {
+      load32(x, to[0], to[V / 8 - 1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V / 8; ++j) to[j] = __ldg(reinterpret_cast<const uint4*>(x) + j);
+    }
+  };
   LaneValues<T> v[U];
   int64_t dst[U];   // cache row; -1: not written
   if constexpr (FILLED) {
@@ -67,9 +76,7 @@ __global__ void __launch_bounds__(kThreads) kv_cache_write_kernel(WriteParams p)
     const int64_t slot = __ldg(p.slots + token);
     const __nv_bfloat16* x = pick(p.x, which) + token * pick(p.stride, which) + h * D + V * l;
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-#pragma unroll
-      for (int j = 0; j < V / 8; ++j) v[i][j] = __ldg(reinterpret_cast<const uint4*>(x + i * (RW * D)) + j);
+    for (int i = 0; i < U; ++i) read(x + i * (RW * D), v[i]);
     if (!slot_ok(p.geom, slot)) return;   // padding, or no slot of this cache
     dst[0] = (slot >> p.geom.page_log2) * page_rows + (h << p.geom.page_log2) + (slot & page_mask);
 #pragma unroll
@@ -83,9 +90,7 @@ __global__ void __launch_bounds__(kThreads) kv_cache_write_kernel(WriteParams p)
       for (int j = 0; j < V / 8; ++j) v[i][j] = uint4{};
       dst[i] = -1;
       if (row < p.rows) {
-#pragma unroll
-        for (int j = 0; j < V / 8; ++j)
-          v[i][j] = __ldg(reinterpret_cast<const uint4*>(pick(p.x, which) + token * pick(p.stride, which) + h * D + V * l) + j);
+        read(pick(p.x, which) + token * pick(p.stride, which) + h * D + V * l, v[i]);
         const int64_t slot = __ldg(p.slots + token);
         if (slot_ok(p.geom, slot)) dst[i] = (slot >> p.geom.page_log2) * page_rows + (h << p.geom.page_log2) + (slot & page_mask);
       }
@@ -110,6 +115,7 @@ struct ReadParams {
   PageGeom geom;
   FastDiv heads;
   int32_t tile;   // tokens a CTA
+  bool wide;      // both outputs at multiples of 32 bytes
 };
 
 constexpr int kReadRows = 256;   // rows a CTA, or those of 8 tokens: so many tokens that a thread each finds their places
@@ -117,7 +123,7 @@ constexpr int kReadRows = 256;   // rows a CTA, or those of 8 tokens: so many to
 // A CTA takes `tile` consecutive tokens of the output; a thread a token finds its sequence and page.
 template <int D, int T>
 __global__ void __launch_bounds__(kThreads) kv_cache_read_kernel(ReadParams p) {
-  constexpr int L = D / 8, RW = 32 / L;
+  constexpr int V = kLaneValues<T>, L = D / V, RW = 32 / L, U = kUnroll * 8 / V;   // passes of RW rows
   __shared__ int64_t src[kReadRows];   // row of head 0 in the cache; -1: outside the batch, -2: no page of this cache
   const int64_t t0 = blockIdx.x * static_cast<int64_t>(p.tile);
   if (threadIdx.x < p.tile) {
@@ -146,13 +152,13 @@ __global__ void __launch_bounds__(kThreads) kv_cache_read_kernel(ReadParams p) {
   const int lane = threadIdx.x & 31, l = lane & (L - 1), sub = lane / L, which = blockIdx.y;
   const uint32_t rows = p.tile * p.geom.hkv;
   const CacheRows cache = pick(p.cache, which);
-  __nv_bfloat16* out = pick(p.out, which) + t0 * p.geom.hkv * D + 8 * l;
-  for (uint32_t r0 = (threadIdx.x >> 5) * (kUnroll * RW) + sub; r0 - sub < rows; r0 += kWarps * kUnroll * RW) {
-    uint4 v[kUnroll];
-    uint32_t e[kUnroll];
-    int64_t at[kUnroll];
+  __nv_bfloat16* out = pick(p.out, which) + t0 * p.geom.hkv * D + V * l;
+  for (uint32_t r0 = (threadIdx.x >> 5) * (U * RW) + sub; r0 - sub < rows; r0 += kWarps * U * RW) {
+    uint4 v[U];
+    uint32_t e[U];
+    int64_t at[U];
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
+    for (int i = 0; i < U; ++i) {
       const uint32_t r = r0 + i * RW, token = divide(p.heads, r);
       at[i] = -1;
       if (r >= rows) continue;
@@ -160,8 +166,8 @@ __global__ void __launch_bounds__(kThreads) kv_cache_read_kernel(ReadParams p) {
       if (at[i] < 0) continue;
       const int64_t row = at[i] + (static_cast<int64_t>(r - token * p.heads.d) << p.geom.page_log2);
       if constexpr (T == kE2m1) {
-        v[i].x = __ldg(static_cast<const uint32_t*>(cache.rows) + row * L + l);
-        v[i].y = __ldg(cache.scales + row * (L / 2) + (l >> 1));
+        const uint2 c = __ldg(static_cast<const uint2*>(cache.rows) + row * L + l);
+        v[i].x = c.x, v[i].y = c.y, v[i].z = __ldg(cache.scales + row * L + l);
         e[i] = __ldg(cache.exps + row);
       } else if constexpr (T == kE4m3) {
         const uint2 c = __ldg(static_cast<const uint2*>(cache.rows) + row * L + l);
@@ -172,35 +178,41 @@ __global__ void __launch_bounds__(kThreads) kv_cache_read_kernel(ReadParams p) {
       }
     }
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
+    for (int i = 0; i < U; ++i) {
       if (at[i] == -1) continue;
-      uint4 o = v[i];
-      if (at[i] == -2) {
-        o = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-      } else if constexpr (T == kE2m1) {
-        const float s = exp_scale(e[i]);
-        const uint32_t scale = e4m3x2_to_f16x2(v[i].y | v[i].y << 8);
-        uint32_t c[4], w[4];
-        e2m1x8_to_f16x2(v[i].x, c);
+      uint4 o[V / 8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {   // code times scale is exact in f16
-          const uint32_t h = mul_f16x2(c[j], scale);
-          const float2 f = mul2(__half22float2(*reinterpret_cast<const __half2*>(&h)), make_float2(s, s));
-          w[j] = pack_bf16x2(f.x, f.y);
-        }
-        o = make_uint4(w[0], w[1], w[2], w[3]);
-      } else if constexpr (T == kE4m3) {
-        const float s = exp_scale(e[i]);
-        const uint32_t c[4] = {v[i].x & 0xffffu, v[i].x >> 16, v[i].y & 0xffffu, v[i].y >> 16};
-        uint32_t w[4];
+      for (int j = 0; j < V / 8; ++j) {
+        o[j] = v[i];
+        if (at[i] == -2) {
+          o[j] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+        } else if constexpr (T != kBf16) {
+          const float s = exp_scale(e[i]);
+          uint32_t c[4], w[4];
+          if constexpr (T == kE2m1) {
+            const uint32_t scale = e4m3x2_to_f16x2(v[i].z | v[i].z << 8);
+            e2m1x8_to_f16x2(j ? v[i].y : v[i].x, c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = mul2(e4m3x2_to_float2(c[j]), make_float2(s, s));
-          w[j] = pack_bf16x2(f.x, f.y);
+            for (int k = 0; k < 4; ++k) c[k] = mul_f16x2(c[k], scale);   // exact
+          } else {
+            e4m3x4_to_f16x2(v[i].x, c[0], c[1]);
+            e4m3x4_to_f16x2(v[i].y, c[2], c[3]);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = mul2(__half22float2(*reinterpret_cast<const __half2*>(&c[k])), make_float2(s, s));
+            w[k] = pack_bf16x2(f.x, f.y);
+          }
+          o[j] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        o = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      *reinterpret_cast<uint4*>(out + static_cast<int64_t>(r0 + i * RW) * D) = o;
+      __nv_bfloat16* to = out + static_cast<int64_t>(r0 + i * RW) * D;
+      if (V == 16 && p.wide) {
+        store32(to, o[0], o[V / 8 - 1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V / 8; ++j) reinterpret_cast<uint4*>(to)[j] = o[j];
+      }
     }
   }
 }
@@ -271,6 +283,7 @@ ffa_status ffa_kv_cache_write(const void* k, int64_t k_stride, const void* v, in
   p.cache[1] = {cache->v, cache->v_exp, cache->v_scale};
   p.slots = slots;
   p.rows = static_cast<uint32_t>(tokens * cache->hkv);
+  p.wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0 && k_stride % 16 == 0 && v_stride % 16 == 0;
   p.heads = fast_div(static_cast<uint32_t>(cache->hkv));
   const int per = kWarps * kUnroll * 256 / cache->d;   // rows a CTA
   const unsigned blocks = (p.rows + per - 1) / per;
@@ -312,6 +325,7 @@ ffa_status ffa_kv_cache_read(const ffa_kv_cache* cache, const int32_t* page_tabl
   p.total = total;
   p.heads = fast_div(static_cast<uint32_t>(cache->hkv));
   p.tile = std::max(8, kReadRows / cache->hkv);
+  p.wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const dim3 grid(static_cast<unsigned>((total + p.tile - 1) / p.tile), 2);
   auto* kernel = cache->d == 128 ? read_kernel<128>(cache->dtype) : read_kernel<64>(cache->dtype);

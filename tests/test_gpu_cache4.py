@@ -49,6 +49,28 @@ def test_write_and_read(ffa, tokens, hkv, d, page):
         assert (got[len(ref):] == 3.25).all()
 
 
+@pytest.mark.parametrize("hkv,d", [(8, 128), (3, 64), (16, 64)])
+def test_rows_at_multiples_of_16_bytes_only(ffa, hkv, d):
+    """Inputs and outputs 16 bytes into an allocation, token strides that are multiples of 8 values: the same as at round addresses."""
+    import torch
+    g = torch.Generator().manual_seed(hkv)
+    n, page = 90, 32
+    k, v = (torch.randn(n, hkv, d, generator=g).bfloat16().cuda() for _ in "kv")
+    wide = torch.zeros(n, 2 * hkv * d + 8, dtype=torch.bfloat16, device="cuda")
+    odd = [wide[:, 8 + i * hkv * d:8 + (i + 1) * hkv * d].unflatten(1, (hkv, d)) for i in range(2)]
+    odd[0].copy_(k), odd[1].copy_(v)
+    a, b = (Cache(4, hkv, page, d, "e2m1") for _ in range(2))
+    slots = torch.randperm(4 * page, generator=g)[:n].cuda()
+    ffa.kv_cache_write(k, v, a.k, a.v, slots, **a.more())
+    ffa.kv_cache_write(*odd, b.k, b.v, slots, **b.more())
+    same_arrays(a.arrays(), b.arrays())
+    table, cu = torch.arange(4, dtype=torch.int32).cuda()[None], torch.tensor([0, 4 * page], dtype=torch.int32).cuda()
+    want = ffa.kv_cache_read(a.k, a.v, table, cu, 4 * page, **a.more())
+    out = [torch.empty(4 * page * hkv * d + 8, dtype=torch.bfloat16, device="cuda")[8:].view(4 * page, hkv, d) for _ in "kv"]
+    ffa.kv_cache_read(a.k, a.v, table, cu, 4 * page, k=out[0], v=out[1], **a.more())
+    assert all((bits(x) == bits(y)).all() for x, y in zip(out, want))
+
+
 def test_every_scale_and_every_tie(ffa):
     """Groups whose scale runs over all e4m3 values beside one that sets the row's exponent; in them, every border between two codes, exactly
     and one bf16 step to either side; scales that are halfway between two."""

@@ -30,8 +30,23 @@
 // pair costs nothing at 64 x 16K keys, but 3 % at 32 x 1K, 4 to 5 % at d = 64 and 4 to 12 % in groups above 8.  Scores, maxima,
 // sums and the output accumulate in fp32.
 //
+// e2m1 cache: codes times their e4m3 scale have 6 bits, exact in f16, so that a K or V operand is a conversion and a product of f16 pairs;
+// the row's power of two goes where the e4m3 cache's does.  A lane's 16-byte piece of a K row has two scales (d = 64: 8 bytes, one), and its
+// columns of V one, so a scale is widened once for 16 codes.  Half the bytes of e4m3 at the same count of conversions, and the products on
+// top: 310 instructions for 16 keys at d = 128, of which 64 convert, 64 multiply by scales and 16 are MMAs.  Issue slots and the pipes
+// of the conversions (ALU, half rate, 49 % busy) and products (FMA, half rate) bound it, not HBM.  So it has 12 or 16 warps, and runs
+// of whole strips in which the walk is a counter and a strip's rows one address (kRuns).
+//
+// First keys beside the range (FIRSTS) are walked as one sequence with it: keys are counted without the strips between them
+// (paged.cuh), so that shares, rings and joins are the same.  A kernel of its own, as what it computes more for every unit costs short units
+// without first keys up to 20 % (246 x 1 key 20.5 and 24.5 us).
+//
 // Split parts go to the workspace as (m, l, O) and a second kernel joins them in a fixed order.
 //
+// Measured on the device, e2m1 (of the 6782 GB/s that a copy reaches): 1M keys, 16 + 4 heads, d = 128: 116 us (78 %; e4m3 165 to 170); 64 x
+// 16K keys, 64 + 8 heads: 170 us (69 %; e4m3 220 to 225); 50 x 20K keys, 64 + 8 heads, d = 64: 104 us (50 %); 24 x 8K keys of 32 heads, d = 64:
+// 103 us (41 %); 128 x 2K keys of 16 heads, d = 64: 114 us (25 %: a unit's end every few strips).  8 x 32K keys with 1024 first ones and a window
+// of 4096, 32 heads, d = 128, bf16: 109 to 111 us (89 to 91 %).
 // Measured on the device (of the 6795 GB/s that a copy reaches; the range is that of several GPUs): 1M keys, 16 + 4 heads, d = 128, e4m3:
 // 164 to 168 us (95 to 97 %); 64 x 16K keys, 64 + 8 heads, e4m3: 219 to 223 us (93 to 94 %); 24 x 8K keys with a window of 4096, 32
 // heads, d = 64, bf16: 115 to 119 us (89 to 92 %), 113 with the products left out; 777 keys, bf16: 6.6 us.  Far from HBM's bound: groups of 16
@@ -53,7 +68,10 @@ namespace {
 // Warps a CTA, and groups of 16 keys a strip.  Warps hide each other's latencies, as far as registers and the ring allow; longer strips
 // spread a strip's fixed instructions over more keys.  Measured before later steps (us; 50 x 20K keys, 64 + 8 heads, d = 64, e4m3): 8 warps x 1 group 165,
 // 8 x 2 137, 8 x 4 120, 12 x 4 118, 16 x 2 118, and later 12 x 2 114 and 16 x 2 116; (1M keys, 16 + 4 heads, d = 128, e4m3): 8 x 1 181, 12 x 1 170, 8 x 2 169; (24 x 8K
-// keys, 32 heads, d = 64, bf16): 8 x 1 119, 8 x 2 122, 12 x 2 117; (380K keys, 32 + 2 heads, d = 128, e4m3): 8 x 1 46, 8 x 2 43.
+// keys, 32 heads, d = 64, bf16): 8 x 1 119, 8 x 2 122, 12 x 2 117; (380K keys, 32 + 2 heads, d = 128, e4m3): 8 x 1 46, 8 x 2 43.  e2m1 (1M
+// keys, 16 + 4 heads, d = 128 / 64 x 16K keys, 64 + 8 heads): 8 x 2 161 / 219, 12 x 2 140 / 204, 16 x 1 155 / 221 in its first version; 8 x 4 137 /
+// 192, 12 x 2 125 / 184, 16 x 2 132 / 192 later; d = 64 (50 x 20K keys, 64 + 8 heads / 24 x 8K, 32 heads): 12 x 4 106 / 107, 12 x 2 108 / 105, 16
+// x 2 103 / 103.
 constexpr int warps_of(int d, int nt, int type) { return nt == 2 ? 8 : d == 64 ? (type == kE2m1 ? 16 : 12) : type == kE2m1 ? 12 : 8; }
 constexpr int groups_of(int d, int type) { return d == 128 && type == kBf16 ? 1 : 2; }
 constexpr int kMaxCtas = 160;          // CTAs (one an SM) the workspace holds parts for: two a CTA
@@ -113,8 +131,9 @@ struct Cfg {
   static constexpr int JOIN = (W / 2) * 8 * NT * D * 4 + (W + 1) * 8 * NT * 8;   // O buffers; (m, l) of every warp, the rows' factors
   static constexpr int MISC = 1024;
   static constexpr int FIT = (kSmemMax - JOIN - MISC) / (W * STAGE);
-  // Two stages, though three would fit e4m3 at d = 128 and groups over 8 at d = 64: more loads in flight are slower (e4m3, 64 x 16K keys
-  // 219 and 224 us, 1M keys 164 and 169 us; 16 x 32K keys of 16-head groups, d = 64, bf16 37 and 39 us).  bf16 at d = 128 takes what
+  // Two stages, though three would fit quantised caches and groups over 8 at d = 64: more loads in flight are slower (e4m3, 64 x 16K keys
+  // 219 and 224 us, 1M keys 164 and 169 us; 16 x 32K keys of 16-head groups, d = 64, bf16 37 and 39 us; e2m1, 64
+  // x 16K keys 170 and 174 us).  bf16 at d = 128 takes what
   // fits (777 keys 6.6 us with three and 6.8 with two, large batches alike).
   static constexpr int STAGES = T != kBf16 || D == 64 ? 2 : FIT;
   static constexpr int SMEM = MISC + JOIN + W * STAGE * STAGES;
@@ -625,7 +644,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
         }
       }
     // keys n and n + 8 of a group are this lane's; columns 2t, 2t + 1 of each query tile
-    float ks[SK][2], vn[SK][2];   // e4m3: the scale of a key's row, n of its value's (byte 0 stands for a value of 0)
+    float ks[SK][2], vn[SK][2];   // quantised: 2^n of a key's row, n of its value's (byte 0 stands for a value of 0)
     if constexpr (QUANT) {
 #pragma unroll
       for (int g = 0; g < SK; ++g)

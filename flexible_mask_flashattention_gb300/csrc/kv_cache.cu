@@ -12,10 +12,11 @@
 //         exact in f16 and in bf16.  d / 2 + d / 16 + 1 bytes: 4.6 bits a value at d = 128.
 //
 // Both kernels are bound by HBM: 2 d bytes a row on the tensors' side, 2 d, d + 1 or 9 d / 16 + 1 on the cache's.  A grid's second
-// dimension is k or v; a warp holds 2 or 4 consecutive rows at once (a pass), whatever tokens and heads they are of, 8 values a
-// lane, and starts the loads of kUnroll passes before it uses the first (168K tokens of 8 heads, d = 128, e4m3, written, all on one GPU: 147
-// us so, 194 us with 8 passes, 167 us with 2).  Measured on another GPU, the same tokens: e4m3 written in 153 us and read in 157 us,
-// 101 and 97 % of a copy's 6795 GB/s; bf16 in 199 and 203 us, 102 and 100 %.
+// dimension is k or v; a warp holds 2 to 8 consecutive rows at once (a pass), whatever tokens and heads they are of, 8 values a
+// lane (e2m1: 16), and starts the loads of its passes, 64 bytes a lane, before it uses the first (168K tokens of 8 heads, d = 128, e4m3,
+// written, all on one GPU: 147 us so, 194 us with twice as many, 167 us with half).  Measured, the same tokens: e4m3 written in 150 us and
+// read in 161 us, 102 and 95 % of a copy's 6782 GB/s; bf16 in 201 and 206 us, 101 and 99 %; e2m1 in 138 and 140 us, 95 and 94 %, where
+// 32-byte stores count: an instruction's 16-byte pieces of the 16 values a lane has lie 32 bytes apart (161 us read so).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -52,7 +53,8 @@ struct WriteParams {
 
 // FILLED: a token's rows fill the passes of a whole number of warps (hkv a multiple of kUnroll * RW), so that token and page are the
 // warp's and addresses a step apart.  Measured (168K tokens of 8 heads, d = 128, e4m3, on the first GPU above): 147 us, and 172 us without; with
-// 3 heads of d = 64, which leave most of such a warp empty, 21.6 us for 30K tokens, and 11.8 us without.
+// 3 heads of d = 64, which leave most of such a warp empty, 21.6 us for 30K tokens, and 11.8 us without.  (32-byte loads: e2m1 138.3 us for
+// 139.8; 72 for 68 where rows are not FILLED.)
 template <int D, int T, bool FILLED>
 __global__ void __launch_bounds__(kThreads) kv_cache_write_kernel(WriteParams p) {
   constexpr int V = kLaneValues<T>, L = D / V, RW = 32 / L, U = kUnroll * 8 / V;   // passes of RW rows

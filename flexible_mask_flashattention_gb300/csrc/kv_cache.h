@@ -99,7 +99,8 @@ struct CacheRows {
 };
 
 // A row as a cache stores it, spread over lanes: lane `l` of the D / V that hold it has columns V l .. V l + V - 1.  V is 8, or 16 for e2m1: a
-// lane then has all of what one scale is of (168K tokens of 8 heads, d = 128, into 4 bits: WRITE16 us, WRITE8 with 8 a lane).
+// lane then has all of what one scale is of (168K tokens of 8 heads, d = 128: written in 138 us and read in 140; with 8 a lane 185
+// and 150).
 template <int T>
 constexpr int kLaneValues = T == kE2m1 ? 16 : 8;
 template <int T>

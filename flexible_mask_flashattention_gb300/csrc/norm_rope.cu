@@ -23,6 +23,13 @@
 // more in flight 127, without the barrier 119 and 176; of 16 warps 110 and 164; units of 4 and 5 heads 110 and 159, of 10 and 7
 // 115 and 185.  Bulk copies (cp.async.bulk) took 110 and 164 where these took 109 and 172, and 0.1 to 0.5 us longer for small
 // batches.
+//
+// Positions of several axes (time, height, width): pair i of a token turns by the angle of the position on its axis, so that a token's cosines and sines
+// come from several rows of the table.  A token's lanes read its positions one each and shuffle them to where a row's address is made.  Where
+// each 16 bytes of a table row, 4 pairs, go by one axis, they are copied as before; otherwise value by value, neighbouring lanes neighbouring pairs.  Measured
+// (128K tokens, 64 + 8 heads, d = 128; 715 us at a copy's rate): one axis 731 us, sections of 16, 24 and 24 pairs 760, axes in
+// turns 813; every lane reading every position took 898 and 963.  Backward (32K tokens, 270 us): 279, 286 and 302.  The rotation alone (no
+// weights) is the same forward kernel, backward too: the gradients' rotation is the other way round.
 #include "norm_rope.cuh"
 
 namespace ffa {

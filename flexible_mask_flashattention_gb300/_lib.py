@@ -7,6 +7,7 @@ There is no fallback: if the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import struct
 from typing import Iterable, Optional, Sequence, Tuple
@@ -660,6 +661,14 @@ def _page_table(t, batch: int, dev):
     return s[0] if batch > 1 else width, width
 
 
+def _pair_axes(axes) -> bytes:
+    """The axes of the rotation pairs as the C call reads them, a byte each."""
+    try:   # bytes() of a list or tuple takes its numbers; of a number or an array it would mean something else
+        return axes if type(axes) is bytes else bytes(axes if type(axes) in (list, tuple) else [operator.index(a) for a in axes])
+    except (TypeError, ValueError):
+        raise FFAError(1, "axes must be a sequence of small numbers")
+
+
 def _rotation_inputs(q_weight, k_weight, cos_sin, positions, axes, tokens, d, dev):
     """Checked (q_weight, k_weight pointers, max_pos, rot_dim, number of axes, bytes of the pairs' axes); 0 axes: one position a token,
     and weights."""
@@ -679,10 +688,7 @@ def _rotation_inputs(q_weight, k_weight, cos_sin, positions, axes, tokens, d, de
             raise FFAError(1, "positions must be a CUDA tensor")
         n = _dims(positions, "positions", 2)[0]
         _check_dense(positions, torch.int32, (n, tokens), dev, "positions")
-        try:
-            pairs = bytes(axes)
-        except (TypeError, ValueError):
-            raise FFAError(1, "axes must be a sequence of small numbers")
+        pairs = _pair_axes(axes)
         if n < 1 or len(pairs) * 2 != table[1]:
             raise FFAError(1, f"axes must hold one of {n} axes for each of {table[1] // 2} pairs")
     _check_dense(cos_sin, f32, table, dev, "cos_sin")

@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
   int page[SK];           // of the next strip's groups of 16 keys, read a strip ahead; -1 for a group outside the range
   const int32_t* table_row;   // the loading unit's sequence's
   auto read_pages = [&]() {
-    real = ld.key < ld.first ? ld.key : ld.key + ld.gap;
+    real = key_of(ld.key, ld.first, ld.gap);
     if (kRuns && one_page) {   // its groups are all of the page that its first key is
       page[0] = ld.end > ld.key ? __ldg(table_row + (real >> p.geom.page_log2)) : -1;
 #pragma unroll

@@ -89,8 +89,9 @@ FFA_HD KeyRange key_range(int32_t len, int32_t start, int32_t first, int64_t max
   return r;
 }
 
-// The key that the first of a strip's counted keys is (`key` a multiple of the strip).
-FFA_HD int64_t key_of(const KeyRange& r, int64_t key) { return key < r.first ? key : key + r.gap; }
+// The key that a strip's first counted key is.
+template <typename I>
+FFA_HD I key_of(I key, I first, I gap) { return key < first ? key : key + gap; }
 
 // Blocks of `block` keys (a multiple of `strip`, itself one of 16) that cover the range.  Blocks are counted from the range's first key
 // rounded down to `strip`, so that a strip's groups of 16 keys never cross a page.  An empty range has one block, which

@@ -73,7 +73,7 @@ int main() {
               for (int64_t i = 0; i < n * warps; ++i) {
                 const int64_t key = range_first(r, strip) + i * strip;   // as counted, without the gap
                 if (key >= r.end) continue;
-                const int64_t real = key_of(r, key);
+                const int64_t real = key_of<int64_t>(key, r.first, r.gap);
                 for (int g = 0; g < strip; g += 16) {
                   bool some = r.end - key > g && (r.start - key < g + 16 || r.first - key > g);
                   if (some) looked.insert((real + g) >> page_log2);
@@ -93,7 +93,7 @@ int main() {
               if (fails > 20) return 1;
             }
   const KeyRange far = key_range(2147483647, 2147483000, 1000000000, int64_t{1} << 27, 4, 64);
-  if (far.gap <= 0 || far.start < 0 || far.end < 0 || key_of(far, far.start / 64 * 64) != 2147483000 / 64 * 64) ++fails, std::printf("far\n");
+  if (far.gap <= 0 || far.start < 0 || far.end < 0 || key_of<int64_t>(far.start / 64 * 64, far.first, far.gap) != 2147483000 / 64 * 64) ++fails, std::printf("far\n");
   if (!key_range(161, 100, 5, 10, 4, 16).bad || key_range(160, 100, 5, 10, 4, 16).bad) ++fails, std::printf("bad lengths\n");
   // 2 chunks a row (4 bits, d = 64): a permutation; each way of reading touches every bank once a pass
   std::set<int> all;
@@ -260,3 +260,14 @@ def test_binding_refuses_tensors_that_are_not_on_the_gpu(lib):  # noqa: F811
     pos, c = torch.zeros(2, dtype=torch.int32), torch.zeros(3, 2, 16, 64, dtype=torch.bfloat16)
     with pytest.raises(ffa.FFAError):
         ffa.kv_cache_append(x, x, x, w, w, t, pos, c, c, pos.long())
+
+
+def test_axes_of_the_pairs_as_bytes():
+    import torch
+    from flexible_mask_flashattention_gb300 import FFAError, _lib
+    want = bytes([0, 1, 2, 3])
+    for axes in (want, [0, 1, 2, 3], (0, 1, 2, 3), range(4), np.arange(4), np.arange(4, dtype=np.uint8), torch.arange(4), bytearray(want)):
+        assert _lib._pair_axes(axes) == want
+    for bad in (4, np.int64(4), None, [0.5], [-1], [256], "01", [None], np.array([0.0, 1.0])):
+        with pytest.raises(FFAError):
+            _lib._pair_axes(bad)

@@ -187,7 +187,7 @@ ffa_status launch(const AppendParams& p, int64_t tokens, cudaStream_t s) {
   static std::atomic<int> known[kDevices];
   static std::atomic<bool> raised[kDevices];
   int ctas = 0;
-  return launch_units<D, false>(kv_append_kernel<D, INTER, T>, p, tokens, s, &ctas, known, raised);
+  return launch_units<D, false, false>(kv_append_kernel<D, INTER, T>, p, tokens, s, &ctas, known, raised);
 }
 template <int D, bool INTER>
 ffa_status launch_type(const AppendParams& p, int type, int64_t tokens, cudaStream_t s) {

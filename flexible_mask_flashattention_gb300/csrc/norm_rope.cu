@@ -26,10 +26,11 @@
 //
 // Positions of several axes (time, height, width): pair i of a token turns by the angle of the position on its axis, so that a token's cosines and sines
 // come from several rows of the table.  A token's lanes read its positions one each and shuffle them to where a row's address is made.  Where
-// each 16 bytes of a table row, 4 pairs, go by one axis, they are copied as before; otherwise value by value, neighbouring lanes neighbouring pairs.  Measured
-// (128K tokens, 64 + 8 heads, d = 128; 715 us at a copy's rate): one axis 731 us, sections of 16, 24 and 24 pairs 760, axes in
-// turns 813; every lane reading every position took 898 and 963.  Backward (32K tokens, 270 us): 279, 286 and 302.  The rotation alone (no
-// weights) is the same forward kernel, backward too: the gradients' rotation is the other way round.
+// each 16 bytes of a table row, 4 pairs, go by one axis, they are copied as before; otherwise value by value, neighbouring lanes neighbouring pairs;
+// both through L1, as thousands of tokens share a row of the time's.  Units are larger, 6 and 5 heads, as their table rows cost more.  Measured
+// (128K tokens, 64 + 8 heads, d = 128; 715 us at a copy's rate): one axis 731 us, sections of 16, 24 and 24 pairs 725, axes in turns
+// 733; units of 5 heads 759 and 812, and every lane reading every position 898 and 963.  Backward (32K tokens, 270 us): 279, 281 and 296.  The
+// rotation alone (no weights) is the same forward kernel, backward too: the gradients' rotation is the other way round.
 #include "norm_rope.cuh"
 
 namespace ffa {
@@ -277,8 +278,8 @@ template <int D, bool INTER, bool BWD, bool AXES>
 ffa_status launch(const NormRopeParams& p, int64_t tokens, cudaStream_t s, int* ctas) {
   static std::atomic<int> known[kDevices];
   static std::atomic<bool> raised[kDevices];
-  if constexpr (BWD) return launch_units<D, true>(norm_rope_bwd_kernel<D, INTER, AXES>, p, tokens, s, ctas, known, raised);
-  else return launch_units<D, false>(norm_rope_fwd_kernel<D, INTER, AXES>, p, tokens, s, ctas, known, raised);
+  if constexpr (BWD) return launch_units<D, true, AXES>(norm_rope_bwd_kernel<D, INTER, AXES>, p, tokens, s, ctas, known, raised);
+  else return launch_units<D, false, AXES>(norm_rope_fwd_kernel<D, INTER, AXES>, p, tokens, s, ctas, known, raised);
 }
 
 template <bool BWD, bool AXES>

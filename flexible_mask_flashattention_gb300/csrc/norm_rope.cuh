@@ -18,12 +18,13 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxBwdCtas = 1024;   // partial weight gradients the workspace holds
 constexpr int kStages = 2;          // units in shared memory: one being used, one on its way
-// Heads of a unit at most, and with so few heads in all that they are one unit (365K tokens of 3 + 3 heads, d = 64: 90 us in one
-// unit, 111 in two; 14K tokens of 64 + 8 heads in units of 6: 87 us, of 5: 82).
+// Heads of a unit: as many as keep the bytes in flight where they do best, or, with so few heads in all that they are one unit, kUnitMost
+// (365K tokens of 3 + 3 heads, d = 64: 90 us in one unit, 111 in two; 14K tokens of 64 + 8 heads in units of 6: 87 us, of 5: 82).
+// Several axes take larger units, as a unit's table rows cost more (unit_heads).
 template <bool BWD>
 constexpr int kUnitHeads = BWD ? 4 : 5;
-template <bool BWD>
-constexpr int kUnitMost = BWD ? 4 : 6;
+template <bool BWD, bool AXES = false>
+constexpr int kUnitMost = BWD ? (AXES ? 5 : 4) : 6;
 
 struct NormRopeParams {
   const __nv_bfloat16* x[3];      // q, k (v, on its way to a cache)
@@ -247,11 +248,13 @@ __device__ __forceinline__ void copy_table(const NormRopeParams& p, uint32_t to,
     auto row_of = [&](int pair) {   // of the axis that the pair goes by; shuffled by all lanes
       return p.cos_sin + static_cast<int64_t>(__shfl_sync(0xffffffffu, w.mine, axis_of(pair), L)) * p.rot;
     };
+    // through L1: thousands of tokens have one time, so that the rows of a few positions are asked of L2 from all sides (128K tokens of 64 + 8
+    // heads: d = 64 367 us, 480 to 546 past L1; d = 128 725 and 734)
     if (p.chunks) {
       const float* row = row_of(4 * l);
       if (live && 4 * l < half) {
-        cp_async16(to + 16 * l, row + 4 * l);
-        cp_async16(to + 16 * l + 4 * half, row + half + 4 * l);
+        cp_async16_l1(to + 16 * l, row + 4 * l);
+        cp_async16_l1(to + 16 * l + 4 * half, row + half + 4 * l);
       }
     } else {
 #pragma unroll
@@ -283,7 +286,7 @@ __device__ __forceinline__ void copy_unit(const P& p, const Stages<D, BWD>& st, 
     const __nv_bfloat16* g = BWD ? p.dout[t] + (token * p.heads[t] + r.head) * D + 8 * l : nullptr;
     const uint32_t to = smem_u32(st.rows(stage, sub, 0)) + r.first * 512 + at, to_g = smem_u32(st.rows(stage, sub, 1)) + r.first * 512 + at;
 #pragma unroll
-    for (int i = 0; i < kUnitMost<BWD>; ++i) {
+    for (int i = 0; i < kUnitMost<BWD, AXES>; ++i) {
       if (i >= r.n) break;
       cp_async16(to + i * 512, x + i * D, bytes);
       if constexpr (BWD) cp_async16(to_g + i * 512, g + i * D, bytes);
@@ -353,13 +356,22 @@ inline void cut_units(NormRopeParams& p, int64_t tokens, int d, int64_t per, int
   p.step_tokens = kWarps / p.per * group;
 }
 
-// Units for `warps` resident warps: equal sizes, kUnitHeads or kUnitMost at most, and smaller ones where there would be fewer units than
-// warps.
+// Heads of a unit at most where there are several units a token.  Of several axes (us, with kUnitHeads and so): forward 128K
+// tokens of 64 + 8 heads, d = 128, sections 759 and 725, axes in turns 812 and 733; backward 32K such tokens 287 and 281, 302 and 296, 128K tokens of
+// 12 + 2 heads 250 and 222, 265 and 243; but 64K tokens of 64 + 8 heads, d = 64, in turns, backward 303 and 315.
+template <bool BWD>
+int64_t unit_heads(const NormRopeParams& p, int d) {
+  const bool larger = p.axes > 1 && (!BWD || p.chunks || d == 128);
+  return larger ? kUnitMost<BWD, true> : kUnitHeads<BWD>;
+}
+
+// Units for `warps` resident warps: equal sizes, unit_heads at most, and smaller ones where there would be fewer units than warps.
 template <bool BWD>
 void set_units(NormRopeParams& p, int64_t tokens, int d, int64_t warps) {
   const int group = 256 / d;
   const int64_t groups = (tokens + group - 1) / group, all = p.heads[0] + p.heads[1];
-  const int64_t fewest = all <= kUnitMost<BWD> ? 1 : (all + kUnitHeads<BWD> - 1) / kUnitHeads<BWD>;
+  const int64_t most = unit_heads<BWD>(p, d);
+  const int64_t fewest = all <= std::max<int64_t>(most, kUnitMost<BWD>) ? 1 : (all + most - 1) / most;
   const int64_t per = std::max(fewest, std::min(all, warps / std::max<int64_t>(groups, 1)));
   const int64_t unit = (all + per - 1) / per;
   cut_units(p, tokens, d, (all + unit - 1) / unit, unit);
@@ -386,10 +398,10 @@ int resident(K* kernel, int smem, int device, int sms, std::atomic<int> (&known)
 }
 
 // Launch a kernel over all units; P is or extends NormRopeParams.  `known` and `raised` are the kernel's own.
-template <int D, bool BWD, typename P>
+template <int D, bool BWD, bool AXES, typename P>
 ffa_status launch_units(void (*kernel)(P), P p, int64_t tokens, cudaStream_t s, int* ctas, std::atomic<int> (&known)[kDevices],
                         std::atomic<bool> (&raised)[kDevices]) {
-  constexpr int kMost = smem_bytes<D, BWD>(kUnitMost<BWD>);
+  constexpr int kMost = smem_bytes<D, BWD>(kUnitMost<BWD, AXES>);
   int device = 0, sms = 0;
   if (!current_device(device, sms)) return FFA_ERR_CUDA;
   const int held = resident(kernel, kMost, device, sms, known);

@@ -139,10 +139,12 @@ def test_padding_and_positions_behind_the_table(ffa, axes, normed):
     assert len(good) == 8
 
 
-@pytest.mark.parametrize("tokens,hq,hkv,d,rot,axes", [(12011, 7, 3, 128, 96, sections(16, 16, 16)), (9001, 11, 4, 64, 48, [i % 3 for i in range(24)])])
+@pytest.mark.parametrize("tokens,hq,hkv,d,rot,axes", [(12011, 7, 3, 128, 96, sections(16, 16, 16)), (9001, 11, 4, 64, 48, [i % 3 for i in range(24)]),
+                                                         (12011, 9, 3, 128, 128, sections(16, 24, 24)), (9001, 13, 5, 64, 64, [i % 4 for i in range(32)]),
+                                                         (9001, 11, 4, 64, 64, sections(8, 12, 12)), (9001, 4, 1, 128, 96, [i % 3 for i in range(48)])])
 def test_several_units_a_warp(ffa, tokens, hq, hkv, d, rot, axes):
     q, k, qw, kw, t, _, dqo, dko = norm_inputs(tokens, hq, hkv, d, rot, tokens)
-    pos = positions(3, tokens, 500, tokens)
+    pos = positions(max(axes) + 1, tokens, 500, tokens)
     pos[1, ::7] = -1
     rows, at = rows_of(t, pos, axes)
     qo, ko = ffa.qk_norm_rope(q, k, qw, kw, t, pos, eps=1e-5, axes=axes)

@@ -218,9 +218,13 @@ struct Walk {
     first = FIRSTS ? r.first : 0;
     gap = FIRSTS ? static_cast<int>(r.gap) : 0;
     bad = r.bad;
+    open(static_cast<uint32_t>(blk));
+  }
+  __device__ __forceinline__ void open(uint32_t blk) {
+    const KeyRange r{start, end, bad, first, gap};
     left = static_cast<int>(range_blocks(r, kBlock, KEYS) - blk);
-    const int64_t k = range_first(r, KEYS) + (blk * W + turn) * KEYS;
-    key = static_cast<int>(k < r.end ? k : r.end);   // a strip behind the end is empty
+    const uint32_t k = range_first(r, KEYS) + (blk * W + turn) * KEYS;
+    key = static_cast<int>(min(k, static_cast<uint32_t>(end)));   // a strip behind the end is empty
   }
   __device__ __forceinline__ void step() {   // to the unit's next block
     --left;
@@ -228,9 +232,8 @@ struct Walk {
   }
   __device__ __forceinline__ void next_unit(const DecodeParams& p, int units) {
     turn = turn == 0 ? W - 1 : turn - 1;
-    const bool wrap = u + 1 == units;
-    const int seq = wrap ? b + 1 : b;
-    set(range_of<FIRSTS>(p, seq, KEYS), seq, wrap ? 0 : u + 1, 0);
+    if (u + 1 == units) set(range_of<FIRSTS>(p, b + 1, KEYS), b + 1, 0, 0);
+    else ++u, open(0);
   }
   // Of this warp's strip: all its keys count; one of its keys, `key - key of the strip` = i, does; one of those from i on, 16 of them.
   __device__ __forceinline__ bool whole() const { return (end - key >= KEYS) & ((key >= start) | (FIRSTS && key + KEYS <= first)); }
@@ -288,7 +291,8 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
   allow_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = lane >> 2, t = lane & 3;   // an MMA fragment's row (or column) group and position in it
-  const int units = p.geom.hkv * p.subs;
+  const int subs = NT == 1 ? 1 : p.subs;   // a group of up to 8 queries is one unit: no divisions
+  const int units = p.geom.hkv * subs;
 
   // ---- this CTA's share of the block list
   auto blocks_of = [&](int seq) { return range_blocks(range_of<FIRSTS>(p, seq, C::KEYS), kBlock, C::KEYS); };
@@ -402,7 +406,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
     }
   };
   auto open_unit = [&]() {
-    head_row = (p.subs == 1 ? ld.u : ld.u / p.subs) << p.geom.page_log2;
+    head_row = (subs == 1 ? ld.u : ld.u / subs) << p.geom.page_log2;
     table_row = p.table + ld.b * p.table_stride;
     read_pages();
   };
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
   float m[NT][2], l[NT][2], vr[NT][2];
   // The query rows of a unit on their way to registers (a warp without a key in the part needs none), and what else begins with it.
   auto load_q = [&](const Walk<kW, C::KEYS, FIRSTS>& w) {
-    const int kvh = w.u / p.subs, s0 = (w.u - kvh * p.subs) * NQ;
+    const int kvh = w.u / subs, s0 = (w.u - kvh * subs) * NQ;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int qi = s0 + nt * 8 + n;
@@ -855,7 +859,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
   // results lie in a warp (pair, lane), so that neither side has a bank conflict.
   constexpr int kPairs = NT * C::MT * 2;
   auto end_part = [&](bool whole, int slot) {
-    const int h0 = (cur.u / p.subs) * p.group, s0 = (cur.u % p.subs) * NQ;
+    const int h0 = (cur.u / subs) * p.group, s0 = (cur.u % subs) * NQ;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -868,16 +872,26 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
         if (n == 0) join_ml[warp * NQ + nt * 8 + 2 * t + c] = make_float2(m[nt][c], s);
       }
     __syncthreads();
-    float f[NT][2];
+    // a row's warps are dealt to 4 lanes: lane 8 i + r has those i, i + 4, ... of row r
+    float f[NT][2], top[NT];
+    float2 ml[NT][(kW + 3) / 4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < (kW + 3) / 4; ++i) {
+        const int w = (lane >> 3) + 4 * i;
+        ml[nt][i] = w < kW ? join_ml[w * NQ + nt * 8 + (lane & 7)] : make_float2(-INFINITY, 0.f);
+        mx = fmaxf(mx, ml[nt][i].x);
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+      top[nt] = mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kW; ++w) mx = fmaxf(mx, join_ml[w * NQ + nt * 8 + 2 * t + c].x);
-        f[nt][c] = m[nt][c] == -INFINITY ? 0.f : QUANT ? ex2_wide(m[nt][c] - mx + vr[nt][c]) : ex2_approx(m[nt][c] - mx);
+        const float mr = __shfl_sync(0xffffffffu, mx, 2 * t + c);
+        f[nt][c] = m[nt][c] == -INFINITY ? 0.f : QUANT ? ex2_wide(m[nt][c] - mr + vr[nt][c]) : ex2_approx(m[nt][c] - mr);
       }
+    }
     if (warp >= kW / 2) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -887,21 +901,15 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
           for (int c = 0; c < 2; ++c)
             join_o[((warp - kW / 2) * kPairs + (nt * C::MT + i) * 2 + c) * 32 + lane] =
                 make_float2(o[nt][i][c] * f[nt][c], o[nt][i][c + 2] * f[nt][c]);
-    } else if (warp < NT) {   // a row's warps are dealt to 4 lanes
+    } else if (warp < NT) {   // the sums of query tile `warp`
       const int row = warp * 8 + (lane & 7);
-      float2 v[(kW + 3) / 4];
-      float mx = -INFINITY, sum = 0.f;
+      const float mx = NT == 2 && warp ? top[NT - 1] : top[0];
+      float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < (kW + 3) / 4; ++i) {
-        const int w = (lane >> 3) + 4 * i;
-        v[i] = w < kW ? join_ml[w * NQ + row] : make_float2(-INFINITY, 0.f);
-        mx = fmaxf(mx, v[i].x);
+        const float2 v = NT == 2 && warp ? ml[NT - 1][i] : ml[0][i];
+        sum += v.x == -INFINITY ? v.y : v.y * ex2_approx(v.x - mx);   // v.y is 0 or NaN without a maximum
       }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-#pragma unroll
-      for (int i = 0; i < (kW + 3) / 4; ++i)
-        sum += v[i].x == -INFINITY ? v[i].y : v[i].y * ex2_approx(v[i].x - mx);   // v.y is 0 or NaN without a maximum
       sum += __shfl_xor_sync(0xffffffffu, sum, 8);
       sum += __shfl_xor_sync(0xffffffffu, sum, 16);
       if (lane < 8) {
@@ -950,7 +958,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
 
   // A unit that was this warp's alone: its rows.  A sequence with a length that its table row cannot hold reads no key and ends here too.
   auto end_alone = [&]() {
-    const int h0 = (cur.u / p.subs) * p.group, s0 = (cur.u % p.subs) * NQ;
+    const int h0 = (cur.u / subs) * p.group, s0 = (cur.u % subs) * NQ;
     const float poison = cur.bad ? __int_as_float(0x7fffffff) : 0.f;   // makes its rows NaN
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)

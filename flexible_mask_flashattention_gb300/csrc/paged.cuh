@@ -96,9 +96,10 @@ FFA_HD I key_of(I key, I first, I gap) { return key < first ? key : key + gap; }
 // Blocks of `block` keys (a multiple of `strip`, itself one of 16) that cover the range.  Blocks are counted from the range's first key
 // rounded down to `strip`, so that a strip's groups of 16 keys never cross a page.  An empty range has one block, which
 // writes its empty row.
-FFA_HD int64_t range_first(const KeyRange& r, int32_t strip) { return r.first > 0 ? 0 : r.start / strip * strip; }
-FFA_HD int64_t range_blocks(const KeyRange& r, int32_t block, int32_t strip) {
-  const int64_t n = (r.end - range_first(r, strip) + block - 1) / block;
+// Keys are numbers of 31 bits, so that 32 do for the divisions.
+FFA_HD uint32_t range_first(const KeyRange& r, uint32_t strip) { return r.first > 0 ? 0 : static_cast<uint32_t>(r.start) / strip * strip; }
+FFA_HD int64_t range_blocks(const KeyRange& r, uint32_t block, uint32_t strip) {
+  const uint32_t n = (static_cast<uint32_t>(r.end) - range_first(r, strip) + block - 1) / block;
   return n > 0 ? n : 1;
 }
 

@@ -43,10 +43,10 @@
 //
 // Split parts go to the workspace as (m, l, O) and a second kernel joins them in a fixed order.
 //
-// Measured on the device, e2m1 (of the 6782 GB/s that a copy reaches): 1M keys, 16 + 4 heads, d = 128: 116 us (78 %; e4m3 165 to 170); 64 x
-// 16K keys, 64 + 8 heads: 170 us (69 %; e4m3 220 to 225); 50 x 20K keys, 64 + 8 heads, d = 64: 104 us (50 %); 24 x 8K keys of 32 heads, d = 64:
-// 103 us (41 %); 128 x 2K keys of 16 heads, d = 64: 114 us (25 %: a unit's end every few strips).  8 x 32K keys with 1024 first ones and a window
-// of 4096, 32 heads, d = 128, bf16: 109 to 111 us (89 to 91 %).
+// Measured on the device, e2m1 (of the 6782 GB/s that a copy reaches): 1M keys, 16 + 4 heads, d = 128: 111 to 114 us (79 to 81 %; e4m3 163 to
+// 166); 64 x 16K keys, 64 + 8 heads: 163 to 165 us (71 %; e4m3 218); 50 x 20K keys, 64 + 8 heads, d = 64: 95 us (55 %); 24 x 8K keys of 32 heads,
+// d = 64: 92 us (46 %); 128 x 2K keys of 16 heads, d = 64: 98 us (29 %: a unit's end every few strips).  8 x 32K keys with 1024 first ones and a
+// window of 4096, 32 heads, d = 128, bf16: 105 to 109 us (91 to 94 %).
 // Measured on the device (of the 6795 GB/s that a copy reaches; the range is that of several GPUs): 1M keys, 16 + 4 heads, d = 128, e4m3:
 // 164 to 168 us (95 to 97 %); 64 x 16K keys, 64 + 8 heads, e4m3: 219 to 223 us (93 to 94 %); 24 x 8K keys with a window of 4096, 32
 // heads, d = 64, bf16: 115 to 119 us (89 to 92 %), 113 with the products left out; 777 keys, bf16: 6.6 us.  Far from HBM's bound: groups of 16

@@ -604,8 +604,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
           } else {
             const uint2 x = lds64(sb + at_k + at);
             w[r][0] = x.x, w[r][1] = x.y;
-            const uint32_t one = lds8(sat);
-            sc[r][0] = e4m3x2_to_f16x2(one | one << 8);
+            sc[r][0] = __byte_perm(e4m3x2_to_f16x2(lds8(sat)), 0, 0x1010);
           }
         }
 #pragma unroll

@@ -49,7 +49,7 @@ void set_units(AppendParams& p, int64_t tokens, int d, int64_t warps) {
   cut_units(p, tokens, d, p.first[3], std::max({p.size[0], p.size[1], p.size[2]}));
 }
 
-template <int D, bool INTER, int T>
+template <int D, bool INTER, int T, bool AS_IS>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendParams p) {
   constexpr int L = D / 8;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendParams p) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               o[j] = mul2(fma2(f[h][j], a[j], mul2(partner<INTER>(f[h], j), b[j])), make_float2(r[h], r[h]));
-            const uint4 v = live ? pack8(o) : constant;
+            const uint4 v = !live ? constant : AS_IS && 8 * l >= p.rot ? cols.load(in + (i + h) * 512, swap) : pack8(o);
             if (t == 1) cols.store(in + (i + h) * 512, swap, v);   // a key's row goes back to its place
             else if (cur.has) cols.store(out + (i + h) * D, v);
           }
@@ -182,16 +182,21 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendParams p) {
   }
 }
 
-template <int D, bool INTER, int T>
+template <int D, bool INTER, int T, bool AS_IS>
 ffa_status launch(const AppendParams& p, int64_t tokens, cudaStream_t s) {
   static std::atomic<int> known[kDevices];
   static std::atomic<bool> raised[kDevices];
   int ctas = 0;
-  return launch_units<D, false, false>(kv_append_kernel<D, INTER, T>, p, tokens, s, &ctas, known, raised);
+  return launch_units<D, false, false>(kv_append_kernel<D, INTER, T, AS_IS>, p, tokens, s, &ctas, known, raised);
+}
+template <int D, bool INTER, bool AS_IS>
+ffa_status launch_type(const AppendParams& p, int type, int64_t tokens, cudaStream_t s) {
+  if (type == kE2m1) return launch<D, INTER, kE2m1, AS_IS>(p, tokens, s);
+  return type == kE4m3 ? launch<D, INTER, kE4m3, AS_IS>(p, tokens, s) : launch<D, INTER, kBf16, AS_IS>(p, tokens, s);
 }
 template <int D, bool INTER>
-ffa_status launch_type(const AppendParams& p, int type, int64_t tokens, cudaStream_t s) {
-  return type == kE2m1 ? launch<D, INTER, kE2m1>(p, tokens, s) : type == kE4m3 ? launch<D, INTER, kE4m3>(p, tokens, s) : launch<D, INTER, kBf16>(p, tokens, s);
+ffa_status launch_any(const AppendParams& p, int type, int64_t tokens, cudaStream_t s) {
+  return copies_columns(p, D) ? launch_type<D, INTER, true>(p, type, tokens, s) : launch_type<D, INTER, false>(p, type, tokens, s);
 }
 
 }  // namespace
@@ -232,8 +237,8 @@ ffa_status ffa_kv_cache_append(const void* q, int64_t q_stride, const void* k, i
   p.cache[1] = {cache->v, cache->v_exp, cache->v_scale};
   p.slots = slots;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d == 128) return interleaved ? launch_type<128, true>(p, cache->dtype, tokens, s) : launch_type<128, false>(p, cache->dtype, tokens, s);
-  return interleaved ? launch_type<64, true>(p, cache->dtype, tokens, s) : launch_type<64, false>(p, cache->dtype, tokens, s);
+  if (d == 128) return interleaved ? launch_any<128, true>(p, cache->dtype, tokens, s) : launch_any<128, false>(p, cache->dtype, tokens, s);
+  return interleaved ? launch_any<64, true>(p, cache->dtype, tokens, s) : launch_any<64, false>(p, cache->dtype, tokens, s);
 }
 
 }  // extern "C"

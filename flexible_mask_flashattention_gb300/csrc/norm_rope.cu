@@ -36,7 +36,7 @@
 namespace ffa {
 namespace {
 
-template <int D, bool INTER, bool AXES>
+template <int D, bool INTER, bool AXES, bool AS_IS>
 __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(NormRopeParams p) {
   constexpr int L = D / 8;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(NormRopeParams 
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             o[j] = mul2(fma2(f[h][j], a[j], mul2(partner<INTER>(f[h], j), b[j])), make_float2(r[h], r[h]));
-          if (live) cols.store(out + (i + h) * D, pack8(o));
+          if (live) cols.store(out + (i + h) * D, AS_IS && 8 * l >= p.rot ? cols.load(in + (i + h) * 512, swap) : pack8(o));
           else if (cur.has) cols.store(out + (i + h) * D, constant);
         }
       };
@@ -274,21 +274,25 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* partial
   }
 }
 
-template <int D, bool INTER, bool BWD, bool AXES>
+template <int D, bool INTER, bool BWD, bool AXES, bool AS_IS>
 ffa_status launch(const NormRopeParams& p, int64_t tokens, cudaStream_t s, int* ctas) {
   static std::atomic<int> known[kDevices];
   static std::atomic<bool> raised[kDevices];
   if constexpr (BWD) return launch_units<D, true, AXES>(norm_rope_bwd_kernel<D, INTER, AXES>, p, tokens, s, ctas, known, raised);
-  else return launch_units<D, false, AXES>(norm_rope_fwd_kernel<D, INTER, AXES>, p, tokens, s, ctas, known, raised);
+  else return launch_units<D, false, AXES>(norm_rope_fwd_kernel<D, INTER, AXES, AS_IS>, p, tokens, s, ctas, known, raised);
 }
 
-template <bool BWD, bool AXES>
+template <bool BWD, bool AXES, bool AS_IS = false>
 ffa_status launch_of(const NormRopeParams& p, int64_t tokens, int d, bool interleaved, cudaStream_t s, int* ctas) {
-  if (d == 128) return interleaved ? launch<128, true, BWD, AXES>(p, tokens, s, ctas) : launch<128, false, BWD, AXES>(p, tokens, s, ctas);
-  return interleaved ? launch<64, true, BWD, AXES>(p, tokens, s, ctas) : launch<64, false, BWD, AXES>(p, tokens, s, ctas);
+  if (d == 128)
+    return interleaved ? launch<128, true, BWD, AXES, AS_IS>(p, tokens, s, ctas) : launch<128, false, BWD, AXES, AS_IS>(p, tokens, s, ctas);
+  return interleaved ? launch<64, true, BWD, AXES, AS_IS>(p, tokens, s, ctas) : launch<64, false, BWD, AXES, AS_IS>(p, tokens, s, ctas);
 }
 template <bool BWD>
 ffa_status launch_any(const NormRopeParams& p, int64_t tokens, int d, bool interleaved, cudaStream_t s, int* ctas) {
+  if constexpr (!BWD) {
+    if (p.axes && copies_columns(p, d)) return launch_of<false, true, true>(p, tokens, d, interleaved, s, ctas);
+  }
   return p.axes ? launch_of<BWD, true>(p, tokens, d, interleaved, s, ctas) : launch_of<BWD, false>(p, tokens, d, interleaved, s, ctas);
 }
 

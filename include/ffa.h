@@ -447,7 +447,8 @@ ffa_status ffa_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, 
  *  pair_axis  host array [rot_dim / 2] of axes in [0, n_axes), read during the
  *             call: sections of neighbouring pairs, axes in turns, or any other
  *             order.  NULL for n_axes = 1.
- *  q_weight, k_weight  both NULL: no norm, the rotation alone
+ *  q_weight, k_weight  both NULL: no norm, the rotation alone (columns from rot_dim
+ *             on are copied)
  * Everything else as ffa_qk_norm_rope (n_axes > 4: FFA_ERR_UNSUPPORTED).
  */
 ffa_status ffa_qk_norm_rope_axes(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int64_t tokens,

@@ -1180,12 +1180,13 @@ ffa_status ffa_fwd_decode_window(const void* q, int64_t q_stride, const ffa_kv_c
   if (any_meet(outs, 3, in, 6 + at.n)) return FFA_ERR_INVALID_ARG;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_stride = q_stride;
-  p.k = cache->k;
-  p.v = cache->v;
-  p.k_exp = cache->k_exp;
-  p.v_exp = cache->v_exp;
-  p.k_scale = cache->k_scale;
-  p.v_scale = cache->v_scale;
+  const CacheRows k = k_rows(*cache), v = v_rows(*cache);
+  p.k = k.rows;
+  p.v = v.rows;
+  p.k_exp = k.exps;
+  p.v_exp = v.exps;
+  p.k_scale = k.scales;
+  p.v_scale = v.scales;
   p.table = page_table;
   p.table_stride = table_stride;
   p.max_pages = max_pages;

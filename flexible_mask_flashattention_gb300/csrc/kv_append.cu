@@ -233,8 +233,8 @@ ffa_status ffa_kv_cache_append(const void* q, int64_t q_stride, const void* k, i
   p.x_stride[2] = v_stride;
   p.heads[2] = hkv;
   p.out[0] = static_cast<__nv_bfloat16*>(q_out);
-  p.cache[0] = {cache->k, cache->k_exp, cache->k_scale};
-  p.cache[1] = {cache->v, cache->v_exp, cache->v_scale};
+  p.cache[0] = k_rows(*cache);
+  p.cache[1] = v_rows(*cache);
   p.slots = slots;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d == 128) return interleaved ? launch_any<128, true>(p, cache->dtype, tokens, s) : launch_any<128, false>(p, cache->dtype, tokens, s);

@@ -281,8 +281,8 @@ ffa_status ffa_kv_cache_write(const void* k, int64_t k_stride, const void* v, in
   p.x[1] = static_cast<const __nv_bfloat16*>(v);
   p.stride[0] = k_stride;
   p.stride[1] = v_stride;
-  p.cache[0] = {cache->k, cache->k_exp, cache->k_scale};
-  p.cache[1] = {cache->v, cache->v_exp, cache->v_scale};
+  p.cache[0] = k_rows(*cache);
+  p.cache[1] = v_rows(*cache);
   p.slots = slots;
   p.rows = static_cast<uint32_t>(tokens * cache->hkv);
   p.wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0 && k_stride % 16 == 0 && v_stride % 16 == 0;
@@ -315,8 +315,8 @@ ffa_status ffa_kv_cache_read(const ffa_kv_cache* cache, const int32_t* page_tabl
   const int64_t bytes = 2 * total * cache->hkv * cache->d;
   const Span out[] = {{k, bytes}, {v, bytes}};
   if (any_meet(out, 2, in, 2 + at.n)) return FFA_ERR_INVALID_ARG;
-  p.cache[0] = {cache->k, cache->k_exp, cache->k_scale};
-  p.cache[1] = {cache->v, cache->v_exp, cache->v_scale};
+  p.cache[0] = k_rows(*cache);
+  p.cache[1] = v_rows(*cache);
   p.out[0] = static_cast<__nv_bfloat16*>(k);
   p.out[1] = static_cast<__nv_bfloat16*>(v);
   p.table = page_table;

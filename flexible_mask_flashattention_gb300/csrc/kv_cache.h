@@ -20,18 +20,34 @@ constexpr int kBf16 = FFA_KV_BF16, kE4m3 = FFA_KV_E4M3, kE2m1 = FFA_KV_E2M1;
 FFA_HD constexpr int value_bytes(int type, int d) { return type == kBf16 ? 2 * d : type == kE4m3 ? d : d / 2; }
 FFA_HD constexpr int scale_bytes(int type, int d) { return type == kE2m1 ? d / 16 : 0; }
 
+// A cache's arrays, of k or of v.
+struct CacheRows {
+  void* rows;
+  uint8_t* exps;
+  uint8_t* scales;
+};
+// Those of a cache, with null for what its type does not have.  The scales' fields are read for their type only: a caller compiled before they were
+// there passes a description without them.
+inline CacheRows k_rows(const ffa_kv_cache& c) {
+  return {c.k, c.dtype == FFA_KV_BF16 ? nullptr : c.k_exp, c.dtype == FFA_KV_E2M1 ? c.k_scale : nullptr};
+}
+inline CacheRows v_rows(const ffa_kv_cache& c) {
+  return {c.v, c.dtype == FFA_KV_BF16 ? nullptr : c.v_exp, c.dtype == FFA_KV_E2M1 ? c.v_scale : nullptr};
+}
+
 // The memory of a checked cache.
 struct CacheSpans {
   Span s[6];
   int n;
   explicit CacheSpans(const ffa_kv_cache& c) {
     const int64_t rows = c.num_pages * c.hkv * c.page_size, bytes = rows * value_bytes(c.dtype, c.d);
-    s[0] = {c.k, bytes};
-    s[1] = {c.v, bytes};
-    s[2] = {c.k_exp, rows};
-    s[3] = {c.v_exp, rows};
-    s[4] = {c.k_scale, rows * scale_bytes(c.dtype, c.d)};
-    s[5] = {c.v_scale, rows * scale_bytes(c.dtype, c.d)};
+    const CacheRows k = k_rows(c), v = v_rows(c);
+    s[0] = {k.rows, bytes};
+    s[1] = {v.rows, bytes};
+    s[2] = {k.exps, rows};
+    s[3] = {v.exps, rows};
+    s[4] = {k.scales, rows * scale_bytes(c.dtype, c.d)};
+    s[5] = {v.scales, rows * scale_bytes(c.dtype, c.d)};
     n = c.dtype == FFA_KV_E2M1 ? 6 : c.dtype == FFA_KV_E4M3 ? 4 : 2;
   }
 };
@@ -90,13 +106,6 @@ __device__ __forceinline__ float2 quotient(float2 y, float s, float over) {
   const float2 e = fma2(z, make_float2(s, s), make_float2(-y.x, -y.y));
   return fma2(e, make_float2(-over, -over), z);
 }
-
-// A cache's arrays, of k or of v.
-struct CacheRows {
-  void* rows;
-  uint8_t* exps;
-  uint8_t* scales;
-};
 
 // A row as a cache stores it, spread over lanes: lane `l` of the D / V that hold it has columns V l .. V l + V - 1.  V is 8, or 16 for e2m1: a
 // lane then has all of what one scale is of (168K tokens of 8 heads, d = 128: written in 138 us and read in 140; with 8 a lane 185

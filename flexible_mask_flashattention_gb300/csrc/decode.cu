@@ -396,10 +396,8 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
   const int32_t* table_row;   // the loading unit's sequence's
   auto read_pages = [&]() {
     real = key_of(ld.key, ld.first, ld.gap);
-    if (kRuns && one_page) {   // its groups are all of the page that its first key is
+    if (kRuns && one_page) {   // its groups are all of the page that its first key is: page[0] alone is read
       page[0] = ld.end > ld.key ? __ldg(table_row + (real >> p.geom.page_log2)) : -1;
-#pragma unroll
-      for (int g = 1; g < SK; ++g) page[g] = page[0];
     } else {
 #pragma unroll
       for (int g = 0; g < SK; ++g) page[g] = ld.some(16 * g) ? __ldg(table_row + ((real + 16 * g) >> p.geom.page_log2)) : -1;
@@ -452,6 +450,10 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
     if (kRuns && have > 0 && full && one_page && page_good()) {
       load_run(stage);
     } else if (have > 0) {
+      if (kRuns && one_page) {   // page[0] is all groups'; a run renews no other
+#pragma unroll
+        for (int g = 1; g < SK; ++g) page[g] = page[0];
+      }
 #pragma unroll
       for (int g = 0; g < SK; ++g) {
         const bool ok = static_cast<uint32_t>(page[g]) < static_cast<uint32_t>(p.geom.num_pages);   // as page_ok, for pages of 32 bits

@@ -987,14 +987,10 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
   bool first_part = true, from_start = !opens_mid;
   int32_t opened = 0;   // parts of the unit this CTA leaves open to later ones
   int stage = 0, fill = C::STAGES - 1;
-  // Blocks from here on whose strips, this warp's and the one to be loaded, are whole ones of the unit, none of them the unit's last, nor the
-  // share's: their walks need no more than a counter.
-  int run = 0, ran = 0;
+  int run = 0, ran = 0;   // blocks from here on that are a run (run_blocks), and all of it
   auto runs = [&]() {
-    if (!one_page || ld.b != cur.b || ld.u != cur.u || cur.key < cur.start) return 0;
-    // ld's key is not before cur's; its strip behind the last of the run is a whole one too, so that its page may be looked up
-    const int most = min(min(cur.left, ld.left) - 1, (cur.end - ld.key - C::KEYS) / kBlock);
-    return static_cast<int>(min(static_cast<int64_t>(most), todo - C::STAGES));
+    if (!one_page || ld.b != cur.b || ld.u != cur.u) return 0;
+    return run_blocks(cur.start, cur.end, cur.key, cur.left, ld.key, ld.left, todo, kBlock, C::KEYS, C::STAGES);
   };
 #pragma unroll 1
   for (;;) {   // a unit's part after the other

@@ -103,6 +103,17 @@ FFA_HD int64_t range_blocks(const KeyRange& r, uint32_t block, uint32_t strip) {
   return n > 0 ? n : 1;
 }
 
+// Blocks of a run, <= 0 for none: those from the current one on whose strips, a warp's own (first key `key`, `left` blocks of the unit from it on) and the one that
+// is being loaded meanwhile (`ahead`, `ahead_left`; of the same unit, not before it), are whole ones of the range, none of them in the unit's last block nor in
+// the last `stages` of the worker's `todo`.  Their walks need no more than a counter: every strip of a run, and the one that the loads then stand at, whose
+// page is looked up, lies inside [start, end).
+FFA_HD int32_t run_blocks(int32_t start, int32_t end, int32_t key, int32_t left, int32_t ahead, int32_t ahead_left, int64_t todo, int32_t block,
+                          int32_t strip, int32_t stages) {
+  if (key < start) return 0;
+  const int32_t here = (left < ahead_left ? left : ahead_left) - 1, whole = (end - ahead - strip) / block, most = here < whole ? here : whole;
+  return static_cast<int32_t>(most < todo - stages ? most : todo - stages);
+}
+
 // `total` blocks are dealt to `parts` (4096 at most) workers in equal contiguous shares: worker c has [share_begin(c),
 // share_begin(c + 1)).  Few enough blocks take 32-bit divisions, a fifth of the 64-bit ones' time.
 FFA_HD int64_t share_begin(int64_t total, int64_t parts, int64_t c) {

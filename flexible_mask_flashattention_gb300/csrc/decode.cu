@@ -33,20 +33,23 @@
 // e2m1 cache: codes times their e4m3 scale have 6 bits, exact in f16, so that a K or V operand is a conversion and a product of f16 pairs;
 // the row's power of two goes where the e4m3 cache's does.  A lane's 16-byte piece of a K row has two scales (d = 64: 8 bytes, one), and its
 // columns of V one, so a scale is widened once for 16 codes.  Half the bytes of e4m3 at the same count of conversions, and the products on
-// top: 310 instructions for 16 keys at d = 128, of which 64 convert, 64 multiply by scales and 16 are MMAs.  Issue slots and the pipes
-// of the conversions (ALU, half rate, 49 % busy) and products (FMA, half rate) bound it, not HBM.  So it has 12 or 16 warps, and runs
-// of whole strips in which the walk is a counter and a strip's rows one address (kRuns).
+// top: 310 instructions for 16 keys at d = 128, of which 64 convert, 64 multiply by scales and 16 are MMAs.  No pipe is full (issue
+// slots 62 % busy, the conversions' ALU 50 %, the products' FMA 38 %, HBM 66 %): the stalls, wait 1.0, not selected 0.9 and math pipe throttle
+// 0.8 cycles an issue, say that several of a scheduler's three warps are ready at one moment and none at the next.  Fewer instructions
+// and more warps help: it has 12 or 16 warps, and runs of whole strips in which the walk is a counter and a strip's rows one address (kRuns).
+// Groups above 8 have two warps a scheduler (231 to 243 registers), and issue slots, ALU and FMA are 47, 35 and 27 % busy.
 //
 // First keys beside the range (FIRSTS) are walked as one sequence with it: keys are counted without the strips between them
 // (paged.cuh), so that shares, rings and joins are the same.  A kernel of its own, as what it computes more for every unit costs short units
-// without first keys up to 20 % (246 x 1 key 20.5 and 24.5 us).
+// without first keys 6 to 9 % (246 x 1 key, d = 64: bf16 13.5 and 14.3 us, e2m1 16.2 and 17.6).
 //
 // Split parts go to the workspace as (m, l, O) and a second kernel joins them in a fixed order.
 //
-// Measured on the device, e2m1 (of the 6782 GB/s that a copy reaches): 1M keys, 16 + 4 heads, d = 128: 111 to 114 us (79 to 81 %; e4m3 163 to
-// 166); 64 x 16K keys, 64 + 8 heads: 163 to 165 us (71 %; e4m3 218); 50 x 20K keys, 64 + 8 heads, d = 64: 95 us (55 %); 24 x 8K keys of 32 heads,
-// d = 64: 92 us (46 %); 128 x 2K keys of 16 heads, d = 64: 98 us (29 %: a unit's end every few strips).  8 x 32K keys with 1024 first ones and a
-// window of 4096, 32 heads, d = 128, bf16: 105 to 109 us (91 to 94 %).
+// Measured on the device, e2m1 (of the 6782 GB/s that a copy reaches): 1M keys, 16 + 4 heads, d = 128: 110 to 111 us (82 %; e4m3 164);
+// 64 x 16K keys, 64 + 8 heads: 162 to 163 us (72 %; e4m3 220); 50 x 20K keys, 64 + 8 heads, d = 64: 92 to 93 us (56 %); 24 x 8K keys of 32 heads,
+// d = 64: 91 us (46 %); 128 x 2K keys of 16 heads, d = 64: 97 us (30 %: a unit's end every few strips); groups of 16, 380K keys, d = 128: 39 us
+// (42 %), 16 x 32K, d = 64: 29 us (26 %).  With 100 first keys and a window of 5000, 64 x 16K keys, 64 + 8 heads: e2m1 90 us (63 %), e4m3 112 (88 %).
+// 8 x 32K keys with 1024 first ones and a window of 4096, 32 heads, d = 128, bf16: 105 to 109 us (91 to 94 %).
 // Measured on the device (of the 6795 GB/s that a copy reaches; the range is that of several GPUs): 1M keys, 16 + 4 heads, d = 128, e4m3:
 // 164 to 168 us (95 to 97 %); 64 x 16K keys, 64 + 8 heads, e4m3: 219 to 223 us (93 to 94 %); 24 x 8K keys with a window of 4096, 32
 // heads, d = 64, bf16: 115 to 119 us (89 to 92 %), 113 with the products left out; 777 keys, bf16: 6.6 us.  Far from HBM's bound: groups of 16
@@ -387,7 +390,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, NT, T), 1) decode_kernel(Deco
   Walk<kW, C::KEYS, FIRSTS> ld = cur;
   const int page_rows = p.geom.hkv << p.geom.page_log2, page_mask = (1 << p.geom.page_log2) - 1;
   // Strips that are one run of rows have a way of their own where issue slots bound the work.  Elsewhere its code costs small calls more than it
-  // gives large ones (e4m3, 32 x 1K keys 14.4 and 15.7 us, 1M keys 170 and 167).
+  // gives large ones (e4m3: 1M keys 164 without and 167 us with it, 32 x 1K 11.5 both ways).
   constexpr bool kRuns = T == kE2m1;
   const bool one_page = page_mask + 1 >= C::KEYS && (C::KEYS & (C::KEYS - 1)) == 0;   // strips start at multiples of their length
   int real;               // the next strip's first key, the gap counted

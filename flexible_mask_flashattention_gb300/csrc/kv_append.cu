@@ -9,11 +9,12 @@
 // behind q and k.  A normalised key's columns lie in its lanes as rotation partners; it goes back to its place in shared memory and is
 // read from there in the order that kv_cache.h's rows want.
 //
-// Unlike there, the warps of a CTA do not start their copies together: units of q's, k's and v's heads take different times (78K tokens
+// Unlike there, the warps of a CTA do not start their copies together: units of q's, k's and v's heads take different times (67K tokens
 // of 16 + 4 heads, d = 128, into 4 bits: 169 us with a barrier a round, 140 without), nor are units cut across tensors (155) or made of
-// equal shares of each (206).  Measured, the same tokens: into bf16 136 us, e4m3 143, e2m1 140 (89, 78 and 76 % of a copy's rate on
-// the bytes); 64 + 8 heads, 29K tokens: 240, 230 and 223 (88, 88 and 88 %); 6 + 2 heads, d = 64: 150, 158 and 158 (75, 65 and 62 %, three
-// units of few heads).  What is left is instructions: some 100 for a q head of a warp's tokens, issue slots 57 % busy.  48 new tokens take 3 us.
+// equal shares of each (206).  Measured since, the same tokens: into bf16 132 us, e4m3 140, e2m1 137 (92, 79 and 78 % of a copy's rate on
+// the bytes); 64 + 8 heads, 29K tokens: 183, 185 and 179 (95, 89 and 90 %); 6 + 2 heads, d = 64, 250K tokens: 127, 132 and 132 (74, 64 and
+// 61 %, three units of few heads).  What is left is instructions: some 100 for a q head of a warp's tokens, issue slots 57 (bf16) and 62 %
+// (e2m1) busy.  48 new tokens take 3 us.
 #include "kv_cache.h"
 #include "norm_rope.cuh"
 
@@ -37,7 +38,7 @@ __device__ __forceinline__ UnitPart part_of(const AppendParams& p, int c, int t)
 // Units of q's, of k's and of v's heads: what a unit begins with (its rotation, coefficients, places) is then of one tensor.  As many as
 // fit, since that costs as much as three heads; smaller ones where there would be fewer units than warps.
 constexpr int kAppendMost = kUnitMost<false>;
-template <bool BWD>
+template <bool>   // as launch_units asks: there is no backward
 void set_units(AppendParams& p, int64_t tokens, int d, int64_t warps) {
   const int group = 256 / d;
   const int64_t groups = std::max<int64_t>((tokens + group - 1) / group, 1), heads = p.heads[0] + p.heads[1] + p.heads[2];
@@ -85,6 +86,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendParams p) {
   __syncthreads();
   const int page_rows = p.geom.hkv << p.geom.page_log2, page_mask = (1 << p.geom.page_log2) - 1;
   int stage = 0, fill = kStages - 1;
+  // cur.left alone ends the loop; without the count beside it the compiler's code is slower (67K tokens into 4 bits, read back: 171.5 and 166.9 us)
   for (int todo = cur.left + warp; todo > 0; todo -= kWarps, cur.next(p)) {
     if (cur.left <= 0) break;
     cur.pos = pos_ahead;

@@ -30,7 +30,8 @@
 // both through L1, as thousands of tokens share a row of the time's.  Units are larger, 6 and 5 heads, as their table rows cost more.  Measured
 // (128K tokens, 64 + 8 heads, d = 128; 715 us at a copy's rate): one axis 731 us, sections of 16, 24 and 24 pairs 725, axes in turns
 // 733; units of 5 heads 759 and 812, and every lane reading every position 898 and 963.  Backward (32K tokens, 270 us): 279, 281 and 296.  The
-// rotation alone (no weights) is the same forward kernel, backward too: the gradients' rotation is the other way round.
+// rotation alone (no weights) is the same forward kernel, backward too: the gradients' rotation is the other way round.  Of fewer columns than a
+// row has it is one that copies the others (rot_dim 96: 729 us).
 #include "norm_rope.cuh"
 
 namespace ffa {

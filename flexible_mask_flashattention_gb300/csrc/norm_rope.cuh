@@ -272,7 +272,7 @@ __device__ __forceinline__ void copy_table(const NormRopeParams& p, uint32_t to,
 
 // The rotation alone, of fewer columns than a row has: a kernel of its own (AS_IS) copies the others, since the products would make NaN of what
 // stands beside an infinity there, as 0 times it.  In one kernel for all, 128K tokens of 64 + 8 heads with a norm took 738 us for 732, and the append
-// of 78K into 4 bits, read back, 176 for 171.
+// of 67K tokens of 16 + 4 into 4 bits, read back, 176 for 171.
 inline bool copies_columns(const NormRopeParams& p, int d) { return !p.w[0] && p.rot < d; }
 
 // Start the copies of one unit into `stage`.  The rows of a token without a valid position, and of none, are filled with zeros:
